@@ -1,7 +1,8 @@
-"""Build libfa.so (the CUDA library behind the C ABI in include/fa_fwd.h) in-tree.
+"""Build libfa.so (the CUDA library behind the C ABI in include/*.h) in-tree.
 
-One translation unit, one -gencode (sm_103a), linked against the static CUDA runtime;
-the driver entry point for TMA tensor maps is fetched at run time, so no libcuda link.
+Two translation units compiled at the same time, one -gencode (sm_103a), linked against the
+static CUDA runtime; the driver entry point for TMA tensor maps is fetched at run time, so no
+libcuda link.
 """
 from __future__ import annotations
 
@@ -11,10 +12,11 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = os.path.join(PKG, "csrc", "fa_fwd.cu")
-DEPS = [SRC, os.path.join(PKG, "csrc", "sm103_ptx.cuh"), os.path.join(PKG, "csrc", "fa_bwd.cuh"),
-        os.path.join(PKG, "csrc", "philox.cuh"), os.path.join(PKG, "csrc", "fa_fwd_kernel.cuh"),
-        os.path.join(ROOT, "include", "fa_fwd.h")]
+CSRC = os.path.join(PKG, "csrc")
+SRCS = [os.path.join(CSRC, "fa_fwd.cu"), os.path.join(CSRC, "fa_decoder.cu")]
+DEPS = SRCS + [os.path.join(CSRC, h) for h in ("sm103_ptx.cuh", "fa_bwd.cuh", "philox.cuh", "fa_fwd_kernel.cuh",
+                                               "fa_rope.cuh", "fa_paged.cuh", "fa_host.h")] + [
+    os.path.join(ROOT, "include", h) for h in ("fa_fwd.h", "fa_decoder.h")]
 LIB = os.path.join(PKG, "libfa.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -24,10 +26,13 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def compile_cmd(out: str, extra=()) -> list[str]:
-    return [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
-            "-I", os.path.join(ROOT, "include"), "-I", os.path.join(PKG, "csrc"),
-            *extra, SRC, "-o", out]
+def compile_cmd(src: str, out: str, extra=()) -> list[str]:
+    return [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-c", "-Xcompiler", "-fPIC",
+            "-I", os.path.join(ROOT, "include"), "-I", CSRC, *extra, src, "-o", out]
+
+
+def link_cmd(objects, out: str) -> list[str]:
+    return [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", *objects, "-o", out]
 
 
 # The same library with device-side range checks of every stream-K workspace access
@@ -46,23 +51,33 @@ def build(force: bool = False, verbose: bool = False, out: str = LIB, extra=()) 
 
 
 def build_many(targets, force: bool = False, verbose: bool = False) -> list[str]:
-    """Compile each (output, extra flags) target that is stale, all nvcc runs at once."""
+    """Compile each (output, extra flags) target that is stale, all nvcc runs at once, and link it."""
     procs = []
     for out, extra in targets:
         if force or _stale(out):
-            tmp = out + f".tmp{os.getpid()}"
-            cmd = compile_cmd(tmp, (*extra, "-Xptxas", "-v") if verbose else extra)
-            procs.append((out, tmp, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE,
-                                                     text=True)))
+            objects = [f"{out}.{os.path.basename(src)}.tmp{os.getpid()}.o" for src in SRCS]
+            flags = (*extra, "-Xptxas", "-v") if verbose else extra
+            procs.append((out, objects, [
+                subprocess.Popen(compile_cmd(src, obj, flags), stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
+                for src, obj in zip(SRCS, objects)]))
     failed = []
-    for out, tmp, pr in procs:
-        so, se = pr.communicate()
-        if pr.returncode != 0:
-            sys.stderr.write(so + se)
+    for out, objects, compiles in procs:
+        said = [pr.communicate() for pr in compiles]
+        ok = all(pr.returncode == 0 for pr in compiles)
+        if ok:
+            tmp = out + f".tmp{os.getpid()}"
+            link = subprocess.run(link_cmd(objects, tmp), capture_output=True, text=True)
+            said.append((link.stdout, link.stderr))
+            ok = link.returncode == 0
+        for obj in objects:
+            if os.path.exists(obj):
+                os.remove(obj)
+        if not ok:
+            sys.stderr.write("".join(so + se for so, se in said))
             failed.append(os.path.basename(out))
             continue
         if verbose:
-            sys.stderr.write(se)
+            sys.stderr.write("".join(se for _, se in said))
         os.replace(tmp, out)
     if failed:
         raise RuntimeError(f"nvcc failed building {', '.join(failed)}")

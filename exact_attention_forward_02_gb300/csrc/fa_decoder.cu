@@ -1,0 +1,294 @@
+// fa_decoder.cu -- the C ABI of include/fa_decoder.h: argument checks and launches. The kernels
+// live in fa_rope.cuh (norm, rotation, append) and fa_paged.cuh (attention over a paged cache).
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "fa_decoder.h"
+#include "fa_host.h"
+#include "fa_paged.cuh"
+#include "fa_rope.cuh"
+
+namespace {
+
+using namespace fa;
+
+bool aligned16(const void* ptr) { return ((uintptr_t)ptr & 15) == 0; }
+bool aligned4(const void* ptr) { return ((uintptr_t)ptr & 3) == 0; }
+
+// Checks of one set of rows; a set with H == 0 passes.
+int check_heads(const fa_heads* h) {
+  if (h->H < 0) return FA_ERR_SHAPE;
+  if (h->H == 0) return FA_OK;
+  if (!h->ptr) return FA_ERR_NULL;
+  if (!aligned16(h->ptr) || ((h->batch_stride | h->token_stride | h->head_stride) & 7)) return FA_ERR_ALIGN;
+  return FA_OK;
+}
+
+int check_rope(const fa_rope* r, int d) {
+  if (!r || !r->table) return FA_OK;
+  if (r->length < 0 || r->rot_dim < 0 || r->rot_dim > d || r->rot_dim % 16) return FA_ERR_RANGE;
+  return aligned16(r->table) ? FA_OK : FA_ERR_ALIGN;
+}
+
+int check_kv(const fa_paged_kv* kv) {
+  if (kv->d != 64 && kv->d != 128) return FA_ERR_HEAD_DIM;
+  if (kv->num_pages < 0 || kv->Hkv < 0) return FA_ERR_SHAPE;
+  const int ps = kv->page_size;
+  if (ps <= 0 || !(ps % 128 == 0 || (ps < 128 && ps >= 8 && (ps & (ps - 1)) == 0))) return FA_ERR_RANGE;
+  if (kv->num_pages == 0 || kv->Hkv == 0) return FA_OK;
+  if (!kv->k || !kv->v) return FA_ERR_NULL;
+  if (!aligned16(kv->k) || !aligned16(kv->v) || ((kv->page_stride | kv->head_stride | kv->token_stride) & 7))
+    return FA_ERR_ALIGN;
+  return FA_OK;
+}
+
+HeadsDev dev(const fa_heads* h) {
+  return HeadsDev{static_cast<uint16_t*>(h->ptr), h->batch_stride, h->token_stride, h->head_stride, h->H};
+}
+RopeDev dev(const fa_rope* r) {
+  if (!r || !r->table) return RopeDev{nullptr, 0, 0};
+  return RopeDev{r->table, r->length, r->rot_dim};
+}
+
+// Heads per warp: all of them (their angles are then loaded once a token), halved while the
+// tokens alone do not give the SMs enough warps to cover the memory latency.
+int head_chunk(long long tokens, int heads, int rows_per_step, int sms) {
+  int chunk = heads;
+  while (chunk > rows_per_step && tokens * ((heads + chunk - 1) / chunk) < (long long)sms * 48) chunk = (chunk + 1) / 2;
+  return chunk;
+}
+
+// f(type, interleaved) for the four instantiations of a kernel of head dimension D
+template <typename F>
+int by_type(bool bf16, bool inter, F f) {
+  if (bf16) return inter ? f(std::true_type{}, std::true_type{}) : f(std::true_type{}, std::false_type{});
+  return inter ? f(std::false_type{}, std::true_type{}) : f(std::false_type{}, std::false_type{});
+}
+
+int norm_rope_args(const fa_heads* const* sets, int n, int B, int N, int d, const void* wq, const void* wk,
+                   float eps, const fa_rope* rope, const int* positions, fa_dtype dtype, bool* noop) {
+  *noop = false;
+  if (dtype != FA_F16 && dtype != FA_BF16) return FA_ERR_DTYPE;
+  if (d != 64 && d != 128) return FA_ERR_HEAD_DIM;
+  if (B < 0 || N < 0) return FA_ERR_SHAPE;
+  if (!(eps >= 0.f) || !isfinite(eps)) return FA_ERR_RANGE;
+  int rc = check_rope(rope, d);
+  if (rc != FA_OK) return rc;
+  for (int i = 0; i < n; ++i)
+    if (!sets[i]) return FA_ERR_NULL;
+  const int Hq = sets[0]->H, Hk = sets[1]->H;
+  for (int i = 0; i < n; ++i)  // q, k, q, k, ...
+    if (sets[i]->H != (i & 1 ? Hk : Hq)) return FA_ERR_SHAPE;
+  if (Hq < 0 || Hk < 0 || (long long)Hq + Hk > 0x7fffffffLL) return FA_ERR_SHAPE;
+  if (B == 0 || N == 0 || Hq + Hk == 0) { *noop = true; return FA_OK; }
+  const long long tokens = (long long)B * N;
+  if (tokens > 0x7fffffffLL || tokens * ((long long)Hq + Hk) > 0x7fffffffLL * ROW_WARPS) return FA_ERR_SHAPE;
+  for (int i = 0; i < n; ++i)
+    if ((rc = check_heads(sets[i])) != FA_OK) return rc;
+  if ((Hq && !wq) || (Hk && !wk)) return FA_ERR_NULL;
+  if ((Hq && !aligned16(wq)) || (Hk && !aligned16(wk)) || !aligned4(positions)) return FA_ERR_ALIGN;
+  return FA_OK;
+}
+
+NormRopeParams norm_rope_params(const fa_heads* q, const fa_heads* k, const fa_heads* qo, const fa_heads* ko, int B,
+                                int N, const void* wq, const void* wk, float eps, const fa_rope* rope,
+                                const int* positions) {
+  NormRopeParams p = {};
+  p.q = dev(q);
+  p.k = dev(k);
+  p.q_out = dev(qo);
+  p.k_out = dev(ko);
+  p.wq = static_cast<const uint16_t*>(wq);
+  p.wk = static_cast<const uint16_t*>(wk);
+  p.eps = eps;
+  p.rope = dev(rope);
+  p.positions = positions;
+  p.N = N;
+  p.tokens = (long long)B * N;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_qk_norm_rope(const fa_heads* q, const fa_heads* k, const fa_heads* q_out, const fa_heads* k_out, int B,
+                    int N, int d, const void* wq, const void* wk, float eps, const fa_rope* rope,
+                    const int* positions, fa_dtype dtype, void* stream) {
+  const fa_heads* sets[4] = {q, k, q_out, k_out};
+  bool noop = false;
+  int rc = norm_rope_args(sets, 4, B, N, d, wq, wk, eps, rope, positions, dtype, &noop);
+  if (rc != FA_OK || noop) return rc;
+  int index = 0, sms = 0;
+  if ((rc = fa_host::current_device(&index, &sms)) != FA_OK) return rc;
+  NormRopeParams p = norm_rope_params(q, k, q_out, k_out, B, N, wq, wk, eps, rope, positions);
+  if ((rc = fa_host::status_word(&p.status)) != FA_OK) return rc;
+  const int H = q->H + k->H;
+  p.chunk = head_chunk(p.tokens, H, 256 / d, sms);
+  p.n_chunks = (H + p.chunk - 1) / p.chunk;
+  const unsigned grid = (unsigned)((p.tokens * p.n_chunks + ROW_WARPS - 1) / ROW_WARPS);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return by_type(dtype == FA_BF16, rope && rope->interleaved, [&](auto bf, auto inter) {
+    if (d == 64) fa_norm_rope_kernel<64, bf, inter><<<grid, ROW_THREADS, 0, st>>>(p);
+    else fa_norm_rope_kernel<128, bf, inter><<<grid, ROW_THREADS, 0, st>>>(p);
+    return fa_host::launched(cudaPeekAtLastError());
+  });
+}
+
+size_t fa_qk_norm_rope_bwd_workspace_bytes(int d) {
+  return d == 64 || d == 128 ? (size_t)ROW_BWD_MAX_BLOCKS * 2 * d * sizeof(float) : 0;
+}
+
+int fa_qk_norm_rope_bwd(const fa_heads* dq_out, const fa_heads* dk_out, const fa_heads* q, const fa_heads* k,
+                        const fa_heads* dq, const fa_heads* dk, float* dwq, float* dwk, int B, int N, int d,
+                        const void* wq, const void* wk, float eps, const fa_rope* rope, const int* positions,
+                        fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  const fa_heads* sets[6] = {dq_out, dk_out, q, k, dq, dk};
+  bool noop = false;
+  int rc = norm_rope_args(sets, 6, B, N, d, wq, wk, eps, rope, positions, dtype, &noop);
+  if (rc != FA_OK) return rc;
+  if ((q->H && !dwq) || (k->H && !dwk)) return FA_ERR_NULL;
+  if (!aligned4(dwq) || !aligned4(dwk)) return FA_ERR_ALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (noop) {  // no rows: the weights' gradients are sums over nothing
+    if (q->H && cudaMemsetAsync(dwq, 0, d * sizeof(float), st) != cudaSuccess) return FA_ERR_CUDA;
+    if (k->H && cudaMemsetAsync(dwk, 0, d * sizeof(float), st) != cudaSuccess) return FA_ERR_CUDA;
+    return FA_OK;
+  }
+  if (!workspace || workspace_bytes < fa_qk_norm_rope_bwd_workspace_bytes(d)) return FA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return FA_ERR_ALIGN;
+  int index = 0, sms = 0;
+  if ((rc = fa_host::current_device(&index, &sms)) != FA_OK) return rc;
+  NormRopeParams p = norm_rope_params(q, k, dq, dk, B, N, wq, wk, eps, rope, positions);
+  if ((rc = fa_host::status_word(&p.status)) != FA_OK) return rc;
+  p.gq = dev(dq_out);
+  p.gk = dev(dk_out);
+  p.part = static_cast<float*>(workspace);
+  const int H = q->H + k->H;
+  p.chunk = head_chunk(p.tokens, H, 256 / d, sms);
+  p.n_chunks = (H + p.chunk - 1) / p.chunk;
+  const long long blocks = (p.tokens * p.n_chunks + ROW_WARPS - 1) / ROW_WARPS;
+  int grid = 4 * sms < ROW_BWD_MAX_BLOCKS ? 4 * sms : ROW_BWD_MAX_BLOCKS;
+  if (blocks < grid) grid = (int)blocks;
+  float* oq = q->H ? dwq : nullptr;
+  float* ok = k->H ? dwk : nullptr;
+  return by_type(dtype == FA_BF16, rope && rope->interleaved, [&](auto bf, auto inter) {
+    if (d == 64) fa_norm_rope_bwd_kernel<64, bf, inter><<<grid, ROW_THREADS, 0, st>>>(p);
+    else fa_norm_rope_bwd_kernel<128, bf, inter><<<grid, ROW_THREADS, 0, st>>>(p);
+    const int rc1 = fa_host::launched(cudaPeekAtLastError());
+    if (rc1 != FA_OK) return rc1;
+    if (d == 64) fa_norm_rope_dw_kernel<64><<<4, dim3(32, 32), 0, st>>>(p.part, grid, oq, ok);
+    else fa_norm_rope_dw_kernel<128><<<8, dim3(32, 32), 0, st>>>(p.part, grid, oq, ok);
+    return fa_host::launched(cudaPeekAtLastError());
+  });
+}
+
+int fa_paged_append(const fa_paged_kv* kv, const fa_heads* k, const fa_heads* v, int B, int T, const int* cu_seqlens,
+                    const int* seq_lens, const int* block_table, int table_stride, const fa_rope* rope,
+                    fa_dtype dtype, void* stream) {
+  if (dtype != FA_F16 && dtype != FA_BF16) return FA_ERR_DTYPE;
+  if (!kv || !k || !v) return FA_ERR_NULL;
+  int rc = check_kv(kv);
+  if (rc != FA_OK) return rc;
+  if (B < 0 || T < 0 || table_stride < 0 || k->H != kv->Hkv || v->H != kv->Hkv) return FA_ERR_SHAPE;
+  if ((rc = check_rope(rope, kv->d)) != FA_OK) return rc;
+  if (B == 0 || T == 0 || kv->Hkv == 0) return FA_OK;
+  if ((long long)T * 2 * kv->Hkv > 0x7fffffffLL || B == 0x7fffffff) return FA_ERR_SHAPE;
+  if ((rc = check_heads(k)) != FA_OK || (rc = check_heads(v)) != FA_OK) return rc;
+  if (!cu_seqlens || !seq_lens || (!block_table && table_stride)) return FA_ERR_NULL;
+  if (!aligned4(cu_seqlens) || !aligned4(seq_lens) || !aligned4(block_table)) return FA_ERR_ALIGN;
+  int index = 0, sms = 0;
+  if ((rc = fa_host::current_device(&index, &sms)) != FA_OK) return rc;
+  AppendParams p = {};
+  if ((rc = fa_host::status_word(&p.status)) != FA_OK) return rc;
+  p.k = dev(k);
+  p.v = dev(v);
+  p.kp = static_cast<uint16_t*>(kv->k);
+  p.vp = static_cast<uint16_t*>(kv->v);
+  p.page_stride = kv->page_stride;
+  p.head_stride = kv->head_stride;
+  p.token_stride = kv->token_stride;
+  p.num_pages = kv->num_pages;
+  p.page_size = kv->page_size;
+  p.cu = cu_seqlens;
+  p.lens = seq_lens;
+  p.table = block_table;
+  p.table_stride = table_stride;
+  p.B = B;
+  p.T = T;
+  p.rope = dev(rope);
+  p.chunk = head_chunk(T, 2 * kv->Hkv, 256 / kv->d, sms);
+  p.n_chunks = (2 * kv->Hkv + p.chunk - 1) / p.chunk;
+  const unsigned grid = (unsigned)(((long long)T * p.n_chunks + ROW_WARPS - 1) / ROW_WARPS);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return by_type(dtype == FA_BF16, rope && rope->interleaved, [&](auto bf, auto inter) {
+    if (kv->d == 64) fa_paged_append_kernel<64, bf, inter><<<grid, ROW_THREADS, 0, st>>>(p);
+    else fa_paged_append_kernel<128, bf, inter><<<grid, ROW_THREADS, 0, st>>>(p);
+    return fa_host::launched(cudaPeekAtLastError());
+  });
+}
+
+size_t fa_fwd_paged_workspace_bytes(int Hq, int Hkv, int d, int max_q) {
+  (void)Hq, (void)Hkv, (void)d, (void)max_q;
+  return 0;
+}
+
+int fa_fwd_paged(const fa_paged_kv* kv, const fa_heads* q, const fa_heads* O, float* L, int B, int T, int max_q,
+                 const int* cu_seqlens, const int* seq_lens, const int* block_table, int table_stride, float scale,
+                 int causal, fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  if (dtype != FA_F16 && dtype != FA_BF16) return FA_ERR_DTYPE;
+  if (!kv || !q || !O) return FA_ERR_NULL;
+  int rc = check_kv(kv);
+  if (rc != FA_OK) return rc;
+  if (B < 0 || T < 0 || table_stride < 0 || max_q < 1 || q->H < 0 || q->H != O->H) return FA_ERR_SHAPE;
+  if (!(scale >= 0.f) || !isfinite(scale)) return FA_ERR_SCALE;
+  if (B == 0 || T == 0 || q->H == 0) return FA_OK;
+  if (kv->Hkv == 0 || q->H % kv->Hkv || q->H / kv->Hkv > 128 || B == 0x7fffffff ||
+      (long long)T * q->H > 0x7fffffffLL)
+    return FA_ERR_SHAPE;
+  if ((rc = check_heads(q)) != FA_OK || (rc = check_heads(O)) != FA_OK) return rc;
+  if (!cu_seqlens || !seq_lens || (!block_table && table_stride)) return FA_ERR_NULL;
+  if (!aligned4(cu_seqlens) || !aligned4(seq_lens) || !aligned4(block_table) || !aligned4(L)) return FA_ERR_ALIGN;
+  (void)workspace, (void)workspace_bytes, (void)max_q;
+  int index = 0, sms = 0;
+  if ((rc = fa_host::current_device(&index, &sms)) != FA_OK) return rc;
+  PagedParams p = {};
+  if ((rc = fa_host::status_word(&p.status)) != FA_OK) return rc;
+  p.q = dev(q);
+  p.o = dev(O);
+  p.L = L;
+  p.kp = static_cast<const uint16_t*>(kv->k);
+  p.vp = static_cast<const uint16_t*>(kv->v);
+  p.page_stride = kv->page_stride;
+  p.head_stride = kv->head_stride;
+  p.token_stride = kv->token_stride;
+  p.num_pages = kv->num_pages;
+  p.page_size = kv->page_size;
+  p.Hkv = kv->Hkv;
+  p.G = q->H / kv->Hkv;
+  p.cu = cu_seqlens;
+  p.lens = seq_lens;
+  p.table = block_table;
+  p.table_stride = table_stride;
+  p.B = B;
+  p.T = T;
+  p.c = scale * 1.4426950408889634f;
+  p.causal = causal != 0;
+  const unsigned grid = (unsigned)(((long long)T * q->H + 7) / 8);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool bf16 = dtype == FA_BF16;
+  if (kv->d == 64) {
+    if (bf16) fa_paged_simple_kernel<64, true><<<grid, 256, 0, st>>>(p);
+    else fa_paged_simple_kernel<64, false><<<grid, 256, 0, st>>>(p);
+  } else {
+    if (bf16) fa_paged_simple_kernel<128, true><<<grid, 256, 0, st>>>(p);
+    else fa_paged_simple_kernel<128, false><<<grid, 256, 0, st>>>(p);
+  }
+  return fa_host::launched(cudaPeekAtLastError());
+}
+
+}  // extern "C"

@@ -12,6 +12,7 @@
 
 #include "fa_fwd.h"
 #include "fa_fwd_kernel.cuh"
+#include "fa_host.h"
 
 // Fixed scratch of fa_fwd_noalloc: the stream-K workspace for callers that cannot
 // allocate device memory. Every device that loads the library holds it until exit.
@@ -568,7 +569,48 @@ HostChunks host_chunks(long long BH, int Nq, int Nk, int d) {
   return c;
 }
 
+// Device address of the status word, looked up once per device (with that device current).
+int* g_status_addr[kMaxDevices] = {};
+
 }  // namespace
+
+// What the library's other translation units use of this one.
+namespace fa_host {
+
+static_assert(MAX_DEVICES == kMaxDevices, "one device limit");
+
+int current_device(int* index, int* sms) {
+  DeviceInfo* di = nullptr;
+  const int rc = device_info(&di);
+  if (rc != FA_OK) return rc;
+  *index = (int)(di - g_dev);
+  *sms = di->sms;
+  return FA_OK;
+}
+
+int status_word(int** out) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FA_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(g_dev_mu);
+  if (!g_status_addr[dev]) {
+    void* ptr = nullptr;
+    if (cudaGetSymbolAddress(&ptr, g_fa_status) != cudaSuccess || !ptr) return FA_ERR_CUDA;
+    g_status_addr[dev] = static_cast<int*>(ptr);
+  }
+  *out = g_status_addr[dev];
+  return FA_OK;
+}
+
+int launched(cudaError_t e) {
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+unsigned long long wait_limit_ns() { return ::wait_limit_ns(); }
+
+EncodeTiledFn encode_tiled() { return get_encode_fn(); }
+
+}  // namespace fa_host
 
 extern "C" {
 
