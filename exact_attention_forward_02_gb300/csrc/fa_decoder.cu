@@ -5,6 +5,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+#include <mutex>
 #include <type_traits>
 
 #include "fa_decoder.h"
@@ -110,6 +112,84 @@ NormRopeParams norm_rope_params(const fa_heads* q, const fa_heads* k, const fa_h
   p.N = N;
   p.tokens = (long long)B * N;
   return p;
+}
+
+// ------------------------------------------------------------------------- paged attention
+// The kernel form for groups of G query heads and at most max_q new tokens: 0 = PAIR, else SPLIT
+// with that many copies of each row, as many as fit into a tile of 128 rows (up to 4).
+int paged_form(int G, int max_q) {
+  const long long rows = (long long)G * max_q;
+  return rows <= 32 ? 4 : rows <= 64 ? 2 : rows <= 128 ? 1 : 0;
+}
+size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
+size_t paged_records_bytes(int sms) { return round256((size_t)sms * 8 * sizeof(int)); }
+size_t paged_parts_bytes(int sms, int d, int form) {
+  return round256((size_t)sms * 2 * paged::part_floats(d, form == 0 ? 256 : 128 / form) * sizeof(float));
+}
+
+// A tensor of 16-bit rows of d elements with `dims - 1` outer axes; boxes of 64 columns, 128-byte
+// swizzle. The stride of an axis of one element is never used; any valid one stands in for it.
+int paged_map(CUtensorMap* m, const void* base, bool bf16, int dims, int d, std::initializer_list<uint64_t> size,
+              std::initializer_list<long long> stride, std::initializer_list<uint32_t> box) {
+  fa_host::EncodeTiledFn enc = fa_host::encode_tiled();
+  if (!enc) return FA_ERR_TENSOR_MAP;
+  cuuint64_t gd[4] = {(cuuint64_t)d}, gs[3];
+  cuuint32_t bx[4] = {64}, es[4] = {1, 1, 1, 1};
+  for (int i = 0; i < dims - 1; ++i) {
+    gd[i + 1] = size.begin()[i];
+    const long long s = stride.begin()[i];
+    if (gd[i + 1] > 1 && s <= 0) return FA_ERR_TENSOR_MAP;
+    gs[i] = gd[i + 1] > 1 ? (cuuint64_t)s * 2 : (cuuint64_t)d * 2;
+    bx[i + 1] = box.begin()[i];
+  }
+  const CUresult r = enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dims,
+                         const_cast<void*>(base), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_TENSOR_MAP;
+}
+
+std::mutex g_attr_mu;
+
+template <int D, bool BF16, bool SPLIT, int REP>
+int launch_paged(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const paged::Params& p,
+                 int index, int sms, cudaStream_t st) {
+  constexpr int SMEM = paged::Layout<D, SPLIT>::SMEM_BYTES, ROWS = SPLIT ? 128 / REP : 256;
+  auto kern = paged::fa_paged_kernel<D, BF16, SPLIT, REP>;
+  static bool attr_set[fa_host::MAX_DEVICES] = {};
+  {
+    std::lock_guard<std::mutex> lk(g_attr_mu);
+    if (!attr_set[index]) {
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess)
+        return FA_ERR_CUDA;
+      attr_set[index] = true;
+    }
+  }
+  kern<<<sms, paged::NUM_THREADS, SMEM, st>>>(mq, mk, mv, p);
+  const int rc = fa_host::launched(cudaPeekAtLastError());
+  if (rc != FA_OK) return rc;
+  // its blocks may be set up while the main kernel runs; they wait for its results on the device
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sms, ROWS / 8 < 8 ? ROWS / 8 : 8);
+  cfg.blockDim = dim3(paged::COMBINE_THREADS);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return fa_host::launched(cudaLaunchKernelEx(&cfg, paged::fa_paged_combine_kernel<D, BF16, ROWS>, p));
+}
+
+template <int D, bool BF16>
+int paged_forms(int form, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                const paged::Params& p, int index, int sms, cudaStream_t st) {
+  switch (form) {
+    case 4: return launch_paged<D, BF16, true, 4>(mq, mk, mv, p, index, sms, st);
+    case 2: return launch_paged<D, BF16, true, 2>(mq, mk, mv, p, index, sms, st);
+    case 1: return launch_paged<D, BF16, true, 1>(mq, mk, mv, p, index, sms, st);
+    default: return launch_paged<D, BF16, false, 1>(mq, mk, mv, p, index, sms, st);
+  }
 }
 
 }  // namespace
@@ -233,8 +313,10 @@ int fa_paged_append(const fa_paged_kv* kv, const fa_heads* k, const fa_heads* v,
 }
 
 size_t fa_fwd_paged_workspace_bytes(int Hq, int Hkv, int d, int max_q) {
-  (void)Hq, (void)Hkv, (void)d, (void)max_q;
-  return 0;
+  int index = 0, sms = 0;
+  if ((d != 64 && d != 128) || Hkv <= 0 || Hq <= 0 || Hq % Hkv || Hq / Hkv > 128 || max_q < 1) return 0;
+  if (fa_host::current_device(&index, &sms) != FA_OK) return 0;
+  return paged_records_bytes(sms) + paged_parts_bytes(sms, d, paged_form(Hq / Hkv, max_q));
 }
 
 int fa_fwd_paged(const fa_paged_kv* kv, const fa_heads* q, const fa_heads* O, float* L, int B, int T, int max_q,
@@ -253,42 +335,47 @@ int fa_fwd_paged(const fa_paged_kv* kv, const fa_heads* q, const fa_heads* O, fl
   if ((rc = check_heads(q)) != FA_OK || (rc = check_heads(O)) != FA_OK) return rc;
   if (!cu_seqlens || !seq_lens || (!block_table && table_stride)) return FA_ERR_NULL;
   if (!aligned4(cu_seqlens) || !aligned4(seq_lens) || !aligned4(block_table) || !aligned4(L)) return FA_ERR_ALIGN;
-  (void)workspace, (void)workspace_bytes, (void)max_q;
+  if ((uintptr_t)workspace & 255) return FA_ERR_ALIGN;
   int index = 0, sms = 0;
   if ((rc = fa_host::current_device(&index, &sms)) != FA_OK) return rc;
-  PagedParams p = {};
+  const int G = q->H / kv->Hkv, form = paged_form(G, max_q);
+  if (!workspace || workspace_bytes < paged_records_bytes(sms) + paged_parts_bytes(sms, kv->d, form))
+    return FA_ERR_WORKSPACE;
+  paged::Params p = {};
   if ((rc = fa_host::status_word(&p.status)) != FA_OK) return rc;
-  p.q = dev(q);
   p.o = dev(O);
   p.L = L;
-  p.kp = static_cast<const uint16_t*>(kv->k);
-  p.vp = static_cast<const uint16_t*>(kv->v);
-  p.page_stride = kv->page_stride;
-  p.head_stride = kv->head_stride;
-  p.token_stride = kv->token_stride;
   p.num_pages = kv->num_pages;
   p.page_size = kv->page_size;
+  p.box_keys = kv->page_size < 128 ? kv->page_size : 128;
   p.Hkv = kv->Hkv;
-  p.G = q->H / kv->Hkv;
+  p.G = G;
+  p.tpt = (form == 0 ? 128 : 128 / form) / G;
   p.cu = cu_seqlens;
   p.lens = seq_lens;
   p.table = block_table;
   p.table_stride = table_stride;
   p.B = B;
   p.T = T;
-  p.c = scale * 1.4426950408889634f;
   p.causal = causal != 0;
-  const unsigned grid = (unsigned)(((long long)T * q->H + 7) / 8);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  p.c = scale * 1.4426950408889634f;
+  p.wait_limit_ns = fa_host::wait_limit_ns();
+  p.records = static_cast<int*>(workspace);
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + paged_records_bytes(sms));
   const bool bf16 = dtype == FA_BF16;
-  if (kv->d == 64) {
-    if (bf16) fa_paged_simple_kernel<64, true><<<grid, 256, 0, st>>>(p);
-    else fa_paged_simple_kernel<64, false><<<grid, 256, 0, st>>>(p);
-  } else {
-    if (bf16) fa_paged_simple_kernel<128, true><<<grid, 256, 0, st>>>(p);
-    else fa_paged_simple_kernel<128, false><<<grid, 256, 0, st>>>(p);
-  }
-  return fa_host::launched(cudaPeekAtLastError());
+  CUtensorMap mq, mk, mv;
+  // Q as [T, Hq, d]: a box is 64 columns of the G heads of a key head for tpt tokens
+  if ((rc = paged_map(&mq, q->ptr, bf16, 3, kv->d, {(uint64_t)q->H, (uint64_t)T}, {q->head_stride, q->token_stride},
+                      {(uint32_t)G, (uint32_t)p.tpt})) != FA_OK)
+    return rc;
+  for (int i = 0; i < 2; ++i)
+    if ((rc = paged_map(i ? &mv : &mk, i ? kv->v : kv->k, bf16, 4, kv->d,
+                        {(uint64_t)kv->page_size, (uint64_t)kv->Hkv, (uint64_t)kv->num_pages},
+                        {kv->token_stride, kv->head_stride, kv->page_stride}, {(uint32_t)p.box_keys, 1, 1})) != FA_OK)
+      return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (kv->d == 64) return bf16 ? paged_forms<64, true>(form, mq, mk, mv, p, index, sms, st) : paged_forms<64, false>(form, mq, mk, mv, p, index, sms, st);
+  return bf16 ? paged_forms<128, true>(form, mq, mk, mv, p, index, sms, st) : paged_forms<128, false>(form, mq, mk, mv, p, index, sms, st);
 }
 
 }  // extern "C"

@@ -316,23 +316,6 @@ __device__ __forceinline__ bool sched_next(Sched& s, Item& it, const Params& p) 
   return true;
 }
 
-// Maximum of the N values of t as a balanced tree of three-input maxima; t is consumed.
-template <int N>
-__device__ __forceinline__ float tree_max(float* t) {
-  if constexpr (N == 1) {
-    return t[0];
-  } else {
-    constexpr int M = (N + 2) / 3;
-#pragma unroll
-    for (int i = 0; i < M; ++i) {
-      const float y = 3 * i + 1 < N ? t[3 * i + 1] : -INFINITY;
-      const float z = 3 * i + 2 < N ? t[3 * i + 2] : -INFINITY;
-      t[i] = max3(t[3 * i], y, z);
-    }
-    return tree_max<M>(t);
-  }
-}
-
 // ----------------------------------------------------------------------------- kernel
 // BF16: type of O (and of Q, K, V unless FP8). FP8: Q, K are E4M3 [BH, N, D] and tmV maps
 // V^T, E4M3 [BH, D, ldvt] (keys contiguous), so that V is a K-major operand of P V.

@@ -66,7 +66,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
       "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-// same, with an L2 cache-policy hint (createpolicy result)
+// 4-D tiled load of one box
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar,
+                                            int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+// 3-D load with an L2 cache-policy hint (createpolicy result)
 __device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const CUtensorMap* m, uint32_t bar,
                                                  int x, int y, int z, uint64_t policy) {
   asm volatile(
@@ -124,6 +133,18 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
 __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, float (&x)[4]) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// ----------------------------------------------------------------------------- dependent launches
+// let the next kernel of the stream start its blocks; wait for the previous one's results
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ----------------------------------------------------------------------------- TMEM
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
@@ -322,6 +343,22 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+// Maximum of the N values of t as a balanced tree of three-input maxima; t is consumed.
+template <int N>
+__device__ __forceinline__ float tree_max(float* t) {
+  if constexpr (N == 1) {
+    return t[0];
+  } else {
+    constexpr int M = (N + 2) / 3;
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      const float y = 3 * i + 1 < N ? t[3 * i + 1] : -INFINITY;
+      const float z = 3 * i + 2 < N ? t[3 * i + 2] : -INFINITY;
+      t[i] = max3(t[3 * i], y, z);
+    }
+    return tree_max<M>(t);
+  }
 }
 // packed pairs of fp32 in one 64-bit register (sm_100+ f32x2 arithmetic)
 __device__ __forceinline__ uint64_t f2(float lo, float hi) {
