@@ -25,6 +25,8 @@ LIB_PATH = os.path.join(PKG, "libfa.so")
 # recorded as FA_ERR_BOUNDS. Tests load it with load_library; FA_LIBRARY=debug in the
 # environment makes it the library this module binds.
 DEBUG_LIB_PATH = os.path.join(PKG, "libfa_debug.so")
+# The native tensor-level calls of the decoder-block operators (csrc/fa_torch.cpp).
+TORCH_CALLS_PATH = os.path.join(PKG, "_fa_torch.so")
 
 FA_F16 = 0
 FA_BF16 = 1
@@ -148,6 +150,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     return lib
 
 
+if not os.path.exists(TORCH_CALLS_PATH):
+    raise ImportError(f"{os.path.basename(TORCH_CALLS_PATH)} is not built ({TORCH_CALLS_PATH} missing); run "
+                      "__graft_entry__.build() first. There is no fallback implementation.")
 _choice = os.environ.get("FA_LIBRARY", "release")
 if _choice not in ("release", "debug"):
     raise ImportError(f"FA_LIBRARY must be 'release' or 'debug', not {_choice!r}")
@@ -374,108 +379,21 @@ def fa_fwd_paged_workspace_bytes(Hq, Hkv, d, max_q) -> int:
     return int(lib.fa_fwd_paged_workspace_bytes(int(Hq), int(Hkv), int(d), int(max_q)))
 
 
-def _type_code(t, what):
-    import torch
-
-    if t.dtype == torch.bfloat16:
-        return FA_BF16
-    if t.dtype == torch.float16:
-        return FA_F16
-    raise TypeError(f"{what} must be float16 or bfloat16")
+_torch_calls = None
 
 
-def _heads(t, what, dtype, shape=None, written=False):
-    """fa_heads of a [..., tokens, heads, d] tensor (3 or 4 dimensions)."""
-    if t.dtype != dtype:
-        raise TypeError(f"{what} must have the other tensors' dtype")
-    size, stride = t.shape, t.stride()
-    if shape is not None and tuple(size) != tuple(shape):
-        raise ValueError(f"{what} must be {list(shape)}, not {list(size)}")
-    if stride[-1] != 1 and size[-1] > 1:
-        raise ValueError(f"the elements of a row of {what} must be adjacent (stride 1)")
-    # the stride of an axis of one element is never used, and torch may report any
-    s = [0 if n <= 1 else st for n, st in zip(size[:-1], stride)]
-    if written and any(n > 1 and st == 0 for n, st in zip(size[:-1], s)):
-        raise ValueError(f"the rows of {what} must not overlap")
-    if len(s) == 2:
-        s.insert(0, 0)
-    return fa_heads(t.data_ptr(), s[0], s[1], s[2], size[-2])
+def _calls():
+    """The native tensor-level calls (csrc/fa_torch.cpp), bound to the library in use."""
+    global _torch_calls
+    if _torch_calls is None:
+        import torch  # noqa: F401  (the module links against libraries that torch loads)
 
-
-def _on_device(tensors):
-    """Every tensor (None: not given) is a CUDA tensor on the first one's device."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and (t.device != dev or not t.is_cuda):
-            raise ValueError("the tensors must be CUDA tensors on one device")
-    return dev
-
-
-def _index(t, what, shape):
-    import torch
-
-    if t.dtype != torch.int32:
-        raise TypeError(f"{what} must be int32")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous {list(shape)}, not {list(t.shape)}")
-    return t.data_ptr()
-
-
-def _rope(rope, interleaved, d):
-    """fa_rope of a [length, rot_dim] fp32 table; None for none."""
-    import torch
-
-    if rope is None:
-        return None
-    if rope.dtype != torch.float32:
-        raise TypeError("rope must be float32")
-    if rope.dim() != 2 or not rope.is_contiguous() or rope.shape[1] % 16 or rope.shape[1] > d:
-        raise ValueError("rope must be a contiguous [length, rot_dim] table, rot_dim a multiple of 16 up to d")
-    return fa_rope(rope.data_ptr(), rope.shape[0], rope.shape[1], int(bool(interleaved)))
-
-
-def _cache(k_pages, v_pages, dtype):
-    """fa_paged_kv of [num_pages, Hkv, page_size, d] tensors with the same strides."""
-    if k_pages.dtype != dtype or v_pages.dtype != dtype:
-        raise TypeError("the cache must have the other tensors' dtype")
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
-        raise ValueError("k_pages and v_pages must both be [num_pages, Hkv, page_size, d]")
-    size, ks, vs = k_pages.shape, k_pages.stride(), v_pages.stride()
-    if any(n > 1 and a != b for n, a, b in zip(size, ks, vs)):
-        raise ValueError("k_pages and v_pages must have the same strides")
-    if ks[3] != 1 and size[3] > 1:
-        raise ValueError("the elements of a cached row must be adjacent (stride 1)")
-    s = [0 if n <= 1 else a for n, a in zip(size, ks)]
-    return fa_paged_kv(k_pages.data_ptr(), v_pages.data_ptr(), s[0], s[1], s[2], size[0], size[2], size[1], size[3])
-
-
-def _table(block_table, B):
-    """(pointer, width) of a [B, width] int32 table."""
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, pages per sequence]")
-    return _index(block_table, "block_table", (B, block_table.shape[1])), block_table.shape[1]
-
-
-class _Launch:
-    """The device and stream of a call: what is allocated inside belongs to that stream."""
-
-    def __init__(self, device, stream):
-        import torch
-
-        self.device = torch.cuda.device(device)
-        self.inner = None if stream is None else torch.cuda.stream(stream)
-        self.stream = stream or torch.cuda.current_stream(device)
-
-    def __enter__(self):
-        self.device.__enter__()
-        if self.inner is not None:
-            self.inner.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
-
-    def __exit__(self, *exc):
-        if self.inner is not None:
-            self.inner.__exit__(*exc)
-        self.device.__exit__(*exc)
+        from . import _fa_torch
+        names = ("fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_bytes", "fa_paged_append",
+                 "fa_fwd_paged", "fa_fwd_paged_workspace_bytes")
+        _fa_torch.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
+        _torch_calls = _fa_torch
+    return _torch_calls
 
 
 def qk_norm_rope(q, k, wq, wk, rope=None, positions=None, eps: float = 1e-6, interleaved: bool = False,
@@ -487,34 +405,13 @@ def qk_norm_rope(q, k, wq, wk, rope=None, positions=None, eps: float = 1e-6, int
     [length, rot_dim] table (cosines, then sines; see include/fa_decoder.h), None: no rotation;
     positions: int32 [B, N], None: 0 .. N-1. Returns (q_out, k_out), allocated as contiguous
     [B, N, H, d] unless given (transposed views, and q and k themselves, are allowed).
+    Launches on `stream` (a torch.cuda.Stream, default: the current one); what it allocates
+    belongs to that stream.
     """
-    import torch
-
-    dt = _type_code(q, "q and k")
-    if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
-        raise ValueError("q and k must be [B, N, H, d] with the same B, N and d")
-    B, N, _, d = q.shape
-    hq, hk = _heads(q, "q", q.dtype), _heads(k, "k", q.dtype)
-    if wq.dtype != q.dtype or wk.dtype != q.dtype:
-        raise TypeError("wq and wk must have q's dtype")
-    if tuple(wq.shape) != (d,) or tuple(wk.shape) != (d,) or not wq.is_contiguous() or not wk.is_contiguous():
-        raise ValueError("wq and wk must be contiguous [d]")
-    rp = _rope(rope, interleaved, d)
-    pos = None if positions is None else _index(positions, "positions", (B, N))
-    oq = None if q_out is None else _heads(q_out, "q_out", q.dtype, q.shape, written=True)
-    ok = None if k_out is None else _heads(k_out, "k_out", q.dtype, k.shape, written=True)
-    dev = _on_device((q, k, wq, wk, rope, positions, q_out, k_out))
-    with _Launch(dev, stream) as st:
-        if oq is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            oq = _heads(q_out, "q_out", q.dtype)
-        if ok is None:
-            k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
-            ok = _heads(k_out, "k_out", q.dtype)
-        rc = fa_qk_norm_rope(hq, hk, oq, ok, B, N, d, wq.data_ptr(), wk.data_ptr(), eps, rp, pos, dt, st)
-    if rc != 0:
-        raise FAError(rc, "fa_qk_norm_rope")
-    return q_out, k_out
+    r = _calls().norm_rope(q, k, wq, wk, rope, positions, eps, interleaved, q_out, k_out, stream)
+    if type(r) is int:
+        raise FAError(r, "fa_qk_norm_rope")
+    return r
 
 
 def qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, rope=None, positions=None, eps: float = 1e-6,
@@ -524,39 +421,10 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, wq, wk, rope=None, positions=Non
     dq_out [B, N, Hq, d] and dk_out [B, N, Hk, d] with any strides; dq and dk are allocated as
     contiguous [B, N, H, d] unless given; dwq and dwk are fp32 [d].
     """
-    import torch
-
-    dt = _type_code(q, "q and k")
-    if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
-        raise ValueError("q and k must be [B, N, H, d] with the same B, N and d")
-    B, N, _, d = q.shape
-    hq, hk = _heads(q, "q", q.dtype), _heads(k, "k", q.dtype)
-    gq, gk = _heads(dq_out, "dq_out", q.dtype, q.shape), _heads(dk_out, "dk_out", q.dtype, k.shape)
-    if wq.dtype != q.dtype or wk.dtype != q.dtype:
-        raise TypeError("wq and wk must have q's dtype")
-    if tuple(wq.shape) != (d,) or tuple(wk.shape) != (d,) or not wq.is_contiguous() or not wk.is_contiguous():
-        raise ValueError("wq and wk must be contiguous [d]")
-    rp = _rope(rope, interleaved, d)
-    pos = None if positions is None else _index(positions, "positions", (B, N))
-    oq = None if dq is None else _heads(dq, "dq", q.dtype, q.shape, written=True)
-    ok = None if dk is None else _heads(dk, "dk", q.dtype, k.shape, written=True)
-    dev = _on_device((q, k, wq, wk, rope, positions, dq_out, dk_out, dq, dk))
-    with _Launch(dev, stream) as st:
-        if oq is None:
-            dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            oq = _heads(dq, "dq", q.dtype)
-        if ok is None:
-            dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
-            ok = _heads(dk, "dk", q.dtype)
-        dw = torch.zeros(2, d, dtype=torch.float32, device=dev) if 0 in (hq.H, hk.H) else torch.empty(
-            2, d, dtype=torch.float32, device=dev)
-        nws = fa_qk_norm_rope_bwd_workspace_bytes(d)
-        ws = torch.empty(nws, dtype=torch.uint8, device=dev)
-        rc = fa_qk_norm_rope_bwd(gq, gk, hq, hk, oq, ok, dw.data_ptr(), dw.data_ptr() + 4 * d, B, N, d,
-                                 wq.data_ptr(), wk.data_ptr(), eps, rp, pos, dt, ws.data_ptr(), nws, st)
-    if rc != 0:
-        raise FAError(rc, "fa_qk_norm_rope_bwd")
-    return dq, dk, dw[0], dw[1]
+    r = _calls().norm_rope_backward(dq_out, dk_out, q, k, wq, wk, rope, positions, eps, interleaved, dq, dk, stream)
+    if type(r) is int:
+        raise FAError(r, "fa_qk_norm_rope_bwd")
+    return r
 
 
 def paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seq_lens, rope=None, interleaved: bool = False,
@@ -568,23 +436,9 @@ def paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seq_lens, rope
     [B + 1] and seq_lens [B] int32: sequence b's new tokens are rows cu_seqlens[b] ..
     cu_seqlens[b+1]-1, the last of its seq_lens[b] positions (see include/fa_decoder.h).
     """
-    dt = _type_code(k, "k and v")
-    if k.dim() != 3:
-        raise ValueError("k and v must be [T, Hkv, d]")
-    hk, hv = _heads(k, "k", k.dtype), _heads(v, "v", k.dtype, k.shape)
-    kv = _cache(k_pages, v_pages, k.dtype)
-    T, Hkv, d = k.shape
-    if (kv.Hkv, kv.d) != (Hkv, d):
-        raise ValueError("the cache must have k's heads and head dimension")
-    B = seq_lens.shape[0]
-    lens, cu = _index(seq_lens, "seq_lens", (B,)), _index(cu_seqlens, "cu_seqlens", (B + 1,))
-    table, width = _table(block_table, B)
-    rp = _rope(rope, interleaved, d)
-    dev = _on_device((k, v, k_pages, v_pages, block_table, cu_seqlens, seq_lens, rope))
-    with _Launch(dev, stream) as st:
-        rc = fa_paged_append(kv, hk, hv, B, T, cu, lens, table, width, rp, dt, st)
-    if rc != 0:
-        raise FAError(rc, "fa_paged_append")
+    r = _calls().append(k, v, k_pages, v_pages, block_table, cu_seqlens, seq_lens, rope, interleaved, stream)
+    if r != 0:
+        raise FAError(r, "fa_paged_append")
 
 
 def attention_paged(q, k_pages, v_pages, block_table, cu_seqlens, seq_lens, max_q: int, causal: bool = True,
@@ -597,38 +451,8 @@ def attention_paged(q, k_pages, v_pages, block_table, cu_seqlens, seq_lens, max_
     tensors allocated here: uninitialised). `workspace`: a uint8 tensor of at least
     fa_fwd_paged_workspace_bytes(...) bytes, allocated for the call when None.
     """
-    import torch
-
-    dt = _type_code(q, "q")
-    if q.dim() != 3:
-        raise ValueError("q must be [T, Hq, d]")
-    T, Hq, d = q.shape
-    hq = _heads(q, "q", q.dtype)
-    kv = _cache(k_pages, v_pages, q.dtype)
-    if kv.d != d:
-        raise ValueError("the cache must have q's head dimension")
-    B = seq_lens.shape[0]
-    lens, cu = _index(seq_lens, "seq_lens", (B,)), _index(cu_seqlens, "cu_seqlens", (B + 1,))
-    table, width = _table(block_table, B)
-    ho = None if out is None else _heads(out, "out", q.dtype, q.shape, written=True)
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous [T, Hq] float32 tensor")
-    if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous uint8 tensor")
-    dev = _on_device((q, k_pages, v_pages, block_table, cu_seqlens, seq_lens, out, lse, workspace))
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    with _Launch(dev, stream) as st:
-        if ho is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            ho = _heads(out, "out", q.dtype)
-        if lse is None:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = torch.empty(max(1, fa_fwd_paged_workspace_bytes(Hq, kv.Hkv, d, max_q)), dtype=torch.uint8,
-                                    device=dev)
-        rc = fa_fwd_paged(kv, hq, ho, lse.data_ptr(), B, T, max_q, cu, lens, table, width, scale, causal, dt,
-                          workspace.data_ptr(), workspace.numel(), st)
-    if rc != 0:
-        raise FAError(rc, "fa_fwd_paged")
-    return out, lse
+    r = _calls().attend(q, k_pages, v_pages, block_table, cu_seqlens, seq_lens, max_q, causal, scale, out, lse,
+                        workspace, stream)
+    if type(r) is int:
+        raise FAError(r, "fa_fwd_paged")
+    return r

@@ -1,6 +1,6 @@
 """Build libfa.so (the CUDA library behind the C ABI in include/*.h) in-tree.
 
-Two translation units compiled at the same time, one -gencode (sm_103a), linked against the
+Two CUDA translation units (and the host-only module of the tensor-level calls) compiled at the same time, one -gencode (sm_103a), linked against the
 static CUDA runtime; the driver entry point for TMA tensor maps is fetched at run time, so no
 libcuda link.
 """
@@ -9,6 +9,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -42,8 +43,25 @@ DEBUG_LIB = os.path.join(PKG, "libfa_debug.so")
 DEBUG_FLAGS = ("-DFA_DEBUG",)
 
 
-def _stale(out: str) -> bool:
-    return not os.path.exists(out) or any(os.path.getmtime(out) < os.path.getmtime(d) for d in DEPS)
+# The tensor-level calls: a CPython module over libtorch's C++ API, host code only.
+TORCH_SRC = os.path.join(CSRC, "fa_torch.cpp")
+TORCH_DEPS = [TORCH_SRC] + [os.path.join(ROOT, "include", h) for h in ("fa_fwd.h", "fa_decoder.h")]
+TORCH_LIB = os.path.join(PKG, "_fa_torch.so")
+
+
+def torch_cmd(out: str) -> list[str]:
+    import importlib.util
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    include = [os.path.join(ROOT, "include"), CSRC, os.path.join(torch, "include"), cuda,
+               sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", *(x for i in include for x in ("-I", i)), TORCH_SRC,
+            "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            "-o", out]
+
+
+def _stale(out: str, deps=None) -> bool:
+    return not os.path.exists(out) or any(os.path.getmtime(out) < os.path.getmtime(d) for d in deps or DEPS)
 
 
 def build(force: bool = False, verbose: bool = False, out: str = LIB, extra=()) -> str:
@@ -51,8 +69,12 @@ def build(force: bool = False, verbose: bool = False, out: str = LIB, extra=()) 
 
 
 def build_many(targets, force: bool = False, verbose: bool = False) -> list[str]:
-    """Compile each (output, extra flags) target that is stale, all nvcc runs at once, and link it."""
-    procs = []
+    """Compile each (output, extra flags) target that is stale, all nvcc runs at once, and link it;
+    with them the tensor-level calls."""
+    procs, calls = [], None
+    if force or _stale(TORCH_LIB, TORCH_DEPS):
+        calls_tmp = TORCH_LIB + f".tmp{os.getpid()}"
+        calls = subprocess.Popen(torch_cmd(calls_tmp), stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
     for out, extra in targets:
         if force or _stale(out):
             objects = [f"{out}.{os.path.basename(src)}.tmp{os.getpid()}.o" for src in SRCS]
@@ -79,8 +101,15 @@ def build_many(targets, force: bool = False, verbose: bool = False) -> list[str]
         if verbose:
             sys.stderr.write("".join(se for _, se in said))
         os.replace(tmp, out)
+    if calls is not None:
+        so, se = calls.communicate()
+        if calls.returncode == 0:
+            os.replace(calls_tmp, TORCH_LIB)
+        else:
+            sys.stderr.write(so + se)
+            failed.append(os.path.basename(TORCH_LIB))
     if failed:
-        raise RuntimeError(f"nvcc failed building {', '.join(failed)}")
+        raise RuntimeError(f"the compiler failed building {', '.join(failed)}")
     return [out for out, _ in targets]
 
 
