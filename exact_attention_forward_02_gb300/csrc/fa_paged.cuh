@@ -16,10 +16,10 @@
 // partial states (m, l, O~) in the workspace; fa_paged_combine_kernel joins them, in the order of
 // the blocks. Nothing in the main kernel waits on another block.
 //
-// Two forms of the kernel, of 12 warps (8: TMA producer, 9: MMA issuer, 10: walks the block's
-// range and hands the others their items through a ring in shared memory, a few ahead, so that
-// nobody waits for the lengths of the next sequence; 0-7: two softmax warpgroups, thread = row =
-// TMEM lane; 11 idle):
+// Two forms of the kernel, of 12 warps (8: loads of Q and K, 11: loads of V, 9: MMA issuer, 10:
+// walks the block's range and hands the others their items through a ring in shared memory, a few
+// ahead, so that nobody waits for the lengths of the next sequence; 0-7: two softmax warpgroups,
+// thread = row = TMEM lane):
 //   PAIR   an item is two tiles of 128 rows, one per warpgroup, over the same keys: long chunks,
 //          bound by the tensor cores.
 //   SPLIT  an item is one tile; the warpgroups take the even and the odd key tiles, each with its
@@ -43,9 +43,9 @@ namespace paged {
 
 constexpr int BM = 128, BN = 128;
 constexpr int NUM_WARPS = 12, NUM_THREADS = NUM_WARPS * 32;
-constexpr int WARP_LOAD = 8, WARP_MMA = 9, WARP_WALK = 10;
+constexpr int WARP_LOAD = 8, WARP_MMA = 9, WARP_WALK = 10, WARP_LOAD_V = 11;
 constexpr int ITEM_SLOTS = 4;
-constexpr int ITEM_READERS = 10;  // warps that read an item: load, MMA, 8 softmax
+constexpr int ITEM_READERS = 11;  // warps that read an item: two loading, MMA, 8 softmax
 // 2*128*200 + 128*104 = 64512 = 384*168 registers, the launch's budget
 constexpr uint32_t REGS_SOFTMAX = 200, REGS_OTHER = 104;
 constexpr uint32_t TMEM_COLS = 512, TMEM_S0 = 0, TMEM_O0 = 256;  // S0 | S1 | O0 | O1
@@ -405,96 +405,87 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   if (warp >= WARP_LOAD) {
     regs_dec<REGS_OTHER>();
-    // Loads are numbered over the block's pieces; load i goes to slot i mod KV_SLOTS. Their order
-    // is that of their use. PAIR: K0 V0 K1 V1 ...; unit u = {V of tile u-1, K of tile u} is
-    // released at once. SPLIT: K0 K1 V0 K2 V1 K3 ...; every load is released by itself.
-    if (warp == WARP_LOAD) {
-      // ======================================================================= producer
-      // All 32 lanes: a tile's boxes (pages, and 64-column halves) are issued side by side.
+    // Loads are numbered over the block's pieces in the order of their use; load i goes to slot
+    // i mod KV_SLOTS. PAIR: K0 V0 K1 V1 ...; unit u = {V of tile u-1, K of tile u} is released at
+    // once. SPLIT: K0 K1 V0 K2 V1 K3 ...; every load is released by itself.
+    if (warp == WARP_LOAD || warp == WARP_LOAD_V) {
+      // ======================================================================= producers
+      // All 32 lanes: a tile's boxes (pages, and 64-column halves) are issued side by side. A box
+      // costs its warp about 100 cycles whatever its size, so K and V have a warp each.
+      const bool is_v = warp == WARP_LOAD_V;
+      const CUtensorMap* tm = is_v ? &tmV : &tmK;
       const int boxes = BN / p.box_keys;                    // page boxes of one 64-column chunk
+      const int tiles_per_page = p.page_size > BN ? p.page_size / BN : 1;
       const int my_box = lane % boxes, my_chunk = lane / boxes;
       const bool issues = my_chunk < LY::CHUNKS;
       const uint32_t box_bytes = (uint32_t)p.box_keys * 128u;
       const uint32_t box_off = (uint32_t)my_chunk * LY::CHUNK_BYTES + (uint32_t)my_box * box_bytes;
-      uint32_t ld = 0, q_ph = 0, issued_mask = 0, last_par = 0;
+      uint32_t ld0 = 0, q_ph = 0, issued_mask = 0, last_par = 0;
       bool ok = true, q_issued = false;
-      Item it = {};
-      // the page of this lane's box in key tile j (num_pages, which reads as zeros, for a bad one)
-      auto page_of = [&](int j) -> int {
-        const long long key = (long long)j * BN + my_box * p.box_keys;
-        if (key >= it.len) return -1;
-        const int page = p.table[(size_t)it.b * p.table_stride + (int)(key / p.page_size)];
-        if (page >= 0 && page < p.num_pages) return page;
-        atomicCAS(p.status, 0, FA_ERR_RANGE);
-        return p.num_pages;
-      };
-      auto load = [&](const CUtensorMap* tm, int j, int page) -> bool {
-        const uint32_t slot = ld % LY::KV_SLOTS, par = (ld / LY::KV_SLOTS) & 1u;
-        if (ld >= (uint32_t)LY::KV_SLOTS) {
-          const uint32_t u = SPLIT ? ld - LY::KV_SLOTS : (ld - LY::KV_SLOTS + 1) >> 1;
-          if (!__all_sync(0xffffffffu, wait_bar(smem_u32(&bars->kv_release[u % LY::KV_SLOTS]),
-                                                (u / LY::KV_SLOTS) & 1u, abort_flag, p)))
-            return false;
-        }
-        const uint32_t full = smem_u32(&bars->kv_full[slot]);
-        const long long keys = it.len - (long long)j * BN;  // boxes that hold a key of the sequence
-        const int live = keys <= 0 ? 0 : (int)min((long long)boxes, (keys + p.box_keys - 1) / p.box_keys);
-        if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)live * LY::CHUNKS * box_bytes);
-        __syncwarp();
-        if (issues && page >= 0) {
-          const int slot0 = p.page_size > BN ? (int)(((long long)j * BN) % p.page_size) : 0;
-          tma_load_4d(sKV + slot * LY::TILE_BYTES + box_off, tm, full, my_chunk * 64, slot0, it.h, page);
-        }
-        issued_mask |= 1u << slot;
-        last_par = (last_par & ~(1u << slot)) | (par << slot);
-        ++ld;
-        return true;
-      };
       while (ok) {
         const Item* src = item_next();
         if (!(ok = src != nullptr)) break;
-        it = *src;
+        const Item it = *src;
         item_done();
         if (it.n == 0) break;
-        // pages of the tiles at hand; in SPLIT order K runs two tiles ahead of V
-        int pg = page_of(it.j0), pg1 = it.n > 1 ? page_of(it.j0 + 1) : -1;
-        ok = load(&tmK, it.j0, pg);
-        if (!ok) break;
-        ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->q_empty), q_ph ^ 1, abort_flag, p));
-        if (!ok) break;
-        q_ph ^= 1;
-        {
-          const uint32_t qf = smem_u32(&bars->q_full);
-          const int tiles = SPLIT ? 1 : (it.nt > p.tpt ? 2 : 1);
-          const int rows = p.tpt * p.G;
-          if (lane == 0) mbar_arrive_expect_tx(qf, (uint32_t)(tiles * REP * LY::CHUNKS * rows) * 128u);
+        // 32 entries of the sequence's table at a time, one per lane; the next 32 are on their way
+        const int* table = p.table + (size_t)it.b * p.table_stride;
+        auto entries = [&](int window) -> int {
+          const int e = window * 32 + lane;
+          if ((long long)e * p.page_size >= it.len) return -1;  // holds no key of the sequence
+          const int page = table[e];
+          if (page >= 0 && page < p.num_pages) return page;
+          atomicCAS(p.status, 0, FA_ERR_RANGE);
+          return p.num_pages;  // reads as zeros
+        };
+        const int first = it.j0 / tiles_per_page * (p.page_size > BN ? 1 : boxes);
+        int window = first / 32, held = entries(window), next = entries(window + 1);
+        for (int i = 0; i < it.n; ++i) {
+          const int j = it.j0 + i;
+          const int e0 = p.page_size > BN ? j / tiles_per_page : j * boxes;  // the tile's first entry
+          if (e0 / 32 != window) {  // 32 is a multiple of a tile's entries
+            window = e0 / 32;
+            held = next;
+            next = entries(window + 1);
+          }
+          const int page = __shfl_sync(0xffffffffu, held, (e0 + my_box) % 32);
+          const uint32_t ld = ld0 + (SPLIT ? (is_v ? 2 + i + min(i, it.n - 2) : i < 2 ? i : 2 * i - 1) : 2 * i + is_v);
+          const uint32_t slot = ld % LY::KV_SLOTS, par = (ld / LY::KV_SLOTS) & 1u;
+          if (ld >= (uint32_t)LY::KV_SLOTS) {
+            const uint32_t u = SPLIT ? ld - LY::KV_SLOTS : (ld - LY::KV_SLOTS + 1) >> 1;
+            ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->kv_release[u % LY::KV_SLOTS]),
+                                                  (u / LY::KV_SLOTS) & 1u, abort_flag, p));
+            if (!ok) break;
+          }
+          const uint32_t full = smem_u32(&bars->kv_full[slot]);
+          const int keys = it.len - j * BN;  // boxes that hold a key of the sequence
+          const int live = keys <= 0 ? 0 : min(boxes, (keys + p.box_keys - 1) / p.box_keys);
+          if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)live * LY::CHUNKS * box_bytes);
           __syncwarp();
-          if (lane < tiles * REP * LY::CHUNKS) {
-            const int c = lane % LY::CHUNKS, a = lane / LY::CHUNKS;  // a: copy (SPLIT) or tile (PAIR)
-            const uint32_t off = SPLIT ? (uint32_t)a * (BM / REP) * 128u : (uint32_t)a * LY::TILE_BYTES;
-            tma_load_3d(sQ + off + c * LY::CHUNK_BYTES, &tmQ, qf, c * 64, it.h * p.G,
-                        it.tok0 + (SPLIT ? 0 : a * p.tpt));
-          }
-          q_issued = true;
-        }
-        if constexpr (SPLIT) {
-          if (it.n > 1) ok = load(&tmK, it.j0 + 1, pg1);
-          for (int i = 0; i < it.n && ok; ++i) {
-            const int pg2 = i + 2 < it.n ? page_of(it.j0 + i + 2) : -1;
-            ok = load(&tmV, it.j0 + i, pg);
-            if (ok && i + 2 < it.n) ok = load(&tmK, it.j0 + i + 2, pg2);
-            pg = pg1;
-            pg1 = pg2;
-          }
-        } else {
-          for (int i = 0; i < it.n && ok; ++i) {
-            const int pg2 = i + 2 < it.n ? page_of(it.j0 + i + 2) : -1;
-            ok = load(&tmV, it.j0 + i, pg);
-            if (ok && i + 1 < it.n) ok = load(&tmK, it.j0 + i + 1, pg1);
-            pg = pg1;
-            pg1 = pg2;
+          if (issues && my_box < live)
+            tma_load_4d(sKV + slot * LY::TILE_BYTES + box_off, tm, full, my_chunk * 64,
+                        p.page_size > BN ? j % tiles_per_page * BN : 0, it.h, page);
+          issued_mask |= 1u << slot;
+          last_par = (last_par & ~(1u << slot)) | (par << slot);
+          if (!is_v && i == 0) {  // Q behind the first K
+            ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->q_empty), q_ph ^ 1, abort_flag, p));
+            if (!ok) break;
+            q_ph ^= 1;
+            const uint32_t qf = smem_u32(&bars->q_full);
+            const int tiles = SPLIT ? 1 : (it.nt > p.tpt ? 2 : 1);
+            if (lane == 0)
+              mbar_arrive_expect_tx(qf, (uint32_t)(tiles * REP * LY::CHUNKS * p.tpt * p.G) * 128u);
+            __syncwarp();
+            if (lane < tiles * REP * LY::CHUNKS) {
+              const int c = lane % LY::CHUNKS, a = lane / LY::CHUNKS;  // a: copy (SPLIT) or tile (PAIR)
+              const uint32_t off = SPLIT ? (uint32_t)a * (BM / REP) * 128u : (uint32_t)a * LY::TILE_BYTES;
+              tma_load_3d(sQ + off + c * LY::CHUNK_BYTES, &tmQ, qf, c * 64, it.h * p.G,
+                          it.tok0 + (SPLIT ? 0 : a * p.tpt));
+            }
+            q_issued = true;
           }
         }
+        ld0 += 2 * it.n;
       }
       if (!ok && lane == 0) {
         // every issued copy must land before the block may exit
