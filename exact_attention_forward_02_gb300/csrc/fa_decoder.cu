@@ -173,7 +173,7 @@ int launch_paged(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sms, ROWS / 8 < 8 ? ROWS / 8 : 8);
+  cfg.gridDim = dim3(sms, ROWS > 128 ? ROWS / 32 : ROWS / 8);  // a warp joins 4 rows, or 1
   cfg.blockDim = dim3(paged::COMBINE_THREADS);
   cfg.stream = st;
   cfg.attrs = &attr;

@@ -9,12 +9,13 @@
 // is token r / G, head r % G, so that a key is loaded once for all of them (for single tokens
 // this is what makes G rows of work from one pass over the cache).
 //
-// Work. An item is (sequence, key head, block of tokens); its keys are cut into tiles of 128,
-// and a unit is one (item, tile). The lengths are device data, so every block adds up the units
-// of all sequences by itself (a closed form per sequence), and block c of Ge takes the units
-// [c W / Ge, (c+1) W / Ge) of the W in order. An item that lies in several blocks' ranges leaves
-// partial states (m, l, O~) in the workspace; fa_paged_combine_kernel joins them, in the order of
-// the blocks. Nothing in the main kernel waits on another block.
+// Work. An item is (sequence, key head, block of tokens); its keys are cut into tiles of 128. It
+// counts as one unit per tile and ITEM_UNITS before them for what an item costs by itself. The
+// lengths are device data, so every block adds up the units of all sequences by itself (a closed
+// form per sequence), and block c of Ge takes the units [c W / Ge, (c+1) W / Ge) of the W in order.
+// An item whose tiles lie in several blocks' ranges leaves partial states (m, l, O~) in the
+// workspace; fa_paged_combine_kernel joins them, in the order of the blocks. Nothing in the main
+// kernel waits on another block.
 //
 // Two forms of the kernel, of 12 warps (8: loads of Q and K, 11: loads of V, 9: MMA issuer, 10:
 // walks the block's range and hands the others their items through a ring in shared memory, a few
@@ -79,6 +80,16 @@ struct Item {
   int slot;             // place of its partial state: 0 = first piece of the block's range
 };
 
+struct Seq {
+  int t0, n, len, nq;  // first row of q, new tokens, tokens in the cache, blocks of tokens
+};
+// Where a block's range begins: `rem` units into sequence b.
+struct Start {
+  long long rem;
+  int b, h, q, off;  // off: units into the item
+  Seq s;
+};
+
 struct Barriers {
   uint64_t q_full, q_empty;
   uint64_t kv_full[MAX_SLOTS], kv_release[MAX_SLOTS];
@@ -87,8 +98,7 @@ struct Barriers {
   uint64_t item_full[ITEM_SLOTS], item_empty[ITEM_SLOTS];
   Item items[ITEM_SLOTS];
   long long warp_units[NUM_WARPS];
-  long long rem;  // units of the first sequence before this block's range
-  int first_b, first_h, first_q, first_j;
+  Start start;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -98,13 +108,17 @@ struct Layout {
   static constexpr int TILE_BYTES = BM * D * 2;
   static constexpr int CHUNK_BYTES = BM * 128, CHUNKS = D / 64;
   static constexpr int Q_TILES = SPLIT ? 1 : 2;
-  static constexpr int STAGE_BYTES = SPLIT ? BM * D * 4 : 0;  // one fp32 tile of O~
-  static constexpr int HEAD_BYTES = 1024 + 1024;              // barriers, alignment
-  static constexpr int FIT = (SMEM_LIMIT - Q_TILES * TILE_BYTES - STAGE_BYTES - HEAD_BYTES) / TILE_BYTES;
+  static constexpr int STAGE_BYTES = SPLIT ? 65536 : 0;  // fp32 rows of O~
+  static constexpr int STAGE_ROWS = STAGE_BYTES / (D * 4);
+  static constexpr int STATE_BYTES = SPLIT ? 2 * BM * 8 : 0;  // (m, l) of both warpgroups' rows
+  static constexpr int HEAD_BYTES = 1024;                     // barriers and items
+  static constexpr int FIT =
+      (SMEM_LIMIT - Q_TILES * TILE_BYTES - STAGE_BYTES - STATE_BYTES - HEAD_BYTES) / TILE_BYTES;
   static constexpr int KV_SLOTS = FIT > MAX_SLOTS ? MAX_SLOTS : FIT;
   static constexpr int OFF_Q = 0, OFF_KV = Q_TILES * TILE_BYTES;
   static constexpr int OFF_STAGE = OFF_KV + KV_SLOTS * TILE_BYTES;
-  static constexpr int OFF_BAR = OFF_STAGE + STAGE_BYTES;
+  static constexpr int OFF_STATE = OFF_STAGE + STAGE_BYTES;
+  static constexpr int OFF_BAR = OFF_STATE + STATE_BYTES;
   static constexpr int SMEM_BYTES = OFF_BAR + HEAD_BYTES;
   static_assert(sizeof(Barriers) <= 1024 && KV_SLOTS >= 4 && SMEM_BYTES <= SMEM_LIMIT, "shared memory budget");
 };
@@ -140,14 +154,9 @@ __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, const 
 }
 
 // ----------------------------------------------------------------------------- schedule
-struct Seq {
-  int t0, n, len, nq;  // first row of q, new tokens, tokens in the cache, blocks of tokens
-};
-
 // Sequence b as the kernels see it: a range of rows outside [0, T] counts as empty, a length
 // past the table's width is cut to it; `report` records either.
-template <int TPT_MUL>
-__device__ __forceinline__ Seq load_seq(const Params& p, int b, bool report) {
+__device__ __forceinline__ Seq load_seq(const Params& p, int b, int tpi, bool report) {
   Seq s;
   s.t0 = p.cu[b];
   const long long n = (long long)p.cu[b + 1] - s.t0;
@@ -156,128 +165,138 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int b, bool report) {
   const bool rows_ok = s.t0 >= 0 && n >= 0 && s.t0 + n <= p.T;
   s.n = rows_ok ? (int)n : 0;
   s.len = len < 0 ? 0 : (int)(len > cap ? cap : len);
-  const int tpi = p.tpt * TPT_MUL;
-  s.nq = (s.n + tpi - 1) / tpi;
+  s.nq = s.n <= tpi ? (s.n > 0) : (s.n - 1) / tpi + 1;
   if (report && (!rows_ok || (s.n && len > cap))) atomicCAS(p.status, 0, FA_ERR_RANGE);
   return s;
 }
 
-// key tiles of block q of a sequence (at least one, so that its rows are written)
+// a / b for b > 0; nearly always 32 bits
+__device__ __forceinline__ long long divide(long long a, int b) {
+  return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// key tiles of a block of tokens that sees `vis` keys (at least one, so that its rows are written)
+__device__ __forceinline__ int tiles_for(long long vis) { return vis <= 0 ? 1 : (int)((vis + BN - 1) / BN); }
+// of block q
 __device__ __forceinline__ int tiles_of(const Params& p, const Seq& s, int q, int tpi) {
-  long long vis = s.len;
-  if (p.causal) {
-    const long long end = (long long)(q + 1) * tpi;
-    vis = (long long)s.len - s.n + (end < s.n ? end : s.n);
-  }
-  return vis <= 0 ? 1 : (int)((vis + BN - 1) / BN);
+  const long long end = (long long)(q + 1) * tpi;
+  return tiles_for(p.causal ? (long long)s.len - s.n + (end < s.n ? end : s.n) : s.len);
 }
 
-// sum over i < n of floor((a i + b) / m), for a, b >= 0 (by Euclid's steps on (a, m))
-__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
-  long long s = 0;
-  while (true) {
-    if (a >= m) s += (n - 1) * n / 2 * (a / m), a %= m;
-    if (b >= m) s += n * (b / m), b %= m;
-    const long long y = a * n + b;
-    if (y < m) return s;
-    n = y / m;
-    b = y % m;
-    const long long t = m;
-    m = a;
-    a = t;
-  }
-}
-
-// key tiles of the blocks before q (q <= nq - 1: whole blocks only)
+// Key tiles of the first q blocks. With a causal mask block i sees x_i = ctx + (i + 1) tpi keys
+// (the last one all of them): the first k0 at most 128, one tile, and the others ceil(x_i / 128)
+// = (x_i + r_i) / 128 tiles with r_i = -x_i mod 128. The r_i of 128 / g blocks in a row, g the
+// largest power of two in tpi (up to 128), are rho, rho + g, rho + 2 g, ... in some order.
 __device__ __forceinline__ long long tiles_before(const Params& p, const Seq& s, int q, int tpi) {
   if (q == 0) return 0;
-  if (!p.causal) return (long long)q * tiles_of(p, s, 0, tpi);
-  // block i ends at key ctx + (i + 1) tpi; the first k0 of them reach key 128 at most: one tile
+  if (!p.causal) return (long long)q * tiles_for(s.len);
+  if (q == 1) return tiles_of(p, s, 0, tpi);
+  const int full = q < s.nq ? q : s.nq - 1;
   const long long ctx = (long long)s.len - s.n;
-  long long k0 = BN - ctx < 0 ? 0 : (BN - ctx) / tpi;
-  if (k0 > q) k0 = q;
-  return k0 + (q > k0 ? floor_sum(q - k0, BN, tpi, ctx + (k0 + 1) * tpi + BN - 1) : 0);
-}
-__device__ __forceinline__ long long tiles_total(const Params& p, const Seq& s, int tpi) {
-  return s.nq ? tiles_before(p, s, s.nq - 1, tpi) + tiles_of(p, s, s.nq - 1, tpi) : 0;
+  long long k0 = ctx >= BN ? 0 : divide(BN - ctx, tpi);
+  if (k0 > full) k0 = full;
+  long long sum = k0;
+  const long long n = full - k0, x0 = ctx + (k0 + 1) * tpi;
+  if (n > 0) {
+    const int g = min(tpi & -tpi, BN), lp = __ffs(BN / g) - 1, period = 1 << lp;
+    long long r = (n >> lp) * ((long long)period * ((int)(-x0) & (g - 1)) + (long long)g * period * (period - 1) / 2);
+#pragma unroll 1
+    for (int i = (int)(n >> lp << lp); i < n; ++i) r += (int)(-(x0 + (long long)i * tpi)) & (BN - 1);
+    sum += (n * x0 + tpi * (n * (n - 1) / 2) + r) / BN;
+  }
+  return sum + (q > full ? tiles_for(s.len) : 0);
 }
 
 struct Range {
   long long W, u0, u1;
   int Ge;  // blocks that take part
 };
-__device__ __forceinline__ long long bound_of(long long c, const Range& r) { return c * r.W / r.Ge; }
+__device__ __forceinline__ long long bound_of(int c, const Range& r) { return divide(c * r.W, r.Ge); }
 __device__ __forceinline__ int owner_of(long long u, const Range& r) {
-  long long c = u * r.Ge / r.W;
+  int c = (int)(u * r.Ge / r.W);
   while (c + 1 < r.Ge && bound_of(c + 1, r) <= u) ++c;
-  return (int)c;
+  return c;
 }
 
 // Walks a block's range.
-template <int TPT_MUL>
+template <int TPT_MUL, int ITEM_UNITS>
 struct Walk {
   Seq s;
-  int b, h, q, j;
-  long long u;
+  int b, h, q;
+  long long u, off;  // next unit, and its place in its item
   bool first;
-  __device__ __forceinline__ void begin(const Params& p, const Range& r, const Barriers* bars) {
-    b = bars->first_b;
-    h = bars->first_h;
-    q = bars->first_q;
-    j = bars->first_j;
+  __device__ __forceinline__ void begin(const Range& r, const Start& st) {
+    s = st.s;
+    b = st.b;
+    h = st.h;
+    q = st.q;
+    off = st.off;
     u = r.u0;
     first = true;
-    if (u < r.u1) s = load_seq<TPT_MUL>(p, b, false);
   }
-  // `last`: the block that ends the item
-  __device__ __forceinline__ bool next(const Params& p, const Range& r, Item& it, int& last) {
-    if (u >= r.u1) return false;
+  // `ustart`: the item's first unit
+  __device__ __forceinline__ bool next(const Params& p, const Range& r, Item& it, long long& ustart) {
     const int tpi = p.tpt * TPT_MUL;
-    if (q == s.nq) {
-      q = 0;
-      if (++h == p.Hkv) {
-        h = 0;
-        do {
-          if (++b >= p.B) return false;
-          s = load_seq<TPT_MUL>(p, b, false);
-        } while (s.n == 0);
+    while (u < r.u1) {
+      if (q == s.nq) {
+        q = 0;
+        if (++h == p.Hkv) {
+          h = 0;
+          do {
+            if (++b >= p.B) return false;
+            s = load_seq(p, b, tpi, false);
+          } while (s.n == 0);
+        }
       }
+      const int ntot = tiles_of(p, s, q, tpi);
+      const long long whole = ntot + ITEM_UNITS, end = off + (r.u1 - u) < whole ? off + (r.u1 - u) : whole;
+      const int j0 = off > ITEM_UNITS ? (int)(off - ITEM_UNITS) : 0;
+      const int j1 = end > ITEM_UNITS ? (int)(end - ITEM_UNITS) : 0;
+      ustart = u - off;
+      u += end - off;
+      off = 0;
+      const int qq = q++;
+      if (j1 == j0) continue;  // none of the item's tiles: they are the next block's
+      it.b = b;
+      it.h = h;
+      it.tok0 = s.t0 + qq * tpi;
+      it.nt = min(tpi, s.n - qq * tpi);
+      it.len = s.len;
+      it.vis0 = s.len - s.n + qq * tpi + 1;
+      it.ntot = ntot;
+      it.j0 = j0;
+      it.n = j1 - j0;
+      it.slot = first ? 0 : 1;
+      it.n0 = it.n;
+      if (TPT_MUL == 2 && p.causal) {
+        const int t = tiles_for((long long)it.vis0 + min(p.tpt, it.nt) - 1) - j0;
+        it.n0 = t < 1 ? 1 : min(t, it.n);
+      }
+      first = false;
+      return true;
     }
-    it.b = b;
-    it.h = h;
-    it.tok0 = s.t0 + q * tpi;
-    it.nt = min(tpi, s.n - q * tpi);
-    it.len = s.len;
-    it.vis0 = s.len - s.n + q * tpi + 1;
-    it.ntot = tiles_of(p, s, q, tpi);
-    it.j0 = j;
-    const long long left = r.u1 - u;
-    it.n = left < it.ntot - j ? (int)left : it.ntot - j;
-    it.slot = first ? 0 : 1;
-    it.n0 = it.n;
-    if (TPT_MUL == 2 && p.causal) {
-      const long long vis = (long long)it.vis0 + min(p.tpt, it.nt) - 1;
-      const long long t = (vis <= 0 ? 1 : (vis + BN - 1) / BN) - j;
-      it.n0 = t < 1 ? 1 : (t < it.n ? (int)t : it.n);
-    }
-    last = it.n == it.ntot ? (int)blockIdx.x : owner_of(u - j + it.ntot - 1, r);
-    first = false;
-    u += it.n;
-    j = 0;
-    ++q;
-    return true;
+    return false;
   }
 };
 
-// The block's share of the units, and where it begins. All threads call this; it ends with a
-// barrier.
-template <int TPT_MUL, int MIN_UNITS>
-__device__ __forceinline__ Range plan(const Params& p, Barriers* bars) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tpi = p.tpt * TPT_MUL;
-  const int chunk = (p.B + NUM_THREADS - 1) / NUM_THREADS;
-  const int b0 = min(tid * chunk, p.B), b1 = min(b0 + chunk, p.B);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += p.Hkv * tiles_total(p, load_seq<TPT_MUL>(p, b, blockIdx.x == 0), tpi);
+// units of the sequences of one thread, [b0, b1)
+template <int TPT_MUL, int ITEM_UNITS>
+__device__ __forceinline__ long long units_of(const Params& p, int b0, int b1, Seq& last, bool report) {
+  const int tpi = p.tpt * TPT_MUL;
+  long long sum = 0;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    last = load_seq(p, b, tpi, report);
+    sum += p.Hkv * (tiles_before(p, last, last.nq, tpi) + (long long)ITEM_UNITS * last.nq);
+  }
+  return sum;
+}
+
+// The block's share of the units, and where it begins (bars->start). All threads call this, with
+// the units of their own sequences; it ends with a barrier.
+template <int TPT_MUL, int ITEM_UNITS, int MIN_UNITS>
+__device__ __forceinline__ Range plan(const Params& p, Barriers* bars, int b0, int b1, long long mine, Seq s) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tpi = p.tpt * TPT_MUL;
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -294,46 +313,60 @@ __device__ __forceinline__ Range plan(const Params& p, Barriers* bars) {
     if (w < warp) before += bars->warp_units[w];
     r.W += bars->warp_units[w];
   }
-  const long long most = (r.W + MIN_UNITS - 1) / MIN_UNITS;
-  r.Ge = most < (long long)gridDim.x ? (int)most : (int)gridDim.x;
+  r.Ge = r.W < (long long)gridDim.x * MIN_UNITS ? ((int)r.W + MIN_UNITS - 1) / MIN_UNITS : (int)gridDim.x;
   r.u0 = r.u1 = 0;
   if ((int)blockIdx.x < r.Ge) {
     r.u0 = bound_of(blockIdx.x, r);
     r.u1 = bound_of(blockIdx.x + 1, r);
   }
+  // the thread whose sequences hold the first unit
   if (r.u0 < r.u1 && before <= r.u0 && r.u0 < before + mine) {
-    for (int b = b0; b < b1; ++b) {
-      const long long x = p.Hkv * tiles_total(p, load_seq<TPT_MUL>(p, b, false), tpi);
-      if (r.u0 < before + x) {
-        bars->first_b = b;
-        bars->rem = r.u0 - before;
-        break;
+    int b = b0;
+    if (b1 - b0 > 1) {
+#pragma unroll 1
+      for (;; ++b) {
+        const long long x = units_of<TPT_MUL, ITEM_UNITS>(p, b, b + 1, s, false);
+        if (r.u0 < before + x) break;
+        before += x;
       }
-      before += x;
+    }
+    Start& st = bars->start;
+    st.s = s;
+    st.b = b;
+    st.rem = r.u0 - before;
+    if (s.nq == 1) {
+      const int item = ITEM_UNITS + tiles_of(p, s, 0, tpi);
+      st.h = (int)divide(st.rem, item);
+      st.q = 0;
+      st.off = (int)(st.rem - (long long)st.h * item);
     }
   }
   __syncthreads();
-  if (warp == 0 && r.u0 < r.u1) {
-    const Seq s = load_seq<TPT_MUL>(p, bars->first_b, false);
-    const long long head = tiles_total(p, s, tpi);
-    const int h = (int)(bars->rem / head);
-    const long long rem = bars->rem - h * head;
-    // the last block q with tiles_before(q) <= rem: 32 candidates at a time
-    int lo = 0, n = s.nq;
-    while (n > 1) {
-      const int step = (n + 31) / 32, cand = lo + lane * step;
-      const bool le = lane * step < n && tiles_before(p, s, cand, tpi) <= rem;
-      const int k = __popc(__ballot_sync(0xffffffffu, le)) - 1;  // candidate 0 always holds
-      lo += k * step;
-      n = min(step, n - k * step);
+  if (r.u0 < r.u1 && bars->start.s.nq > 1) {  // the same for the whole block
+    if (warp == 0) {
+      Start& st = bars->start;
+      s = st.s;
+      const long long head = tiles_before(p, s, s.nq, tpi) + (long long)ITEM_UNITS * s.nq;
+      const int h = (int)(st.rem / head);
+      const long long rem = st.rem - h * head;
+      // the last block with at most `rem` units before it: 32 candidates at a time
+      int lo = 0, n = s.nq;
+#pragma unroll 1
+      while (n > 1) {
+        const int step = (n + 31) / 32, cand = lo + lane * step;
+        const bool le = lane * step < n && tiles_before(p, s, cand, tpi) + (long long)ITEM_UNITS * cand <= rem;
+        const int k = __popc(__ballot_sync(0xffffffffu, le)) - 1;  // candidate 0 always holds
+        lo += k * step;
+        n = min(step, n - k * step);
+      }
+      if (lane == 0) {
+        st.h = h;
+        st.q = lo;
+        st.off = (int)(rem - tiles_before(p, s, lo, tpi) - (long long)ITEM_UNITS * lo);
+      }
     }
-    if (lane == 0) {
-      bars->first_h = h;
-      bars->first_q = lo;
-      bars->first_j = (int)(rem - tiles_before(p, s, lo, tpi));
-    }
+    __syncthreads();
   }
-  __syncthreads();
   return r;
 }
 
@@ -344,16 +377,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
   static_assert(SPLIT || REP == 1, "copies of rows belong to the SPLIT form");
   using LY = Layout<D, SPLIT>;
-  constexpr int TPT_MUL = SPLIT ? 1 : 2;
+  constexpr int TPT_MUL = SPLIT ? 1 : 2, ITEM_UNITS = SPLIT ? 1 : 0;
   constexpr int ROWS = SPLIT ? BM / REP : 2 * BM;  // rows of an item's partial state
   constexpr int CW = BN / REP;                     // keys of a tile that one row copy covers
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* smem = smem_raw;  // 1024-byte aligned, as the 128-byte swizzle wants it
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, FA_ERR_ALIGN);
+    return;
+  }
   Barriers* bars = reinterpret_cast<Barriers*>(smem + LY::OFF_BAR);
   const uint32_t sQ = smem_u32(smem + LY::OFF_Q), sKV = smem_u32(smem + LY::OFF_KV);
   const uint32_t sStage = smem_u32(smem + LY::OFF_STAGE);
   volatile int* abort_flag = &bars->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per_thread = (p.B + NUM_THREADS - 1) / NUM_THREADS;
+  const int b0 = min((int)threadIdx.x * per_thread, p.B), b1 = min(b0 + per_thread, p.B);
+  Seq seq = {};
+  const long long my_units = units_of<TPT_MUL, ITEM_UNITS>(p, b0, b1, seq, blockIdx.x == 0);
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&bars->q_full), 1);
@@ -387,7 +428,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
   launch_dependents();
   tc_fence_before();
-  const Range range = plan<TPT_MUL, SPLIT ? 2 : 1>(p, bars);
+  const Range range = plan<TPT_MUL, ITEM_UNITS, SPLIT ? ITEM_UNITS + 2 : 1>(p, bars, b0, b1, my_units, seq);
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   // Items in order: the reader's place in the ring, and the item there (nullptr: the wait gave up).
@@ -438,7 +479,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           atomicCAS(p.status, 0, FA_ERR_RANGE);
           return p.num_pages;  // reads as zeros
         };
-        const int first = it.j0 / tiles_per_page * (p.page_size > BN ? 1 : boxes);
+        const int first = p.page_size > BN ? it.j0 / tiles_per_page : it.j0 * boxes;
         int window = first / 32, held = entries(window), next = entries(window + 1);
         for (int i = 0; i < it.n; ++i) {
           const int j = it.j0 + i;
@@ -666,21 +707,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (lane == 0) {
         int* rec = p.records + blockIdx.x * 8;
         rec[0] = 0;  // no item begins here and ends elsewhere, as yet
-        Walk<TPT_MUL> walk;
-        walk.begin(p, range, bars);
+        Walk<TPT_MUL, ITEM_UNITS> walk;
+        walk.begin(range, bars->start);
         for (uint32_t i = 0;; ++i) {
           const uint32_t s = i % ITEM_SLOTS;
           if (i >= ITEM_SLOTS && !wait_bar(smem_u32(&bars->item_empty[s]), (i / ITEM_SLOTS - 1) & 1u, abort_flag, p)) break;
           Item it;
-          int last;
-          const bool more = walk.next(p, range, it, last);
+          long long ustart;
+          const bool more = walk.next(p, range, it, ustart);
           if (!more) it.n = 0;
           bars->items[s] = it;
           mbar_arrive(smem_u32(&bars->item_full[s]));
           if (!more) break;
           if (it.j0 == 0 && it.n != it.ntot) {
             rec[1] = it.slot;
-            rec[2] = last;
+            rec[2] = owner_of(ustart + ITEM_UNITS + it.ntot - 1, range);
             rec[3] = it.h;
             rec[4] = it.tok0;
             rec[5] = it.nt;
@@ -839,27 +880,48 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       if (!ok) break;
       // ------------------------------------------------------------------ epilogue
-      const bool worked = !SPLIT || item->n > g;
+      const bool worked = !SPLIT || item->n > g, partial = item->n != item->ntot;
+      float* part = p.parts + (size_t)(blockIdx.x * 2 + item->slot) * part_floats(D, ROWS);
+      float m = m_run, l = l_run, f;
+      if constexpr (SPLIT) {
+        // A row's 2 REP states (two warpgroups, REP copies) become one. (m, l) are final before the
+        // last product is: they meet here, so that O~ is scaled as it is read. The barrier also
+        // says that the previous item's sums are done with the stage.
+        float2* states = reinterpret_cast<float2*>(smem + LY::OFF_STATE);
+        states[g * BM + r] = make_float2(m_run, l_run);
+        if (!(ok = epi_sync())) break;
+        m = -INFINITY;
+        l = 0.f;
+#pragma unroll
+        for (int x = 0; x < 2 * REP; ++x) m = fmaxf(m, states[x * (BM / REP) + row].x);
+        auto weight = [&](float mx) { return mx == -INFINITY ? 0.f : ex2_approx(mx - m); };
+#pragma unroll
+        for (int x = 0; x < 2 * REP; ++x) {
+          const float2 st = states[x * (BM / REP) + row];
+          l += st.y * weight(st.x);
+        }
+        f = weight(m_run);
+      } else {
+        f = 1.f;
+      }
+      // a whole item's O~ is divided by l; a partial state stays as it is
+      if (!partial) f *= l > 0.f ? 1.f / l : 0.f;
+      const int prow = SPLIT ? row : g * BM + row;
+      const long long t = item->tok0 + tok;
+      const int head = item->h * p.G + row % p.G;
+      if (valid && (!SPLIT || (g == 0 && copy == 0))) {
+        if (partial) *reinterpret_cast<float2*>(part + ROWS * D + 2 * prow) = make_float2(m, l);
+        else if (p.L) p.L[t * (p.Hkv * p.G) + head] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      }
       if (worked) {
         ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->o_done[g]), o_ph, abort_flag, p));
         if (!ok) break;
         o_ph ^= 1;
         tc_fence_after();
       }
-      const bool partial = item->n != item->ntot;
-      float* part = p.parts + (size_t)(blockIdx.x * 2 + item->slot) * part_floats(D, ROWS);
       if constexpr (!SPLIT) {
-        const int prow = g * BM + row;
-        const long long t = item->tok0 + tok;
-        const int head = item->h * p.G + row % p.G;
-        if (partial) {
-          if (valid) *reinterpret_cast<float2*>(part + ROWS * D + 2 * prow) = make_float2(m_run, l_run);
-        } else if (valid && p.L) {
-          p.L[t * (p.Hkv * p.G) + head] = l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
-        }
-        const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
         uint16_t* orow = p.o.ptr + t * p.o.ts + (long long)head * p.o.hs;
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
           uint32_t o[32];
           tmem_ld32(tO + q * 32, o);
@@ -875,7 +937,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int k = 0; k < 4; ++k) {
               float x[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[8 * k + e]) * inv;
+              for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[8 * k + e]) * f;
               reinterpret_cast<uint4*>(orow + q * 32)[k] = pack8<BF16>(x);
             }
           }
@@ -883,84 +945,60 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         tc_fence_before();
       } else {
-        // The row's 2 REP states (two warpgroups, REP copies) become one: their (m, l) meet in
-        // the stage, then the second warpgroup's scaled O~, then the sums of both.
-        st_shared_u32(sStage + (uint32_t)((g * BM + r) * 8), __float_as_uint(m_run));
-        st_shared_u32(sStage + (uint32_t)((g * BM + r) * 8 + 4), __float_as_uint(l_run));
-        if (!(ok = epi_sync())) break;
-        const float2* states = reinterpret_cast<const float2*>(smem + LY::OFF_STAGE);
-        float m = -INFINITY, l = 0.f;
+        // All states of the item's rows side by side in the stage, row x R + row for state x; if
+        // they are too many, half of the columns at a time. 16-byte piece i stands at i ^ (row & 7).
+        const int R = item->nt * p.G;
+        const int phases = 2 * REP * R <= LY::STAGE_ROWS ? 1 : 2;
+        const int cols = D / phases, states_n = item->n > 1 ? 2 * REP : REP  /* the second warpgroup had a tile */;
+        const int srow = (g * REP + copy) * R + row;
+        auto stage_at = [&](int rr, int i) { return sStage + (uint32_t)(rr * cols * 4 + ((i ^ (rr & 7)) << 4)); };
+#pragma unroll 1
+        for (int ph = 0; ph < phases; ++ph) {
+          if (worked) {
+#pragma unroll 1
+            for (int q = 0; q < cols; q += 32) {
+              uint32_t o[32];
+              tmem_ld32(tO + ph * cols + q, o);
+              tmem_wait_ld();
+              reg_fence(o);
+              if (valid) {
 #pragma unroll
-        for (int x = 0; x < 2 * REP; ++x) m = fmaxf(m, states[x * (BM / REP) + row].x);
-        auto scale_of = [&](float mx) { return mx == -INFINITY ? 0.f : ex2_approx(mx - m); };
-#pragma unroll
-        for (int x = 0; x < 2 * REP; ++x) {
-          const float2 st = states[x * (BM / REP) + row];
-          l += st.y * scale_of(st.x);
-        }
-        // a whole item's O is divided by l here already; a partial state stays as it is
-        const float f = scale_of(m_run) * (partial ? 1.f : l > 0.f ? 1.f / l : 0.f);
-        if (!(ok = epi_sync())) break;
-        // 16-byte piece x of row r stands at place x ^ (r & 7)
-        auto stage_at = [&](int rr, int x) { return sStage + (uint32_t)(rr * D * 4 + ((x ^ (rr & 7)) << 4)); };
-        auto put = [&](bool add) {
-#pragma unroll
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t o[32];
-            tmem_ld32(tO + q * 32, o);
-            tmem_wait_ld();
-            reg_fence(o);
-            if (valid) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                float x[4] = {};
-                if (add) ld_shared_v4(stage_at(r, q * 8 + k), x);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = fmaf(__uint_as_float(o[4 * k + e]), f, x[e]);
-                st_shared_v4(stage_at(r, q * 8 + k), __float_as_uint(x[0]), __float_as_uint(x[1]),
-                             __float_as_uint(x[2]), __float_as_uint(x[3]));
+                for (int k = 0; k < 8; ++k)
+                  st_shared_v4(stage_at(srow, q / 4 + k), __float_as_uint(__uint_as_float(o[4 * k]) * f),
+                               __float_as_uint(__uint_as_float(o[4 * k + 1]) * f),
+                               __float_as_uint(__uint_as_float(o[4 * k + 2]) * f),
+                               __float_as_uint(__uint_as_float(o[4 * k + 3]) * f));
               }
+              __syncwarp();
             }
-            __syncwarp();
+            tc_fence_before();
           }
-        };
-        if (g == 1 && worked) put(false);
-        if (!(ok = epi_sync())) break;
-        if (g == 0) put(item->n > 1);
-        tc_fence_before();
-        const long long t = item->tok0 + tok;
-        const int head = item->h * p.G + row % p.G;
-        if (g == 0 && copy == 0 && valid) {
-          if (partial) *reinterpret_cast<float2*>(part + ROWS * D + 2 * row) = make_float2(m, l);
-          else if (p.L) p.L[t * (p.Hkv * p.G) + head] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-        }
-        if (!(ok = epi_sync())) break;
-        // sums of the copies: thread = 8 columns of a row
-        const int rows = min(item->nt, p.tpt) * p.G;
-        for (int x = threadIdx.x; x < rows * (D / 8); x += 256) {
-          const int rr = x / (D / 8), c8 = x % (D / 8);
-          float sum[8] = {};
+          if (!(ok = epi_sync())) break;
+          // sums over the states: thread = 4 columns of a row
+#pragma unroll 1
+          for (int x = threadIdx.x; x < R * (cols / 4); x += 256) {
+            const int rr = x / (cols / 4), c4 = x % (cols / 4);
+            float sum[4] = {};
 #pragma unroll
-          for (int a = 0; a < REP; ++a) {
-            float y[4];
+            for (int a = 0; a < 2 * REP; ++a) {
+              if (a >= states_n) break;
+              float y[4];
+              ld_shared_v4(stage_at(a * R + rr, c4), y);
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              ld_shared_v4(stage_at(a * (BM / REP) + rr, 2 * c8 + hh), y);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) sum[4 * hh + e] += y[e];
+              for (int e = 0; e < 4; ++e) sum[e] += y[e];
+            }
+            const int col = ph * cols + 4 * c4;
+            if (partial) {
+              *reinterpret_cast<float4*>(part + (size_t)rr * D + col) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+            } else {
+              uint16_t* dst = p.o.ptr + (long long)(item->tok0 + rr / p.G) * p.o.ts +
+                              (long long)(item->h * p.G + rr % p.G) * p.o.hs + col;
+              *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(sum[0], sum[1]), pack2<BF16>(sum[2], sum[3]));
             }
           }
-          if (partial) {
-            float4* dst = reinterpret_cast<float4*>(part + (size_t)rr * D + 8 * c8);
-            dst[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
-            dst[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
-          } else {
-            const long long tt = item->tok0 + rr / p.G;
-            uint16_t* dst = p.o.ptr + tt * p.o.ts + (long long)(item->h * p.G + rr % p.G) * p.o.hs + 8 * c8;
-            *reinterpret_cast<uint4*>(dst) = pack8<BF16>(sum);
-          }
+          if (ph + 1 < phases && !(ok = epi_sync())) break;
         }
-        if (!(ok = epi_sync())) break;
+        if (!ok) break;
       }
       item_done();
     }
@@ -969,61 +1007,79 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 }
 
-// Joins the partial states of the items that lie in several blocks' ranges: blocks (c, y) take
-// the item that begins in block c's range, one warp per row.
+// Joins the partial states of the items that lie in several blocks' ranges: blocks (c, y) take the
+// item that begins in block c's range. A warp joins RW rows at once, so that their loads overlap:
+// lane = (row, piece) for the pieces' weights, then all lanes along the columns.
 template <int D, bool BF16, int ROWS>
 __global__ void __launch_bounds__(COMBINE_THREADS) fa_paged_combine_kernel(const __grid_constant__ Params p) {
   constexpr int E = D / 32;  // columns per lane
+  constexpr int RW = ROWS > 128 ? 4 : 1, PB = 32 / RW;  // rows of a warp, pieces at a time
   wait_previous_grid();
-  const int* rec = p.records + blockIdx.x * 8;
-  if (rec[0] == 0) return;
-  const int c0 = blockIdx.x, slot0 = rec[1], c1 = rec[2], h = rec[3], tok0 = rec[4], nt = rec[5];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int Hq = p.Hkv * p.G, n = c1 - c0 + 1;
+  const int4 rec0 = *reinterpret_cast<const int4*>(p.records + blockIdx.x * 8);
+  const int2 rec1 = *reinterpret_cast<const int2*>(p.records + blockIdx.x * 8 + 4);
+  if (rec0.x == 0) return;
+  const int c0 = blockIdx.x, slot0 = rec0.y, n = rec0.z - c0 + 1, h = rec0.w, tok0 = rec1.x, nt = rec1.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, Hq = p.Hkv * p.G;
   auto part = [&](int x) {  // piece x of the item
     return p.parts + (size_t)((c0 + x) * 2 + (x == 0 ? slot0 : 0)) * part_floats(D, ROWS);
   };
-  for (int pr = blockIdx.y * (COMBINE_THREADS / 32) + warp; pr < ROWS; pr += gridDim.y * (COMBINE_THREADS / 32)) {
+  const int pr0 = (blockIdx.y * (COMBINE_THREADS / 32) + warp) * RW;
+  auto token_of = [&](int pr) {  // -1: the place holds no row
     const int row = pr % BM, tok = row / p.G + pr / BM * p.tpt;
-    if (row >= p.tpt * p.G || tok >= nt) continue;
-    float m = -INFINITY, l = 0.f;
-    for (int x = lane; x < n; x += 32) m = fmaxf(m, part(x)[ROWS * D + 2 * pr]);
+    return row < p.tpt * p.G && tok < nt ? tok : -1;
+  };
+  const int my_row = lane / PB, my_piece = lane % PB;
+  const bool mine = token_of(pr0 + my_row) >= 0;
+  float m = -INFINITY;
+  for (int x = my_piece; x < n; x += PB)
+    if (mine) m = fmaxf(m, part(x)[ROWS * D + 2 * (pr0 + my_row)]);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float acc[E] = {};
-    for (int x0 = 0; x0 < n; x0 += 32) {
-      float w = 0.f;
-      if (x0 + lane < n) {
-        const float2 st = *reinterpret_cast<const float2*>(part(x0 + lane) + ROWS * D + 2 * pr);
-        if (st.x != -INFINITY) w = ex2_approx(st.x - m);
-        l += st.y * w;
-      }
-      const int k = min(32, n - x0);
-#pragma unroll 4
-      for (int y = 0; y < k; ++y) {
-        const float wy = __shfl_sync(0xffffffffu, w, y);
-        const float* src = part(x0 + y) + (size_t)pr * D + lane * E;
-        float v[E];
-        if constexpr (E == 4) {
-          const float4 q = *reinterpret_cast<const float4*>(src);
-          v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-        } else {
-          const float2 q = *reinterpret_cast<const float2*>(src);
-          v[0] = q.x, v[1] = q.y;
+  for (int o = PB / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float acc[RW][E] = {}, l = 0.f;
+  for (int x0 = 0; x0 < n; x0 += PB) {
+    float w = 0.f;
+    if (mine && x0 + my_piece < n) {
+      const float2 st = *reinterpret_cast<const float2*>(part(x0 + my_piece) + ROWS * D + 2 * (pr0 + my_row));
+      if (st.x != -INFINITY) w = ex2_approx(st.x - m);
+      l += st.y * w;
+    }
+    const int k = min(PB, n - x0);
+#pragma unroll 2
+    for (int y = 0; y < k; ++y) {
+      const float* src = part(x0 + y) + (size_t)pr0 * D + lane * E;
+#pragma unroll
+      for (int r = 0; r < RW; ++r) {
+        const float wy = __shfl_sync(0xffffffffu, w, r * PB + y);
+        float v[E] = {};
+        if (wy != 0.f) {
+          if constexpr (E == 4) {
+            const float4 q = *reinterpret_cast<const float4*>(src + r * D);
+            v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+          } else {
+            const float2 q = *reinterpret_cast<const float2*>(src + r * D);
+            v[0] = q.x, v[1] = q.y;
+          }
         }
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = wy != 0.f ? fmaf(v[e], wy, acc[e]) : acc[e];
+        for (int e = 0; e < E; ++e) acc[r][e] = fmaf(v[e], wy, acc[r][e]);
       }
     }
-    l = row_sum<32>(l);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+  }
+#pragma unroll
+  for (int o = PB / 2; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+  for (int r = 0; r < RW; ++r) {
+    const float lr = __shfl_sync(0xffffffffu, l, r * PB), mr = __shfl_sync(0xffffffffu, m, r * PB);
+    const int tok = token_of(pr0 + r);
+    if (tok < 0) continue;
+    const float inv = lr > 0.f ? 1.f / lr : 0.f;
     const long long t = tok0 + tok;
-    const int head = h * p.G + row % p.G;
+    const int head = h * p.G + (pr0 + r) % BM % p.G;
     uint16_t* dst = p.o.ptr + t * p.o.ts + (long long)head * p.o.hs + lane * E;
 #pragma unroll
     for (int e = 0; e < E; e += 2)
-      *reinterpret_cast<uint32_t*>(dst + e) = pack2<BF16>(acc[e] * inv, acc[e + 1] * inv);
-    if (p.L && lane == 0) p.L[t * Hq + head] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      *reinterpret_cast<uint32_t*>(dst + e) = pack2<BF16>(acc[r][e] * inv, acc[r][e + 1] * inv);
+    if (p.L && lane == 0) p.L[t * Hq + head] = lr > 0.f ? (mr + log2f(lr)) * 0.69314718055994531f : -INFINITY;
   }
 }
 
