@@ -60,8 +60,25 @@ RopeDev dev(const fa_rope* r) {
 // tokens alone do not give the SMs enough warps to cover the memory latency.
 int head_chunk(long long tokens, int heads, int rows_per_step, int sms) {
   int chunk = heads;
-  while (chunk > rows_per_step && tokens * ((heads + chunk - 1) / chunk) < (long long)sms * 48) chunk = (chunk + 1) / 2;
+  while (chunk > rows_per_step && tokens * ((heads + chunk - 1) / chunk) < (long long)sms * 48)
+    chunk = (chunk / 2 + rows_per_step - 1) / rows_per_step * rows_per_step;
   return chunk;
+}
+
+// A kernel that waits on the device for the previous kernel of the stream (wait_previous_grid):
+// its blocks may be set up while that one still runs.
+template <typename... P, typename... A>
+int launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t st, A... args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return fa_host::launched(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
 // f(type, interleaved) for the four instantiations of a kernel of head dimension D
@@ -100,12 +117,12 @@ NormRopeParams norm_rope_params(const fa_heads* q, const fa_heads* k, const fa_h
                                 int N, const void* wq, const void* wk, float eps, const fa_rope* rope,
                                 const int* positions) {
   NormRopeParams p = {};
-  p.q = dev(q);
-  p.k = dev(k);
-  p.q_out = dev(qo);
-  p.k_out = dev(ko);
-  p.wq = static_cast<const uint16_t*>(wq);
-  p.wk = static_cast<const uint16_t*>(wk);
+  p.x[0] = dev(q);
+  p.x[1] = dev(k);
+  p.y[0] = dev(qo);
+  p.y[1] = dev(ko);
+  p.w[0] = static_cast<const uint16_t*>(wq);
+  p.w[1] = static_cast<const uint16_t*>(wk);
   p.eps = eps;
   p.rope = dev(rope);
   p.positions = positions;
@@ -168,17 +185,9 @@ int launch_paged(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap
   kern<<<sms, paged::NUM_THREADS, SMEM, st>>>(mq, mk, mv, p);
   const int rc = fa_host::launched(cudaPeekAtLastError());
   if (rc != FA_OK) return rc;
-  // its blocks may be set up while the main kernel runs; they wait for its results on the device
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sms, ROWS > 128 ? ROWS / 32 : ROWS / 8);  // a warp joins 4 rows, or 1
-  cfg.blockDim = dim3(paged::COMBINE_THREADS);
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return fa_host::launched(cudaLaunchKernelEx(&cfg, paged::fa_paged_combine_kernel<D, BF16, ROWS>, p));
+  // a warp joins 4 rows, or 1
+  return launch_dependent(paged::fa_paged_combine_kernel<D, BF16, ROWS>, dim3(sms, ROWS > 128 ? ROWS / 32 : ROWS / 8),
+                          dim3(paged::COMBINE_THREADS), st, p);
 }
 
 template <int D, bool BF16>
@@ -245,8 +254,8 @@ int fa_qk_norm_rope_bwd(const fa_heads* dq_out, const fa_heads* dk_out, const fa
   if ((rc = fa_host::current_device(&index, &sms)) != FA_OK) return rc;
   NormRopeParams p = norm_rope_params(q, k, dq, dk, B, N, wq, wk, eps, rope, positions);
   if ((rc = fa_host::status_word(&p.status)) != FA_OK) return rc;
-  p.gq = dev(dq_out);
-  p.gk = dev(dk_out);
+  p.g[0] = dev(dq_out);
+  p.g[1] = dev(dk_out);
   p.part = static_cast<float*>(workspace);
   const int H = q->H + k->H;
   p.chunk = head_chunk(p.tokens, H, 256 / d, sms);
@@ -261,9 +270,8 @@ int fa_qk_norm_rope_bwd(const fa_heads* dq_out, const fa_heads* dk_out, const fa
     else fa_norm_rope_bwd_kernel<128, bf, inter><<<grid, ROW_THREADS, 0, st>>>(p);
     const int rc1 = fa_host::launched(cudaPeekAtLastError());
     if (rc1 != FA_OK) return rc1;
-    if (d == 64) fa_norm_rope_dw_kernel<64><<<4, dim3(32, 32), 0, st>>>(p.part, grid, oq, ok);
-    else fa_norm_rope_dw_kernel<128><<<8, dim3(32, 32), 0, st>>>(p.part, grid, oq, ok);
-    return fa_host::launched(cudaPeekAtLastError());
+    return launch_dependent(d == 64 ? fa_norm_rope_dw_kernel<64> : fa_norm_rope_dw_kernel<128>, dim3(2 * d / 32),
+                            dim3(32, 32), st, (const float*)p.part, grid, oq, ok);
   });
 }
 

@@ -2,9 +2,11 @@
 // (forward and backward) and the append to a paged cache. Included by fa_decoder.cu.
 //
 // All of them read and write each row of d 16-bit elements once and are bound by HBM. A row is
-// held by d/8 lanes, 8 elements (16 bytes) each, so that a warp has 2 (d = 128) or 4 (d = 64)
-// rows in flight per load; a warp works on ONE token, so that its lanes load their angles of the
-// rotation table once and keep them in registers over that token's heads.
+// held by d/8 lanes, 8 elements each, so that a warp has 2 (d = 128) or 4 (d = 64) rows in flight
+// per load; a warp works on ONE token, so that its lanes load their angles of the rotation table
+// once and keep them in registers over that token's heads. A lane holds both elements of each of
+// its 4 pairs (A and B below), so the rotation needs no exchange between lanes, and works on them
+// two at a time (f32x2).
 #pragma once
 
 #include <cuda.h>
@@ -30,66 +32,86 @@ constexpr int ROW_WARPS = ROW_THREADS / 32;
 constexpr int ROW_UNROLL = 4;          // rows of one lane group loaded before the first is used
 constexpr int ROW_BWD_MAX_BLOCKS = 1024;
 
-// 8 consecutive 16-bit elements <-> fp32
-template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
-  unpack2<BF16>(u.x, x[0], x[1]);
-  unpack2<BF16>(u.y, x[2], x[3]);
-  unpack2<BF16>(u.z, x[4], x[5]);
-  unpack2<BF16>(u.w, x[6], x[7]);
-}
+// 8 consecutive 16-bit elements from fp32
 template <bool BF16>
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]), pack2<BF16>(x[4], x[5]),
                     pack2<BF16>(x[6], x[7]));
 }
 
-// A lane's part of one token's rotation: its 8 elements become x*cs + partner*sn. Split halves:
-// the partner elements sit rot/16 lanes away (rot is a multiple of 16, so a lane lies wholly in
-// the first half, the second, or behind both); pairs (2i, 2i+1) sit in the lane itself.
-template <int D, bool INTER>
-struct Turn {
-  float cs[INTER ? 4 : 8], sn[INTER ? 4 : 8];
-  int partner;
+// A lane's 8 elements of a row as 4 pairs (A_i, B_i) in fp32, two pairs to a register pair.
+struct Pairs {
+  uint64_t a[2], b[2];
+};
+__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
+// Where a lane's pairs stand in a row, and a token's rotation of them. Pairs (2i, 2i+1): the lane
+// holds 8 consecutive elements. Split halves (i, i + rot/2): lane l < rot/8 holds elements
+// 4l .. 4l+3 (A) and rot/2 + 4l .. (B); the other lanes hold 8 consecutive elements behind rot,
+// which pass through (cosine 1, sine 0). rot is a multiple of 16.
+template <int D, bool BF16, bool INTER>
+struct Lane {
+  int l, ea, eb;  // lane of the row, first elements of its two runs of 4
+  uint64_t c[2], s[2];
+
+  __device__ __forceinline__ void place(int lane, int rot) {
+    l = lane % (D / 8);
+    const bool split = !INTER && 8 * l < rot;
+    ea = split ? 4 * l : 8 * l;
+    eb = split ? 4 * l + rot / 2 : 8 * l + 4;
+  }
+  // index in the row of A_i and B_i
+  __device__ __forceinline__ int at(int i, bool second) const {
+    return INTER ? 8 * l + 2 * i + second : (second ? eb : ea) + i;
+  }
   // sign = 1 for the rotation, -1 for its transpose
-  __device__ __forceinline__ void load(const RopeDev& rp, int pos, int l, int lane, float sign) {
-    const int half = rp.rot >> 1, e = 8 * l;
-    partner = lane;
-#pragma unroll
-    for (int i = 0; i < (INTER ? 4 : 8); ++i) cs[i] = 1.f, sn[i] = 0.f;
-    if (e >= rp.rot) return;
-    const float* row = rp.table + (size_t)pos * rp.rot;
+  __device__ __forceinline__ void angles(const RopeDev& rp, int pos, float sign) {
+    c[0] = c[1] = f2(1.f, 1.f);
+    s[0] = s[1] = 0;
+    if (8 * l >= rp.rot) return;
+    const float* row = rp.table + (size_t)pos * rp.rot + 4 * l;
+    const float4 x = *reinterpret_cast<const float4*>(row), y = *reinterpret_cast<const float4*>(row + rp.rot / 2);
+    c[0] = f2(x.x, x.y), c[1] = f2(x.z, x.w);
+    s[0] = f2(sign * y.x, sign * y.y), s[1] = f2(sign * y.z, sign * y.w);
+  }
+  __device__ __forceinline__ uint4 load(const uint16_t* row) const {
+    if constexpr (INTER) return *reinterpret_cast<const uint4*>(row + 8 * l);
+    const uint2 x = *reinterpret_cast<const uint2*>(row + ea), y = *reinterpret_cast<const uint2*>(row + eb);
+    return make_uint4(x.x, x.y, y.x, y.y);
+  }
+  __device__ __forceinline__ void store(uint16_t* row, const uint4& u) const {
     if constexpr (INTER) {
-      const float4 c = *reinterpret_cast<const float4*>(row + e / 2);
-      const float4 s = *reinterpret_cast<const float4*>(row + half + e / 2);
-      cs[0] = c.x, cs[1] = c.y, cs[2] = c.z, cs[3] = c.w;
-      sn[0] = sign * s.x, sn[1] = sign * s.y, sn[2] = sign * s.z, sn[3] = sign * s.w;
+      *reinterpret_cast<uint4*>(row + 8 * l) = u;
     } else {
-      const bool second = e >= half;
-      const float* c = row + (second ? e - half : e);
-      const float4 c0 = *reinterpret_cast<const float4*>(c), c1 = *reinterpret_cast<const float4*>(c + 4);
-      const float4 s0 = *reinterpret_cast<const float4*>(c + half), s1 = *reinterpret_cast<const float4*>(c + half + 4);
-      const float sg = second ? sign : -sign;
-      cs[0] = c0.x, cs[1] = c0.y, cs[2] = c0.z, cs[3] = c0.w;
-      cs[4] = c1.x, cs[5] = c1.y, cs[6] = c1.z, cs[7] = c1.w;
-      sn[0] = sg * s0.x, sn[1] = sg * s0.y, sn[2] = sg * s0.z, sn[3] = sg * s0.w;
-      sn[4] = sg * s1.x, sn[5] = sg * s1.y, sn[6] = sg * s1.z, sn[7] = sg * s1.w;
-      partner = second ? lane - half / 8 : lane + half / 8;
+      *reinterpret_cast<uint2*>(row + ea) = make_uint2(u.x, u.y);
+      *reinterpret_cast<uint2*>(row + eb) = make_uint2(u.z, u.w);
     }
   }
-  // every lane of the warp calls this
-  __device__ __forceinline__ void apply(float (&x)[8]) const {
-    if constexpr (INTER) {
+  __device__ __forceinline__ Pairs unpack(const uint4& u) const {
+    float x0, x1, x2, x3, y0, y1, y2, y3;
+    unpack2<BF16>(u.x, x0, x1);
+    unpack2<BF16>(u.y, x2, x3);
+    unpack2<BF16>(u.z, y0, y1);
+    unpack2<BF16>(u.w, y2, y3);
+    if constexpr (INTER) return Pairs{{f2(x0, x2), f2(y0, y2)}, {f2(x1, x3), f2(y1, y3)}};
+    return Pairs{{f2(x0, x1), f2(x2, x3)}, {f2(y0, y1), f2(y2, y3)}};
+  }
+  __device__ __forceinline__ uint4 pack(const Pairs& v) const {
+    if constexpr (INTER)
+      return make_uint4(pack2<BF16>(lo_of(v.a[0]), lo_of(v.b[0])), pack2<BF16>(hi_of(v.a[0]), hi_of(v.b[0])),
+                        pack2<BF16>(lo_of(v.a[1]), lo_of(v.b[1])), pack2<BF16>(hi_of(v.a[1]), hi_of(v.b[1])));
+    return make_uint4(pack2<BF16>(lo_of(v.a[0]), hi_of(v.a[0])), pack2<BF16>(lo_of(v.a[1]), hi_of(v.a[1])),
+                      pack2<BF16>(lo_of(v.b[0]), hi_of(v.b[0])), pack2<BF16>(lo_of(v.b[1]), hi_of(v.b[1])));
+  }
+  // (A, B) -> (A cos - B sin, B cos + A sin)
+  __device__ __forceinline__ void turn(Pairs& v) const {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = a * cs[i] - b * sn[i];
-        x[2 * i + 1] = b * cs[i] + a * sn[i];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * cs[i] + __shfl_sync(0xffffffffu, x[i], partner) * sn[i];
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t minus = s[i] ^ 0x8000000080000000ull;
+      const uint64_t a = f2_fma(v.a[i], c[i], f2_mul(v.b[i], minus));
+      v.b[i] = f2_fma(v.b[i], c[i], f2_mul(v.a[i], s[i]));
+      v.a[i] = a;
     }
   }
 };
@@ -103,24 +125,28 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 
 struct NormRopeParams {
-  HeadsDev q, k, q_out, k_out;  // backward: inputs and their gradients (outputs)
-  HeadsDev gq, gk;              // backward: gradients of the outputs
-  const uint16_t *wq, *wk;
+  HeadsDev x[2], y[2];  // q and k: inputs, and outputs (backward: the inputs' gradients)
+  HeadsDev g[2];        // backward: gradients of the outputs
+  const uint16_t* w[2];
   float eps;
   RopeDev rope;
   const int* positions;
   int N;
-  long long tokens;       // B * N
-  int chunk, n_chunks;    // heads of q then k, `chunk` of them per warp
-  float* part;            // backward: [block][2][D] sums of the weights' gradients
+  long long tokens;     // B * N
+  int chunk, n_chunks;  // heads of q then k, `chunk` of them per warp
+  float* part;          // backward: [block][2][D] sums of the weights' gradients
   int* status;
 };
+
+__device__ __forceinline__ float sum4(const uint64_t (&v)[2]) {
+  return (lo_of(v[0]) + hi_of(v[0])) + (lo_of(v[1]) + hi_of(v[1]));
+}
 
 // y = R(p) (x r w): one warp per (token, chunk of heads).
 template <int D, bool BF16, bool INTER>
 __global__ void __launch_bounds__(ROW_THREADS) fa_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int LPR = D / 8, GPW = 32 / LPR;
-  const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
+  const int lane = threadIdx.x & 31, sub = lane / LPR;
   const long long unit = (long long)blockIdx.x * ROW_WARPS + (threadIdx.x >> 5);
   const long long t = unit / p.n_chunks;
   if (t >= p.tokens) return;
@@ -131,40 +157,44 @@ __global__ void __launch_bounds__(ROW_THREADS) fa_norm_rope_kernel(const __grid_
     if (lane == 0) atomicCAS(p.status, 0, FA_ERR_RANGE);
     return;
   }
-  Turn<D, INTER> turn;
-  turn.load(p.rope, pos, l, lane, 1.f);
-  const int H = p.q.H + p.k.H, h_end = min((c + 1) * p.chunk, H);
-  const uint16_t* qi = p.q.ptr + b * p.q.bs + n * p.q.ts + 8 * l;
-  const uint16_t* ki = p.k.ptr + b * p.k.bs + n * p.k.ts + 8 * l;
-  uint16_t* qo = p.q_out.ptr + b * p.q_out.bs + n * p.q_out.ts + 8 * l;
-  uint16_t* ko = p.k_out.ptr + b * p.k_out.bs + n * p.k_out.ts + 8 * l;
-  for (int h0 = c * p.chunk; h0 < h_end; h0 += GPW * ROW_UNROLL) {
-    uint4 u[ROW_UNROLL];
+  Lane<D, BF16, INTER> ln;
+  ln.place(lane, p.rope.rot);
+  ln.angles(p.rope, pos, 1.f);
+#pragma unroll 1
+  for (int set = 0; set < 2; ++set) {
+    const HeadsDev &in = p.x[set], &out = p.y[set];
+    const int first = set ? p.x[0].H : 0;
+    const int h_begin = max(c * p.chunk - first, 0), h_end = min((c + 1) * p.chunk - first, in.H);
+    if (h_begin >= h_end) continue;
+    const Pairs w = ln.unpack(ln.load(p.w[set]));
+    const uint16_t* src = in.ptr + b * in.bs + n * in.ts;
+    uint16_t* dst = out.ptr + b * out.bs + n * out.ts;
+#pragma unroll 1
+    for (int h0 = h_begin; h0 < h_end; h0 += GPW * ROW_UNROLL) {
+      uint4 u[ROW_UNROLL];
 #pragma unroll
-    for (int i = 0; i < ROW_UNROLL; ++i) {
-      const int h = h0 + i * GPW + sub;
-      u[i] = make_uint4(0, 0, 0, 0);
-      if (h < h_end)
-        u[i] = *reinterpret_cast<const uint4*>(h < p.q.H ? qi + h * p.q.hs : ki + (h - p.q.H) * p.k.hs);
-    }
+      for (int i = 0; i < ROW_UNROLL; ++i) {
+        const int h = h0 + i * GPW + sub;
+        u[i] = make_uint4(0, 0, 0, 0);
+        if (h < h_end) u[i] = ln.load(src + h * in.hs);
+      }
 #pragma unroll
-    for (int i = 0; i < ROW_UNROLL; ++i) {
-      const int h = h0 + i * GPW + sub;
-      float x[8], w[8];
-      unpack8<BF16>(u[i], x);
-      float ss = 0.f;
+      for (int i = 0; i < ROW_UNROLL; ++i) {
+        const int h = h0 + i * GPW + sub;
+        Pairs x = ln.unpack(u[i]);
+        uint64_t sq[2];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-      const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-      const uint16_t* wp = h < p.q.H ? p.wq : p.wk;
-      uint4 wu = make_uint4(0, 0, 0, 0);
-      if (h < h_end) wu = *reinterpret_cast<const uint4*>(wp + 8 * l);
-      unpack8<BF16>(wu, w);
+        for (int e = 0; e < 2; ++e) sq[e] = f2_fma(x.b[e], x.b[e], f2_mul(x.a[e], x.a[e]));
+        const float r = rsqrtf(row_sum<LPR>(sum4(sq)) * (1.f / D) + p.eps);
+        const uint64_t r2 = f2(r, r);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= r * w[e];
-      turn.apply(x);
-      if (h < h_end)
-        *reinterpret_cast<uint4*>(h < p.q.H ? qo + h * p.q_out.hs : ko + (h - p.q.H) * p.k_out.hs) = pack8<BF16>(x);
+        for (int e = 0; e < 2; ++e) {
+          x.a[e] = f2_mul(x.a[e], f2_mul(w.a[e], r2));
+          x.b[e] = f2_mul(x.b[e], f2_mul(w.b[e], r2));
+        }
+        ln.turn(x);
+        if (h < h_end) ln.store(dst + h * out.hs, ln.pack(x));
+      }
     }
   }
 }
@@ -173,18 +203,15 @@ __global__ void __launch_bounds__(ROW_THREADS) fa_norm_rope_kernel(const __grid_
 // A fixed number of blocks walks the (token, chunk) units, so each sum has a fixed order.
 template <int D, bool BF16, bool INTER>
 __global__ void __launch_bounds__(ROW_THREADS) fa_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
-  constexpr int LPR = D / 8, GPW = 32 / LPR;
+  constexpr int LPR = D / 8, GPW = 32 / LPR, UNROLL = 2;
   __shared__ float sums[ROW_WARPS][2][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, sub = lane / LPR;
-  const int H = p.q.H + p.k.H;
-  float aq[8] = {}, ak[8] = {}, wq[8], wk[8];
-  uint4 wu = make_uint4(0, 0, 0, 0);
-  if (p.q.H) wu = *reinterpret_cast<const uint4*>(p.wq + 8 * l);
-  unpack8<BF16>(wu, wq);
-  wu = make_uint4(0, 0, 0, 0);
-  if (p.k.H) wu = *reinterpret_cast<const uint4*>(p.wk + 8 * l);
-  unpack8<BF16>(wu, wk);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR;
+  Lane<D, BF16, INTER> ln;
+  ln.place(lane, p.rope.rot);
+  launch_dependents();
+  Pairs dw[2] = {};
   const long long units = p.tokens * p.n_chunks, step = (long long)gridDim.x * ROW_WARPS;
+#pragma unroll 1
   for (long long unit = (long long)blockIdx.x * ROW_WARPS + warp; unit < units; unit += step) {
     const long long t = unit / p.n_chunks;
     const int c = (int)(unit % p.n_chunks);
@@ -194,62 +221,68 @@ __global__ void __launch_bounds__(ROW_THREADS) fa_norm_rope_bwd_kernel(const __g
       if (lane == 0) atomicCAS(p.status, 0, FA_ERR_RANGE);
       continue;
     }
-    Turn<D, INTER> turn;
-    turn.load(p.rope, pos, l, lane, -1.f);
-    const int h_end = min((c + 1) * p.chunk, H);
-    const long long oq = b * p.q.bs + n * p.q.ts + 8 * l, ok = b * p.k.bs + n * p.k.ts + 8 * l;
-    const long long ogq = b * p.gq.bs + n * p.gq.ts + 8 * l, ogk = b * p.gk.bs + n * p.gk.ts + 8 * l;
-    const long long ooq = b * p.q_out.bs + n * p.q_out.ts + 8 * l, ook = b * p.k_out.bs + n * p.k_out.ts + 8 * l;
-    for (int h0 = c * p.chunk; h0 < h_end; h0 += GPW * 2) {
-      uint4 ux[2], ug[2];
+    ln.angles(p.rope, pos, -1.f);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int h = h0 + i * GPW + sub;
-        ux[i] = ug[i] = make_uint4(0, 0, 0, 0);
-        if (h < h_end) {
-          const bool isq = h < p.q.H;
-          const long long hk = h - p.q.H;
-          ux[i] = *reinterpret_cast<const uint4*>(isq ? p.q.ptr + oq + h * p.q.hs : p.k.ptr + ok + hk * p.k.hs);
-          ug[i] = *reinterpret_cast<const uint4*>(isq ? p.gq.ptr + ogq + h * p.gq.hs : p.gk.ptr + ogk + hk * p.gk.hs);
+    for (int set = 0; set < 2; ++set) {
+      const HeadsDev &in = p.x[set], &gr = p.g[set], &out = p.y[set];
+      const int first = set ? p.x[0].H : 0;
+      const int h_begin = max(c * p.chunk - first, 0), h_end = min((c + 1) * p.chunk - first, in.H);
+      if (h_begin >= h_end) continue;
+      const Pairs w = ln.unpack(ln.load(p.w[set]));
+      const uint16_t* src = in.ptr + b * in.bs + n * in.ts;
+      const uint16_t* gsrc = gr.ptr + b * gr.bs + n * gr.ts;
+      uint16_t* dst = out.ptr + b * out.bs + n * out.ts;
+#pragma unroll 1
+      for (int h0 = h_begin; h0 < h_end; h0 += GPW * UNROLL) {
+        uint4 ux[UNROLL], ug[UNROLL];
+#pragma unroll
+        for (int i = 0; i < UNROLL; ++i) {
+          const int h = h0 + i * GPW + sub;
+          ux[i] = ug[i] = make_uint4(0, 0, 0, 0);
+          if (h < h_end) {
+            ux[i] = ln.load(src + h * in.hs);
+            ug[i] = ln.load(gsrc + h * gr.hs);
+          }
         }
-      }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int h = h0 + i * GPW + sub;
-        const bool isq = h < p.q.H;
-        float x[8], g[8];
-        unpack8<BF16>(ux[i], x);
-        unpack8<BF16>(ug[i], g);
-        turn.apply(g);
-        float ss = 0.f, gx = 0.f;
+        for (int i = 0; i < UNROLL; ++i) {
+          const int h = h0 + i * GPW + sub;
+          Pairs x = ln.unpack(ux[i]), g = ln.unpack(ug[i]), u;
+          ln.turn(g);
+          uint64_t sq[2], gx[2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          ss = fmaf(x[e], x[e], ss);
-          gx = fmaf(g[e] * (isq ? wq[e] : wk[e]), x[e], gx);
+          for (int e = 0; e < 2; ++e) {
+            sq[e] = f2_fma(x.b[e], x.b[e], f2_mul(x.a[e], x.a[e]));
+            u.a[e] = f2_mul(g.a[e], w.a[e]);
+            u.b[e] = f2_mul(g.b[e], w.b[e]);
+            gx[e] = f2_fma(u.b[e], x.b[e], f2_mul(u.a[e], x.a[e]));
+          }
+          const float r = rsqrtf(row_sum<LPR>(sum4(sq)) * (1.f / D) + p.eps);
+          const float m = row_sum<LPR>(sum4(gx)) * r * (-1.f / D);  // - mean(u x r)
+          const uint64_t r2 = f2(r, r), m2 = f2(m, m);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {  // rows past h_end hold zeros
+            const uint64_t xa = f2_mul(x.a[e], r2), xb = f2_mul(x.b[e], r2);
+            dw[set].a[e] = f2_fma(g.a[e], xa, dw[set].a[e]);
+            dw[set].b[e] = f2_fma(g.b[e], xb, dw[set].b[e]);
+            x.a[e] = f2_mul(f2_fma(xa, m2, u.a[e]), r2);
+            x.b[e] = f2_mul(f2_fma(xb, m2, u.b[e]), r2);
+          }
+          if (h < h_end) ln.store(dst + h * out.hs, ln.pack(x));
         }
-        const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-        const float m = row_sum<LPR>(gx) * r * (1.f / D);  // mean(u x r)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float xr = x[e] * r, gw = g[e] * xr;  // rows past h_end hold zeros
-          if (isq) aq[e] += gw; else ak[e] += gw;
-          x[e] = r * (g[e] * (isq ? wq[e] : wk[e]) - xr * m);
-        }
-        if (h < h_end)
-          *reinterpret_cast<uint4*>(isq ? p.q_out.ptr + ooq + h * p.q_out.hs
-                                        : p.k_out.ptr + ook + (long long)(h - p.q.H) * p.k_out.hs) = pack8<BF16>(x);
       }
     }
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int set = 0; set < 2; ++set)
 #pragma unroll
-    for (int o = LPR; o < 32; o <<= 1) {
-      aq[e] += __shfl_xor_sync(0xffffffffu, aq[e], o);
-      ak[e] += __shfl_xor_sync(0xffffffffu, ak[e], o);
+    for (int i = 0; i < 8; ++i) {
+      const uint64_t v = i < 4 ? dw[set].a[i >> 1] : dw[set].b[(i >> 1) - 2];
+      float x = i & 1 ? hi_of(v) : lo_of(v);
+#pragma unroll
+      for (int o = LPR; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      if (sub == 0) sums[warp][set][ln.at(i & 3, i >= 4)] = x;
     }
-    if (sub == 0) sums[warp][0][8 * l + e] = aq[e], sums[warp][1][8 * l + e] = ak[e];
-  }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * D; i += ROW_THREADS) {
     float s = 0.f;
@@ -263,6 +296,7 @@ __global__ void __launch_bounds__(ROW_THREADS) fa_norm_rope_bwd_kernel(const __g
 template <int D>
 __global__ void __launch_bounds__(1024) fa_norm_rope_dw_kernel(const float* part, int blocks, float* dwq, float* dwk) {
   __shared__ float s[32][33];
+  wait_previous_grid();
   const int col = blockIdx.x * 32 + threadIdx.x;
   float a = 0.f;
   for (int i = threadIdx.y; i < blocks; i += 32) a += part[(size_t)i * 2 * D + col];
@@ -310,7 +344,7 @@ __device__ __forceinline__ int find_sequence(const int* cu, int B, int t, int la
 template <int D, bool BF16, bool INTER>
 __global__ void __launch_bounds__(ROW_THREADS) fa_paged_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LPR = D / 8, GPW = 32 / LPR;
-  const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
+  const int lane = threadIdx.x & 31, sub = lane / LPR;
   const long long unit = (long long)blockIdx.x * ROW_WARPS + (threadIdx.x >> 5);
   const int t = (int)(unit / p.n_chunks);
   if (t >= p.T) return;
@@ -325,31 +359,31 @@ __global__ void __launch_bounds__(ROW_THREADS) fa_paged_append_kernel(const __gr
     if (lane == 0) atomicCAS(p.status, 0, FA_ERR_RANGE);
     return;
   }
-  const long long base = page * p.page_stride + (long long)(pos % p.page_size) * p.token_stride + 8 * l;
-  Turn<D, INTER> turn;
-  turn.load(p.rope, pos, l, lane, 1.f);
+  const long long base = page * p.page_stride + (long long)(pos % p.page_size) * p.token_stride;
+  Lane<D, BF16, INTER> ln;
+  ln.place(lane, p.rope.rot);
+  ln.angles(p.rope, pos, 1.f);
   const int Hk = p.k.H, h_end = min((c + 1) * p.chunk, 2 * Hk);
-  const uint16_t* ki = p.k.ptr + t * p.k.ts + 8 * l;
-  const uint16_t* vi = p.v.ptr + t * p.v.ts + 8 * l;
+  const uint16_t* ki = p.k.ptr + t * p.k.ts;
+  const uint16_t* vi = p.v.ptr + t * p.v.ts;
   for (int h0 = c * p.chunk; h0 < h_end; h0 += GPW * ROW_UNROLL) {
     uint4 u[ROW_UNROLL];
 #pragma unroll
     for (int i = 0; i < ROW_UNROLL; ++i) {
       const int h = h0 + i * GPW + sub;
       u[i] = make_uint4(0, 0, 0, 0);
-      if (h < h_end) u[i] = *reinterpret_cast<const uint4*>(h < Hk ? ki + h * p.k.hs : vi + (h - Hk) * p.v.hs);
+      if (h < h_end) u[i] = ln.load(h < Hk ? ki + h * p.k.hs : vi + (h - Hk) * p.v.hs);
     }
 #pragma unroll
     for (int i = 0; i < ROW_UNROLL; ++i) {
       const int h = h0 + i * GPW + sub;
-      if (p.rope.rot && h0 + i * GPW < Hk) {  // a warp's rows of this step may straddle k and v
-        float x[8];
-        unpack8<BF16>(u[i], x);
-        turn.apply(x);
-        if (h < Hk) u[i] = pack8<BF16>(x);
+      if (h >= h_end) continue;
+      if (p.rope.rot && h < Hk) {
+        Pairs x = ln.unpack(u[i]);
+        ln.turn(x);
+        u[i] = ln.pack(x);
       }
-      if (h < h_end)
-        *reinterpret_cast<uint4*>((h < Hk ? p.kp + h * p.head_stride : p.vp + (h - Hk) * p.head_stride) + base) = u[i];
+      ln.store((h < Hk ? p.kp + h * p.head_stride : p.vp + (h - Hk) * p.head_stride) + base, u[i]);
     }
   }
 }
