@@ -105,7 +105,7 @@ int norm_rope_args(const fa_heads* const* sets, int n, int B, int N, int d, cons
   if (Hq < 0 || Hk < 0 || (long long)Hq + Hk > 0x7fffffffLL) return FA_ERR_SHAPE;
   if (B == 0 || N == 0 || Hq + Hk == 0) { *noop = true; return FA_OK; }
   const long long tokens = (long long)B * N;
-  if (tokens > 0x7fffffffLL || tokens * ((long long)Hq + Hk) > 0x7fffffffLL * ROW_WARPS) return FA_ERR_SHAPE;
+  if (tokens > 0x7fffffffLL || tokens * ((long long)Hq + Hk) > 0x7fffffffLL) return FA_ERR_SHAPE;
   for (int i = 0; i < n; ++i)
     if ((rc = check_heads(sets[i])) != FA_OK) return rc;
   if ((Hq && !wq) || (Hk && !wk)) return FA_ERR_NULL;
@@ -127,7 +127,6 @@ NormRopeParams norm_rope_params(const fa_heads* q, const fa_heads* k, const fa_h
   p.rope = dev(rope);
   p.positions = positions;
   p.N = N;
-  p.tokens = (long long)B * N;
   return p;
 }
 
@@ -201,6 +200,12 @@ int paged_forms(int form, const CUtensorMap& mq, const CUtensorMap& mk, const CU
   }
 }
 
+void row_units(NormRopeParams* p, long long tokens, int heads, int d, int sms) {
+  p->chunk = head_chunk(tokens, heads, 256 / d, sms);
+  p->n_chunks = (heads + p->chunk - 1) / p->chunk;
+  p->units = (uint32_t)(tokens * p->n_chunks);
+}
+
 }  // namespace
 
 extern "C" {
@@ -217,9 +222,8 @@ int fa_qk_norm_rope(const fa_heads* q, const fa_heads* k, const fa_heads* q_out,
   NormRopeParams p = norm_rope_params(q, k, q_out, k_out, B, N, wq, wk, eps, rope, positions);
   if ((rc = fa_host::status_word(&p.status)) != FA_OK) return rc;
   const int H = q->H + k->H;
-  p.chunk = head_chunk(p.tokens, H, 256 / d, sms);
-  p.n_chunks = (H + p.chunk - 1) / p.chunk;
-  const unsigned grid = (unsigned)((p.tokens * p.n_chunks + ROW_WARPS - 1) / ROW_WARPS);
+  row_units(&p, (long long)B * N, H, d, sms);
+  const unsigned grid = (p.units - 1) / ROW_WARPS + 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return by_type(dtype == FA_BF16, rope && rope->interleaved, [&](auto bf, auto inter) {
     if (d == 64) fa_norm_rope_kernel<64, bf, inter><<<grid, ROW_THREADS, 0, st>>>(p);
@@ -258,11 +262,10 @@ int fa_qk_norm_rope_bwd(const fa_heads* dq_out, const fa_heads* dk_out, const fa
   p.g[1] = dev(dk_out);
   p.part = static_cast<float*>(workspace);
   const int H = q->H + k->H;
-  p.chunk = head_chunk(p.tokens, H, 256 / d, sms);
-  p.n_chunks = (H + p.chunk - 1) / p.chunk;
-  const long long blocks = (p.tokens * p.n_chunks + ROW_WARPS - 1) / ROW_WARPS;
-  int grid = 4 * sms < ROW_BWD_MAX_BLOCKS ? 4 * sms : ROW_BWD_MAX_BLOCKS;
-  if (blocks < grid) grid = (int)blocks;
+  row_units(&p, (long long)B * N, H, d, sms);
+  const int most = 2 * sms < ROW_BWD_MAX_BLOCKS ? 2 * sms : ROW_BWD_MAX_BLOCKS;
+  const unsigned blocks = (p.units - 1) / ROW_WARPS + 1;
+  const int grid = blocks < (unsigned)most ? (int)blocks : most;
   float* oq = q->H ? dwq : nullptr;
   float* ok = k->H ? dwk : nullptr;
   return by_type(dtype == FA_BF16, rope && rope->interleaved, [&](auto bf, auto inter) {

@@ -132,7 +132,7 @@ struct NormRopeParams {
   RopeDev rope;
   const int* positions;
   int N;
-  long long tokens;     // B * N
+  uint32_t units;       // tokens * n_chunks
   int chunk, n_chunks;  // heads of q then k, `chunk` of them per warp
   float* part;          // backward: [block][2][D] sums of the weights' gradients
   int* status;
@@ -142,17 +142,34 @@ __device__ __forceinline__ float sum4(const uint64_t (&v)[2]) {
   return (lo_of(v[0]) + hi_of(v[0])) + (lo_of(v[1]) + hi_of(v[1]));
 }
 
-// y = R(p) (x r w): one warp per (token, chunk of heads).
+// A warp's unit: one token's heads [c chunk, (c+1) chunk) of q's, then k's. 32-bit divisions: the
+// host checks that the units fit.
+struct RowUnit {
+  int t, b, n, c;
+  __device__ __forceinline__ RowUnit(const NormRopeParams& p, uint32_t unit) {
+    t = p.n_chunks == 1 ? unit : unit / (uint32_t)p.n_chunks;
+    c = (int)(unit - (uint32_t)t * p.n_chunks) * p.chunk;
+    b = (uint32_t)t / (uint32_t)p.N;
+    n = t - b * p.N;
+  }
+  // the unit's heads of a set whose first head is `first`
+  __device__ __forceinline__ int begin(int first) const { return max(c - first, 0); }
+  __device__ __forceinline__ int end(const NormRopeParams& p, int first, int H) const { return min(c + p.chunk - first, H); }
+  // first row of this lane group
+  __device__ __forceinline__ uint16_t* row(const HeadsDev& x, int h) const {
+    return x.ptr + b * x.bs + n * x.ts + h * x.hs;
+  }
+};
+
+// y = R(p) (x r w): one warp per unit.
 template <int D, bool BF16, bool INTER>
-__global__ void __launch_bounds__(ROW_THREADS) fa_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(ROW_THREADS, 4) fa_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int LPR = D / 8, GPW = 32 / LPR;
   const int lane = threadIdx.x & 31, sub = lane / LPR;
-  const long long unit = (long long)blockIdx.x * ROW_WARPS + (threadIdx.x >> 5);
-  const long long t = unit / p.n_chunks;
-  if (t >= p.tokens) return;
-  const int c = (int)(unit % p.n_chunks);
-  const int b = (int)(t / p.N), n = (int)(t % p.N);
-  const int pos = p.positions ? p.positions[t] : n;
+  const uint32_t unit = blockIdx.x * ROW_WARPS + (threadIdx.x >> 5);
+  if (unit >= p.units) return;
+  const RowUnit at(p, unit);
+  const int pos = p.positions ? p.positions[at.t] : at.n;
   if (p.rope.rot && (pos < 0 || pos >= p.rope.length)) {
     if (lane == 0) atomicCAS(p.status, 0, FA_ERR_RANGE);
     return;
@@ -163,60 +180,60 @@ __global__ void __launch_bounds__(ROW_THREADS) fa_norm_rope_kernel(const __grid_
 #pragma unroll 1
   for (int set = 0; set < 2; ++set) {
     const HeadsDev &in = p.x[set], &out = p.y[set];
-    const int first = set ? p.x[0].H : 0;
-    const int h_begin = max(c * p.chunk - first, 0), h_end = min((c + 1) * p.chunk - first, in.H);
+    const int first = set ? p.x[0].H : 0, h_begin = at.begin(first), h_end = at.end(p, first, in.H);
     if (h_begin >= h_end) continue;
     const Pairs w = ln.unpack(ln.load(p.w[set]));
-    const uint16_t* src = in.ptr + b * in.bs + n * in.ts;
-    uint16_t* dst = out.ptr + b * out.bs + n * out.ts;
+    const uint16_t* src = at.row(in, h_begin + sub);
+    uint16_t* dst = at.row(out, h_begin + sub);
+    const long long src_step = GPW * in.hs, dst_step = GPW * out.hs;
+    auto finish = [&](const uint4& u, uint16_t* to, bool live) {
+      Pairs x = ln.unpack(u);
+      uint64_t sq[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) sq[e] = f2_fma(x.b[e], x.b[e], f2_mul(x.a[e], x.a[e]));
+      const float r = rsqrtf(row_sum<LPR>(sum4(sq)) * (1.f / D) + p.eps);
+      const uint64_t r2 = f2(r, r);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        x.a[e] = f2_mul(x.a[e], f2_mul(w.a[e], r2));
+        x.b[e] = f2_mul(x.b[e], f2_mul(w.b[e], r2));
+      }
+      ln.turn(x);
+      if (live) ln.store(to, ln.pack(x));
+    };
+    int left = h_end - h_begin;  // heads
 #pragma unroll 1
-    for (int h0 = h_begin; h0 < h_end; h0 += GPW * ROW_UNROLL) {
+    for (; left >= GPW * ROW_UNROLL; left -= GPW * ROW_UNROLL) {
       uint4 u[ROW_UNROLL];
 #pragma unroll
-      for (int i = 0; i < ROW_UNROLL; ++i) {
-        const int h = h0 + i * GPW + sub;
-        u[i] = make_uint4(0, 0, 0, 0);
-        if (h < h_end) u[i] = ln.load(src + h * in.hs);
-      }
+      for (int i = 0; i < ROW_UNROLL; ++i, src += src_step) u[i] = ln.load(src);
 #pragma unroll
-      for (int i = 0; i < ROW_UNROLL; ++i) {
-        const int h = h0 + i * GPW + sub;
-        Pairs x = ln.unpack(u[i]);
-        uint64_t sq[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) sq[e] = f2_fma(x.b[e], x.b[e], f2_mul(x.a[e], x.a[e]));
-        const float r = rsqrtf(row_sum<LPR>(sum4(sq)) * (1.f / D) + p.eps);
-        const uint64_t r2 = f2(r, r);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          x.a[e] = f2_mul(x.a[e], f2_mul(w.a[e], r2));
-          x.b[e] = f2_mul(x.b[e], f2_mul(w.b[e], r2));
-        }
-        ln.turn(x);
-        if (h < h_end) ln.store(dst + h * out.hs, ln.pack(x));
-      }
+      for (int i = 0; i < ROW_UNROLL; ++i, dst += dst_step) finish(u[i], dst, true);
+    }
+#pragma unroll 1
+    for (; left > 0; left -= GPW, src += src_step, dst += dst_step) {
+      const bool live = sub < left;
+      finish(live ? ln.load(src) : make_uint4(0, 0, 0, 0), dst, live);
     }
   }
 }
 
 // dx = r (u - x r mean(u x r)), u = R^T dy * w; the block's sums of R^T dy * x * r go to `part`.
-// A fixed number of blocks walks the (token, chunk) units, so each sum has a fixed order.
+// A fixed number of blocks walks the units, so each sum has a fixed order. Four rows of both
+// tensors in flight per lane group and two blocks per SM (128 registers).
 template <int D, bool BF16, bool INTER>
-__global__ void __launch_bounds__(ROW_THREADS) fa_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
-  constexpr int LPR = D / 8, GPW = 32 / LPR, UNROLL = 2;
+__global__ void __launch_bounds__(ROW_THREADS, 2) fa_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
+  constexpr int LPR = D / 8, GPW = 32 / LPR;
   __shared__ float sums[ROW_WARPS][2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR;
   Lane<D, BF16, INTER> ln;
   ln.place(lane, p.rope.rot);
   launch_dependents();
   Pairs dw[2] = {};
-  const long long units = p.tokens * p.n_chunks, step = (long long)gridDim.x * ROW_WARPS;
 #pragma unroll 1
-  for (long long unit = (long long)blockIdx.x * ROW_WARPS + warp; unit < units; unit += step) {
-    const long long t = unit / p.n_chunks;
-    const int c = (int)(unit % p.n_chunks);
-    const int b = (int)(t / p.N), n = (int)(t % p.N);
-    const int pos = p.positions ? p.positions[t] : n;
+  for (uint32_t unit = blockIdx.x * ROW_WARPS + warp; unit < p.units; unit += gridDim.x * ROW_WARPS) {
+    const RowUnit at(p, unit);
+    const int pos = p.positions ? p.positions[at.t] : at.n;
     if (p.rope.rot && (pos < 0 || pos >= p.rope.length)) {
       if (lane == 0) atomicCAS(p.status, 0, FA_ERR_RANGE);
       continue;
@@ -225,51 +242,54 @@ __global__ void __launch_bounds__(ROW_THREADS) fa_norm_rope_bwd_kernel(const __g
 #pragma unroll
     for (int set = 0; set < 2; ++set) {
       const HeadsDev &in = p.x[set], &gr = p.g[set], &out = p.y[set];
-      const int first = set ? p.x[0].H : 0;
-      const int h_begin = max(c * p.chunk - first, 0), h_end = min((c + 1) * p.chunk - first, in.H);
+      const int first = set ? p.x[0].H : 0, h_begin = at.begin(first), h_end = at.end(p, first, in.H);
       if (h_begin >= h_end) continue;
       const Pairs w = ln.unpack(ln.load(p.w[set]));
-      const uint16_t* src = in.ptr + b * in.bs + n * in.ts;
-      const uint16_t* gsrc = gr.ptr + b * gr.bs + n * gr.ts;
-      uint16_t* dst = out.ptr + b * out.bs + n * out.ts;
+      const uint16_t* src = at.row(in, h_begin + sub);
+      const uint16_t* gsrc = at.row(gr, h_begin + sub);
+      uint16_t* dst = at.row(out, h_begin + sub);
+      const long long src_step = GPW * in.hs, g_step = GPW * gr.hs, dst_step = GPW * out.hs;
+      auto finish = [&](const uint4& ux, const uint4& ug, uint16_t* to, bool live) {  // zeros where not live
+        Pairs x = ln.unpack(ux), g = ln.unpack(ug), u;
+        ln.turn(g);
+        uint64_t sq[2], gx[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sq[e] = f2_fma(x.b[e], x.b[e], f2_mul(x.a[e], x.a[e]));
+          u.a[e] = f2_mul(g.a[e], w.a[e]);
+          u.b[e] = f2_mul(g.b[e], w.b[e]);
+          gx[e] = f2_fma(u.b[e], x.b[e], f2_mul(u.a[e], x.a[e]));
+        }
+        const float r = rsqrtf(row_sum<LPR>(sum4(sq)) * (1.f / D) + p.eps);
+        const float m = row_sum<LPR>(sum4(gx)) * r * (-1.f / D);  // - mean(u x r)
+        const uint64_t r2 = f2(r, r), m2 = f2(m, m);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint64_t xa = f2_mul(x.a[e], r2), xb = f2_mul(x.b[e], r2);
+          dw[set].a[e] = f2_fma(g.a[e], xa, dw[set].a[e]);
+          dw[set].b[e] = f2_fma(g.b[e], xb, dw[set].b[e]);
+          x.a[e] = f2_mul(f2_fma(xa, m2, u.a[e]), r2);
+          x.b[e] = f2_mul(f2_fma(xb, m2, u.b[e]), r2);
+        }
+        if (live) ln.store(to, ln.pack(x));
+      };
+      int left = h_end - h_begin;  // heads
 #pragma unroll 1
-      for (int h0 = h_begin; h0 < h_end; h0 += GPW * UNROLL) {
-        uint4 ux[UNROLL], ug[UNROLL];
+      for (; left >= GPW * ROW_UNROLL; left -= GPW * ROW_UNROLL) {
+        uint4 ux[ROW_UNROLL], ug[ROW_UNROLL];
 #pragma unroll
-        for (int i = 0; i < UNROLL; ++i) {
-          const int h = h0 + i * GPW + sub;
-          ux[i] = ug[i] = make_uint4(0, 0, 0, 0);
-          if (h < h_end) {
-            ux[i] = ln.load(src + h * in.hs);
-            ug[i] = ln.load(gsrc + h * gr.hs);
-          }
+        for (int i = 0; i < ROW_UNROLL; ++i, src += src_step, gsrc += g_step) {
+          ux[i] = ln.load(src);
+          ug[i] = ln.load(gsrc);
         }
 #pragma unroll
-        for (int i = 0; i < UNROLL; ++i) {
-          const int h = h0 + i * GPW + sub;
-          Pairs x = ln.unpack(ux[i]), g = ln.unpack(ug[i]), u;
-          ln.turn(g);
-          uint64_t sq[2], gx[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            sq[e] = f2_fma(x.b[e], x.b[e], f2_mul(x.a[e], x.a[e]));
-            u.a[e] = f2_mul(g.a[e], w.a[e]);
-            u.b[e] = f2_mul(g.b[e], w.b[e]);
-            gx[e] = f2_fma(u.b[e], x.b[e], f2_mul(u.a[e], x.a[e]));
-          }
-          const float r = rsqrtf(row_sum<LPR>(sum4(sq)) * (1.f / D) + p.eps);
-          const float m = row_sum<LPR>(sum4(gx)) * r * (-1.f / D);  // - mean(u x r)
-          const uint64_t r2 = f2(r, r), m2 = f2(m, m);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {  // rows past h_end hold zeros
-            const uint64_t xa = f2_mul(x.a[e], r2), xb = f2_mul(x.b[e], r2);
-            dw[set].a[e] = f2_fma(g.a[e], xa, dw[set].a[e]);
-            dw[set].b[e] = f2_fma(g.b[e], xb, dw[set].b[e]);
-            x.a[e] = f2_mul(f2_fma(xa, m2, u.a[e]), r2);
-            x.b[e] = f2_mul(f2_fma(xb, m2, u.b[e]), r2);
-          }
-          if (h < h_end) ln.store(dst + h * out.hs, ln.pack(x));
-        }
+        for (int i = 0; i < ROW_UNROLL; ++i, dst += dst_step) finish(ux[i], ug[i], dst, true);
+      }
+#pragma unroll 1
+      for (; left > 0; left -= GPW, src += src_step, gsrc += g_step, dst += dst_step) {
+        const bool live = sub < left;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        finish(live ? ln.load(src) : zero, live ? ln.load(gsrc) : zero, dst, live);
       }
     }
   }
