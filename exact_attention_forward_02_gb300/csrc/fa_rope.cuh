@@ -362,13 +362,13 @@ __device__ __forceinline__ int find_sequence(const int* cu, int B, int t, int la
 // One warp per (token, chunk of heads): the token's sequence, position, page and slot, then its
 // rows of k (rotated) and v (copied).
 template <int D, bool BF16, bool INTER>
-__global__ void __launch_bounds__(ROW_THREADS) fa_paged_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(ROW_THREADS, 4) fa_paged_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LPR = D / 8, GPW = 32 / LPR;
   const int lane = threadIdx.x & 31, sub = lane / LPR;
-  const long long unit = (long long)blockIdx.x * ROW_WARPS + (threadIdx.x >> 5);
-  const int t = (int)(unit / p.n_chunks);
+  const uint32_t unit = blockIdx.x * ROW_WARPS + (threadIdx.x >> 5);
+  const int t = unit / (uint32_t)p.n_chunks;
   if (t >= p.T) return;
-  const int c = (int)(unit % p.n_chunks);
+  const int c = (int)(unit - (uint32_t)t * p.n_chunks);
   const int b = find_sequence(p.cu, p.B, t, lane);
   if (b < 0) return;
   const int pos = p.lens[b] - (p.cu[b + 1] - t);
@@ -383,28 +383,36 @@ __global__ void __launch_bounds__(ROW_THREADS) fa_paged_append_kernel(const __gr
   Lane<D, BF16, INTER> ln;
   ln.place(lane, p.rope.rot);
   ln.angles(p.rope, pos, 1.f);
-  const int Hk = p.k.H, h_end = min((c + 1) * p.chunk, 2 * Hk);
-  const uint16_t* ki = p.k.ptr + t * p.k.ts;
-  const uint16_t* vi = p.v.ptr + t * p.v.ts;
-  for (int h0 = c * p.chunk; h0 < h_end; h0 += GPW * ROW_UNROLL) {
-    uint4 u[ROW_UNROLL];
-#pragma unroll
-    for (int i = 0; i < ROW_UNROLL; ++i) {
-      const int h = h0 + i * GPW + sub;
-      u[i] = make_uint4(0, 0, 0, 0);
-      if (h < h_end) u[i] = ln.load(h < Hk ? ki + h * p.k.hs : vi + (h - Hk) * p.v.hs);
-    }
-#pragma unroll
-    for (int i = 0; i < ROW_UNROLL; ++i) {
-      const int h = h0 + i * GPW + sub;
-      if (h >= h_end) continue;
-      if (p.rope.rot && h < Hk) {
-        Pairs x = ln.unpack(u[i]);
+#pragma unroll 1
+  for (int set = 0; set < 2; ++set) {
+    const HeadsDev& in = set ? p.v : p.k;
+    const int first = set ? p.k.H : 0;
+    const int h_begin = max(c * p.chunk - first, 0), h_end = min((c + 1) * p.chunk - first, in.H);
+    if (h_begin >= h_end) continue;
+    const uint16_t* src = in.ptr + t * in.ts + (long long)(h_begin + sub) * in.hs;
+    uint16_t* dst = (set ? p.vp : p.kp) + base + (long long)(h_begin + sub) * p.head_stride;
+    const long long src_step = GPW * in.hs, dst_step = GPW * p.head_stride;
+    const bool turned = set == 0 && p.rope.rot;
+    auto finish = [&](uint4 u, uint16_t* to) {
+      if (turned) {
+        Pairs x = ln.unpack(u);
         ln.turn(x);
-        u[i] = ln.pack(x);
+        u = ln.pack(x);
       }
-      ln.store((h < Hk ? p.kp + h * p.head_stride : p.vp + (h - Hk) * p.head_stride) + base, u[i]);
+      ln.store(to, u);
+    };
+    int left = h_end - h_begin;  // heads
+#pragma unroll 1
+    for (; left >= GPW * ROW_UNROLL; left -= GPW * ROW_UNROLL) {
+      uint4 u[ROW_UNROLL];
+#pragma unroll
+      for (int i = 0; i < ROW_UNROLL; ++i, src += src_step) u[i] = ln.load(src);
+#pragma unroll
+      for (int i = 0; i < ROW_UNROLL; ++i, dst += dst_step) finish(u[i], dst);
     }
+#pragma unroll 1
+    for (; left > 0; left -= GPW, src += src_step, dst += dst_step)
+      if (sub < left) finish(ln.load(src), dst);
   }
 }
 
