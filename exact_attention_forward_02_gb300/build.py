@@ -56,8 +56,8 @@ def torch_cmd(out: str) -> list[str]:
     include = [os.path.join(ROOT, "include"), CSRC, os.path.join(torch, "include"), cuda,
                sysconfig.get_paths()["include"]]
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", *(x for i in include for x in ("-I", i)), TORCH_SRC,
-            "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
-            "-o", out]
+            "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10",
+            "-lc10_cuda", "-o", out]
 
 
 def _stale(out: str, deps=None) -> bool:

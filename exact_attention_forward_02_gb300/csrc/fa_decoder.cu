@@ -68,13 +68,14 @@ int head_chunk(long long tokens, int heads, int rows_per_step, int sms) {
 // A kernel that waits on the device for the previous kernel of the stream (wait_previous_grid):
 // its blocks may be set up while that one still runs.
 template <typename... P, typename... A>
-int launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t st, A... args) {
+int launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const A&... args) {
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
@@ -181,12 +182,11 @@ int launch_paged(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap
       attr_set[index] = true;
     }
   }
-  kern<<<sms, paged::NUM_THREADS, SMEM, st>>>(mq, mk, mv, p);
-  const int rc = fa_host::launched(cudaPeekAtLastError());
+  const int rc = launch_dependent(kern, dim3(sms), dim3(paged::NUM_THREADS), SMEM, st, mq, mk, mv, p);
   if (rc != FA_OK) return rc;
   // a warp joins 4 rows, or 1
   return launch_dependent(paged::fa_paged_combine_kernel<D, BF16, ROWS>, dim3(sms, ROWS > 128 ? ROWS / 32 : ROWS / 8),
-                          dim3(paged::COMBINE_THREADS), st, p);
+                          dim3(paged::COMBINE_THREADS), 0, st, p);
 }
 
 template <int D, bool BF16>
@@ -226,9 +226,8 @@ int fa_qk_norm_rope(const fa_heads* q, const fa_heads* k, const fa_heads* q_out,
   const unsigned grid = (p.units - 1) / ROW_WARPS + 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return by_type(dtype == FA_BF16, rope && rope->interleaved, [&](auto bf, auto inter) {
-    if (d == 64) fa_norm_rope_kernel<64, bf, inter><<<grid, ROW_THREADS, 0, st>>>(p);
-    else fa_norm_rope_kernel<128, bf, inter><<<grid, ROW_THREADS, 0, st>>>(p);
-    return fa_host::launched(cudaPeekAtLastError());
+    return launch_dependent(d == 64 ? fa_norm_rope_kernel<64, bf, inter> : fa_norm_rope_kernel<128, bf, inter>,
+                            dim3(grid), dim3(ROW_THREADS), 0, st, p);
   });
 }
 
@@ -269,12 +268,11 @@ int fa_qk_norm_rope_bwd(const fa_heads* dq_out, const fa_heads* dk_out, const fa
   float* oq = q->H ? dwq : nullptr;
   float* ok = k->H ? dwk : nullptr;
   return by_type(dtype == FA_BF16, rope && rope->interleaved, [&](auto bf, auto inter) {
-    if (d == 64) fa_norm_rope_bwd_kernel<64, bf, inter><<<grid, ROW_THREADS, 0, st>>>(p);
-    else fa_norm_rope_bwd_kernel<128, bf, inter><<<grid, ROW_THREADS, 0, st>>>(p);
-    const int rc1 = fa_host::launched(cudaPeekAtLastError());
+    const int rc1 = launch_dependent(d == 64 ? fa_norm_rope_bwd_kernel<64, bf, inter> : fa_norm_rope_bwd_kernel<128, bf, inter>,
+                                     dim3(grid), dim3(ROW_THREADS), 0, st, p);
     if (rc1 != FA_OK) return rc1;
     return launch_dependent(d == 64 ? fa_norm_rope_dw_kernel<64> : fa_norm_rope_dw_kernel<128>, dim3(2 * d / 32),
-                            dim3(32, 32), st, (const float*)p.part, grid, oq, ok);
+                            dim3(32, 32), 0, st, (const float*)p.part, grid, oq, ok);
   });
 }
 
@@ -317,9 +315,8 @@ int fa_paged_append(const fa_paged_kv* kv, const fa_heads* k, const fa_heads* v,
   const unsigned grid = (unsigned)(((long long)T * p.n_chunks + ROW_WARPS - 1) / ROW_WARPS);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return by_type(dtype == FA_BF16, rope && rope->interleaved, [&](auto bf, auto inter) {
-    if (kv->d == 64) fa_paged_append_kernel<64, bf, inter><<<grid, ROW_THREADS, 0, st>>>(p);
-    else fa_paged_append_kernel<128, bf, inter><<<grid, ROW_THREADS, 0, st>>>(p);
-    return fa_host::launched(cudaPeekAtLastError());
+    return launch_dependent(kv->d == 64 ? fa_paged_append_kernel<64, bf, inter> : fa_paged_append_kernel<128, bf, inter>,
+                            dim3(grid), dim3(ROW_THREADS), 0, st, p);
   });
 }
 

@@ -391,11 +391,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t sStage = smem_u32(smem + LY::OFF_STAGE);
   volatile int* abort_flag = &bars->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per_thread = (p.B + NUM_THREADS - 1) / NUM_THREADS;
-  const int b0 = min((int)threadIdx.x * per_thread, p.B), b1 = min(b0 + per_thread, p.B);
-  Seq seq = {};
-  const long long my_units = units_of<TPT_MUL, ITEM_UNITS>(p, b0, b1, seq, blockIdx.x == 0);
-
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&bars->q_full), 1);
     mbar_init(smem_u32(&bars->q_empty), 1);
@@ -427,6 +422,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_relinquish();
   }
   launch_dependents();
+  wait_previous_grid();  // no global memory is read or written before this
+  const int per_thread = (p.B + NUM_THREADS - 1) / NUM_THREADS;
+  const int b0 = min((int)threadIdx.x * per_thread, p.B), b1 = min(b0 + per_thread, p.B);
+  Seq seq = {};
+  const long long my_units = units_of<TPT_MUL, ITEM_UNITS>(p, b0, b1, seq, blockIdx.x == 0);
   tc_fence_before();
   const Range range = plan<TPT_MUL, ITEM_UNITS, SPLIT ? ITEM_UNITS + 2 : 1>(p, bars, b0, b1, my_units, seq);
   tc_fence_after();
@@ -1014,6 +1014,7 @@ template <int D, bool BF16, int ROWS>
 __global__ void __launch_bounds__(COMBINE_THREADS) fa_paged_combine_kernel(const __grid_constant__ Params p) {
   constexpr int E = D / 32;  // columns per lane
   constexpr int RW = ROWS > 128 ? 4 : 1, PB = 32 / RW;  // rows of a warp, pieces at a time
+  launch_dependents();
   wait_previous_grid();
   const int4 rec0 = *reinterpret_cast<const int4*>(p.records + blockIdx.x * 8);
   const int2 rec1 = *reinterpret_cast<const int2*>(p.records + blockIdx.x * 8 + 4);

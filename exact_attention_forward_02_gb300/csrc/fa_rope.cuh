@@ -7,6 +7,10 @@
 // once and keep them in registers over that token's heads. A lane holds both elements of each of
 // its 4 pairs (A and B below), so the rotation needs no exchange between lanes, and works on them
 // two at a time (f32x2).
+//
+// Every kernel here is launched so that its blocks may be set up while the previous kernel of the
+// stream still runs (launch_dependent in fa_decoder.cu): it waits for that kernel's results
+// (wait_previous_grid) before it reads or writes global memory.
 #pragma once
 
 #include <cuda.h>
@@ -169,6 +173,8 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) fa_norm_rope_kernel(const __gr
   const uint32_t unit = blockIdx.x * ROW_WARPS + (threadIdx.x >> 5);
   if (unit >= p.units) return;
   const RowUnit at(p, unit);
+  launch_dependents();
+  wait_previous_grid();
   const int pos = p.positions ? p.positions[at.t] : at.n;
   if (p.rope.rot && (pos < 0 || pos >= p.rope.length)) {
     if (lane == 0) atomicCAS(p.status, 0, FA_ERR_RANGE);
@@ -229,6 +235,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 2) fa_norm_rope_bwd_kernel(const 
   Lane<D, BF16, INTER> ln;
   ln.place(lane, p.rope.rot);
   launch_dependents();
+  wait_previous_grid();
   Pairs dw[2] = {};
 #pragma unroll 1
   for (uint32_t unit = blockIdx.x * ROW_WARPS + warp; unit < p.units; unit += gridDim.x * ROW_WARPS) {
@@ -316,6 +323,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 2) fa_norm_rope_bwd_kernel(const 
 template <int D>
 __global__ void __launch_bounds__(1024) fa_norm_rope_dw_kernel(const float* part, int blocks, float* dwq, float* dwk) {
   __shared__ float s[32][33];
+  launch_dependents();
   wait_previous_grid();
   const int col = blockIdx.x * 32 + threadIdx.x;
   float a = 0.f;
@@ -369,6 +377,8 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) fa_paged_append_kernel(const _
   const int t = unit / (uint32_t)p.n_chunks;
   if (t >= p.T) return;
   const int c = (int)(unit - (uint32_t)t * p.n_chunks);
+  launch_dependents();
+  wait_previous_grid();
   const int b = find_sequence(p.cu, p.B, t, lane);
   if (b < 0) return;
   const int pos = p.lens[b] - (p.cu[b + 1] - t);
