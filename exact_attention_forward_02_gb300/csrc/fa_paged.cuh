@@ -108,7 +108,8 @@ struct Layout {
   static constexpr int TILE_BYTES = BM * D * 2;
   static constexpr int CHUNK_BYTES = BM * 128, CHUNKS = D / 64;
   static constexpr int Q_TILES = SPLIT ? 1 : 2;
-  static constexpr int STAGE_BYTES = SPLIT ? 65536 : 0;  // fp32 rows of O~
+  // SPLIT: fp32 rows of O~. PAIR: 4 KB per softmax warp, 32 rows of 128 bytes on their way out.
+  static constexpr int STAGE_BYTES = SPLIT ? 65536 : 32768;
   static constexpr int STAGE_ROWS = STAGE_BYTES / (D * 4);
   static constexpr int STATE_BYTES = SPLIT ? 2 * BM * 8 : 0;  // (m, l) of both warpgroups' rows
   static constexpr int HEAD_BYTES = 1024;                     // barriers and items
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
   static_assert(SPLIT || REP == 1, "copies of rows belong to the SPLIT form");
   using LY = Layout<D, SPLIT>;
-  constexpr int TPT_MUL = SPLIT ? 1 : 2, ITEM_UNITS = SPLIT ? 1 : 0;
+  constexpr int TPT_MUL = SPLIT ? 1 : 2, ITEM_UNITS = SPLIT ? 2 : 0;
   constexpr int ROWS = SPLIT ? BM / REP : 2 * BM;  // rows of an item's partial state
   constexpr int CW = BN / REP;                     // keys of a tile that one row copy covers
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -463,31 +464,42 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const uint32_t box_off = (uint32_t)my_chunk * LY::CHUNK_BYTES + (uint32_t)my_box * box_bytes;
       uint32_t ld0 = 0, q_ph = 0, issued_mask = 0, last_par = 0;
       bool ok = true, q_issued = false;
+      // 32 entries of a sequence's table, one per lane (num_pages, which reads as zeros, for a bad one)
+      auto entries = [&](int b, int len, int window) -> int {
+        const int e = window * 32 + lane;
+        if ((long long)e * p.page_size >= len) return -1;  // holds no key of the sequence
+        const int page = p.table[(size_t)b * p.table_stride + e];
+        if (page >= 0 && page < p.num_pages) return page;
+        atomicCAS(p.status, 0, FA_ERR_RANGE);
+        return p.num_pages;
+      };
+      auto first_window = [&](int j) { return (p.page_size > BN ? j / tiles_per_page : j * boxes) / 32; };
+      // those of the block's first tile are asked for before its item has been handed over
+      int early_b = -1, early_window = 0, early = 0;
+      if (range.u0 < range.u1) {
+        const Start& st = bars->start;
+        early_b = st.b;
+        early_window = first_window(max(st.off - ITEM_UNITS, 0));
+        early = entries(st.b, st.s.len, early_window);
+      }
       while (ok) {
         const Item* src = item_next();
         if (!(ok = src != nullptr)) break;
         const Item it = *src;
         item_done();
         if (it.n == 0) break;
-        // 32 entries of the sequence's table at a time, one per lane; the next 32 are on their way
-        const int* table = p.table + (size_t)it.b * p.table_stride;
-        auto entries = [&](int window) -> int {
-          const int e = window * 32 + lane;
-          if ((long long)e * p.page_size >= it.len) return -1;  // holds no key of the sequence
-          const int page = table[e];
-          if (page >= 0 && page < p.num_pages) return page;
-          atomicCAS(p.status, 0, FA_ERR_RANGE);
-          return p.num_pages;  // reads as zeros
-        };
-        const int first = p.page_size > BN ? it.j0 / tiles_per_page : it.j0 * boxes;
-        int window = first / 32, held = entries(window), next = entries(window + 1);
+        // the next 32 entries are always on their way
+        int window = first_window(it.j0);
+        int held = it.b == early_b && window == early_window ? early : entries(it.b, it.len, window);
+        int next = entries(it.b, it.len, window + 1);
+        early_b = -1;
         for (int i = 0; i < it.n; ++i) {
           const int j = it.j0 + i;
           const int e0 = p.page_size > BN ? j / tiles_per_page : j * boxes;  // the tile's first entry
           if (e0 / 32 != window) {  // 32 is a multiple of a tile's entries
             window = e0 / 32;
             held = next;
-            next = entries(window + 1);
+            next = entries(it.b, it.len, window + 1);
           }
           const int page = __shfl_sync(0xffffffffu, held, (e0 + my_box) % 32);
           const uint32_t ld = ld0 + (SPLIT ? (is_v ? 2 + i + min(i, it.n - 2) : i < 2 ? i : 2 * i - 1) : 2 * i + is_v);
@@ -920,28 +932,64 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tc_fence_after();
       }
       if constexpr (!SPLIT) {
-        uint16_t* orow = p.o.ptr + t * p.o.ts + (long long)head * p.o.hs;
-#pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
-          uint32_t o[32];
-          tmem_ld32(tO + q * 32, o);
-          tmem_wait_ld();
-          reg_fence(o);
-          if (valid && partial) {
+        // A warp's 32 rows leave through its own 4 KB of the stage, 128 bytes of each row at a time
+        // (64 columns of O, 32 of a partial state), so that its stores are whole 128-byte lines: 16-byte
+        // stores of 32 different rows took 5 us for an item's partial state (d = 128). 16-byte piece k
+        // of row r stands at place k ^ (r & 7).
+        const uint32_t mine = sStage + (uint32_t)warp * 4096u;
+        const unsigned long long to = reinterpret_cast<unsigned long long>(
+            partial ? (void*)(part + (size_t)prow * D)
+                    : (void*)(p.o.ptr + t * p.o.ts + (long long)head * p.o.hs));
+        const uint32_t live = __ballot_sync(0xffffffffu, valid);
+        auto send = [&](int byte0) {
+          __syncwarp();
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              reinterpret_cast<uint4*>(part + (size_t)prow * D + q * 32)[k] =
-                  make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          } else if (valid) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float x[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[8 * k + e]) * f;
-              reinterpret_cast<uint4*>(orow + q * 32)[k] = pack8<BF16>(x);
-            }
+          for (int i = 0; i < 8; ++i) {  // 4 rows at a time, 8 lanes each
+            const int rr = 4 * i + (lane >> 3);
+            uint32_t v[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                         : "r"(mine + (uint32_t)rr * 128u + (uint32_t)(((lane & 7) ^ (rr & 7)) << 4))
+                         : "memory");
+            const unsigned long long dst = __shfl_sync(0xffffffffu, to, rr);
+            if (live >> rr & 1)
+              *reinterpret_cast<uint4*>(dst + byte0 + (lane & 7) * 16) = make_uint4(v[0], v[1], v[2], v[3]);
           }
           __syncwarp();
+        };
+        auto put = [&](int k, uint32_t a, uint32_t b, uint32_t c4, uint32_t d4) {
+          st_shared_v4(mine + (uint32_t)lane * 128u + (uint32_t)((k ^ (lane & 7)) << 4), a, b, c4, d4);
+        };
+        if (partial) {
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld32(tO + q * 32, o);
+            tmem_wait_ld();
+            reg_fence(o);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) put(k, o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            send(q * 128);
+          }
+        } else {
+#pragma unroll 1
+          for (int q = 0; q < D / 64; ++q) {
+            uint32_t o[2][32];
+            tmem_ld32(tO + q * 64, o[0]);
+            tmem_ld32(tO + q * 64 + 32, o[1]);
+            tmem_wait_ld();
+            reg_fence(o[0]);
+            reg_fence(o[1]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float x[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[k >> 2][8 * (k & 3) + e]) * f;
+              const uint4 w16 = pack8<BF16>(x);
+              put(k, w16.x, w16.y, w16.z, w16.w);
+            }
+            send(q * 128);
+          }
         }
         tc_fence_before();
       } else {
@@ -956,18 +1004,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int ph = 0; ph < phases; ++ph) {
           if (worked) {
 #pragma unroll 1
-            for (int q = 0; q < cols; q += 32) {
-              uint32_t o[32];
-              tmem_ld32(tO + ph * cols + q, o);
+            for (int q = 0; q < cols; q += 64) {
+              uint32_t o[2][32];
+              tmem_ld32(tO + ph * cols + q, o[0]);
+              tmem_ld32(tO + ph * cols + q + 32, o[1]);
               tmem_wait_ld();
-              reg_fence(o);
+              reg_fence(o[0]);
+              reg_fence(o[1]);
               if (valid) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  st_shared_v4(stage_at(srow, q / 4 + k), __float_as_uint(__uint_as_float(o[4 * k]) * f),
-                               __float_as_uint(__uint_as_float(o[4 * k + 1]) * f),
-                               __float_as_uint(__uint_as_float(o[4 * k + 2]) * f),
-                               __float_as_uint(__uint_as_float(o[4 * k + 3]) * f));
+                for (int k = 0; k < 16; ++k) {
+                  const uint32_t* v = &o[k >> 3][4 * (k & 7)];
+                  st_shared_v4(stage_at(srow, q / 4 + k), __float_as_uint(__uint_as_float(v[0]) * f),
+                               __float_as_uint(__uint_as_float(v[1]) * f), __float_as_uint(__uint_as_float(v[2]) * f),
+                               __float_as_uint(__uint_as_float(v[3]) * f));
+                }
               }
               __syncwarp();
             }
