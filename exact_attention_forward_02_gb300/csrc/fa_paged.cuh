@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
   static_assert(SPLIT || REP == 1, "copies of rows belong to the SPLIT form");
   using LY = Layout<D, SPLIT>;
-  constexpr int TPT_MUL = SPLIT ? 1 : 2, ITEM_UNITS = SPLIT ? 2 : 0;
+  constexpr int TPT_MUL = SPLIT ? 1 : 2, ITEM_UNITS = SPLIT ? (REP == 1 ? 4 : REP == 2 ? 3 : 2) : 2;
   constexpr int ROWS = SPLIT ? BM / REP : 2 * BM;  // rows of an item's partial state
   constexpr int CW = BN / REP;                     // keys of a tile that one row copy covers
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   Seq seq = {};
   const long long my_units = units_of<TPT_MUL, ITEM_UNITS>(p, b0, b1, seq, blockIdx.x == 0);
   tc_fence_before();
-  const Range range = plan<TPT_MUL, ITEM_UNITS, SPLIT ? ITEM_UNITS + 2 : 1>(p, bars, b0, b1, my_units, seq);
+  const Range range = plan<TPT_MUL, ITEM_UNITS, SPLIT ? 2 : 1>(p, bars, b0, b1, my_units, seq);
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   // Items in order: the reader's place in the ring, and the item there (nullptr: the wait gave up).
