@@ -358,6 +358,7 @@ int fa_fwd_paged(const fa_paged_kv* kv, const fa_heads* q, const fa_heads* O, fl
   p.box_keys = kv->page_size < 128 ? kv->page_size : 128;
   p.Hkv = kv->Hkv;
   p.G = G;
+  p.by_g = (65536u + G - 1) / G;
   p.tpt = (form == 0 ? 128 : 128 / form) / G;
   p.cu = cu_seqlens;
   p.lens = seq_lens;

@@ -37,6 +37,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "fa_rope.cuh"
 
 namespace fa {
@@ -60,6 +62,7 @@ struct Params {
   float* L;
   int num_pages, page_size, box_keys;  // box_keys: keys per TMA box, min(page_size, 128)
   int Hkv, G, tpt;                     // tpt: tokens per tile, (128 / REP) / G
+  uint32_t by_g;                       // ceil(2^16 / G): row / G = row * by_g >> 16, exact for row, G <= 128
   const int *cu, *lens, *table;
   int table_stride, B, T, causal;
   float c;  // scale * log2(e)
@@ -69,6 +72,7 @@ struct Params {
   float* parts;  // [block][2][rows]: D floats of O~ per row, then [rows][2] of (m, l)
 };
 
+__device__ __forceinline__ int token_of_row(const Params& p, int row) { return (int)((uint32_t)row * p.by_g >> 16); }
 __host__ __device__ constexpr int part_floats(int d, int rows) { return rows * (d + 2); }
 
 // One block's part of one item.
@@ -754,9 +758,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // ======================================================================= softmax
     const int g = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
     const int copy = r / (BM / REP), row = r % (BM / REP);  // REP = 1: copy 0, row r
+    const int row_tok = token_of_row(p, row), row_head = row - row_tok * p.G;
+    const bool row_used = row < p.tpt * p.G;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t tS = tmem + lane_off + TMEM_S0 + g * 128, tO = tmem + lane_off + TMEM_O0 + g * 128;
-    const float c = p.c;
+    const float c = fmaxf(p.c, 1e-30f);  // a scale of zero: every finite score still counts as zero
     uint32_t s_ph = 0, o_ph = 0, e_ph = 0;
     bool ok = true;
     // both warpgroups (8 warps)
@@ -770,8 +776,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     while (ok) {
       const Item* item = item_next();
       if (!(ok = item != nullptr) || item->n == 0) break;
-      const int tok = row / p.G + (SPLIT ? 0 : g * p.tpt);  // token of this row in the item
-      const bool valid = row < p.tpt * p.G && tok < item->nt;
+      const int tok = row_tok + (SPLIT ? 0 : g * p.tpt);  // token of this row in the item
+      const bool valid = row_used && tok < item->nt;
       if (!SPLIT && g == 1 && item->nt <= p.tpt) {
         item_done();
         continue;
@@ -793,22 +799,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int q = 0; q < CW / 32; ++q) reg_fence(sr[q]);
         auto sv = [&](int k) { return __uint_as_float(sr[k >> 5][k & 31]); };
         const int vis = lim - i * BN - copy * CW;
-        // rows that hold no query do not decide which path the warp takes
-        const bool full = __all_sync(0xffffffffu, !valid || vis >= CW);
+        // Scores of keys that a row does not see become -inf, 32 columns at a time where some row of
+        // the warp needs it (rows that hold no query do not count). c > 0 keeps them at -inf, and
+        // their weights at zero.
+        if (!__all_sync(0xffffffffu, !valid || vis >= CW)) {
+#pragma unroll
+          for (int q = 0; q < CW / 32; ++q) {
+            if (__all_sync(0xffffffffu, !valid || vis >= 32 * (q + 1))) continue;
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (32 * q + k >= vis) sr[q][k] = 0xff800000u;
+          }
+        }
         float mt;
         {
           constexpr int NT = (CW + 2) / 3;
           float t[NT];
-          if (full) {
 #pragma unroll
-            for (int x = 0; x < NT; ++x)
-              t[x] = max3(sv(3 * x), 3 * x + 1 < CW ? sv(3 * x + 1) : -INFINITY, 3 * x + 2 < CW ? sv(3 * x + 2) : -INFINITY);
-          } else {
-            auto mv = [&](int e) { return e < vis ? sv(e) : -INFINITY; };
-#pragma unroll
-            for (int x = 0; x < NT; ++x)
-              t[x] = max3(mv(3 * x), 3 * x + 1 < CW ? mv(3 * x + 1) : -INFINITY, 3 * x + 2 < CW ? mv(3 * x + 2) : -INFINITY);
-          }
+          for (int x = 0; x < NT; ++x)
+            t[x] = max3(sv(3 * x), 3 * x + 1 < CW ? sv(3 * x + 1) : -INFINITY, 3 * x + 2 < CW ? sv(3 * x + 2) : -INFINITY);
           mt = tree_max<NT>(t);
         }
         const float m_tile = (mt == -INFINITY || !valid) ? -INFINITY : mt * c;
@@ -825,25 +834,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint64_t c2 = f2(c, c), nb2 = f2(nb, nb);
         uint64_t acc[4] = {0, 0, 0, 0};
         uint32_t pk[CW / 2];
-        if (full) {
 #pragma unroll
-          for (int k = 0; k < CW / 2; ++k) {
-            float t0, t1;
-            f2_split(f2_fma(f2(sv(2 * k), sv(2 * k + 1)), c2, nb2), t0, t1);
-            const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
-            acc[k & 3] = f2_add(acc[k & 3], f2(p0, p1));
-            pk[k] = pack2<BF16>(p0, p1);
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < CW / 2; ++k) {
-            float t0, t1;
-            f2_split(f2_fma(f2(sv(2 * k), sv(2 * k + 1)), c2, nb2), t0, t1);
-            const float p0 = 2 * k < vis ? ex2_approx(t0) : 0.f;
-            const float p1 = 2 * k + 1 < vis ? ex2_approx(t1) : 0.f;
-            acc[k & 3] = f2_add(acc[k & 3], f2(p0, p1));
-            pk[k] = pack2<BF16>(p0, p1);
-          }
+        for (int k = 0; k < CW / 2; ++k) {
+          float t0, t1;
+          f2_split(f2_fma(f2(sv(2 * k), sv(2 * k + 1)), c2, nb2), t0, t1);
+          const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+          acc[k & 3] = f2_add(acc[k & 3], f2(p0, p1));
+          pk[k] = pack2<BF16>(p0, p1);
         }
         float a0, a1;
         f2_split(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a0, a1);
@@ -920,7 +917,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (!partial) f *= l > 0.f ? 1.f / l : 0.f;
       const int prow = SPLIT ? row : g * BM + row;
       const long long t = item->tok0 + tok;
-      const int head = item->h * p.G + row % p.G;
+      const int head = item->h * p.G + row_head;
       if (valid && (!SPLIT || (g == 0 && copy == 0))) {
         if (partial) *reinterpret_cast<float2*>(part + ROWS * D + 2 * prow) = make_float2(m, l);
         else if (p.L) p.L[t * (p.Hkv * p.G) + head] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
@@ -995,19 +992,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       } else {
         // All states of the item's rows side by side in the stage, row x R + row for state x; if
         // they are too many, half of the columns at a time. 16-byte piece i stands at i ^ (row & 7).
-        const int R = item->nt * p.G;
-        const int phases = 2 * REP * R <= LY::STAGE_ROWS ? 1 : 2;
-        const int cols = D / phases, states_n = item->n > 1 ? 2 * REP : REP  /* the second warpgroup had a tile */;
+        const int R = item->nt * p.G, states_n = item->n > 1 ? 2 * REP : REP;  // (the second warpgroup's)
         const int srow = (g * REP + copy) * R + row;
-        auto stage_at = [&](int rr, int i) { return sStage + (uint32_t)(rr * cols * 4 + ((i ^ (rr & 7)) << 4)); };
-#pragma unroll 1
-        for (int ph = 0; ph < phases; ++ph) {
+        auto join = [&](auto cols_c, int col0) -> bool {
+          constexpr int COLS = decltype(cols_c)::value;
+          auto stage_at = [&](int rr, int i) { return sStage + (uint32_t)(rr * COLS * 4 + ((i ^ (rr & 7)) << 4)); };
           if (worked) {
 #pragma unroll 1
-            for (int q = 0; q < cols; q += 64) {
+            for (int q = 0; q < COLS; q += 64) {
               uint32_t o[2][32];
-              tmem_ld32(tO + ph * cols + q, o[0]);
-              tmem_ld32(tO + ph * cols + q + 32, o[1]);
+              tmem_ld32(tO + col0 + q, o[0]);
+              tmem_ld32(tO + col0 + q + 32, o[1]);
               tmem_wait_ld();
               reg_fence(o[0]);
               reg_fence(o[1]);
@@ -1024,30 +1019,35 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             tc_fence_before();
           }
-          if (!(ok = epi_sync())) break;
+          if (!epi_sync()) return false;
           // sums over the states: thread = 4 columns of a row
 #pragma unroll 1
-          for (int x = threadIdx.x; x < R * (cols / 4); x += 256) {
-            const int rr = x / (cols / 4), c4 = x % (cols / 4);
+          for (int x = threadIdx.x; x < R * (COLS / 4); x += 256) {
+            const int rr = x / (COLS / 4), c4 = x % (COLS / 4);
             float sum[4] = {};
 #pragma unroll
             for (int a = 0; a < 2 * REP; ++a) {
-              if (a >= states_n) break;
-              float y[4];
-              ld_shared_v4(stage_at(a * R + rr, c4), y);
+              float y[4] = {};
+              if (a < states_n) ld_shared_v4(stage_at(a * R + rr, c4), y);
 #pragma unroll
               for (int e = 0; e < 4; ++e) sum[e] += y[e];
             }
-            const int col = ph * cols + 4 * c4;
+            const int col = col0 + 4 * c4;
             if (partial) {
               *reinterpret_cast<float4*>(part + (size_t)rr * D + col) = make_float4(sum[0], sum[1], sum[2], sum[3]);
             } else {
-              uint16_t* dst = p.o.ptr + (long long)(item->tok0 + rr / p.G) * p.o.ts +
-                              (long long)(item->h * p.G + rr % p.G) * p.o.hs + col;
+              const int rt = token_of_row(p, rr);
+              uint16_t* dst = p.o.ptr + (long long)(item->tok0 + rt) * p.o.ts +
+                              (long long)(item->h * p.G + rr - rt * p.G) * p.o.hs + col;
               *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(sum[0], sum[1]), pack2<BF16>(sum[2], sum[3]));
             }
           }
-          if (ph + 1 < phases && !(ok = epi_sync())) break;
+          return true;
+        };
+        if (D == 64 || 2 * REP * R <= LY::STAGE_ROWS) {
+          ok = join(std::integral_constant<int, D>{}, 0);
+        } else if constexpr (D == 128) {
+          ok = join(std::integral_constant<int, 64>{}, 0) && epi_sync() && join(std::integral_constant<int, 64>{}, 64);
         }
         if (!ok) break;
       }
@@ -1077,7 +1077,7 @@ __global__ void __launch_bounds__(COMBINE_THREADS) fa_paged_combine_kernel(const
   };
   const int pr0 = (blockIdx.y * (COMBINE_THREADS / 32) + warp) * RW;
   auto token_of = [&](int pr) {  // -1: the place holds no row
-    const int row = pr % BM, tok = row / p.G + pr / BM * p.tpt;
+    const int row = pr % BM, tok = token_of_row(p, row) + pr / BM * p.tpt;
     return row < p.tpt * p.G && tok < nt ? tok : -1;
   };
   const int my_row = lane / PB, my_piece = lane % PB;
