@@ -74,6 +74,18 @@ def test_attention(fa, new, total, Hq, Hkv, d, page, causal):
     check(fa, b, b.rows(Hq), causal)
 
 
+@pytest.mark.parametrize("B", [31, 32, 33, 255, 256, 257, 700])
+def test_many_sequences_some_without_tokens(fa, B):
+    """The share of each SM is found from the lengths by one warp or by the whole block."""
+    new = [(0, 1, 1, 3, 0)[i % 5] for i in range(B)]
+    total = [n + (i * 53) % 400 for i, n in enumerate(new)]
+    b = lib.Batch(new, total, 2, 64, 16, torch.bfloat16, seed=B, lead=1)
+    check(fa, b, b.rows(4), True)
+    new = [(0, 40, 1)[i % 3] for i in range(B)]
+    b = lib.Batch(new, [n + (i * 37) % 90 for i, n in enumerate(new)], 1, 64, 16, torch.float16, seed=B)
+    check(fa, b, b.rows(8), True)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_types_and_sharp_scores(fa, d, dtype):
