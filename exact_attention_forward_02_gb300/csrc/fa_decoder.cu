@@ -183,7 +183,7 @@ int launch_paged(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap
     }
   }
   const int rc = launch_dependent(kern, dim3(sms), dim3(paged::NUM_THREADS), SMEM, st, mq, mk, mv, p);
-  if (rc != FA_OK) return rc;
+  if (rc != FA_OK || p.whole) return rc;
   // a warp joins 4 rows, or 1
   return launch_dependent(paged::fa_paged_combine_kernel<D, BF16, ROWS>, dim3(sms, ROWS > 128 ? ROWS / 32 : ROWS / 8),
                           dim3(paged::COMBINE_THREADS), 0, st, p);
@@ -347,7 +347,8 @@ int fa_fwd_paged(const fa_paged_kv* kv, const fa_heads* q, const fa_heads* O, fl
   int index = 0, sms = 0;
   if ((rc = fa_host::current_device(&index, &sms)) != FA_OK) return rc;
   const int G = q->H / kv->Hkv, form = paged_form(G, max_q);
-  if (!workspace || workspace_bytes < paged_records_bytes(sms) + paged_parts_bytes(sms, kv->d, form))
+  const bool whole = (long long)table_stride * kv->page_size <= paged::WHOLE_TILES * paged::BN;
+  if (!whole && (!workspace || workspace_bytes < paged_records_bytes(sms) + paged_parts_bytes(sms, kv->d, form)))
     return FA_ERR_WORKSPACE;
   paged::Params p = {};
   if ((rc = fa_host::status_word(&p.status)) != FA_OK) return rc;
@@ -369,8 +370,11 @@ int fa_fwd_paged(const fa_paged_kv* kv, const fa_heads* q, const fa_heads* O, fl
   p.causal = causal != 0;
   p.c = scale * 1.4426950408889634f;
   p.wait_limit_ns = fa_host::wait_limit_ns();
-  p.records = static_cast<int*>(workspace);
-  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + paged_records_bytes(sms));
+  p.whole = whole;
+  if (!whole) {
+    p.records = static_cast<int*>(workspace);
+    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + paged_records_bytes(sms));
+  }
   const bool bf16 = dtype == FA_BF16;
   CUtensorMap mq, mk, mv;
   // Q as [T, Hq, d]: a box is 64 columns of the G heads of a key head for tpt tokens

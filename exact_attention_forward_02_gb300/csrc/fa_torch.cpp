@@ -345,10 +345,11 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Launch on(q, a[12]);
     if (!out.defined()) ho = heads_of(out = rows_like(q), "out", q);
     if (!lse.defined()) lse = fresh(q, {T, hq.H}, at::kFloat);
-    if (!ws.defined()) ws = bytes(q, lib.attend_bytes(hq.H, kv.Hkv, kv.d, max_q));
+    const bool narrow = (int64_t)batch.width * kv.page_size <= FA_PAGED_WHOLE_KEYS;  // needs no workspace
+    if (!ws.defined() && !narrow) ws = bytes(q, lib.attend_bytes(hq.H, kv.Hkv, kv.d, max_q));
     const int rc = lib.attend(&kv, &hq, &ho, static_cast<float*>(lse.data_ptr()), batch.B, T, max_q, batch.cu,
-                              batch.lens, batch.table, batch.width, scale, causal, dt, ws.data_ptr(),
-                              (size_t)ws.numel(), on.stream);
+                              batch.lens, batch.table, batch.width, scale, causal, dt,
+                              ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (size_t)ws.numel() : 0, on.stream);
     return rc == FA_OK ? tuple_of({out, lse}) : PyLong_FromLong(rc);
   });
 }

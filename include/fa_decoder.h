@@ -100,6 +100,9 @@ int fa_paged_append(const fa_paged_kv* kv, const fa_heads* k, const fa_heads* v,
                     const int* cu_seqlens, const int* seq_lens, const int* block_table,
                     int table_stride, const fa_rope* rope, fa_dtype dtype, void* stream);
 
+/* A table of at most this many keys per sequence (table_stride * page_size) needs no workspace. */
+#define FA_PAGED_WHOLE_KEYS 512
+
 /* fa_fwd_paged -- attention of each sequence's new tokens over its cache (which already holds
  * their own keys and values). Query head h reads key head h / (Hq / Hkv); Hq is a multiple of
  * Hkv, at most 128 * Hkv.
@@ -111,15 +114,16 @@ int fa_paged_append(const fa_paged_kv* kv, const fa_heads* k, const fa_heads* v,
  *   max_q     the most new tokens that a sequence of this batch has: it chooses the kernel and
  *             sizes the workspace; a larger batch still gets right results, more slowly. >= 1
  *   workspace fa_fwd_paged_workspace_bytes() bytes on the current device, 256-byte aligned, no
- *             initialisation; calls that share one must not overlap on the GPU
+ *             initialisation; calls that share one must not overlap on the GPU. Not used, and may
+ *             be NULL, when table_stride * page_size <= FA_PAGED_WHOLE_KEYS
  * The key ranges of all sequences are cut into equal shares for the SMs on the device, from the
  * arrays at the time the kernels run, so a captured call may be replayed with other lengths (up
  * to max_q, B, T and the table's width). Results do not change from run to run.
  * Whatever cached rows hold that no query of the batch sees (the rest of a sequence's last page,
- * pages it does not use) does not matter; a key or value that some query of a tile of 128 rows
- * sees must be finite, also for the rows of the tile that do not see it.
+ * pages it does not use) does not matter, NaN included; the keys and values of every position
+ * below seq_lens must be finite.
  * A length past the table's width is cut to it, a page outside [0, num_pages) reads as zeros;
- * either records FA_ERR_RANGE in the status word. Two kernels.
+ * either records FA_ERR_RANGE in the status word. Two kernels (one without a workspace).
  * Errors as fa_fwd: FA_ERR_NULL, FA_ERR_HEAD_DIM, FA_ERR_SHAPE, FA_ERR_SCALE, FA_ERR_ALIGN,
  * FA_ERR_DTYPE, FA_ERR_WORKSPACE, and FA_ERR_RANGE for a page size that is not allowed. */
 size_t fa_fwd_paged_workspace_bytes(int Hq, int Hkv, int d, int max_q);
