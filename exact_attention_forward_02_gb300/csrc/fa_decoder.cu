@@ -337,7 +337,7 @@ int fa_fwd_paged(const fa_paged_kv* kv, const fa_heads* q, const fa_heads* O, fl
   if (B < 0 || T < 0 || table_stride < 0 || max_q < 1 || q->H < 0 || q->H != O->H) return FA_ERR_SHAPE;
   if (!(scale >= 0.f) || !isfinite(scale)) return FA_ERR_SCALE;
   if (B == 0 || T == 0 || q->H == 0) return FA_OK;
-  if (kv->Hkv == 0 || q->H % kv->Hkv || q->H / kv->Hkv > 128 || B == 0x7fffffff ||
+  if (kv->num_pages == 0 || kv->Hkv == 0 || q->H % kv->Hkv || q->H / kv->Hkv > 128 || B == 0x7fffffff ||
       (long long)T * q->H > 0x7fffffffLL)
     return FA_ERR_SHAPE;
   if ((rc = check_heads(q)) != FA_OK || (rc = check_heads(O)) != FA_OK) return rc;

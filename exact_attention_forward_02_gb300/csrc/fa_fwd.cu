@@ -912,7 +912,7 @@ const char* fa_strerror(int code) {
     case FA_ERR_TENSOR_MAP: return "the driver rejected a TMA tensor map";
     case FA_ERR_DEVICE: return "the current device is not an sm_103 GPU";
     case FA_ERR_TIMEOUT: return "a device-side pipeline wait exceeded its time limit";
-    case FA_ERR_WORKSPACE: return "workspace missing or smaller than fa_fwd_workspace_bytes()";
+    case FA_ERR_WORKSPACE: return "workspace missing or smaller than the entry point's workspace_bytes()";
     case FA_ERR_SCRATCH_LIMIT:
       return "the problem needs more scratch than fa_fwd_noalloc's fixed array (FA_NOALLOC_SCRATCH_BYTES)";
     case FA_ERR_DROPOUT:

@@ -944,6 +944,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             partial ? (void*)(part + (size_t)prow * D)
                     : (void*)(p.o.ptr + t * p.o.ts + (long long)head * p.o.hs));
         const uint32_t live = __ballot_sync(0xffffffffu, valid);
+        unsigned long long dsts[8];  // of the 8 rows that this lane sends pieces of
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dsts[i] = __shfl_sync(0xffffffffu, to, 4 * i + (lane >> 3)) + (lane & 7) * 16;
         auto send = [&](int byte0) {
           __syncwarp();
 #pragma unroll
@@ -954,9 +957,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                          : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                          : "r"(mine + (uint32_t)rr * 128u + (uint32_t)(((lane & 7) ^ (rr & 7)) << 4))
                          : "memory");
-            const unsigned long long dst = __shfl_sync(0xffffffffu, to, rr);
             if (live >> rr & 1)
-              *reinterpret_cast<uint4*>(dst + byte0 + (lane & 7) * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+              *reinterpret_cast<uint4*>(dsts[i] + byte0) = make_uint4(v[0], v[1], v[2], v[3]);
           }
           __syncwarp();
         };

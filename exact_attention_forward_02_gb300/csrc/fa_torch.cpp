@@ -200,6 +200,8 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
     PyErr_SetString(r.type, r.text.c_str());
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    PyErr_SetString(PyExc_RuntimeError, "an unknown C++ exception");
   }
   return nullptr;
 }

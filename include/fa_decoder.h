@@ -109,7 +109,8 @@ int fa_paged_append(const fa_paged_kv* kv, const fa_heads* k, const fa_heads* v,
  *     s_j = scale <q, k_j>,  j in [0, seq_lens[b]), and with `causal` j <= the token's position
  *     O = sum_j softmax_j(s) v_j,   L = ln sum_j exp(s_j)
  * A row that sees no key (an empty sequence, or a negative position) gets O = 0 and L = -inf.
- *   q, O      [T, Hq] rows of d elements (batch_stride unused); kv->d 64 or 128
+ *   q, O      [T, Hq] rows of d elements (batch_stride unused); kv->d 64 or 128. O may be q's own
+ *             memory with the same strides
  *   L         fp32 [T, Hq], or NULL
  *   max_q     the most new tokens that a sequence of this batch has: it chooses the kernel and
  *             sizes the workspace; a larger batch still gets right results, more slowly. >= 1
@@ -124,8 +125,12 @@ int fa_paged_append(const fa_paged_kv* kv, const fa_heads* k, const fa_heads* v,
  * below seq_lens must be finite.
  * A length past the table's width is cut to it, a page outside [0, num_pages) reads as zeros;
  * either records FA_ERR_RANGE in the status word. Two kernels (one without a workspace).
+ * A sequence whose rows do not lie in [0, T] is passed over and FA_ERR_RANGE recorded; a negative
+ * length counts as zero.
  * Errors as fa_fwd: FA_ERR_NULL, FA_ERR_HEAD_DIM, FA_ERR_SHAPE, FA_ERR_SCALE, FA_ERR_ALIGN,
- * FA_ERR_DTYPE, FA_ERR_WORKSPACE, and FA_ERR_RANGE for a page size that is not allowed. */
+ * FA_ERR_DTYPE, FA_ERR_WORKSPACE, FA_ERR_TENSOR_MAP for strides that TMA cannot walk (zero or
+ * negative along an axis of more than one element, 2^40 bytes and more), and FA_ERR_RANGE for a
+ * page size that is not allowed. */
 size_t fa_fwd_paged_workspace_bytes(int Hq, int Hkv, int d, int max_q);
 int fa_fwd_paged(const fa_paged_kv* kv, const fa_heads* q, const fa_heads* O, float* L, int B, int T,
                  int max_q, const int* cu_seqlens, const int* seq_lens, const int* block_table,

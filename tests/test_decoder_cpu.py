@@ -143,6 +143,7 @@ def attend(kv=None, q=None, O=None, L=P, B=2, T=8, max_q=4, cu=P, lens=P, table=
     (dict(q=heads(H=1024), O=heads(H=1024)), "FA_ERR_SHAPE"),  # 256 query heads a key head
     (dict(kv=cache(Hkv=0)), "FA_ERR_SHAPE"),
     (dict(max_q=0), "FA_ERR_SHAPE"),
+    (dict(kv=cache(pages=0)), "FA_ERR_SHAPE"),
     (dict(scale=-1.0), "FA_ERR_SCALE"),
     (dict(scale=math.nan), "FA_ERR_SCALE"),
     (dict(L=P + 2), "FA_ERR_ALIGN"),

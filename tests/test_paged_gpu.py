@@ -121,6 +121,37 @@ def test_strided_queries_and_outputs(fa):
     check(fa, b, fused[:, :6], True, out=out)
 
 
+def test_output_over_the_queries(fa):
+    b = lib.Batch([3, 1, 200, 1], [3, 900, 700, 4000], 2, 128, 16, torch.float16)
+    for rows in (b.rows(8), b.rows(12)[:, 4:]):
+        want = attend(fa, b, rows, True)
+        got = attend(fa, b, rows, True, out=rows)
+        assert got[0] is rows or got[0].data_ptr() == rows.data_ptr()
+        assert torch.equal(rows, want[0]) and torch.equal(got[1], want[1])
+
+
+def test_rows_outside_the_packed_tokens_are_passed_over(fa):
+    """cu_seqlens that decrease, or run past T: those sequences are skipped and reported."""
+    b = lib.Batch([2, 3, 2], [40, 300, 9], 2, 64, 16, torch.float16)
+    q = b.rows(4)
+    want = attend(fa, b, q, True)
+    out = torch.full_like(q, 7.0)
+    b.cu_seqlens[3] = 9                    # the last sequence would end behind T = 7
+    attend(fa, b, q, True, out=out)
+    assert fa.fa_last_status() == fa.FA_ERR_RANGE
+    fa.fa_clear_status()
+    assert torch.equal(out[:5], want[0][:5]) and (out[5:] == 7).all()
+    b.cu_seqlens[3], b.cu_seqlens[1] = 7, -4
+    out.fill_(7.0)
+    attend(fa, b, q, True, out=out)
+    assert fa.fa_last_status() == fa.FA_ERR_RANGE
+    fa.fa_clear_status()
+    assert torch.equal(out[5:], want[0][5:]) and (out[:5] == 7).all()
+    b.cu_seqlens[1], b.seq_lens[0] = 2, -5  # no keys at all
+    got = attend(fa, b, q, True)
+    assert not got[0][:2].any() and torch.isinf(got[1][:2]).all() and torch.equal(got[0][2:], want[0][2:])
+
+
 def test_results_do_not_change_from_run_to_run(fa):
     b = lib.Batch([1] * 5 + [70], [3000, 20, 400, 1, 700, 2000], 4, 128, 16, torch.bfloat16)
     q = b.rows(16)
