@@ -2,11 +2,12 @@
 // (forward and backward) and the append to a paged cache. Included by fa_decoder.cu.
 //
 // All of them read and write each row of d 16-bit elements once and are bound by HBM. A row is
-// held by d/8 lanes, 8 elements each, so that a warp has 2 (d = 128) or 4 (d = 64) rows in flight
-// per load; a warp works on ONE token, so that its lanes load their angles of the rotation table
-// once and keep them in registers over that token's heads. A lane holds both elements of each of
-// its 4 pairs (A and B below), so the rotation needs no exchange between lanes, and works on them
-// two at a time (f32x2).
+// held by d/8 lanes, 8 elements each: 2 (d = 128) or 4 (d = 64) groups of lanes to a warp. A group
+// works on ONE token and walks its heads, so that its lanes load their angles of the rotation
+// table, and work out their addresses, once for all of them. (A warp per token, its groups side by
+// side on the token's heads, paid for that 2 or 4 times as often: 10.2 us for 16384 tokens of 2 + 1
+// heads, d = 64.) A lane holds both elements of each of its 4 pairs (A and B below), so the rotation
+// needs no exchange between lanes, and works on them two at a time (f32x2).
 //
 // Every kernel here is launched so that its blocks may be set up while the previous kernel of the
 // stream still runs (launch_dependent in fa_decoder.cu): it waits for that kernel's results
@@ -34,6 +35,7 @@ struct RopeDev {
 constexpr int ROW_THREADS = 256;
 constexpr int ROW_WARPS = ROW_THREADS / 32;
 constexpr int ROW_UNROLL = 4;          // rows of one lane group loaded before the first is used
+constexpr int ROW_MIN_WARPS = 16;      // warps per SM below which heads are shared out further
 constexpr int ROW_BWD_MAX_BLOCKS = 1024;
 
 // 8 consecutive 16-bit elements from fp32
@@ -70,10 +72,10 @@ struct Lane {
     return INTER ? 8 * l + 2 * i + second : (second ? eb : ea) + i;
   }
   // sign = 1 for the rotation, -1 for its transpose
-  __device__ __forceinline__ void angles(const RopeDev& rp, int pos, float sign) {
+  __device__ __forceinline__ void angles(const RopeDev& rp, int pos, float sign, bool known) {
     c[0] = c[1] = f2(1.f, 1.f);
     s[0] = s[1] = 0;
-    if (8 * l >= rp.rot) return;
+    if (8 * l >= rp.rot || !known) return;
     const float* row = rp.table + (size_t)pos * rp.rot + 4 * l;
     const float4 x = *reinterpret_cast<const float4*>(row), y = *reinterpret_cast<const float4*>(row + rp.rot / 2);
     c[0] = f2(x.x, x.y), c[1] = f2(x.z, x.w);
@@ -135,9 +137,9 @@ struct NormRopeParams {
   float eps;
   RopeDev rope;
   const int* positions;
-  int N;
-  uint32_t units;       // tokens * n_chunks
-  int chunk, n_chunks;  // heads of q then k, `chunk` of them per warp
+  int N, tokens;        // tokens = B * N
+  uint32_t units;       // of a warp: ceil(tokens / groups of lanes) * n_chunks
+  int chunk, n_chunks;  // heads of q then k, `chunk` of them per unit
   float* part;          // backward: [block][2][D] sums of the weights' gradients
   int* status;
 };
@@ -146,20 +148,31 @@ __device__ __forceinline__ float sum4(const uint64_t (&v)[2]) {
   return (lo_of(v[0]) + hi_of(v[0])) + (lo_of(v[1]) + hi_of(v[1]));
 }
 
-// A warp's unit: one token's heads [c chunk, (c+1) chunk) of q's, then k's. 32-bit divisions: the
-// host checks that the units fit.
+// A warp's unit: heads [c, c + chunk) of q's, then k's, of one token for each group of lanes.
+// 32-bit divisions: the host checks that the units fit.
+template <int GPW>
 struct RowUnit {
-  int t, b, n, c;
-  __device__ __forceinline__ RowUnit(const NormRopeParams& p, uint32_t unit) {
-    t = p.n_chunks == 1 ? unit : unit / (uint32_t)p.n_chunks;
-    c = (int)(unit - (uint32_t)t * p.n_chunks) * p.chunk;
+  int t, b, n, c, pos;
+  bool alive;  // the group has a token, and its position a row of the table
+  __device__ __forceinline__ RowUnit(const NormRopeParams& p, uint32_t unit, int sub) {
+    const uint32_t tg = p.n_chunks == 1 ? unit : unit / (uint32_t)p.n_chunks;
+    c = (int)(unit - tg * p.n_chunks) * p.chunk;
+    t = (int)(tg * GPW) + sub;
+    alive = t < p.tokens;
+    if (!alive) t = p.tokens - 1;
     b = (uint32_t)t / (uint32_t)p.N;
     n = t - b * p.N;
+  }
+  __device__ __forceinline__ void locate(const NormRopeParams& p, int l) {
+    pos = p.positions ? p.positions[t] : n;
+    if (alive && p.rope.rot && (pos < 0 || pos >= p.rope.length)) {
+      if (l == 0) atomicCAS(p.status, 0, FA_ERR_RANGE);
+      alive = false;
+    }
   }
   // the unit's heads of a set whose first head is `first`
   __device__ __forceinline__ int begin(int first) const { return max(c - first, 0); }
   __device__ __forceinline__ int end(const NormRopeParams& p, int first, int H) const { return min(c + p.chunk - first, H); }
-  // first row of this lane group
   __device__ __forceinline__ uint16_t* row(const HeadsDev& x, int h) const {
     return x.ptr + b * x.bs + n * x.ts + h * x.hs;
   }
@@ -172,27 +185,23 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) fa_norm_rope_kernel(const __gr
   const int lane = threadIdx.x & 31, sub = lane / LPR;
   const uint32_t unit = blockIdx.x * ROW_WARPS + (threadIdx.x >> 5);
   if (unit >= p.units) return;
-  const RowUnit at(p, unit);
-  launch_dependents();
-  wait_previous_grid();
-  const int pos = p.positions ? p.positions[at.t] : at.n;
-  if (p.rope.rot && (pos < 0 || pos >= p.rope.length)) {
-    if (lane == 0) atomicCAS(p.status, 0, FA_ERR_RANGE);
-    return;
-  }
+  RowUnit<GPW> at(p, unit, sub);
   Lane<D, BF16, INTER> ln;
   ln.place(lane, p.rope.rot);
-  ln.angles(p.rope, pos, 1.f);
+  launch_dependents();
+  wait_previous_grid();
+  at.locate(p, ln.l);
+  if (!__any_sync(0xffffffffu, at.alive)) return;
+  ln.angles(p.rope, at.pos, 1.f, at.alive);
 #pragma unroll 1
   for (int set = 0; set < 2; ++set) {
     const HeadsDev &in = p.x[set], &out = p.y[set];
     const int first = set ? p.x[0].H : 0, h_begin = at.begin(first), h_end = at.end(p, first, in.H);
     if (h_begin >= h_end) continue;
     const Pairs w = ln.unpack(ln.load(p.w[set]));
-    const uint16_t* src = at.row(in, h_begin + sub);
-    uint16_t* dst = at.row(out, h_begin + sub);
-    const long long src_step = GPW * in.hs, dst_step = GPW * out.hs;
-    auto finish = [&](const uint4& u, uint16_t* to, bool live) {
+    const uint16_t* src = at.row(in, h_begin);
+    uint16_t* dst = at.row(out, h_begin);
+    auto finish = [&](const uint4& u, uint16_t* to) {
       Pairs x = ln.unpack(u);
       uint64_t sq[2];
 #pragma unroll
@@ -205,22 +214,19 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) fa_norm_rope_kernel(const __gr
         x.b[e] = f2_mul(x.b[e], f2_mul(w.b[e], r2));
       }
       ln.turn(x);
-      if (live) ln.store(to, ln.pack(x));
+      if (at.alive) ln.store(to, ln.pack(x));
     };
     int left = h_end - h_begin;  // heads
 #pragma unroll 1
-    for (; left >= GPW * ROW_UNROLL; left -= GPW * ROW_UNROLL) {
+    for (; left >= ROW_UNROLL; left -= ROW_UNROLL) {
       uint4 u[ROW_UNROLL];
 #pragma unroll
-      for (int i = 0; i < ROW_UNROLL; ++i, src += src_step) u[i] = ln.load(src);
+      for (int i = 0; i < ROW_UNROLL; ++i, src += in.hs) u[i] = ln.load(src);
 #pragma unroll
-      for (int i = 0; i < ROW_UNROLL; ++i, dst += dst_step) finish(u[i], dst, true);
+      for (int i = 0; i < ROW_UNROLL; ++i, dst += out.hs) finish(u[i], dst);
     }
 #pragma unroll 1
-    for (; left > 0; left -= GPW, src += src_step, dst += dst_step) {
-      const bool live = sub < left;
-      finish(live ? ln.load(src) : make_uint4(0, 0, 0, 0), dst, live);
-    }
+    for (; left > 0; --left, src += in.hs, dst += out.hs) finish(ln.load(src), dst);
   }
 }
 
@@ -239,24 +245,21 @@ __global__ void __launch_bounds__(ROW_THREADS, 2) fa_norm_rope_bwd_kernel(const 
   Pairs dw[2] = {};
 #pragma unroll 1
   for (uint32_t unit = blockIdx.x * ROW_WARPS + warp; unit < p.units; unit += gridDim.x * ROW_WARPS) {
-    const RowUnit at(p, unit);
-    const int pos = p.positions ? p.positions[at.t] : at.n;
-    if (p.rope.rot && (pos < 0 || pos >= p.rope.length)) {
-      if (lane == 0) atomicCAS(p.status, 0, FA_ERR_RANGE);
-      continue;
-    }
-    ln.angles(p.rope, pos, -1.f);
+    RowUnit<GPW> at(p, unit, sub);
+    at.locate(p, ln.l);
+    if (!__any_sync(0xffffffffu, at.alive)) continue;
+    ln.angles(p.rope, at.pos, -1.f, at.alive);
 #pragma unroll
     for (int set = 0; set < 2; ++set) {
       const HeadsDev &in = p.x[set], &gr = p.g[set], &out = p.y[set];
       const int first = set ? p.x[0].H : 0, h_begin = at.begin(first), h_end = at.end(p, first, in.H);
       if (h_begin >= h_end) continue;
       const Pairs w = ln.unpack(ln.load(p.w[set]));
-      const uint16_t* src = at.row(in, h_begin + sub);
-      const uint16_t* gsrc = at.row(gr, h_begin + sub);
-      uint16_t* dst = at.row(out, h_begin + sub);
-      const long long src_step = GPW * in.hs, g_step = GPW * gr.hs, dst_step = GPW * out.hs;
-      auto finish = [&](const uint4& ux, const uint4& ug, uint16_t* to, bool live) {  // zeros where not live
+      const uint16_t* src = at.row(in, h_begin);
+      const uint16_t* gsrc = at.row(gr, h_begin);
+      uint16_t* dst = at.row(out, h_begin);
+      auto load_g = [&]() { return at.alive ? ln.load(gsrc) : make_uint4(0, 0, 0, 0); };  // adds nothing to dw
+      auto finish = [&](const uint4& ux, const uint4& ug, uint16_t* to) {
         Pairs x = ln.unpack(ux), g = ln.unpack(ug), u;
         ln.turn(g);
         uint64_t sq[2], gx[2];
@@ -278,26 +281,22 @@ __global__ void __launch_bounds__(ROW_THREADS, 2) fa_norm_rope_bwd_kernel(const 
           x.a[e] = f2_mul(f2_fma(xa, m2, u.a[e]), r2);
           x.b[e] = f2_mul(f2_fma(xb, m2, u.b[e]), r2);
         }
-        if (live) ln.store(to, ln.pack(x));
+        if (at.alive) ln.store(to, ln.pack(x));
       };
       int left = h_end - h_begin;  // heads
 #pragma unroll 1
-      for (; left >= GPW * ROW_UNROLL; left -= GPW * ROW_UNROLL) {
+      for (; left >= ROW_UNROLL; left -= ROW_UNROLL) {
         uint4 ux[ROW_UNROLL], ug[ROW_UNROLL];
 #pragma unroll
-        for (int i = 0; i < ROW_UNROLL; ++i, src += src_step, gsrc += g_step) {
+        for (int i = 0; i < ROW_UNROLL; ++i, src += in.hs, gsrc += gr.hs) {
           ux[i] = ln.load(src);
-          ug[i] = ln.load(gsrc);
+          ug[i] = load_g();
         }
 #pragma unroll
-        for (int i = 0; i < ROW_UNROLL; ++i, dst += dst_step) finish(ux[i], ug[i], dst, true);
+        for (int i = 0; i < ROW_UNROLL; ++i, dst += out.hs) finish(ux[i], ug[i], dst);
       }
 #pragma unroll 1
-      for (; left > 0; left -= GPW, src += src_step, gsrc += g_step, dst += dst_step) {
-        const bool live = sub < left;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        finish(live ? ln.load(src) : zero, live ? ln.load(gsrc) : zero, dst, live);
-      }
+      for (; left > 0; --left, src += in.hs, gsrc += gr.hs, dst += out.hs) finish(ln.load(src), load_g(), dst);
     }
   }
 #pragma unroll
@@ -347,7 +346,8 @@ struct AppendParams {
   const int *cu, *lens, *table;
   int table_stride, B, T;
   RopeDev rope;
-  int chunk, n_chunks;  // heads of k then v, `chunk` of them per warp
+  uint32_t units;       // of a warp: ceil(T / groups of lanes) * n_chunks
+  int chunk, n_chunks;  // heads of k then v, `chunk` of them per unit
   int* status;
 };
 
@@ -367,41 +367,47 @@ __device__ __forceinline__ int find_sequence(const int* cu, int B, int t, int la
   return lo >= 1 && lo <= B ? lo - 1 : -1;
 }
 
-// One warp per (token, chunk of heads): the token's sequence, position, page and slot, then its
-// rows of k (rotated) and v (copied).
+// One warp per unit: each group's token's sequence, position, page and slot, then its rows of k
+// (rotated) and v (copied).
 template <int D, bool BF16, bool INTER>
 __global__ void __launch_bounds__(ROW_THREADS, 4) fa_paged_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LPR = D / 8, GPW = 32 / LPR;
   const int lane = threadIdx.x & 31, sub = lane / LPR;
   const uint32_t unit = blockIdx.x * ROW_WARPS + (threadIdx.x >> 5);
-  const int t = unit / (uint32_t)p.n_chunks;
-  if (t >= p.T) return;
-  const int c = (int)(unit - (uint32_t)t * p.n_chunks);
-  launch_dependents();
-  wait_previous_grid();
-  const int b = find_sequence(p.cu, p.B, t, lane);
-  if (b < 0) return;
-  const int pos = p.lens[b] - (p.cu[b + 1] - t);
-  int page = -1;
-  const bool in = pos >= 0 && pos / p.page_size < p.table_stride && (!p.rope.rot || pos < p.rope.length);
-  if (in) page = p.table[(size_t)b * p.table_stride + pos / p.page_size];
-  if (page < 0 || page >= p.num_pages) {
-    if (lane == 0) atomicCAS(p.status, 0, FA_ERR_RANGE);
-    return;
-  }
-  const long long base = page * p.page_stride + (long long)(pos % p.page_size) * p.token_stride;
+  if (unit >= p.units) return;
+  const uint32_t tg = unit / (uint32_t)p.n_chunks;
+  const int c = (int)(unit - tg * p.n_chunks), t0 = (int)(tg * GPW), t = t0 + sub;
   Lane<D, BF16, INTER> ln;
   ln.place(lane, p.rope.rot);
-  ln.angles(p.rope, pos, 1.f);
+  launch_dependents();
+  wait_previous_grid();
+  int b = -1;
+#pragma unroll
+  for (int i = 0; i < GPW; ++i) {
+    const int bi = find_sequence(p.cu, p.B, min(t0 + i, p.T - 1), lane);
+    if (i == sub && t < p.T) b = bi;
+  }
+  int pos = 0, page = -1;
+  if (b >= 0) {
+    pos = p.lens[b] - (p.cu[b + 1] - t);
+    const bool in = pos >= 0 && pos / p.page_size < p.table_stride && (!p.rope.rot || pos < p.rope.length);
+    if (in) page = p.table[(size_t)b * p.table_stride + pos / p.page_size];
+    if (page < 0 || page >= p.num_pages) {
+      if (ln.l == 0) atomicCAS(p.status, 0, FA_ERR_RANGE);
+      b = -1;
+    }
+  }
+  if (b < 0) return;  // nothing below is shared between lanes
+  const long long base = page * p.page_stride + (long long)(pos % p.page_size) * p.token_stride;
+  ln.angles(p.rope, pos, 1.f, true);
 #pragma unroll 1
   for (int set = 0; set < 2; ++set) {
     const HeadsDev& in = set ? p.v : p.k;
     const int first = set ? p.k.H : 0;
     const int h_begin = max(c * p.chunk - first, 0), h_end = min((c + 1) * p.chunk - first, in.H);
     if (h_begin >= h_end) continue;
-    const uint16_t* src = in.ptr + t * in.ts + (long long)(h_begin + sub) * in.hs;
-    uint16_t* dst = (set ? p.vp : p.kp) + base + (long long)(h_begin + sub) * p.head_stride;
-    const long long src_step = GPW * in.hs, dst_step = GPW * p.head_stride;
+    const uint16_t* src = in.ptr + t * in.ts + h_begin * in.hs;
+    uint16_t* dst = (set ? p.vp : p.kp) + base + h_begin * p.head_stride;
     const bool turned = set == 0 && p.rope.rot;
     auto finish = [&](uint4 u, uint16_t* to) {
       if (turned) {
@@ -413,16 +419,15 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) fa_paged_append_kernel(const _
     };
     int left = h_end - h_begin;  // heads
 #pragma unroll 1
-    for (; left >= GPW * ROW_UNROLL; left -= GPW * ROW_UNROLL) {
+    for (; left >= ROW_UNROLL; left -= ROW_UNROLL) {
       uint4 u[ROW_UNROLL];
 #pragma unroll
-      for (int i = 0; i < ROW_UNROLL; ++i, src += src_step) u[i] = ln.load(src);
+      for (int i = 0; i < ROW_UNROLL; ++i, src += in.hs) u[i] = ln.load(src);
 #pragma unroll
-      for (int i = 0; i < ROW_UNROLL; ++i, dst += dst_step) finish(u[i], dst);
+      for (int i = 0; i < ROW_UNROLL; ++i, dst += p.head_stride) finish(u[i], dst);
     }
 #pragma unroll 1
-    for (; left > 0; left -= GPW, src += src_step, dst += dst_step)
-      if (sub < left) finish(ln.load(src), dst);
+    for (; left > 0; --left, src += in.hs, dst += p.head_stride) finish(ln.load(src), dst);
   }
 }
 
