@@ -11,6 +11,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/as_strided.h>
 #include <ATen/ops/zeros.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -181,7 +182,24 @@ at::Tensor fresh(const at::Tensor& t, at::IntArrayRef size, at::ScalarType type)
   return at::detail::empty_cuda(size, t.options().dtype(type));
 }
 at::Tensor rows_like(const at::Tensor& t) { return fresh(t, t.sizes(), t.scalar_type()); }
-at::Tensor bytes(const at::Tensor& t, size_t n) { return fresh(t, {(int64_t)(n ? n : 1)}, at::kByte); }
+
+// Device memory for the length of a call, from torch's allocator (so from the graph's own pool
+// while one is captured): given back when the call returns, for later work on the same stream.
+struct Scratch {
+  void* ptr = nullptr;
+  size_t size = 0;
+  void take(size_t n, void* stream) {
+    if (!n) return;
+    ptr = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(n, static_cast<cudaStream_t>(stream));
+    size = n;
+  }
+  Scratch() = default;
+  Scratch(const Scratch&) = delete;
+  Scratch& operator=(const Scratch&) = delete;
+  ~Scratch() {
+    if (ptr) c10::cuda::CUDACachingAllocator::raw_delete(ptr);
+  }
+};
 
 PyObject* tuple_of(std::initializer_list<at::Tensor> ts) {
   PyObject* out = PyTuple_New((Py_ssize_t)ts.size());
@@ -267,11 +285,11 @@ PyObject* norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!dk.defined()) ok = heads_of(dk = rows_like(k), "dk", q);
     // a set without heads leaves its weights' gradient unwritten: zero
     const at::Tensor dw = hq.H && hk.H ? fresh(q, {2, d}, at::kFloat) : at::zeros({2, d}, q.options().dtype(at::kFloat));
-    const size_t nws = lib.norm_rope_bwd_bytes(d);
-    const at::Tensor ws = bytes(q, nws);
+    Scratch ws;
+    ws.take(lib.norm_rope_bwd_bytes(d), on.stream);
     float* w = static_cast<float*>(dw.data_ptr());
     const int rc = lib.norm_rope_bwd(&hgq, &hgk, &hq, &hk, &oq, &ok, w, w + d, B, N, d, wq.data_ptr(), wk.data_ptr(),
-                                     eps, &rp, positions, dt, ws.data_ptr(), nws, on.stream);
+                                     eps, &rp, positions, dt, ws.ptr, ws.size, on.stream);
     if (rc != FA_OK) return PyLong_FromLong(rc);
     c10::impl::ExcludeDispatchKeyGuard plain(c10::autograd_dispatch_keyset_with_ADInplaceOrView);
     return tuple_of({dq, dk, at::as_strided(dw, {d}, {1}, 0), at::as_strided(dw, {d}, {1}, d)});
@@ -324,8 +342,8 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor &q = tensor(a[0], "q"), &kp = tensor(a[1], "k_pages"), &vp = tensor(a[2], "v_pages"),
                      &table = tensor(a[3], "block_table"), &cu = tensor(a[4], "cu_seqlens"),
                      &lens = tensor(a[5], "seq_lens");
-    at::Tensor out = optional_tensor(a[9], "out"), lse = optional_tensor(a[10], "lse"),
-               ws = optional_tensor(a[11], "workspace");
+    at::Tensor out = optional_tensor(a[9], "out"), lse = optional_tensor(a[10], "lse");
+    const at::Tensor ws = optional_tensor(a[11], "workspace");
     const fa_dtype dt = type_code(q, "q");
     if (q.dim() != 3) bad_value("q must be [T, Hq, d]");
     const int T = as_int(q.size(0), "T");
@@ -348,10 +366,12 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!out.defined()) ho = heads_of(out = rows_like(q), "out", q);
     if (!lse.defined()) lse = fresh(q, {T, hq.H}, at::kFloat);
     const bool narrow = (int64_t)batch.width * kv.page_size <= FA_PAGED_WHOLE_KEYS;  // needs no workspace
-    if (!ws.defined() && !narrow) ws = bytes(q, lib.attend_bytes(hq.H, kv.Hkv, kv.d, max_q));
+    Scratch own;
+    if (!ws.defined() && !narrow) own.take(lib.attend_bytes(hq.H, kv.Hkv, kv.d, max_q), on.stream);
     const int rc = lib.attend(&kv, &hq, &ho, static_cast<float*>(lse.data_ptr()), batch.B, T, max_q, batch.cu,
                               batch.lens, batch.table, batch.width, scale, causal, dt,
-                              ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (size_t)ws.numel() : 0, on.stream);
+                              ws.defined() ? ws.data_ptr() : own.ptr, ws.defined() ? (size_t)ws.numel() : own.size,
+                              on.stream);
     return rc == FA_OK ? tuple_of({out, lse}) : PyLong_FromLong(rc);
   });
 }
