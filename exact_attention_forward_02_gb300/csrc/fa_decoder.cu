@@ -385,6 +385,8 @@ int fa_fwd_paged(const fa_paged_kv* kv, const fa_heads* q, const fa_heads* O, fl
   p.table_stride = table_stride;
   p.B = B;
   p.T = T;
+  const long long cap = (long long)table_stride * kv->page_size;
+  p.cap = cap < 0x7fffff00LL ? (int)cap : 0x7fffff00;
   p.causal = causal != 0;
   p.c = scale * 1.4426950408889634f;
   p.wait_limit_ns = fa_host::wait_limit_ns();

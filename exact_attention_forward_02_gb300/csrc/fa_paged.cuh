@@ -19,7 +19,7 @@
 // WHOLE_TILES tiles, items stay whole and the second kernel falls away: joining takes 2.5 us on the
 // GPU and as much on the host, an item of 4 tiles by one block 1 us more than by two.
 //
-// Two forms of the kernel, of 12 warps (8: loads of Q and K, 11: loads of V, 9: MMA issuer, 10:
+// Two forms of the kernel, of 12 warps (8, 11: loads, 9: MMA issuer, 10:
 // walks the block's range and hands the others their items through a ring in shared memory, a few
 // ahead, so that nobody waits for the lengths of the next sequence; 0-7: two softmax warpgroups,
 // thread = row = TMEM lane):
@@ -48,7 +48,7 @@ namespace paged {
 
 constexpr int BM = 128, BN = 128;
 constexpr int NUM_WARPS = 12, NUM_THREADS = NUM_WARPS * 32;
-constexpr int WARP_LOAD = 8, WARP_MMA = 9, WARP_WALK = 10, WARP_LOAD_V = 11;
+constexpr int WARP_LOAD = 8, WARP_MMA = 9, WARP_WALK = 10, WARP_LOAD2 = 11;
 constexpr int ITEM_SLOTS = 4;
 constexpr int ITEM_READERS = 11;  // warps that read an item: two loading, MMA, 8 softmax
 // 2*128*200 + 128*104 = 64512 = 384*168 registers, the launch's budget
@@ -68,6 +68,7 @@ struct Params {
   uint32_t by_g;                       // ceil(2^16 / G): row / G = row * by_g >> 16, exact for row, G <= 128
   const int *cu, *lens, *table;
   int table_stride, B, T, causal;
+  int cap;    // keys that a row of the table covers
   int whole;  // no item is split: a block takes the items that begin in its range
   float c;  // scale * log2(e)
   unsigned long long wait_limit_ns;
@@ -168,14 +169,12 @@ __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, const 
 __device__ __forceinline__ Seq load_seq(const Params& p, int b, int tpi, bool report) {
   Seq s;
   s.t0 = p.cu[b];
-  const long long n = (long long)p.cu[b + 1] - s.t0;
-  const long long cap = (long long)p.table_stride * p.page_size;
-  const int len = p.lens[b];
-  const bool rows_ok = s.t0 >= 0 && n >= 0 && s.t0 + n <= p.T;
-  s.n = rows_ok ? (int)n : 0;
-  s.len = len < 0 ? 0 : (int)(len > cap ? cap : len);
+  const int end = p.cu[b + 1], len = p.lens[b];
+  const bool rows_ok = s.t0 >= 0 && end >= s.t0 && end <= p.T;
+  s.n = rows_ok ? end - s.t0 : 0;
+  s.len = max(0, min(len, p.cap));
   s.nq = s.n <= tpi ? (s.n > 0) : (s.n - 1) / tpi + 1;
-  if (report && (!rows_ok || (s.n && len > cap))) atomicCAS(p.status, 0, FA_ERR_RANGE);
+  if (report && (!rows_ok || (s.n && len > p.cap))) atomicCAS(p.status, 0, FA_ERR_RANGE);
   return s;
 }
 
@@ -185,11 +184,11 @@ __device__ __forceinline__ long long divide(long long a, int b) {
 }
 
 // key tiles of a block of tokens that sees `vis` keys (at least one, so that its rows are written)
-__device__ __forceinline__ int tiles_for(long long vis) { return vis <= 0 ? 1 : (int)((vis + BN - 1) / BN); }
+__device__ __forceinline__ int tiles_for(int vis) { return vis <= 0 ? 1 : (int)((uint32_t)(vis + BN - 1) / BN); }
 // of block q
 __device__ __forceinline__ int tiles_of(const Params& p, const Seq& s, int q, int tpi) {
-  const long long end = (long long)(q + 1) * tpi;
-  return tiles_for(p.causal ? (long long)s.len - s.n + (end < s.n ? end : s.n) : s.len);
+  const uint32_t end = min((uint32_t)(q + 1) * (uint32_t)tpi, (uint32_t)s.n);
+  return tiles_for(p.causal ? s.len - s.n + (int)end : s.len);
 }
 
 // Key tiles of the first q blocks. With a causal mask block i sees x_i = ctx + (i + 1) tpi keys
@@ -280,7 +279,7 @@ struct Walk {
       it.slot = first ? 0 : 1;
       it.n0 = it.n;
       if (TPT_MUL == 2 && p.causal) {
-        const int t = tiles_for((long long)it.vis0 + min(p.tpt, it.nt) - 1) - j0;
+        const int t = tiles_for(it.vis0 + min(p.tpt, it.nt) - 1) - j0;
         it.n0 = t < 1 ? 1 : min(t, it.n);
       }
       first = false;
@@ -459,21 +458,43 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     regs_dec<REGS_OTHER>();
     // Loads are numbered over the block's pieces in the order of their use; load i goes to slot
     // i mod KV_SLOTS. PAIR: K0 V0 K1 V1 ...; unit u = {V of tile u-1, K of tile u} is released at
-    // once. SPLIT: K0 K1 V0 K2 V1 K3 ...; every load is released by itself.
-    if (warp == WARP_LOAD || warp == WARP_LOAD_V) {
+    // once. SPLIT: K0 K1 V0 K2 V1 K3 ...; every load is released by itself. Loads are released in
+    // order, and two loads in a row of one warp are at most 3 apart: when a warp waits for the release
+    // of load i - KV_SLOTS, those up to i - 3 - KV_SLOTS are past, so that the slot's barrier stands
+    // in the phase waited for or behind it, never two phases before (where the parity would lie).
+    if (warp == WARP_LOAD || warp == WARP_LOAD2) {
       // ======================================================================= producers
       // All 32 lanes: a tile's boxes (pages, and 64-column halves) are issued side by side. A box
-      // costs its warp about 100 cycles whatever its size, so K and V have a warp each.
-      const bool is_v = warp == WARP_LOAD_V;
-      const CUtensorMap* tm = is_v ? &tmV : &tmK;
+      // costs its warp about 100 cycles whatever its size, 1600 for a tile's keys in pages of 16
+      // (d = 128), so two warps share the work. SPLIT: the block's key tiles in turn, so that an item's
+      // first two tiles are asked for at once (8 x 32768 keys of 8 heads, d 64, pages of 16: 93 us
+      // against 100 with a warp for K and one for V; pages of 8, d 128: 186 against 203). PAIR: K and
+      // V, which are used apart (32 prompts of 500 tokens, pages of 16: 64 us against 69 in turn).
+      const uint32_t me = warp == WARP_LOAD2;
       const int boxes = BN / p.box_keys;                    // page boxes of one 64-column chunk
       const int tiles_per_page = p.page_size > BN ? p.page_size / BN : 1;
       const int my_box = lane % boxes, my_chunk = lane / boxes;
       const bool issues = my_chunk < LY::CHUNKS;
       const uint32_t box_bytes = (uint32_t)p.box_keys * 128u;
       const uint32_t box_off = (uint32_t)my_chunk * LY::CHUNK_BYTES + (uint32_t)my_box * box_bytes;
-      uint32_t ld0 = 0, q_ph = 0, issued_mask = 0, last_par = 0;
-      bool ok = true, q_issued = false;
+      uint32_t ld0 = 0, n_q = 0, issued_mask = 0, last_par = 0;  // n_q: Q loads of the items so far
+      bool ok = true;
+      // An item's Q, by the first of the two warps for every item: it has then waited for every
+      // release of the buffer, and a parity cannot stand for one two phases back.
+      auto load_q = [&](const Item& it) -> bool {
+        if (!__all_sync(0xffffffffu, wait_bar(smem_u32(&bars->q_empty), (n_q & 1u) ^ 1u, abort_flag, p))) return false;
+        const uint32_t qf = smem_u32(&bars->q_full);
+        const int tiles = SPLIT ? 1 : (it.nt > p.tpt ? 2 : 1);
+        if (lane == 0) mbar_arrive_expect_tx(qf, (uint32_t)(tiles * REP * LY::CHUNKS * p.tpt * p.G) * 128u);
+        __syncwarp();
+        if (lane < tiles * REP * LY::CHUNKS) {
+          const int c = lane % LY::CHUNKS, a = lane / LY::CHUNKS;  // a: copy (SPLIT) or tile (PAIR)
+          const uint32_t off = SPLIT ? (uint32_t)a * (BM / REP) * 128u : (uint32_t)a * LY::TILE_BYTES;
+          tma_load_3d(sQ + off + c * LY::CHUNK_BYTES, &tmQ, qf, c * 64, it.h * p.G, it.tok0 + (SPLIT ? 0 : a * p.tpt));
+        }
+        ++n_q;
+        return true;
+      };
       // 32 entries of a sequence's table, one per lane (num_pages, which reads as zeros, for a bad one)
       auto entries = [&](int b, int len, int window) -> int {
         const int e = window * 32 + lane;
@@ -503,49 +524,40 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         int held = it.b == early_b && window == early_window ? early : entries(it.b, it.len, window);
         int next = entries(it.b, it.len, window + 1);
         early_b = -1;
-        for (int i = 0; i < it.n; ++i) {
+        const int first_i = SPLIT ? (int)(((ld0 >> 1) ^ me) & 1u) : 0;
+        if (me == 0 && first_i != 0 && !(ok = load_q(it))) break;
+        for (int i = first_i; i < it.n && ok; i += SPLIT ? 2 : 1) {
           const int j = it.j0 + i;
           const int e0 = p.page_size > BN ? j / tiles_per_page : j * boxes;  // the tile's first entry
           if (e0 / 32 != window) {  // 32 is a multiple of a tile's entries
+            held = e0 / 32 == window + 1 ? next : entries(it.b, it.len, e0 / 32);
             window = e0 / 32;
-            held = next;
             next = entries(it.b, it.len, window + 1);
           }
           const int page = __shfl_sync(0xffffffffu, held, (e0 + my_box) % 32);
-          const uint32_t ld = ld0 + (SPLIT ? (is_v ? 2 + i + min(i, it.n - 2) : i < 2 ? i : 2 * i - 1) : 2 * i + is_v);
-          const uint32_t slot = ld % LY::KV_SLOTS, par = (ld / LY::KV_SLOTS) & 1u;
-          if (ld >= (uint32_t)LY::KV_SLOTS) {
-            const uint32_t u = SPLIT ? ld - LY::KV_SLOTS : (ld - LY::KV_SLOTS + 1) >> 1;
-            ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->kv_release[u % LY::KV_SLOTS]),
-                                                  (u / LY::KV_SLOTS) & 1u, abort_flag, p));
-            if (!ok) break;
-          }
-          const uint32_t full = smem_u32(&bars->kv_full[slot]);
           const int keys = it.len - j * BN;  // boxes that hold a key of the sequence
           const int live = keys <= 0 ? 0 : min(boxes, (keys + p.box_keys - 1) / p.box_keys);
-          if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)live * LY::CHUNKS * box_bytes);
-          __syncwarp();
-          if (issues && my_box < live)
-            tma_load_4d(sKV + slot * LY::TILE_BYTES + box_off, tm, full, my_chunk * 64,
-                        p.page_size > BN ? j % tiles_per_page * BN : 0, it.h, page);
-          issued_mask |= 1u << slot;
-          last_par = (last_par & ~(1u << slot)) | (par << slot);
-          if (!is_v && i == 0) {  // Q behind the first K
-            ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->q_empty), q_ph ^ 1, abort_flag, p));
-            if (!ok) break;
-            q_ph ^= 1;
-            const uint32_t qf = smem_u32(&bars->q_full);
-            const int tiles = SPLIT ? 1 : (it.nt > p.tpt ? 2 : 1);
-            if (lane == 0)
-              mbar_arrive_expect_tx(qf, (uint32_t)(tiles * REP * LY::CHUNKS * p.tpt * p.G) * 128u);
-            __syncwarp();
-            if (lane < tiles * REP * LY::CHUNKS) {
-              const int c = lane % LY::CHUNKS, a = lane / LY::CHUNKS;  // a: copy (SPLIT) or tile (PAIR)
-              const uint32_t off = SPLIT ? (uint32_t)a * (BM / REP) * 128u : (uint32_t)a * LY::TILE_BYTES;
-              tma_load_3d(sQ + off + c * LY::CHUNK_BYTES, &tmQ, qf, c * 64, it.h * p.G,
-                          it.tok0 + (SPLIT ? 0 : a * p.tpt));
+#pragma unroll(SPLIT ? 2 : 1)
+          for (int is_v = SPLIT ? 0 : (int)me; is_v < (SPLIT ? 2 : (int)me + 1); ++is_v) {
+            const uint32_t ld =
+                ld0 + (SPLIT ? (is_v ? 2 + i + min(i, it.n - 2) : i < 2 ? i : 2 * i - 1) : 2 * i + is_v);
+            const uint32_t slot = ld % LY::KV_SLOTS, par = (ld / LY::KV_SLOTS) & 1u;
+            if (ld >= (uint32_t)LY::KV_SLOTS) {
+              const uint32_t u = SPLIT ? ld - LY::KV_SLOTS : (ld - LY::KV_SLOTS + 1) >> 1;
+              ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->kv_release[u % LY::KV_SLOTS]),
+                                                    (u / LY::KV_SLOTS) & 1u, abort_flag, p));
+              if (!ok) break;
             }
-            q_issued = true;
+            const uint32_t full = smem_u32(&bars->kv_full[slot]);
+            if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)live * LY::CHUNKS * box_bytes);
+            __syncwarp();
+            if (issues && my_box < live)
+              tma_load_4d(sKV + slot * LY::TILE_BYTES + box_off, is_v ? &tmV : &tmK, full, my_chunk * 64,
+                          p.page_size > BN ? j % tiles_per_page * BN : 0, it.h, page);
+            issued_mask |= 1u << slot;
+            last_par = (last_par & ~(1u << slot)) | (par << slot);
+            // Q behind the first K
+            if (me == 0 && is_v == 0 && i == 0 && !(ok = load_q(it))) break;
           }
         }
         ld0 += 2 * it.n;
@@ -554,7 +566,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // every issued copy must land before the block may exit
         for (int s = 0; s < LY::KV_SLOTS; ++s)
           if (issued_mask & (1u << s)) wait_drain(smem_u32(&bars->kv_full[s]), (last_par >> s) & 1u, p);
-        if (q_issued) wait_drain(smem_u32(&bars->q_full), q_ph ^ 1, p);
+        if (n_q) wait_drain(smem_u32(&bars->q_full), (n_q - 1) & 1u, p);
       }
       __syncwarp();
     } else if (warp == WARP_MMA) {
