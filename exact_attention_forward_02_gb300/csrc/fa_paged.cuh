@@ -75,7 +75,20 @@ struct Params {
   int* status;
   int* records;  // [block][8]: the item that begins in a block's range and ends in another's
   float* parts;  // [block][2][rows]: D floats of O~ per row, then [rows][2] of (m, l)
+  long long parts_len;  // floats there (checked by debug builds)
 };
+
+// Debug builds (FA_DEBUG) check the places of tile copies, partial states and output rows; one
+// outside records FA_ERR_BOUNDS and what it guards is skipped. Release builds compile it out.
+__device__ __forceinline__ bool in_bounds(const Params& p, bool ok) {
+#ifdef FA_DEBUG
+  if (!ok) atomicCAS(p.status, 0, FA_ERR_BOUNDS);
+  return ok;
+#else
+  (void)p, (void)ok;
+  return true;
+#endif
+}
 
 __device__ __forceinline__ int token_of_row(const Params& p, int row) { return (int)((uint32_t)row * p.by_g >> 16); }
 __host__ __device__ constexpr int part_floats(int d, int rows) { return rows * (d + 2); }
@@ -487,6 +500,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int tiles = SPLIT ? 1 : (it.nt > p.tpt ? 2 : 1);
         if (lane == 0) mbar_arrive_expect_tx(qf, (uint32_t)(tiles * REP * LY::CHUNKS * p.tpt * p.G) * 128u);
         __syncwarp();
+        in_bounds(p, it.tok0 >= 0 && it.tok0 + it.nt <= p.T && (it.h + 1) * p.G <= p.o.H);
         if (lane < tiles * REP * LY::CHUNKS) {
           const int c = lane % LY::CHUNKS, a = lane / LY::CHUNKS;  // a: copy (SPLIT) or tile (PAIR)
           const uint32_t off = SPLIT ? (uint32_t)a * (BM / REP) * 128u : (uint32_t)a * LY::TILE_BYTES;
@@ -551,6 +565,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const uint32_t full = smem_u32(&bars->kv_full[slot]);
             if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)live * LY::CHUNKS * box_bytes);
             __syncwarp();
+            in_bounds(p, !issues || my_box >= live || (it.h < p.Hkv && page >= 0 && page <= p.num_pages));
             if (issues && my_box < live)
               tma_load_4d(sKV + slot * LY::TILE_BYTES + box_off, is_v ? &tmV : &tmK, full, my_chunk * 64,
                           p.page_size > BN ? j % tiles_per_page * BN : 0, it.h, page);
@@ -795,7 +810,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const Item* item = item_next();
       if (!(ok = item != nullptr) || item->n == 0) break;
       const int tok = row_tok + (SPLIT ? 0 : g * p.tpt);  // token of this row in the item
-      const bool valid = row_used && tok < item->nt;
+      const bool valid =
+          row_used && tok < item->nt &&
+          in_bounds(p, item->tok0 + tok < p.T && item->h * p.G + row_head < p.o.H &&
+                           (p.whole || (blockIdx.x * 2 + item->slot + 1ll) * part_floats(D, ROWS) <= p.parts_len));
       if (!SPLIT && g == 1 && item->nt <= p.tpt) {
         item_done();
         continue;
