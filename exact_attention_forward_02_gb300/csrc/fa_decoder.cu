@@ -184,7 +184,7 @@ std::mutex g_attr_mu;
 
 template <int D, bool BF16, bool SPLIT, int REP>
 int launch_paged(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const paged::Params& p,
-                 int index, int sms, cudaStream_t st) {
+                 int index, int blocks, cudaStream_t st) {
   constexpr int SMEM = paged::Layout<D, SPLIT>::SMEM_BYTES, ROWS = SPLIT ? 128 / REP : 256;
   auto kern = paged::fa_paged_kernel<D, BF16, SPLIT, REP>;
   static bool attr_set[fa_host::MAX_DEVICES] = {};
@@ -196,21 +196,21 @@ int launch_paged(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap
       attr_set[index] = true;
     }
   }
-  const int rc = launch_dependent(kern, dim3(sms), dim3(paged::NUM_THREADS), SMEM, st, mq, mk, mv, p);
+  const int rc = launch_dependent(kern, dim3(blocks), dim3(paged::NUM_THREADS), SMEM, st, mq, mk, mv, p);
   if (rc != FA_OK || p.whole) return rc;
   // a warp joins 4 rows, or 1
-  return launch_dependent(paged::fa_paged_combine_kernel<D, BF16, ROWS>, dim3(sms, ROWS > 128 ? ROWS / 32 : ROWS / 8),
+  return launch_dependent(paged::fa_paged_combine_kernel<D, BF16, ROWS>, dim3(blocks, ROWS > 128 ? ROWS / 32 : ROWS / 8),
                           dim3(paged::COMBINE_THREADS), 0, st, p);
 }
 
 template <int D, bool BF16>
 int paged_forms(int form, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                const paged::Params& p, int index, int sms, cudaStream_t st) {
+                const paged::Params& p, int index, int blocks, cudaStream_t st) {
   switch (form) {
-    case 4: return launch_paged<D, BF16, true, 4>(mq, mk, mv, p, index, sms, st);
-    case 2: return launch_paged<D, BF16, true, 2>(mq, mk, mv, p, index, sms, st);
-    case 1: return launch_paged<D, BF16, true, 1>(mq, mk, mv, p, index, sms, st);
-    default: return launch_paged<D, BF16, false, 1>(mq, mk, mv, p, index, sms, st);
+    case 4: return launch_paged<D, BF16, true, 4>(mq, mk, mv, p, index, blocks, st);
+    case 2: return launch_paged<D, BF16, true, 2>(mq, mk, mv, p, index, blocks, st);
+    case 1: return launch_paged<D, BF16, true, 1>(mq, mk, mv, p, index, blocks, st);
+    default: return launch_paged<D, BF16, false, 1>(mq, mk, mv, p, index, blocks, st);
   }
 }
 
@@ -391,6 +391,13 @@ int fa_fwd_paged(const fa_paged_kv* kv, const fa_heads* q, const fa_heads* O, fl
   p.c = scale * 1.4426950408889634f;
   p.wait_limit_ns = fa_host::wait_limit_ns();
   p.whole = whole;
+  // without units: one sequence whose key heads divide (nearly) all SMs, or whole items that fit them
+  const long long items = (long long)B * kv->Hkv;
+  if (form != 0 && items <= sms) {
+    if (whole) p.direct = 1;
+    else if (B == 1 && sms / kv->Hkv * kv->Hkv * 10 >= sms * 9) p.direct = sms / kv->Hkv;
+  }
+  const int blocks = p.direct ? (int)items * p.direct : sms;
   if (!whole) {
     p.records = static_cast<int*>(workspace);
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + paged_records_bytes(sms));
@@ -408,8 +415,8 @@ int fa_fwd_paged(const fa_paged_kv* kv, const fa_heads* q, const fa_heads* O, fl
                         {kv->token_stride, kv->head_stride, kv->page_stride}, {(uint32_t)p.box_keys, 1, 1})) != FA_OK)
       return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (kv->d == 64) return bf16 ? paged_forms<64, true>(form, mq, mk, mv, p, index, sms, st) : paged_forms<64, false>(form, mq, mk, mv, p, index, sms, st);
-  return bf16 ? paged_forms<128, true>(form, mq, mk, mv, p, index, sms, st) : paged_forms<128, false>(form, mq, mk, mv, p, index, sms, st);
+  if (kv->d == 64) return bf16 ? paged_forms<64, true>(form, mq, mk, mv, p, index, blocks, st) : paged_forms<64, false>(form, mq, mk, mv, p, index, blocks, st);
+  return bf16 ? paged_forms<128, true>(form, mq, mk, mv, p, index, blocks, st) : paged_forms<128, false>(form, mq, mk, mv, p, index, blocks, st);
 }
 
 }  // extern "C"

@@ -18,6 +18,9 @@
 // kernel waits on another block. Where the table is so narrow that no item has more than
 // WHOLE_TILES tiles, items stay whole and the second kernel falls away: joining takes 2.5 us on the
 // GPU and as much on the host, an item of 4 tiles by one block 1 us more than by two.
+// Small batches of single tokens go without units at all ("direct"): one sequence, whose key heads
+// share the SMs evenly, or whole items that fit the SMs at once. Block c then is part c % direct of
+// item c / direct and reads the lengths of its own sequence only: 1 us less before the first load.
 //
 // Two forms of the kernel, of 12 warps (8, 11: loads, 9: MMA issuer, 10:
 // walks the block's range and hands the others their items through a ring in shared memory, a few
@@ -59,6 +62,7 @@ constexpr int SMEM_LIMIT = 232448;
 constexpr int MAX_SLOTS = 8;
 constexpr int COMBINE_THREADS = 256;
 constexpr int WHOLE_TILES = FA_PAGED_WHOLE_KEYS / BN;
+constexpr int DIRECT_TILES = 2;  // key tiles of a part at least, one for each warpgroup
 
 struct Params {
   HeadsDev o;
@@ -70,6 +74,7 @@ struct Params {
   int table_stride, B, T, causal;
   int cap;    // keys that a row of the table covers
   int whole;  // no item is split: a block takes the items that begin in its range
+  int direct; // SPLIT: that many blocks to a (sequence, key head), without units (0: by units)
   float c;  // scale * log2(e)
   unsigned long long wait_limit_ns;
   int* status;
@@ -239,6 +244,30 @@ __device__ __forceinline__ int owner_of(long long u, const Range& r) {
   return c;
 }
 
+// The item of block of tokens q of a sequence, key tiles [j0, j1).
+template <int TPT_MUL>
+__device__ __forceinline__ Item make_item(const Params& p, const Seq& s, int b, int h, int q, int ntot, int j0, int j1,
+                                          int slot) {
+  const int tpi = p.tpt * TPT_MUL;
+  Item it;
+  it.b = b;
+  it.h = h;
+  it.tok0 = s.t0 + q * tpi;
+  it.nt = min(tpi, s.n - q * tpi);
+  it.len = s.len;
+  it.vis0 = s.len - s.n + q * tpi + 1;
+  it.ntot = ntot;
+  it.j0 = j0;
+  it.n = j1 - j0;
+  it.slot = slot;
+  it.n0 = it.n;
+  if (TPT_MUL == 2 && p.causal) {
+    const int t = tiles_for(it.vis0 + min(p.tpt, it.nt) - 1) - j0;
+    it.n0 = t < 1 ? 1 : min(t, it.n);
+  }
+  return it;
+}
+
 // Walks a block's range.
 template <int TPT_MUL, int ITEM_UNITS>
 struct Walk {
@@ -280,21 +309,7 @@ struct Walk {
       const int qq = q++;
       if (j1 == j0) continue;            // none of the item's tiles: they are the next block's
       if (p.whole && ustart < r.u0) continue;  // the block before has taken it
-      it.b = b;
-      it.h = h;
-      it.tok0 = s.t0 + qq * tpi;
-      it.nt = min(tpi, s.n - qq * tpi);
-      it.len = s.len;
-      it.vis0 = s.len - s.n + qq * tpi + 1;
-      it.ntot = ntot;
-      it.j0 = j0;
-      it.n = j1 - j0;
-      it.slot = first ? 0 : 1;
-      it.n0 = it.n;
-      if (TPT_MUL == 2 && p.causal) {
-        const int t = tiles_for(it.vis0 + min(p.tpt, it.nt) - 1) - j0;
-        it.n0 = t < 1 ? 1 : min(t, it.n);
-      }
+      it = make_item<TPT_MUL>(p, s, b, h, qq, ntot, j0, j1, first ? 0 : 1);
       first = false;
       return true;
     }
@@ -446,12 +461,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
   launch_dependents();
   wait_previous_grid();  // no global memory is read or written before this
-  const int per_thread = (p.B + NUM_THREADS - 1) / NUM_THREADS;
-  const int b0 = min((int)threadIdx.x * per_thread, p.B), b1 = min(b0 + per_thread, p.B);
-  Seq seq = {};
-  const long long my_units = units_of<TPT_MUL, ITEM_UNITS>(p, b0, b1, seq, blockIdx.x == 0);
+  Range range = {};
   tc_fence_before();
-  const Range range = plan<TPT_MUL, ITEM_UNITS, SPLIT ? 2 : 1>(p, bars, b0, b1, my_units, seq);
+  if (SPLIT && p.direct) {
+    __syncthreads();
+  } else {
+    const int per_thread = (p.B + NUM_THREADS - 1) / NUM_THREADS;
+    const int b0 = min((int)threadIdx.x * per_thread, p.B), b1 = min(b0 + per_thread, p.B);
+    Seq seq = {};
+    const long long my_units = units_of<TPT_MUL, ITEM_UNITS>(p, b0, b1, seq, blockIdx.x == 0);
+    range = plan<TPT_MUL, ITEM_UNITS, SPLIT ? 2 : 1>(p, bars, b0, b1, my_units, seq);
+  }
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   // Items in order: the reader's place in the ring, and the item there (nullptr: the wait gave up).
@@ -509,24 +529,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ++n_q;
         return true;
       };
-      // 32 entries of a sequence's table, one per lane (num_pages, which reads as zeros, for a bad one)
-      auto entries = [&](int b, int len, int window) -> int {
+      // 32 entries of a sequence's table, one per lane; -1 where one holds no key of the sequence,
+      // num_pages (which reads as zeros) for a bad one
+      auto ask = [&](int b, int window) -> int {
         const int e = window * 32 + lane;
-        if ((long long)e * p.page_size >= len) return -1;  // holds no key of the sequence
-        const int page = p.table[(size_t)b * p.table_stride + e];
+        return e < p.table_stride ? p.table[(size_t)b * p.table_stride + e] : -1;
+      };
+      auto check = [&](int page, int len, int window) -> int {
+        if ((long long)(window * 32 + lane) * p.page_size >= len) return -1;
         if (page >= 0 && page < p.num_pages) return page;
         atomicCAS(p.status, 0, FA_ERR_RANGE);
         return p.num_pages;
       };
-      auto first_window = [&](int j) { return (p.page_size > BN ? j / tiles_per_page : j * boxes) / 32; };
+      auto window_of = [&](int j) { return (p.page_size > BN ? j / tiles_per_page : j * boxes) / 32; };
       // those of the block's first tile are asked for before its item has been handed over
       int early_b = -1, early_window = 0, early = 0;
-      if (range.u0 < range.u1) {
-        const Start& st = bars->start;
-        early_b = st.b;
-        early_window = first_window(max(st.off - ITEM_UNITS, 0));
-        early = entries(st.b, st.s.len, early_window);
+      if (SPLIT && p.direct) {
+        if (p.whole) early_b = (int)blockIdx.x / p.direct / p.Hkv;
+      } else if (range.u0 < range.u1) {
+        early_b = bars->start.b;
+        early_window = window_of(max(bars->start.off - ITEM_UNITS, 0));
       }
+      if (early_b >= 0) early = ask(early_b, early_window);
       while (ok) {
         const Item* src = item_next();
         if (!(ok = src != nullptr)) break;
@@ -534,9 +558,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         item_done();
         if (it.n == 0) break;
         // the next 32 entries are always on their way
-        int window = first_window(it.j0);
-        int held = it.b == early_b && window == early_window ? early : entries(it.b, it.len, window);
-        int next = entries(it.b, it.len, window + 1);
+        auto entries = [&](int w) { return check(ask(it.b, w), it.len, w); };
+        int window = window_of(it.j0);
+        int held = it.b == early_b && window == early_window ? check(early, it.len, window) : entries(window);
+        int next = entries(window + 1);
         early_b = -1;
         const int first_i = SPLIT ? (int)(((ld0 >> 1) ^ me) & 1u) : 0;
         if (me == 0 && first_i != 0 && !(ok = load_q(it))) break;
@@ -544,9 +569,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const int j = it.j0 + i;
           const int e0 = p.page_size > BN ? j / tiles_per_page : j * boxes;  // the tile's first entry
           if (e0 / 32 != window) {  // 32 is a multiple of a tile's entries
-            held = e0 / 32 == window + 1 ? next : entries(it.b, it.len, e0 / 32);
+            held = e0 / 32 == window + 1 ? next : entries(e0 / 32);
             window = e0 / 32;
-            next = entries(it.b, it.len, window + 1);
+            next = entries(window + 1);
           }
           const int page = __shfl_sync(0xffffffffu, held, (e0 + my_box) % 32);
           const int keys = it.len - j * BN;  // boxes that hold a key of the sequence
@@ -756,27 +781,50 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (lane == 0) {
         int* rec = p.records + blockIdx.x * 8;
         if (!p.whole) rec[0] = 0;  // no item begins here and ends elsewhere, as yet
-        Walk<TPT_MUL, ITEM_UNITS> walk;
-        walk.begin(range, bars->start);
-        for (uint32_t i = 0;; ++i) {
+        uint32_t i = 0;
+        auto publish = [&](const Item& it) -> bool {
           const uint32_t s = i % ITEM_SLOTS;
-          if (i >= ITEM_SLOTS && !wait_bar(smem_u32(&bars->item_empty[s]), (i / ITEM_SLOTS - 1) & 1u, abort_flag, p)) break;
-          Item it;
-          long long ustart;
-          const bool more = walk.next(p, range, it, ustart);
-          if (!more) it.n = 0;
+          if (i >= ITEM_SLOTS && !wait_bar(smem_u32(&bars->item_empty[s]), (i / ITEM_SLOTS - 1) & 1u, abort_flag, p))
+            return false;
           bars->items[s] = it;
           mbar_arrive(smem_u32(&bars->item_full[s]));
-          if (!more) break;
-          if (it.j0 == 0 && it.n != it.ntot) {
-            rec[1] = it.slot;
-            rec[2] = owner_of(ustart + ITEM_UNITS + it.ntot - 1, range);
-            rec[3] = it.h;
-            rec[4] = it.tok0;
-            rec[5] = it.nt;
-            rec[0] = 1;
+          ++i;
+          return true;
+        };
+        auto record = [&](const Item& it, int last) {  // its last block
+          rec[1] = it.slot;
+          rec[2] = last;
+          rec[3] = it.h;
+          rec[4] = it.tok0;
+          rec[5] = it.nt;
+          rec[0] = 1;
+        };
+        bool go = true;
+        if (SPLIT && p.direct) {
+          const int item = (int)blockIdx.x / p.direct, part = (int)blockIdx.x - item * p.direct;
+          const int b = item / p.Hkv, h = item - b * p.Hkv, tpi = p.tpt * TPT_MUL;
+          const Seq s = load_seq(p, b, tpi, part == 0 && h == 0);
+          for (int q = 0; q < s.nq && go; ++q) {  // (more than one block of tokens only if max_q was too small)
+            const int ntot = tiles_of(p, s, q, tpi);
+            const int np = p.whole || q > 0 ? 1 : min(p.direct, (ntot + DIRECT_TILES - 1) / DIRECT_TILES);
+            if (part >= np) continue;
+            const uint32_t n = (uint32_t)ntot, j0 = part * n / np, j1 = (part + 1) * n / np;
+            const Item it = make_item<TPT_MUL>(p, s, b, h, q, ntot, (int)j0, (int)j1, 0);
+            go = publish(it);
+            if (go && part == 0 && np > 1) record(it, (int)blockIdx.x + np - 1);
+          }
+        } else {
+          Walk<TPT_MUL, ITEM_UNITS> walk;
+          walk.begin(range, bars->start);
+          Item it;
+          long long ustart;
+          while (go && walk.next(p, range, it, ustart)) {
+            go = publish(it);
+            if (go && it.j0 == 0 && it.n != it.ntot) record(it, owner_of(ustart + ITEM_UNITS + it.ntot - 1, range));
           }
         }
+        Item end = {};
+        if (go) publish(end);
       }
       __syncwarp();
     }

@@ -38,7 +38,7 @@ typedef struct {
  *                        and behind the last sequence are neither read nor written
  *   seq_lens    [B]      tokens of sequence b in the cache, the new ones counted
  *   block_table [B, table_stride]  entry i of row b: the page of tokens i*page_size ...; at least
- *                        ceil(seq_lens[b] / page_size) valid entries, others are not read.
+ *                        ceil(seq_lens[b] / page_size) valid entries, others are not used.
  * New token i of the n of sequence b stands at position seq_lens[b] - n + i. */
 typedef struct {
   void *k, *v;
