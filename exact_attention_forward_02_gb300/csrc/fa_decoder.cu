@@ -182,11 +182,11 @@ int paged_map(CUtensorMap* m, const void* base, bool bf16, int dims, int d, std:
 
 std::mutex g_attr_mu;
 
-template <int D, bool BF16, bool SPLIT, int REP>
+template <int D, bool BF16, bool SPLIT, int REP, bool DIRECT = true>
 int launch_paged(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const paged::Params& p,
                  int index, int blocks, cudaStream_t st) {
   constexpr int SMEM = paged::Layout<D, SPLIT>::SMEM_BYTES, ROWS = SPLIT ? 128 / REP : 256;
-  auto kern = paged::fa_paged_kernel<D, BF16, SPLIT, REP>;
+  auto kern = paged::fa_paged_kernel<D, BF16, SPLIT, REP, DIRECT>;
   static bool attr_set[fa_host::MAX_DEVICES] = {};
   {
     std::lock_guard<std::mutex> lk(g_attr_mu);
@@ -210,7 +210,9 @@ int paged_forms(int form, const CUtensorMap& mq, const CUtensorMap& mk, const CU
     case 4: return launch_paged<D, BF16, true, 4>(mq, mk, mv, p, index, blocks, st);
     case 2: return launch_paged<D, BF16, true, 2>(mq, mk, mv, p, index, blocks, st);
     case 1: return launch_paged<D, BF16, true, 1>(mq, mk, mv, p, index, blocks, st);
-    default: return launch_paged<D, BF16, false, 1>(mq, mk, mv, p, index, blocks, st);
+    default:
+      return p.direct ? launch_paged<D, BF16, false, 1, true>(mq, mk, mv, p, index, blocks, st)
+                      : launch_paged<D, BF16, false, 1, false>(mq, mk, mv, p, index, blocks, st);
   }
 }
 
@@ -392,12 +394,15 @@ int fa_fwd_paged(const fa_paged_kv* kv, const fa_heads* q, const fa_heads* O, fl
   p.wait_limit_ns = fa_host::wait_limit_ns();
   p.whole = whole;
   // without units: one sequence whose key heads divide (nearly) all SMs, or whole items that fit them
-  const long long items = (long long)B * kv->Hkv;
-  if (form != 0 && items <= sms) {
-    if (whole) p.direct = 1;
-    else if (B == 1 && sms / kv->Hkv * kv->Hkv * 10 >= sms * 9) p.direct = sms / kv->Hkv;
+  const long long heads = (long long)B * kv->Hkv;
+  if (whole) {
+    const int per_item = p.tpt * (form == 0 ? 2 : 1);
+    const long long parts = max_q <= per_item ? 1 : (max_q - 1) / per_item + 1;  // blocks of tokens
+    if (heads * parts <= sms) p.direct = (int)parts;
+  } else if (form != 0 && B == 1 && kv->Hkv <= sms && sms / kv->Hkv * kv->Hkv * 10 >= sms * 9) {
+    p.direct = sms / kv->Hkv;
   }
-  const int blocks = p.direct ? (int)items * p.direct : sms;
+  const int blocks = p.direct ? (int)heads * p.direct : sms;
   if (!whole) {
     p.records = static_cast<int*>(workspace);
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + paged_records_bytes(sms));

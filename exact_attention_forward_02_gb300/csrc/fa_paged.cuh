@@ -18,9 +18,10 @@
 // kernel waits on another block. Where the table is so narrow that no item has more than
 // WHOLE_TILES tiles, items stay whole and the second kernel falls away: joining takes 2.5 us on the
 // GPU and as much on the host, an item of 4 tiles by one block 1 us more than by two.
-// Small batches of single tokens go without units at all ("direct"): one sequence, whose key heads
+// Small batches go without units at all ("direct"): one sequence of single tokens, whose key heads
 // share the SMs evenly, or whole items that fit the SMs at once. Block c then is part c % direct of
-// item c / direct and reads the lengths of its own sequence only: 1 us less before the first load.
+// (sequence, key head) c / direct, a range of its keys or one of its blocks of tokens, and reads the
+// lengths of its own sequence only: 1 us less before the first load.
 //
 // Two forms of the kernel, of 12 warps (8, 11: loads, 9: MMA issuer, 10:
 // walks the block's range and hands the others their items through a ring in shared memory, a few
@@ -74,7 +75,7 @@ struct Params {
   int table_stride, B, T, causal;
   int cap;    // keys that a row of the table covers
   int whole;  // no item is split: a block takes the items that begin in its range
-  int direct; // SPLIT: that many blocks to a (sequence, key head), without units (0: by units)
+  int direct; // that many blocks to a (sequence, key head), without units (0: by units)
   float c;  // scale * log2(e)
   unsigned long long wait_limit_ns;
   int* status;
@@ -409,7 +410,9 @@ __device__ __forceinline__ Range plan(const Params& p, Barriers* bars, int b0, i
 }
 
 // ----------------------------------------------------------------------------- kernel
-template <int D, bool BF16, bool SPLIT, int REP>
+// DIRECT: batches that go without units may come (SPLIT: always; PAIR has an instantiation with and
+// one without that code, whose mere presence slowed the long chunks' loop from 339 to 351 us).
+template <int D, bool BF16, bool SPLIT, int REP, bool DIRECT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
@@ -463,7 +466,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   wait_previous_grid();  // no global memory is read or written before this
   Range range = {};
   tc_fence_before();
-  if (SPLIT && p.direct) {
+  if (DIRECT && p.direct) {
     __syncthreads();
   } else {
     const int per_thread = (p.B + NUM_THREADS - 1) / NUM_THREADS;
@@ -544,7 +547,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       auto window_of = [&](int j) { return (p.page_size > BN ? j / tiles_per_page : j * boxes) / 32; };
       // those of the block's first tile are asked for before its item has been handed over
       int early_b = -1, early_window = 0, early = 0;
-      if (SPLIT && p.direct) {
+      if (DIRECT && p.direct) {
         if (p.whole) early_b = (int)blockIdx.x / p.direct / p.Hkv;
       } else if (range.u0 < range.u1) {
         early_b = bars->start.b;
@@ -800,18 +803,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           rec[0] = 1;
         };
         bool go = true;
-        if (SPLIT && p.direct) {
+        if (DIRECT && p.direct) {
           const int item = (int)blockIdx.x / p.direct, part = (int)blockIdx.x - item * p.direct;
           const int b = item / p.Hkv, h = item - b * p.Hkv, tpi = p.tpt * TPT_MUL;
           const Seq s = load_seq(p, b, tpi, part == 0 && h == 0);
-          for (int q = 0; q < s.nq && go; ++q) {  // (more than one block of tokens only if max_q was too small)
+          // more blocks of tokens than the host knew of (max_q was too small): whole, by the last part
+          // (whole items) or the first
+          for (int q = p.whole ? part : 0; q < s.nq && go; ++q) {
             const int ntot = tiles_of(p, s, q, tpi);
             const int np = p.whole || q > 0 ? 1 : min(p.direct, (ntot + DIRECT_TILES - 1) / DIRECT_TILES);
-            if (part >= np) continue;
-            const uint32_t n = (uint32_t)ntot, j0 = part * n / np, j1 = (part + 1) * n / np;
+            const int k = p.whole ? 0 : part;
+            if (k >= np) continue;
+            const uint32_t n = (uint32_t)ntot, j0 = k * n / np, j1 = (k + 1) * n / np;
             const Item it = make_item<TPT_MUL>(p, s, b, h, q, ntot, (int)j0, (int)j1, 0);
             go = publish(it);
-            if (go && part == 0 && np > 1) record(it, (int)blockIdx.x + np - 1);
+            if (go && k == 0 && np > 1) record(it, (int)blockIdx.x + np - 1);
+            if (p.whole && part < p.direct - 1) break;
           }
         } else {
           Walk<TPT_MUL, ITEM_UNITS> walk;

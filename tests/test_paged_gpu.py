@@ -161,6 +161,18 @@ def test_results_do_not_change_from_run_to_run(fa):
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+@pytest.mark.parametrize("new,total,Hq,Hkv,d", [
+    ([200], [1500], 4, 2, 64), ([70, 300], [80, 500], 4, 2, 128), ([9, 0, 40], [400, 100, 41], 6, 1, 64),
+    ([500], [512], 8, 1, 128), ([129], [129], 1, 1, 64)])
+def test_small_batches_shared_out_without_units(fa, new, total, Hq, Hkv, d):
+    """One sequence, or whole items: every max_q, too small ones too."""
+    b = lib.Batch(new, total, Hkv, d, 16, torch.bfloat16, seed=d)
+    q = b.rows(Hq)
+    for b.max_q in (1, 3, 30, 64, 300, 5000):
+        check(fa, b, q, True)
+        check(fa, b, q, False)
+
+
 def test_max_q_is_a_hint(fa):
     """A batch with more new tokens than max_q says, and one with far fewer, are still right."""
     b = lib.Batch([150, 1, 40], [600, 300, 41], 2, 64, 32, torch.float16)
