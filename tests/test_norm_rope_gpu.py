@@ -69,6 +69,8 @@ CASES = [  # B, N, Hq, Hk, d, rot, interleaved, dtype, layout
     (4, 1025, 8, 4, 64, 48, False, "bf16", "tokens"),
     (1, 4097, 16, 2, 128, 112, True, "fp16", "fused"),
     (1, 5000, 40, 8, 64, 64, True, "bf16", "heads"),
+    (2, 3001, 2, 1, 64, 64, False, "fp16", "fused"),
+    (3, 2047, 1, 1, 128, 32, True, "bf16", "heads"),
 ]
 
 

@@ -397,3 +397,36 @@ def test_calls_on_another_stream_and_side_by_side(fa):
     for g, w in zip(got, want):
         assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
     assert fa.fa_last_status() == 0
+
+
+def test_captured_calls_replayed_with_other_lengths(fa):
+    """Graphs of split single tokens and of chunks, each with the workspace its capture took; replayed
+    in turn and at once with lengths that change between replays."""
+    batches = [lib.Batch([1, 1, 1], [3000, 900, 50], 2, 128, 16, torch.bfloat16, seed=1),
+               lib.Batch([300, 40], [2500, 700], 2, 64, 64, torch.float16, seed=2)]
+    qs = [b.rows(8) for b in batches]
+    for b, q in zip(batches, qs):
+        attend(fa, b, q, True)  # the plain call, before it is captured
+    graphs, outs = [], []
+    for b, q in zip(batches, qs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(attend(fa, b, q, True))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    lengths = [b.seq_lens.clone() for b in batches]
+    for cut in (0, 37, 400, 1):
+        want = []
+        for b, q, n in zip(batches, qs, lengths):
+            b.seq_lens.copy_((n - cut).clamp(min=1))
+            want.append(attend(fa, b, q, True))
+        for o in outs:
+            o[0].fill_(5.0), o[1].fill_(5.0)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for g, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        assert fa.fa_last_status() == 0
+        for o, w in zip(outs, want):
+            assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
