@@ -198,8 +198,8 @@ int launch_paged(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap
   }
   const int rc = launch_dependent(kern, dim3(blocks), dim3(paged::NUM_THREADS), SMEM, st, mq, mk, mv, p);
   if (rc != FA_OK || p.whole) return rc;
-  // a warp joins 4 rows, or 1
-  return launch_dependent(paged::fa_paged_combine_kernel<D, BF16, ROWS>, dim3(blocks, ROWS > 128 ? ROWS / 32 : ROWS / 8),
+  // a warp joins 2 rows, or 1
+  return launch_dependent(paged::fa_paged_combine_kernel<D, BF16, ROWS>, dim3(blocks, ROWS > 128 ? ROWS / 16 : ROWS / 8),
                           dim3(paged::COMBINE_THREADS), 0, st, p);
 }
 

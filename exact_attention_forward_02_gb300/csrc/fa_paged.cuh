@@ -63,6 +63,9 @@ constexpr int SMEM_LIMIT = 232448;
 constexpr int MAX_SLOTS = 8;
 constexpr int COMBINE_THREADS = 256;
 constexpr int WHOLE_TILES = FA_PAGED_WHOLE_KEYS / BN;
+// units of a block at least: with fewer, more pieces of an item to join than the shorter pieces gain
+// (100 tokens over 4000 keys of one head: 25.6 us, with 1 unit 38; 1 to 8 measured on small chunks)
+constexpr int MIN_UNITS = 3;
 constexpr int DIRECT_TILES = 2;  // key tiles of a part at least, one for each warpgroup
 
 struct Params {
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int b0 = min((int)threadIdx.x * per_thread, p.B), b1 = min(b0 + per_thread, p.B);
     Seq seq = {};
     const long long my_units = units_of<TPT_MUL, ITEM_UNITS>(p, b0, b1, seq, blockIdx.x == 0);
-    range = plan<TPT_MUL, ITEM_UNITS, SPLIT ? 2 : 1>(p, bars, b0, b1, my_units, seq);
+    range = plan<TPT_MUL, ITEM_UNITS, MIN_UNITS>(p, bars, b0, b1, my_units, seq);
   }
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
@@ -1157,7 +1160,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 template <int D, bool BF16, int ROWS>
 __global__ void __launch_bounds__(COMBINE_THREADS) fa_paged_combine_kernel(const __grid_constant__ Params p) {
   constexpr int E = D / 32;  // columns per lane
-  constexpr int RW = ROWS > 128 ? 4 : 1, PB = 32 / RW;  // rows of a warp, pieces at a time
+  constexpr int RW = ROWS > 128 ? 2 : 1, PB = 32 / RW;  // rows of a warp, pieces at a time
   launch_dependents();
   wait_previous_grid();
   const int4 rec0 = *reinterpret_cast<const int4*>(p.records + blockIdx.x * 8);
@@ -1189,26 +1192,41 @@ __global__ void __launch_bounds__(COMBINE_THREADS) fa_paged_combine_kernel(const
       l += st.y * w;
     }
     const int k = min(PB, n - x0);
-#pragma unroll 2
-    for (int y = 0; y < k; ++y) {
-      const float* src = part(x0 + y) + (size_t)pr0 * D + lane * E;
+    // N pieces' rows in flight at once
+    auto add = [&](auto n_c, int y) {
+      constexpr int N = decltype(n_c)::value;
+      float v[N][RW][E], wy[N][RW];
 #pragma unroll
-      for (int r = 0; r < RW; ++r) {
-        const float wy = __shfl_sync(0xffffffffu, w, r * PB + y);
-        float v[E] = {};
-        if (wy != 0.f) {
-          if constexpr (E == 4) {
-            const float4 q = *reinterpret_cast<const float4*>(src + r * D);
-            v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-          } else {
-            const float2 q = *reinterpret_cast<const float2*>(src + r * D);
-            v[0] = q.x, v[1] = q.y;
+      for (int i = 0; i < N; ++i) {
+        const float* src = part(x0 + y + i) + (size_t)pr0 * D + lane * E;
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+          wy[i][r] = __shfl_sync(0xffffffffu, w, r * PB + y + i);
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[i][r][e] = 0.f;
+          if (wy[i][r] != 0.f) {
+            if constexpr (E == 4) {
+              const float4 q = *reinterpret_cast<const float4*>(src + r * D);
+              v[i][r][0] = q.x, v[i][r][1] = q.y, v[i][r][2] = q.z, v[i][r][3] = q.w;
+            } else {
+              const float2 q = *reinterpret_cast<const float2*>(src + r * D);
+              v[i][r][0] = q.x, v[i][r][1] = q.y;
+            }
           }
         }
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[r][e] = fmaf(v[e], wy, acc[r][e]);
       }
-    }
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int r = 0; r < RW; ++r)
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[r][e] = fmaf(v[i][r][e], wy[i][r], acc[r][e]);
+    };
+    int y = 0;
+#pragma unroll 1
+    for (; y + 4 <= k; y += 4) add(std::integral_constant<int, 4>{}, y);
+    if (y + 2 <= k) add(std::integral_constant<int, 2>{}, y), y += 2;
+    if (y < k) add(std::integral_constant<int, 1>{}, y);
   }
 #pragma unroll
   for (int o = PB / 2; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
