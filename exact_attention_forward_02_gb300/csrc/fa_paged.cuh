@@ -1156,9 +1156,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
 // Joins the partial states of the items that lie in several blocks' ranges: blocks (c, y) take the
 // item that begins in block c's range. A warp joins RW rows at once, so that their loads overlap:
-// lane = (row, piece) for the pieces' weights, then all lanes along the columns.
+// lane = (row, piece) for the pieces' weights, then all lanes along the columns. (With no bound on the
+// blocks the compiler saved registers by loading one piece after another: 25.8 against 20.4 us.)
 template <int D, bool BF16, int ROWS>
-__global__ void __launch_bounds__(COMBINE_THREADS) fa_paged_combine_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(COMBINE_THREADS, 4) fa_paged_combine_kernel(const __grid_constant__ Params p) {
   constexpr int E = D / 32;  // columns per lane
   constexpr int RW = ROWS > 128 ? 2 : 1, PB = 32 / RW;  // rows of a warp, pieces at a time
   launch_dependents();
@@ -1178,19 +1179,20 @@ __global__ void __launch_bounds__(COMBINE_THREADS) fa_paged_combine_kernel(const
   };
   const int my_row = lane / PB, my_piece = lane % PB;
   const bool mine = token_of(pr0 + my_row) >= 0;
-  float m = -INFINITY;
-  for (int x = my_piece; x < n; x += PB)
-    if (mine) m = fmaxf(m, part(x)[ROWS * D + 2 * (pr0 + my_row)]);
+  auto state = [&](int x) {
+    return mine && x < n ? *reinterpret_cast<const float2*>(part(x) + ROWS * D + 2 * (pr0 + my_row))
+                         : make_float2(-INFINITY, 0.f);
+  };
+  const float2 st0 = state(my_piece);
+  float m = st0.x;
+  for (int x = my_piece + PB; x < n; x += PB) m = fmaxf(m, state(x).x);
 #pragma unroll
   for (int o = PB / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float acc[RW][E] = {}, l = 0.f;
   for (int x0 = 0; x0 < n; x0 += PB) {
-    float w = 0.f;
-    if (mine && x0 + my_piece < n) {
-      const float2 st = *reinterpret_cast<const float2*>(part(x0 + my_piece) + ROWS * D + 2 * (pr0 + my_row));
-      if (st.x != -INFINITY) w = ex2_approx(st.x - m);
-      l += st.y * w;
-    }
+    const float2 st = x0 == 0 ? st0 : state(x0 + my_piece);
+    const float w = st.x != -INFINITY ? ex2_approx(st.x - m) : 0.f;
+    l += st.y * w;
     const int k = min(PB, n - x0);
     // N pieces' rows in flight at once
     auto add = [&](auto n_c, int y) {
