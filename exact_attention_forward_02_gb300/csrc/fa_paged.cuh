@@ -16,8 +16,9 @@
 // An item whose tiles lie in several blocks' ranges leaves partial states (m, l, O~) in the
 // workspace; fa_paged_combine_kernel joins them, in the order of the blocks. Nothing in the main
 // kernel waits on another block. Where the table is so narrow that no item has more than
-// WHOLE_TILES tiles, items stay whole and the second kernel falls away: joining takes 2 us on the
-// GPU and as much on the host, an item of 4 tiles by one block 1 us more than by two (8 tiles: 3 more).
+// WHOLE_TILES tiles, items stay whole and the second kernel falls away: an item of 4 tiles by one
+// block takes 1 us more than by two, less than the second kernel costs; with whole items of up to 8
+// tiles one token over 1000 keys took 2.5 us more, fresh prompts of 1000 tokens 2 less.
 // Small batches go without units at all ("direct"): one sequence of single tokens, whose key heads
 // share the SMs evenly, or whole items that fit the SMs at once. Block c then is part c % direct of
 // (sequence, key head) c / direct, a range of its keys or one of its blocks of tokens, and reads the
@@ -27,9 +28,9 @@
 // hands the others their items through a ring in shared memory, a few ahead, so that nobody waits
 // for the lengths of the next sequence; 0-7: two softmax warpgroups, thread = row = TMEM lane):
 //   PAIR   an item is two tiles of 128 rows, one per warpgroup, over the same keys: chunks. d = 128 is
-//          bound by the tensor cores and the chain S - softmax - P V (2760 cycles a key tile, 2048 of
-//          them products), d = 64 by the exponentials. 2048 tokens at 30720, Hq 16, Hkv 2, d 128: 345
-//          us, 1.55 PFLOP/s; 4 x 1000 over 4097 keys, 12 heads, d 64: 75 us, 0.67 PFLOP/s.
+//          bound by the tensor cores and the chain S - softmax - P V, d = 64 by the exponentials. 2048
+//          tokens at 30720, Hq 16, Hkv 2, d 128: 331 us replayed in a graph, 1.61 PFLOP/s, and 351 us
+//          called one by one; 4 x 1000 over 4097 keys, 12 heads, d 64: 76 us, 0.66 PFLOP/s.
 //   SPLIT  an item is one tile; the warpgroups take the even and the odd key tiles, each with its
 //          own (m, l, O~). Its rows stand REP times in the tile (REP = 4 for up to 32 rows): copy
 //          a covers keys [a 128/REP, (a+1) 128/REP) of each key tile only, with its own (m, l, O~)
@@ -38,7 +39,7 @@
 //          drafts: bound by HBM; the tensor cores run mostly empty and still hide behind the
 //          loads (1024 cycles of products per 64 KB of keys and values, which take 2900 at this
 //          SM's share of the bandwidth). 64 sequences of 201 to 8020 keys, 8 key heads, d 128, pages
-//          of 16: 163 us, 6.45 TB/s; one sequence of 1001 keys: 9.5 us, latency.
+//          of 16: 163 us, 6.45 TB/s; one sequence of 1001 keys: 9.6 us with the join, latency.
 #pragma once
 
 #include <cuda.h>
@@ -1160,7 +1161,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // item that begins in block c's range. A warp joins RW rows at once, so that their loads overlap:
 // lane = (row, piece) for the pieces' weights, then all lanes along the columns. (With no bound on the
 // blocks the compiler saved registers by loading one piece after another: 25.8 against 20.4 us.)
-// Latency for single tokens (2 us); for a chunk the L2's rate, 37 MB of partial states in 5 to 7 us.
+// Latency bounds it for single tokens; a chunk of 2048 tokens reads 37 MB of partial states (16.5 us
+// with cold caches, 6 us for one token of one sequence).
 template <int D, bool BF16, int ROWS>
 __global__ void __launch_bounds__(COMBINE_THREADS, 4) fa_paged_combine_kernel(const __grid_constant__ Params p) {
   constexpr int E = D / 32;  // columns per lane

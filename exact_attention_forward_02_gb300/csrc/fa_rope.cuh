@@ -233,9 +233,8 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) fa_norm_rope_kernel(const __gr
 
 // dx = r (u - x r mean(u x r)), u = R^T dy * w; the block's sums of R^T dy * x * r go to `part`.
 // A fixed number of blocks walks the units, so each sum has a fixed order. Four rows of both
-// tensors in flight per lane group and two blocks per SM (128 registers; three or four blocks with
-// fewer rows in flight: 105 to 123 us). 16384 tokens of 32 + 8 heads, d 128: 87 us with the sums, 5.8
-// TB/s; the units do not divide evenly among the blocks (6.7 rounds), which costs the most.
+// tensors in flight per lane group and two blocks per SM (128 registers; 1, 3 and 4 blocks: 127,
+// 108 and 123 us against 87). 16384 tokens of 32 + 8 heads, d 128: 88 us with the sums, 5.8 TB/s.
 template <int D, bool BF16, bool INTER>
 __global__ void __launch_bounds__(ROW_THREADS, 2) fa_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int LPR = D / 8, GPW = 32 / LPR;
@@ -370,7 +369,7 @@ __device__ __forceinline__ int find_sequence(const int* cu, int B, int t, int la
   return lo >= 1 && lo <= B ? lo - 1 : -1;
 }
 
-// Bound by HBM: 65536 tokens of 8 heads, d 128, in 83 us (the copy's rate), 29582 ragged ones in 40;
+// Bound by HBM: 65536 tokens of 8 heads, d 128, in 84 us (the copy's rate), 29582 ragged ones in 41;
 // 64 single tokens in 2.9 us. One warp per unit: each group's token's sequence, position, page and slot, then its rows of k
 // (rotated) and v (copied).
 template <int D, bool BF16, bool INTER>
