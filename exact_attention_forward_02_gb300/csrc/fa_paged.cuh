@@ -85,7 +85,7 @@ struct Params {
   float c;  // scale * log2(e)
   unsigned long long wait_limit_ns;
   int* status;
-  int* records;  // [block][8]: the item that begins in a block's range and ends in another's
+  int* records;  // [block][8]: the item that begins in a block's range and ends in another's (7 in use)
   float* parts;  // [block][2][rows]: D floats of O~ per row, then [rows][2] of (m, l)
   long long parts_len;  // floats there (checked by debug builds)
 };
@@ -806,6 +806,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           rec[3] = it.h;
           rec[4] = it.tok0;
           rec[5] = it.nt;
+          rec[6] = p.causal ? it.vis0 : it.len;  // keys that its first token sees
           rec[0] = 1;
         };
         bool go = true;
@@ -987,6 +988,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (!ok) break;
       // ------------------------------------------------------------------ epilogue
       const bool worked = !SPLIT || item->n > g, partial = item->n != item->ntot;
+      // A row that sees no key gets O = 0 and L = -inf, and no other row does: where a score is NaN or
+      // past fp32's range, l or m carries it (the maximum alone drops NaN), so neither is asked here.
+      const bool sees = lim + item->j0 * BN > 0;
       float* part = p.parts + (size_t)(blockIdx.x * 2 + item->slot) * part_floats(D, ROWS);
       float m = m_run, l = l_run, f;
       if constexpr (SPLIT) {
@@ -1011,13 +1015,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         f = 1.f;
       }
       // a whole item's O~ is divided by l; a partial state stays as it is
-      if (!partial) f *= l > 0.f ? 1.f / l : 0.f;
+      if (!partial) f *= sees ? 1.f / l : 0.f;
       const int prow = SPLIT ? row : g * BM + row;
       const long long t = item->tok0 + tok;
       const int head = item->h * p.G + row_head;
       if (valid && (!SPLIT || (g == 0 && copy == 0))) {
         if (partial) *reinterpret_cast<float2*>(part + ROWS * D + 2 * prow) = make_float2(m, l);
-        else if (p.L) p.L[t * (p.Hkv * p.G) + head] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        else if (p.L) p.L[t * (p.Hkv * p.G) + head] = sees ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
       }
       if (worked) {
         ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->o_done[g]), o_ph, abort_flag, p));
@@ -1170,7 +1174,7 @@ __global__ void __launch_bounds__(COMBINE_THREADS, 4) fa_paged_combine_kernel(co
   launch_dependents();
   wait_previous_grid();
   const int4 rec0 = *reinterpret_cast<const int4*>(p.records + blockIdx.x * 8);
-  const int2 rec1 = *reinterpret_cast<const int2*>(p.records + blockIdx.x * 8 + 4);
+  const int4 rec1 = *reinterpret_cast<const int4*>(p.records + blockIdx.x * 8 + 4);
   if (rec0.x == 0) return;
   const int c0 = blockIdx.x, slot0 = rec0.y, n = rec0.z - c0 + 1, h = rec0.w, tok0 = rec1.x, nt = rec1.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, Hq = p.Hkv * p.G;
@@ -1242,14 +1246,15 @@ __global__ void __launch_bounds__(COMBINE_THREADS, 4) fa_paged_combine_kernel(co
     const float lr = __shfl_sync(0xffffffffu, l, r * PB), mr = __shfl_sync(0xffffffffu, m, r * PB);
     const int tok = token_of(pr0 + r);
     if (tok < 0) continue;
-    const float inv = lr > 0.f ? 1.f / lr : 0.f;
+    const bool sees = rec1.z + (p.causal ? tok : 0) > 0;  // as in the main kernel; a piece's NaN is in its l
+    const float inv = sees ? 1.f / lr : 0.f;
     const long long t = tok0 + tok;
     const int head = h * p.G + (pr0 + r) % BM % p.G;
     uint16_t* dst = p.o.ptr + t * p.o.ts + (long long)head * p.o.hs + lane * E;
 #pragma unroll
     for (int e = 0; e < E; e += 2)
       *reinterpret_cast<uint32_t*>(dst + e) = pack2<BF16>(acc[r][e] * inv, acc[r][e + 1] * inv);
-    if (p.L && lane == 0) p.L[t * Hq + head] = lr > 0.f ? (mr + log2f(lr)) * 0.69314718055994531f : -INFINITY;
+    if (p.L && lane == 0) p.L[t * Hq + head] = sees ? (mr + log2f(lr)) * 0.69314718055994531f : -INFINITY;
   }
 }
 

@@ -108,7 +108,9 @@ int fa_paged_append(const fa_paged_kv* kv, const fa_heads* k, const fa_heads* v,
  * Hkv, at most 128 * Hkv.
  *     s_j = scale <q, k_j>,  j in [0, seq_lens[b]), and with `causal` j <= the token's position
  *     O = sum_j softmax_j(s) v_j,   L = ln sum_j exp(s_j)
- * A row that sees no key (an empty sequence, or a negative position) gets O = 0 and L = -inf.
+ * A row that sees no key (an empty sequence, or a negative position) gets O = 0 and L = -inf,
+ * whatever its query holds. A row that sees keys and whose scores hold a NaN, or pass the range of
+ * fp32, gets NaN in O, and in L the NaN (or -inf where every score lies below that range).
  *   q, O      [T, Hq] rows of d elements (batch_stride unused); kv->d 64 or 128. O may be q's own
  *             memory with the same strides
  *   L         fp32 [T, Hq], or NULL

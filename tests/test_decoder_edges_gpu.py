@@ -1,0 +1,95 @@
+"""The decoder-block operators at the edges of what they accept."""
+import math
+
+import pytest
+import torch
+
+from tests import decoder_testlib as lib
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fa():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import exact_attention_forward_02_gb300 as fa
+    fa.fa_clear_status()
+    yield fa
+    assert fa.fa_last_status() == 0
+
+
+def attend(fa, b, q, causal, **kw):
+    return fa.attention_paged(q, b.k_pages, b.v_pages, b.block_table, b.cu_seqlens, b.seq_lens, b.max_q,
+                              causal=causal, **kw)
+
+
+# ---------------------------------------------------------------- scores that are not finite
+# new, total, Hq, Hkv, d, page, table width: whole items with and without units, one sequence in parts,
+# items over several SMs' ranges; single tokens and drafts (SPLIT, 4 to 1 copies of a row), chunks (PAIR)
+KINDS = [
+    ([1], [40], 8, 2, 128, 16, None),
+    ([1, 3, 2], [300, 3, 512], 4, 1, 64, 16, None),
+    ([1] * 200, [1 + (37 * i) % 300 for i in range(200)], 4, 2, 64, 32, None),
+    ([1], [1001], 32, 8, 128, 16, None),
+    ([1, 1, 1, 1], [3000, 20, 400, 2100], 8, 2, 64, 16, None),
+    ([7, 9], [5000, 700], 6, 1, 128, 64, None),
+    ([20], [9000], 4, 1, 128, 64, None),
+    ([60, 1], [200, 2000], 4, 2, 128, 16, 200),
+    ([300, 40], [300, 500], 4, 2, 64, 64, None),
+    ([300], [6000], 4, 1, 128, 64, None),
+    ([257, 100], [3000, 100], 6, 2, 64, 16, None),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new,total,Hq,Hkv,d,page,wide", KINDS)
+def test_a_nan_query_gives_nan_and_nothing_else_changes(fa, new, total, Hq, Hkv, d, page, wide, causal):
+    """As in the dense kernels: a row whose scores are NaN is NaN in O and in L, whatever way its keys
+    are shared out; O = 0 and L = -inf are for rows that see no key."""
+    b = lib.Batch(new, total, Hkv, d, page, torch.bfloat16, seed=7, wide=wide)
+    q = b.rows(Hq)
+    want = attend(fa, b, q, causal)
+    g = torch.Generator().manual_seed(3)
+    hit = (torch.rand(q.shape[:2], generator=g) < 0.3).cuda()
+    hit[0, 0] = hit[-1, -1] = True
+    bad = q.clone()
+    bad[hit] = math.nan
+    one = torch.rand(q.shape[:2], generator=g).cuda() < 0.5   # one element of the row alone
+    bad[hit & one] = q[hit & one]
+    bad[hit & one, d // 2] = math.nan
+    O, L = attend(fa, b, bad, causal)
+    assert torch.isnan(O[hit]).all() and torch.isnan(L[hit]).all()
+    assert torch.equal(O[~hit], want[0][~hit]) and torch.equal(L[~hit], want[1][~hit])
+
+
+def test_rows_without_a_key_are_zero_whatever_the_query_holds(fa):
+    """More new tokens than cached ones: the leading rows see nothing. Of an item in several parts, too."""
+    for new, total, Hq in (([5, 700], [2, 300], 3), ([1, 2], [0, 1], 4), ([250], [180], 1), ([120], [100], 2)):
+        b = lib.Batch(new, total, 1, 64, 16, torch.float16, seed=2, wide=300)
+        q = b.rows(Hq)
+        dead = torch.cat([torch.arange(n) < n - t for n, t in zip(new, total)]).cuda()
+        q[:, 0] = math.nan
+        O, L = attend(fa, b, q, True)
+        assert not O[dead].any() and (L[dead] == -math.inf).all()
+        assert torch.isnan(O[~dead][:, 0]).all() and torch.isnan(L[~dead][:, 0]).all()
+        assert torch.isfinite(O[~dead][:, 1:]).all() and torch.isfinite(L[~dead][:, 1:]).all()
+
+
+@pytest.mark.parametrize("new,total,Hq,Hkv,d,page,wide", KINDS)
+def test_scores_past_32_bits_are_not_the_result_of_no_key(fa, new, total, Hq, Hkv, d, page, wide):
+    """q.k beyond fp32: no weights can be had, so O is NaN; below -fp32's largest L rounds to -inf."""
+    b = lib.Batch(new, total, Hkv, d, page, torch.bfloat16, seed=7, wide=wide)
+    for x in (b.k_pages, b.v_pages):
+        x.abs_().add_(0.5)
+    q = b.rows(Hq)
+    want = attend(fa, b, q, True)
+    bad = q.clone()
+    bad[0, 0], bad[-1, -1] = 3e38, -3e38
+    O, L = attend(fa, b, bad, True)
+    assert torch.isnan(O[0, 0]).all() and not L[0, 0] == -math.inf
+    if q.shape[0] * q.shape[1] > 1:
+        assert torch.isnan(O[-1, -1]).all() and not torch.isfinite(L[-1, -1])
+    same = torch.ones(q.shape[:2], dtype=torch.bool, device="cuda")
+    same[0, 0] = same[-1, -1] = False
+    assert torch.equal(O[same], want[0][same]) and torch.equal(L[same], want[1][same])
