@@ -170,6 +170,14 @@ struct RowUnit {
       alive = false;
     }
   }
+  // A group without a token takes the rows of one that has one (`some`: the lanes of those), so that
+  // what it works out and drops is no worse than that token's own: its own rows may hold anything.
+  __device__ __forceinline__ void borrow(uint32_t some) {
+    const int from = alive ? threadIdx.x & 31 : __ffs(some) - 1;
+    t = __shfl_sync(0xffffffffu, t, from);
+    b = __shfl_sync(0xffffffffu, b, from);
+    n = __shfl_sync(0xffffffffu, n, from);
+  }
   // the unit's heads of a set whose first head is `first`
   __device__ __forceinline__ int begin(int first) const { return max(c - first, 0); }
   __device__ __forceinline__ int end(const NormRopeParams& p, int first, int H) const { return min(c + p.chunk - first, H); }
@@ -232,7 +240,8 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) fa_norm_rope_kernel(const __gr
 }
 
 // dx = r (u - x r mean(u x r)), u = R^T dy * w; the block's sums of R^T dy * x * r go to `part`.
-// A fixed number of blocks walks the units, so each sum has a fixed order. Four rows of both
+// A group without a token adds g = 0 times a borrowed row to them (zeroing its x and r in the loop as
+// well costs 1 us of 88). A fixed number of blocks walks the units, so each sum has a fixed order. Four rows of both
 // tensors in flight per lane group and two blocks per SM (128 registers; 1, 3 and 4 blocks: 127,
 // 108 and 123 us against 87). 16384 tokens of 32 + 8 heads, d 128: 88 us with the sums, 5.8 TB/s.
 template <int D, bool BF16, bool INTER>
@@ -249,7 +258,9 @@ __global__ void __launch_bounds__(ROW_THREADS, 2) fa_norm_rope_bwd_kernel(const 
   for (uint32_t unit = blockIdx.x * ROW_WARPS + warp; unit < p.units; unit += gridDim.x * ROW_WARPS) {
     RowUnit<GPW> at(p, unit, sub);
     at.locate(p, ln.l);
-    if (!__any_sync(0xffffffffu, at.alive)) continue;
+    const uint32_t some = __ballot_sync(0xffffffffu, at.alive);
+    if (!some) continue;
+    at.borrow(some);
     ln.angles(p.rope, at.pos, -1.f, at.alive);
 #pragma unroll
     for (int set = 0; set < 2; ++set) {

@@ -93,3 +93,32 @@ def test_scores_past_32_bits_are_not_the_result_of_no_key(fa, new, total, Hq, Hk
     same = torch.ones(q.shape[:2], dtype=torch.bool, device="cuda")
     same[0, 0] = same[-1, -1] = False
     assert torch.equal(O[same], want[0][same]) and torch.equal(L[same], want[1][same])
+
+
+# ------------------------------------------------------------------- tokens without a position
+@pytest.mark.parametrize("d,Hq,Hk", [(64, 2, 1), (128, 3, 2), (64, 1, 1)])
+@pytest.mark.parametrize("eps", [1e-6, 0.0])
+def test_padding_rows_add_nothing_to_the_weights_gradients(fa, d, Hq, Hk, eps):
+    """Rows whose position is outside the table may hold anything, zeros with eps = 0 too."""
+    N = 11
+    g = torch.Generator().manual_seed(0)
+    q, k, gq, gk = (torch.randn(1, N, H, d, generator=g).bfloat16().cuda() for H in (Hq, Hk, Hq, Hk))
+    wq, wk = ((1 + 0.1 * torch.randn(d, generator=g)).bfloat16().cuda() for _ in range(2))
+    table = lib.rope_table(20, d).cuda()
+    pos = torch.tensor([[3, -1, 0, 20, 5, 6, 7, -9, 8, 9, 1000]], dtype=torch.int32).cuda()
+    good = (pos[0] >= 0) & (pos[0] < 20)
+    zeroed = [x.clone() for x in (gq, gk)]
+    for x in zeroed:
+        x[:, ~good] = 0
+    clean = fa.qk_norm_rope_backward(*zeroed, q, k, wq, wk, table, pos, eps)
+    for fill in (math.nan, math.inf, -math.inf, 0.0, 3e38):
+        for x in (q, k, gq, gk):
+            x[:, ~good] = fill
+        out = [torch.full_like(x, 7.0) for x in (q, k)]
+        got = fa.qk_norm_rope_backward(gq, gk, q, k, wq, wk, table, pos, eps, dq=out[0], dk=out[1])
+        assert fa.fa_last_status() == fa.FA_ERR_RANGE
+        fa.fa_clear_status()
+        for x, y in zip(got[2:], clean[2:]):
+            assert torch.isfinite(x).all() and torch.equal(x, y)
+        for x, y in zip(got[:2], clean[:2]):
+            assert torch.equal(x[:, good], y[:, good]) and (x[:, ~good] == 7).all()
