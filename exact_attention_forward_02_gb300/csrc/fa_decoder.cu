@@ -96,11 +96,17 @@ int launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, c
   return fa_host::launched(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
-// f(type, interleaved) for the four instantiations of a kernel of head dimension D
+// f(type, interleaved, full) for the eight instantiations of a kernel of head dimension d
 template <typename F>
-int by_type(bool bf16, bool inter, F f) {
-  if (bf16) return inter ? f(std::true_type{}, std::true_type{}) : f(std::true_type{}, std::false_type{});
-  return inter ? f(std::false_type{}, std::true_type{}) : f(std::false_type{}, std::false_type{});
+int by_type(fa_dtype dtype, const fa_rope* rope, int d, F f) {
+  const bool full = rope && rope->table && rope->rot_dim == d;
+  auto with_pairs = [&](auto bf, auto inter) {
+    return full ? f(bf, inter, std::true_type{}) : f(bf, inter, std::false_type{});
+  };
+  auto with_type = [&](auto bf) {
+    return rope && rope->interleaved ? with_pairs(bf, std::true_type{}) : with_pairs(bf, std::false_type{});
+  };
+  return dtype == FA_BF16 ? with_type(std::true_type{}) : with_type(std::false_type{});
 }
 
 int norm_rope_args(const fa_heads* const* sets, int n, int B, int N, int d, const void* wq, const void* wk,
@@ -243,8 +249,8 @@ int fa_qk_norm_rope(const fa_heads* q, const fa_heads* k, const fa_heads* q_out,
   row_units(&p, (long long)B * N, H, d, sms, false);
   const unsigned grid = (p.units - 1) / ROW_WARPS + 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return by_type(dtype == FA_BF16, rope && rope->interleaved, [&](auto bf, auto inter) {
-    return launch_dependent(d == 64 ? fa_norm_rope_kernel<64, bf, inter> : fa_norm_rope_kernel<128, bf, inter>,
+  return by_type(dtype, rope, d, [&](auto bf, auto inter, auto full) {
+    return launch_dependent(d == 64 ? fa_norm_rope_kernel<64, bf, inter, full> : fa_norm_rope_kernel<128, bf, inter, full>,
                             dim3(grid), dim3(ROW_THREADS), 0, st, p);
   });
 }
@@ -285,9 +291,10 @@ int fa_qk_norm_rope_bwd(const fa_heads* dq_out, const fa_heads* dk_out, const fa
   const int grid = blocks < (unsigned)most ? (int)blocks : most;
   float* oq = q->H ? dwq : nullptr;
   float* ok = k->H ? dwk : nullptr;
-  return by_type(dtype == FA_BF16, rope && rope->interleaved, [&](auto bf, auto inter) {
-    const int rc1 = launch_dependent(d == 64 ? fa_norm_rope_bwd_kernel<64, bf, inter> : fa_norm_rope_bwd_kernel<128, bf, inter>,
-                                     dim3(grid), dim3(ROW_THREADS), 0, st, p);
+  return by_type(dtype, rope, d, [&](auto bf, auto inter, auto full) {
+    const int rc1 = launch_dependent(
+        d == 64 ? fa_norm_rope_bwd_kernel<64, bf, inter, full> : fa_norm_rope_bwd_kernel<128, bf, inter, full>,
+        dim3(grid), dim3(ROW_THREADS), 0, st, p);
     if (rc1 != FA_OK) return rc1;
     return launch_dependent(d == 64 ? fa_norm_rope_dw_kernel<64> : fa_norm_rope_dw_kernel<128>, dim3(2 * d / 32),
                             dim3(32, 32), 0, st, (const float*)p.part, grid, oq, ok);
@@ -334,9 +341,10 @@ int fa_paged_append(const fa_paged_kv* kv, const fa_heads* k, const fa_heads* v,
   p.units = r.units;
   const unsigned grid = (p.units - 1) / ROW_WARPS + 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return by_type(dtype == FA_BF16, rope && rope->interleaved, [&](auto bf, auto inter) {
-    return launch_dependent(kv->d == 64 ? fa_paged_append_kernel<64, bf, inter> : fa_paged_append_kernel<128, bf, inter>,
-                            dim3(grid), dim3(ROW_THREADS), 0, st, p);
+  return by_type(dtype, rope, kv->d, [&](auto bf, auto inter, auto full) {
+    return launch_dependent(
+        kv->d == 64 ? fa_paged_append_kernel<64, bf, inter, full> : fa_paged_append_kernel<128, bf, inter, full>,
+        dim3(grid), dim3(ROW_THREADS), 0, st, p);
   });
 }
 

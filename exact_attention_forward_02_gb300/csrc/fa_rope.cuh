@@ -55,15 +55,19 @@ __device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uin
 // Where a lane's pairs stand in a row, and a token's rotation of them. Pairs (2i, 2i+1): the lane
 // holds 8 consecutive elements. Split halves (i, i + rot/2): lane l < rot/8 holds elements
 // 4l .. 4l+3 (A) and rot/2 + 4l .. (B); the other lanes hold 8 consecutive elements behind rot,
-// which pass through (cosine 1, sine 0). rot is a multiple of 16.
-template <int D, bool BF16, bool INTER>
+// which pass through as they are, whatever stands beside them. rot is a multiple of 16; FULL: it is
+// D, and no lane has to choose between its turned and its own elements (a choice in every row costs
+// the gradients 2 us of 88).
+template <int D, bool BF16, bool INTER, bool FULL>
 struct Lane {
   int l, ea, eb;  // lane of the row, first elements of its two runs of 4
+  bool turns;     // its pairs are rotated
   uint64_t c[2], s[2];
 
   __device__ __forceinline__ void place(int lane, int rot) {
     l = lane % (D / 8);
-    const bool split = !INTER && 8 * l < rot;
+    turns = FULL || 8 * l < rot;
+    const bool split = !INTER && turns;
     ea = split ? 4 * l : 8 * l;
     eb = split ? 4 * l + rot / 2 : 8 * l + 4;
   }
@@ -75,7 +79,7 @@ struct Lane {
   __device__ __forceinline__ void angles(const RopeDev& rp, int pos, float sign, bool known) {
     c[0] = c[1] = f2(1.f, 1.f);
     s[0] = s[1] = 0;
-    if (8 * l >= rp.rot || !known) return;
+    if (!turns || !known) return;
     const float* row = rp.table + (size_t)pos * rp.rot + 4 * l;
     const float4 x = *reinterpret_cast<const float4*>(row), y = *reinterpret_cast<const float4*>(row + rp.rot / 2);
     c[0] = f2(x.x, x.y), c[1] = f2(x.z, x.w);
@@ -116,8 +120,9 @@ struct Lane {
     for (int i = 0; i < 2; ++i) {
       const uint64_t minus = s[i] ^ 0x8000000080000000ull;
       const uint64_t a = f2_fma(v.a[i], c[i], f2_mul(v.b[i], minus));
-      v.b[i] = f2_fma(v.b[i], c[i], f2_mul(v.a[i], s[i]));
-      v.a[i] = a;
+      const uint64_t b = f2_fma(v.b[i], c[i], f2_mul(v.a[i], s[i]));
+      v.a[i] = turns ? a : v.a[i];
+      v.b[i] = turns ? b : v.b[i];
     }
   }
 };
@@ -188,14 +193,14 @@ struct RowUnit {
 
 // y = R(p) (x r w): one warp per unit. 4 rows in flight per group and 64 registers, so that 32 warps
 // fit an SM. 16384 tokens of 32 + 8 heads, d 128: 56 us, 6.1 TB/s of the copy's 6.8.
-template <int D, bool BF16, bool INTER>
+template <int D, bool BF16, bool INTER, bool FULL>
 __global__ void __launch_bounds__(ROW_THREADS, 4) fa_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int LPR = D / 8, GPW = 32 / LPR;
   const int lane = threadIdx.x & 31, sub = lane / LPR;
   const uint32_t unit = blockIdx.x * ROW_WARPS + (threadIdx.x >> 5);
   if (unit >= p.units) return;
   RowUnit<GPW> at(p, unit, sub);
-  Lane<D, BF16, INTER> ln;
+  Lane<D, BF16, INTER, FULL> ln;
   ln.place(lane, p.rope.rot);
   launch_dependents();
   wait_previous_grid();
@@ -244,12 +249,12 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) fa_norm_rope_kernel(const __gr
 // well costs 1 us of 88). A fixed number of blocks walks the units, so each sum has a fixed order. Four rows of both
 // tensors in flight per lane group and two blocks per SM (128 registers; 1, 3 and 4 blocks: 127,
 // 108 and 123 us against 87). 16384 tokens of 32 + 8 heads, d 128: 88 us with the sums, 5.8 TB/s.
-template <int D, bool BF16, bool INTER>
+template <int D, bool BF16, bool INTER, bool FULL>
 __global__ void __launch_bounds__(ROW_THREADS, 2) fa_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int LPR = D / 8, GPW = 32 / LPR;
   __shared__ float sums[ROW_WARPS][2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR;
-  Lane<D, BF16, INTER> ln;
+  Lane<D, BF16, INTER, FULL> ln;
   ln.place(lane, p.rope.rot);
   launch_dependents();
   wait_previous_grid();
@@ -383,7 +388,7 @@ __device__ __forceinline__ int find_sequence(const int* cu, int B, int t, int la
 // Bound by HBM: 65536 tokens of 8 heads, d 128, in 84 us (the copy's rate), 29582 ragged ones in 41;
 // 64 single tokens in 2.9 us. One warp per unit: each group's token's sequence, position, page and slot, then its rows of k
 // (rotated) and v (copied).
-template <int D, bool BF16, bool INTER>
+template <int D, bool BF16, bool INTER, bool FULL>
 __global__ void __launch_bounds__(ROW_THREADS, 4) fa_paged_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LPR = D / 8, GPW = 32 / LPR;
   const int lane = threadIdx.x & 31, sub = lane / LPR;
@@ -391,7 +396,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) fa_paged_append_kernel(const _
   if (unit >= p.units) return;
   const uint32_t tg = unit / (uint32_t)p.n_chunks;
   const int c = (int)(unit - tg * p.n_chunks), t0 = (int)(tg * GPW), t = t0 + sub;
-  Lane<D, BF16, INTER> ln;
+  Lane<D, BF16, INTER, FULL> ln;
   ln.place(lane, p.rope.rot);
   launch_dependents();
   wait_previous_grid();
@@ -427,7 +432,8 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) fa_paged_append_kernel(const _
       if (turned) {
         Pairs x = ln.unpack(u);
         ln.turn(x);
-        u = ln.pack(x);
+        const uint4 w = ln.pack(x);
+        u = ln.turns ? w : u;  // bit by bit where it passes through
       }
       ln.store(to, u);
     };

@@ -24,6 +24,10 @@ def attend(fa, b, q, causal, **kw):
                               causal=causal, **kw)
 
 
+def bits(x):
+    return x.contiguous().view({2: torch.int16, 4: torch.int32}[x.element_size()])
+
+
 # ---------------------------------------------------------------- scores that are not finite
 # new, total, Hq, Hkv, d, page, table width: whole items with and without units, one sequence in parts,
 # items over several SMs' ranges; single tokens and drafts (SPLIT, 4 to 1 copies of a row), chunks (PAIR)
@@ -122,3 +126,44 @@ def test_padding_rows_add_nothing_to_the_weights_gradients(fa, d, Hq, Hk, eps):
             assert torch.isfinite(x).all() and torch.equal(x, y)
         for x, y in zip(got[:2], clean[:2]):
             assert torch.equal(x[:, good], y[:, good]) and (x[:, ~good] == 7).all()
+
+
+# ---------------------------------------------------------- elements that the rotation leaves out
+SPECIAL = [math.inf, -math.inf, math.nan, -0.0, 0.0, 65504.0, -1.0]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("d,rot", [(64, 16), (64, 48), (128, 64), (128, 112)])
+def test_elements_behind_the_rotation_are_copied(fa, d, rot, interleaved, dtype):
+    """Bit by bit, whatever stands beside them."""
+    b = lib.Batch([40, 1, 7], [40, 90, 30], 3, d, 16, lib.DTYPES[dtype], fill=5.0)
+    k, v = b.rows(3), b.rows(3)
+    g = torch.Generator().manual_seed(1)
+    rest = k[..., rot:]
+    pick = torch.randint(0, 2 * len(SPECIAL), rest.shape, generator=g).cuda()
+    values = torch.tensor(SPECIAL, dtype=torch.float32).to(k.dtype).cuda()
+    rest.copy_(torch.where(pick < len(SPECIAL), values[pick.clamp(max=len(SPECIAL) - 1)], rest))
+    fa.paged_append(k, v, b.k_pages, b.v_pages, b.block_table, b.cu_seqlens, b.seq_lens,
+                    rope=lib.rope_table(100, rot).cuda(), interleaved=interleaved)
+    assert fa.fa_last_status() == 0
+    for i, n in enumerate(b.new):
+        got = b.cached(i)[0][:, b.total[i] - n:].transpose(0, 1)
+        rows = k[b.cu[i]:b.cu[i] + n]
+        assert torch.equal(bits(got[..., rot:]), bits(rows[..., rot:]))
+        assert torch.isfinite(got[..., :rot]).all()
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_gradients_behind_the_rotation_stay_in_their_places(fa, interleaved):
+    """An infinite gradient of one element that is not rotated: the weights' gradients of its neighbours
+    do not see it (u = g w couples the elements of dx, not those of dw)."""
+    d, rot = 64, 16
+    x, g = (torch.randn(1, 5, 2, d).bfloat16().cuda() for _ in range(2))
+    w = torch.ones(d).bfloat16().cuda()
+    table, none = lib.rope_table(5, rot).cuda(), x[:, :, :0]
+    clean = fa.qk_norm_rope_backward(g, none, x, none, w, w, table, interleaved=interleaved)[2]
+    g[0, 2, 1, 41] = math.inf
+    got = fa.qk_norm_rope_backward(g, none, x, none, w, w, table, interleaved=interleaved)[2]
+    keep = torch.arange(d) != 41
+    assert not torch.isfinite(got[41]) and torch.equal(got[keep], clean[keep])
