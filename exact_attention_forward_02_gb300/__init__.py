@@ -150,9 +150,6 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     return lib
 
 
-if not os.path.exists(TORCH_CALLS_PATH):
-    raise ImportError(f"{os.path.basename(TORCH_CALLS_PATH)} is not built ({TORCH_CALLS_PATH} missing); run "
-                      "__graft_entry__.build() first. There is no fallback implementation.")
 _choice = os.environ.get("FA_LIBRARY", "release")
 if _choice not in ("release", "debug"):
     raise ImportError(f"FA_LIBRARY must be 'release' or 'debug', not {_choice!r}")
@@ -386,6 +383,10 @@ def _calls():
     """The native tensor-level calls (csrc/fa_torch.cpp), bound to the library in use."""
     global _torch_calls
     if _torch_calls is None:
+        if not os.path.exists(TORCH_CALLS_PATH):
+            raise ImportError(f"{os.path.basename(TORCH_CALLS_PATH)} is not built ({TORCH_CALLS_PATH} missing); run "
+                              "__graft_entry__.build() with a CUDA build of torch first. There is no fallback "
+                              "implementation.")
         import torch  # noqa: F401  (the module links against libraries that torch loads)
 
         from . import _fa_torch

@@ -1,11 +1,13 @@
 """Build libfa.so (the CUDA library behind the C ABI in include/*.h) in-tree.
 
-Two CUDA translation units (and the host-only module of the tensor-level calls) compiled at the same time, one -gencode (sm_103a), linked against the
-static CUDA runtime; the driver entry point for TMA tensor maps is fetched at run time, so no
-libcuda link.
+Two CUDA translation units compiled at the same time, one -gencode (sm_103a), linked against
+the static CUDA runtime; the driver entry point for TMA tensor maps is fetched at run time, so
+no libcuda link. Beside it the tensor-level calls (_fa_torch.so), a host-only module over
+libtorch: it is left out where there is no CUDA build of torch, which the library does not need.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
@@ -49,14 +51,39 @@ TORCH_DEPS = [TORCH_SRC] + [os.path.join(ROOT, "include", h) for h in ("fa_fwd.h
 TORCH_LIB = os.path.join(PKG, "_fa_torch.so")
 
 
-def torch_cmd(out: str) -> list[str]:
-    import importlib.util
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+# the torch that the module on disk was compiled against
+TORCH_STAMP = os.path.join(PKG, "_build", "torch_version")
+
+
+def torch_root() -> str | None:
+    """The folder of an installed torch that can be linked against for CUDA, or None."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    root = os.path.dirname(spec.origin)
+    return root if os.path.exists(os.path.join(root, "lib", "libtorch_cuda.so")) else None
+
+
+def torch_version(root: str) -> str:
+    """What tells one build of torch from another (its version.py, and where it lies)."""
+    path = os.path.join(root, "version.py")
+    text = open(path).read() if os.path.exists(path) else ""
+    return f"{root}\n{sys.version}\n{text}"
+
+
+def _calls_stale(root: str) -> bool:
+    if _stale(TORCH_LIB, TORCH_DEPS) or not os.path.exists(TORCH_STAMP):
+        return True
+    with open(TORCH_STAMP) as f:
+        return f.read() != torch_version(root)
+
+
+def torch_cmd(root: str, out: str) -> list[str]:
     cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
-    include = [os.path.join(ROOT, "include"), CSRC, os.path.join(torch, "include"), cuda,
+    include = [os.path.join(ROOT, "include"), CSRC, os.path.join(root, "include"), cuda,
                sysconfig.get_paths()["include"]]
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", *(x for i in include for x in ("-I", i)), TORCH_SRC,
-            "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10",
+            "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10",
             "-lc10_cuda", "-o", out]
 
 
@@ -70,11 +97,13 @@ def build(force: bool = False, verbose: bool = False, out: str = LIB, extra=()) 
 
 def build_many(targets, force: bool = False, verbose: bool = False) -> list[str]:
     """Compile each (output, extra flags) target that is stale, all nvcc runs at once, and link it;
-    with them the tensor-level calls."""
-    procs, calls = [], None
-    if force or _stale(TORCH_LIB, TORCH_DEPS):
+    with them the tensor-level calls, where torch can be linked."""
+    procs, calls, torch = [], None, torch_root()
+    if torch is None:
+        sys.stderr.write(f"no CUDA build of torch: {os.path.basename(TORCH_LIB)} (the tensor-level calls) is not built\n")
+    elif force or _calls_stale(torch):
         calls_tmp = TORCH_LIB + f".tmp{os.getpid()}"
-        calls = subprocess.Popen(torch_cmd(calls_tmp), stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
+        calls = subprocess.Popen(torch_cmd(torch, calls_tmp), stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
     for out, extra in targets:
         if force or _stale(out):
             objects = [f"{out}.{os.path.basename(src)}.tmp{os.getpid()}.o" for src in SRCS]
@@ -105,6 +134,9 @@ def build_many(targets, force: bool = False, verbose: bool = False) -> list[str]
         so, se = calls.communicate()
         if calls.returncode == 0:
             os.replace(calls_tmp, TORCH_LIB)
+            os.makedirs(os.path.dirname(TORCH_STAMP), exist_ok=True)
+            with open(TORCH_STAMP, "w") as f:
+                f.write(torch_version(torch))
         else:
             sys.stderr.write(so + se)
             failed.append(os.path.basename(TORCH_LIB))
