@@ -128,8 +128,11 @@ fa_rope rope_of(const at::Tensor& t, bool interleaved, int64_t d) {
   if (t.scalar_type() != at::kFloat) bad_type("rope must be float32");
   if (t.dim() != 2 || !t.is_contiguous() || t.size(1) % 16 || t.size(1) > d)
     bad_value("rope must be a contiguous [length, rot_dim] table, rot_dim a multiple of 16 up to d");
-  return fa_rope{static_cast<const float*>(t.data_ptr()), as_int(t.size(0), "the table's length"), (int)t.size(1),
-                 interleaved};
+  // torch has no address for a table without rows, and a null pointer would mean no rotation: this
+  // one is never read, for no position lies below a length of 0
+  alignas(16) static const float no_rows[4] = {};
+  return fa_rope{t.numel() ? static_cast<const float*>(t.data_ptr()) : no_rows,
+                 as_int(t.size(0), "the table's length"), (int)t.size(1), interleaved};
 }
 
 // fa_paged_kv of [num_pages, Hkv, page_size, d] tensors with the same strides

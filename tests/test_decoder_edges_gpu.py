@@ -128,6 +128,30 @@ def test_padding_rows_add_nothing_to_the_weights_gradients(fa, d, Hq, Hk, eps):
             assert torch.equal(x[:, good], y[:, good]) and (x[:, ~good] == 7).all()
 
 
+def test_a_table_without_rows_is_a_table(fa):
+    """Every position is outside of it: reported, nothing written; no unrotated results."""
+    empty = torch.zeros(0, 64, device="cuda")
+    q, w = torch.randn(1, 3, 2, 64).half().cuda(), torch.ones(64).half().cuda()
+    pos = torch.zeros(1, 3, dtype=torch.int32, device="cuda")
+    out = [torch.full_like(q, 7.0) for _ in range(2)]
+    fa.qk_norm_rope(q, q, w, w, empty, pos, q_out=out[0], k_out=out[1])
+    assert fa.fa_last_status() == fa.FA_ERR_RANGE
+    fa.fa_clear_status()
+    grads = fa.qk_norm_rope_backward(q, q, q, q, w, w, empty, pos, dq=out[0], dk=out[1])
+    assert fa.fa_last_status() == fa.FA_ERR_RANGE
+    fa.fa_clear_status()
+    assert all((x == 7).all() for x in out) and not grads[2].any() and not grads[3].any()
+    b = lib.Batch([1, 2], [5, 20], 2, 64, 16, torch.float16, fill=5.0)
+    k, before = b.rows(2), b.k_pages.clone()
+    fa.paged_append(k, k, b.k_pages, b.v_pages, b.block_table, b.cu_seqlens, b.seq_lens, rope=empty)
+    assert fa.fa_last_status() == fa.FA_ERR_RANGE
+    fa.fa_clear_status()
+    assert torch.equal(b.k_pages, before)
+    none = q[:, :0]
+    fa.qk_norm_rope(none, none, w, w, empty, pos[:, :0])  # no tokens: nothing to report
+    assert fa.fa_last_status() == 0
+
+
 # ---------------------------------------------------------- elements that the rotation leaves out
 SPECIAL = [math.inf, -math.inf, math.nan, -0.0, 0.0, 65504.0, -1.0]
 
