@@ -404,7 +404,7 @@ def qk_norm_rope(q, k, wq, wk, rope=None, positions=None, eps: float = 1e-6, int
     q [B, N, Hq, d] and k [B, N, Hk, d] (fp16/bf16, d 64 or 128), any strides with adjacent row
     elements, so views of a fused projection serve; wq, wk [d] of the same dtype; rope: fp32
     [length, rot_dim] table (cosines, then sines; see include/fa_decoder.h), None: no rotation;
-    positions: int32 [B, N], None: 0 .. N-1. Returns (q_out, k_out), allocated as contiguous
+    positions: int32 [B, N], None: 0 .. N-1 (refused if the table has fewer rows). Returns (q_out, k_out), allocated as contiguous
     [B, N, H, d] unless given (transposed views, and q and k themselves, are allowed).
     Launches on `stream` (a torch.cuda.Stream, default: the current one); what it allocates
     belongs to that stream.

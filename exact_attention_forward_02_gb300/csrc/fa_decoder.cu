@@ -125,6 +125,8 @@ int norm_rope_args(const fa_heads* const* sets, int n, int B, int N, int d, cons
     if (sets[i]->H != (i & 1 ? Hk : Hq)) return FA_ERR_SHAPE;
   if (Hq < 0 || Hk < 0 || (long long)Hq + Hk > 0x7fffffffLL) return FA_ERR_SHAPE;
   if (B == 0 || N == 0 || Hq + Hk == 0) { *noop = true; return FA_OK; }
+  // token n without a position of its own takes row n of the table
+  if (rope && rope->table && rope->rot_dim && !positions && N > rope->length) return FA_ERR_RANGE;
   const long long tokens = (long long)B * N;
   if (tokens > 0x7fffffffLL || tokens * ((long long)Hq + Hk) > 0x7fffffffLL) return FA_ERR_SHAPE;
   for (int i = 0; i < n; ++i)

@@ -64,7 +64,8 @@ typedef struct {
  *                 and its pointers are not looked at)
  *   q_out, k_out  outputs; may be the same memory as the inputs with the same strides (in place)
  *   wq, wk        [d] weights, `dtype`, 16-byte aligned
- *   positions     int32 [B, N] rows of the table, or NULL for position n of row n
+ *   positions     int32 [B, N] rows of the table, or NULL for position n of row n (the table then
+ *                 has at least N rows, or the call is refused with FA_ERR_RANGE)
  *   d 64 or 128; eps >= 0 and finite
  * Sums and products are fp32, rounded once. A position outside the table records FA_ERR_RANGE in
  * the status word; that token's outputs are left as they were. One kernel. B, N == 0: no-op.

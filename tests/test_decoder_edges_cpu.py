@@ -5,6 +5,7 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 import exact_attention_forward_02_gb300 as fa
 
@@ -77,3 +78,36 @@ open({str(version)!r}, "w").write("__version__ = '2'")
 assert b._calls_stale(root)
 """, bare)
     assert r.returncode == 0, r.stderr
+
+
+P = 1 << 20  # 16-byte aligned, not null, never touched
+
+
+def heads(H=4, token=256, head=64):
+    return fa.fa_heads(P, 0, token, head, H)
+
+
+def test_a_table_shorter_than_the_tokens_is_refused_without_positions():
+    def norm(N, length, positions, rot=64, B=1):
+        return fa.fa_qk_norm_rope(heads(), heads(), heads(), heads(), B, N, 64, P, P, 1e-6,
+                                  fa.fa_rope(P, length, rot, 0), positions, fa.FA_F16, None)
+
+    def backward(N, length, positions):
+        return fa.fa_qk_norm_rope_bwd(*(heads() for _ in range(6)), P, P, 1, N, 64, P, P, 1e-6,
+                                      fa.fa_rope(P, length, 64, 0), positions, fa.FA_F16, P, 1 << 30, None)
+
+    for call in (norm, backward):
+        assert call(9, 8, None) == fa.FA_ERR_RANGE
+        assert call(1, 0, None) == fa.FA_ERR_RANGE
+    assert norm(0, 0, None) == fa.FA_OK and norm(9, 8, None, B=0) == fa.FA_OK
+
+
+def test_a_table_as_long_as_the_tokens_is_not_refused():
+    if torch.cuda.is_available():
+        pytest.skip("a GPU would be given the pointers of this test")
+    for args in (dict(N=8, length=8, positions=None), dict(N=9, length=8, positions=P),
+                 dict(N=9, length=8, positions=None, rot=0)):
+        rot = args.pop("rot", 64)
+        rc = fa.fa_qk_norm_rope(heads(), heads(), heads(), heads(), 1, args["N"], 64, P, P, 1e-6,
+                                fa.fa_rope(P, args["length"], rot, 0), args["positions"], fa.FA_F16, None)
+        assert rc in (fa.FA_ERR_CUDA, fa.FA_ERR_DEVICE)  # past the checks, and no device here

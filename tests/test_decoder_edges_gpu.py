@@ -128,6 +128,18 @@ def test_padding_rows_add_nothing_to_the_weights_gradients(fa, d, Hq, Hk, eps):
             assert torch.equal(x[:, good], y[:, good]) and (x[:, ~good] == 7).all()
 
 
+def test_more_tokens_than_the_table_has_rows_are_refused(fa):
+    """Without positions token n takes row n: the host knows that some have none."""
+    q, w = torch.randn(2, 9, 2, 64).half().cuda(), torch.ones(64).half().cuda()
+    table = lib.rope_table(8, 64).cuda()
+    for call in (lambda: fa.qk_norm_rope(q, q, w, w, table), lambda: fa.qk_norm_rope_backward(q, q, q, q, w, w, table)):
+        with pytest.raises(fa.FAError) as e:
+            call()
+        assert e.value.code == fa.FA_ERR_RANGE
+    fa.qk_norm_rope(q[:, :8], q[:, :8], w, w, table)
+    assert fa.fa_last_status() == 0
+
+
 def test_a_table_without_rows_is_a_table(fa):
     """Every position is outside of it: reported, nothing written; no unrotated results."""
     empty = torch.zeros(0, 64, device="cuda")
