@@ -341,7 +341,7 @@ int fa_paged_append(const fa_paged_kv* kv, const fa_heads* k, const fa_heads* v,
   p.chunk = r.chunk;
   p.n_chunks = r.n_chunks;
   p.units = r.units;
-  const unsigned grid = (p.units - 1) / ROW_WARPS + 1;
+  const unsigned grid = (p.units - 1) / ROW_WARPS + 2;  // the last block looks over cu_seqlens
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return by_type(dtype, rope, kv->d, [&](auto bf, auto inter, auto full) {
     return launch_dependent(

@@ -369,8 +369,13 @@ struct AppendParams {
   int* status;
 };
 
+// A sequence's rows lie within the T that there are (the attention passes over the others as well).
+__device__ __forceinline__ bool rows_fit(const AppendParams& p, int begin, int end) {
+  return begin >= 0 && end >= begin && end <= p.T;
+}
+
 // The sequence whose new tokens hold row t (cu[b] <= t < cu[b+1]), or -1; the warp's 32 lanes
-// look at 32 places at a time. cu has B + 1 entries that do not decrease.
+// look at 32 places at a time. cu has B + 1 entries that do not decrease (if they do: any sequence, or -1).
 __device__ __forceinline__ int find_sequence(const int* cu, int B, int t, int lane) {
   int lo = 0, n = B + 1;  // the answer + 1 = number of entries <= t, all of them in [0, lo + n)
   while (n > 0) {
@@ -393,6 +398,15 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) fa_paged_append_kernel(const _
   constexpr int LPR = D / 8, GPW = 32 / LPR;
   const int lane = threadIdx.x & 31, sub = lane / LPR;
   const uint32_t unit = blockIdx.x * ROW_WARPS + (threadIdx.x >> 5);
+  if (blockIdx.x == gridDim.x - 1) {  // looks over the offsets; the others skip what does not fit them
+    launch_dependents();
+    wait_previous_grid();
+    bool bad = false;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < p.B; i += ROW_THREADS) bad |= !rows_fit(p, p.cu[i], p.cu[i + 1]);
+    if (bad) atomicCAS(p.status, 0, FA_ERR_RANGE);
+    return;
+  }
   if (unit >= p.units) return;
   const uint32_t tg = unit / (uint32_t)p.n_chunks;
   const int c = (int)(unit - tg * p.n_chunks), t0 = (int)(tg * GPW), t = t0 + sub;
@@ -408,7 +422,11 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) fa_paged_append_kernel(const _
   }
   int pos = 0, page = -1;
   if (b >= 0) {
-    pos = p.lens[b] - (p.cu[b + 1] - t);
+    const int begin = p.cu[b], end = p.cu[b + 1];
+    pos = p.lens[b] - (end - t);
+    if (!rows_fit(p, begin, end) || t < begin || t >= end) b = -1;
+  }
+  if (b >= 0) {
     const bool in = pos >= 0 && pos / p.page_size < p.table_stride && (!p.rope.rot || pos < p.rope.length);
     if (in) page = p.table[(size_t)b * p.table_stride + pos / p.page_size];
     if (page < 0 || page >= p.num_pages) {

@@ -92,11 +92,13 @@ int fa_qk_norm_rope_bwd(const fa_heads* dq_out, const fa_heads* dk_out, const fa
  * their positions (no rotation without a table: a plain copy).
  *   kv      the cache; kv->d 64 or 128
  *   k, v    [T, Hkv] rows of d elements (batch_stride unused), dtype as the cache
- *   B, T    sequences, and token rows behind k and v (cu_seqlens never reads past T)
+ *   B, T    sequences, and token rows behind k and v
  * Two new tokens never share a slot as long as no page stands twice in the tables of sequences
  * that are being written. A token whose position is negative, past the table's width or the
  * rotation table, or whose page is not in [0, num_pages) is skipped and FA_ERR_RANGE recorded in
- * the status word. One kernel. B or T == 0: no-op. */
+ * the status word. So is a sequence whose rows do not lie in [0, T]; where cu_seqlens decreases, other
+ * sequences' tokens may be skipped with it, and nothing is written but a sequence's own tokens in
+ * their own places. One kernel. B or T == 0: no-op. */
 int fa_paged_append(const fa_paged_kv* kv, const fa_heads* k, const fa_heads* v, int B, int T,
                     const int* cu_seqlens, const int* seq_lens, const int* block_table,
                     int table_stride, const fa_rope* rope, fa_dtype dtype, void* stream);

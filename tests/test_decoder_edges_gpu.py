@@ -203,3 +203,53 @@ def test_gradients_behind_the_rotation_stay_in_their_places(fa, interleaved):
     got = fa.qk_norm_rope_backward(g, none, x, none, w, w, table, interleaved=interleaved)[2]
     keep = torch.arange(d) != 41
     assert not torch.isfinite(got[41]) and torch.equal(got[keep], clean[keep])
+
+
+# ------------------------------------------------------------------------- rows of no sequence
+@pytest.mark.parametrize("cu,fine", [
+    ([0, 2, 5, 9], (0, 1)), ([-1, 2, 5, 7], (1, 2)), ([0, 9, 9, 9], ()), ([-5, -2, 0, 7], (2,)),
+    ([0, 2, 5, 7], (0, 1, 2)),
+    # decreasing
+    ([0, -4, 5, 7], (2,)), ([0, 5, 2, 7], (0, 2)), ([0, 2, 8, 7], (0,)), ([3, 2, 5, 7], (1, 2)), ([7, 5, 2, 0], ())])
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_passes_over_rows_outside_the_packed_tokens(fa, cu, fine, d):
+    """cu_seqlens that leave [0, T] or decrease: as in the attention such a sequence is passed over and
+    reported. Nothing is written but a sequence's own tokens in their own places; where no offset
+    decreases, all of the others' are."""
+    b = lib.Batch([2, 3, 2], [40, 300, 9], 2, d, 16, torch.float16, fill=5.0, wide=25)
+    b.block_table[b.block_table < 0] = b.k_pages.shape[0] - 1  # entries behind a sequence: nobody's page
+    k, was = b.rows(2), (b.k_pages.clone(), b.v_pages.clone())
+    b.cu_seqlens.copy_(torch.tensor(cu, dtype=torch.int32))
+    fa.paged_append(k, k, b.k_pages, b.v_pages, b.block_table, b.cu_seqlens, b.seq_lens)
+    assert fa.fa_last_status() == (0 if len(fine) == 3 else fa.FA_ERR_RANGE)
+    fa.fa_clear_status()
+    for pages, before in zip((b.k_pages, b.v_pages), was):
+        full = before.clone()
+        for i in fine:
+            for t in range(cu[i], cu[i + 1]):
+                pos = b.total[i] - (cu[i + 1] - t)
+                full[b.block_table[i, pos // 16].long(), :, pos % 16] = k[t]
+        if cu == sorted(cu):
+            assert torch.equal(pages, full)
+        assert ((pages == before) | (pages == full)).all()
+
+
+def test_append_finds_a_bad_offset_among_many(fa):
+    """The offsets of 3000 sequences, one of them past the rows."""
+    new = [1] * 3000
+    b = lib.Batch(new, [1 + i % 20 for i in range(3000)], 1, 64, 16, torch.float16, fill=5.0)
+    k = b.rows(1)
+    for at in (0, 1500, 3000):
+        before, good = b.k_pages.clone(), b.cu_seqlens.clone()
+        b.cu_seqlens[at] = 3001
+        fa.paged_append(k, k, b.k_pages, b.v_pages, b.block_table, b.cu_seqlens, b.seq_lens)
+        assert fa.fa_last_status() == fa.FA_ERR_RANGE
+        fa.fa_clear_status()
+        full = before.clone()
+        at_pos = torch.tensor(b.total, device="cuda") - 1
+        full[b.block_table.long().gather(1, (at_pos // 16)[:, None])[:, 0], :, at_pos % 16] = k
+        assert ((b.k_pages == before) | (b.k_pages == full)).all()
+        b.cu_seqlens.copy_(good)
+        fa.paged_append(k, k, b.k_pages, b.v_pages, b.block_table, b.cu_seqlens, b.seq_lens)
+        assert fa.fa_last_status() == 0 and torch.equal(b.k_pages, full)
+        b.k_pages.copy_(before)
