@@ -417,6 +417,8 @@ int fa_fwd_paged(const fa_paged_kv* kv, const fa_heads* q, const fa_heads* O, fl
     p.records = static_cast<int*>(workspace);
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + paged_records_bytes(sms));
     p.parts_len = (long long)((workspace_bytes - paged_records_bytes(sms)) / sizeof(float));
+    const long long most = fa_host::debug_part_cap();
+    if (most >= 0 && most < p.parts_len) p.parts_len = most;
   }
   const bool bf16 = dtype == FA_BF16;
   CUtensorMap mq, mk, mv;

@@ -608,6 +608,8 @@ int launched(cudaError_t e) {
 
 unsigned long long wait_limit_ns() { return ::wait_limit_ns(); }
 
+long long debug_part_cap() { return g_debug_part_cap.load(); }
+
 EncodeTiledFn encode_tiled() { return get_encode_fn(); }
 
 }  // namespace fa_host

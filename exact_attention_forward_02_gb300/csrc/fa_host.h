@@ -14,6 +14,8 @@ __attribute__((visibility("hidden"))) int status_word(int** out);
 // Counts a launch and turns its outcome into a status code.
 __attribute__((visibility("hidden"))) int launched(cudaError_t e);
 __attribute__((visibility("hidden"))) unsigned long long wait_limit_ns();
+// The cut of fa_debug_cap_workspace in floats, or -1 (always, in release builds).
+__attribute__((visibility("hidden"))) long long debug_part_cap();
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
                                   CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,

@@ -91,7 +91,9 @@ struct Params {
 };
 
 // Debug builds (FA_DEBUG) check the places of tile copies, partial states and output rows; one
-// outside records FA_ERR_BOUNDS and what it guards is skipped. Release builds compile it out.
+// outside records FA_ERR_BOUNDS. Stores, and the join of an item whose pieces it concerns, are then
+// skipped; a tile copy is only recorded (TMA reads zeros outside, and its barrier expects the bytes).
+// Release builds compile it out.
 __device__ __forceinline__ bool in_bounds(const Params& p, bool ok) {
 #ifdef FA_DEBUG
   if (!ok) atomicCAS(p.status, 0, FA_ERR_BOUNDS);
@@ -872,10 +874,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const Item* item = item_next();
       if (!(ok = item != nullptr) || item->n == 0) break;
       const int tok = row_tok + (SPLIT ? 0 : g * p.tpt);  // token of this row in the item
-      const bool valid =
-          row_used && tok < item->nt &&
-          in_bounds(p, item->tok0 + tok < p.T && item->h * p.G + row_head < p.o.H &&
-                           (p.whole || (blockIdx.x * 2 + item->slot + 1ll) * part_floats(D, ROWS) <= p.parts_len));
+      // may a row of the item be stored, as output or in the block's partial state?
+      auto storable = [&](int token, int head) {
+        return in_bounds(p, item->tok0 >= 0 && item->tok0 + token < p.T && item->h * p.G + head < p.o.H &&
+                                (item->n == item->ntot ||
+                                 (blockIdx.x * 2 + item->slot + 1ll) * part_floats(D, ROWS) <= p.parts_len));
+      };
+      const bool valid = row_used && tok < item->nt && storable(tok, row_head);
       if (!SPLIT && g == 1 && item->nt <= p.tpt) {
         item_done();
         continue;
@@ -1127,6 +1132,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll 1
           for (int x = threadIdx.x; x < R * (COLS / 4); x += 256) {
             const int rr = x / (COLS / 4), c4 = x % (COLS / 4);
+            const int rt = token_of_row(p, rr);
+            if (!storable(rt, rr - rt * p.G)) continue;
             float sum[4] = {};
 #pragma unroll
             for (int a = 0; a < 2 * REP; ++a) {
@@ -1139,7 +1146,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (partial) {
               *reinterpret_cast<float4*>(part + (size_t)rr * D + col) = make_float4(sum[0], sum[1], sum[2], sum[3]);
             } else {
-              const int rt = token_of_row(p, rr);
               uint16_t* dst = p.o.ptr + (long long)(item->tok0 + rt) * p.o.ts +
                               (long long)(item->h * p.G + rr - rt * p.G) * p.o.hs + col;
               *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(sum[0], sum[1]), pack2<BF16>(sum[2], sum[3]));
@@ -1178,6 +1184,10 @@ __global__ void __launch_bounds__(COMBINE_THREADS, 4) fa_paged_combine_kernel(co
   if (rec0.x == 0) return;
   const int c0 = blockIdx.x, slot0 = rec0.y, n = rec0.z - c0 + 1, h = rec0.w, tok0 = rec1.x, nt = rec1.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, Hq = p.Hkv * p.G;
+  if (!in_bounds(p, n > 1 && rec0.z < (int)gridDim.x && (c0 * 2 + slot0 + 1ll) * part_floats(D, ROWS) <= p.parts_len &&
+                        (rec0.z * 2 + 1ll) * part_floats(D, ROWS) <= p.parts_len && tok0 >= 0 && tok0 + nt <= p.T &&
+                        (h + 1) * p.G <= p.o.H))
+    return;
   auto part = [&](int x) {  // piece x of the item
     return p.parts + (size_t)((c0 + x) * 2 + (x == 0 ? slot0 : 0)) * part_floats(D, ROWS);
   };

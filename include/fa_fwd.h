@@ -306,9 +306,9 @@ unsigned long long fa_get_wait_limit_us(void);
 
 /* fa_debug_cap_workspace -- test hook of the range-checked build (compiled with FA_DEBUG,
  * libfa_debug.so), which checks every stream-K workspace access and every TMA tile
- * coordinate on the device and records FA_ERR_BOUNDS for one outside its range (the access
- * is skipped, or for a load only recorded). In that build, later fa_fwd_ws launches tell the
- * kernel that the partial-state area holds at most `part_elems` floats, so that the checks
+ * coordinate on the device (and those of fa_fwd_paged, with its output rows) and records
+ * FA_ERR_BOUNDS for one outside its range (the access is skipped, or for a load only
+ * recorded). In that build, later fa_fwd_ws and fa_fwd_paged launches tell the kernel that the partial-state area holds at most `part_elems` floats, so that the checks
  * fire while every access still lies inside the real workspace; a negative value removes
  * the cut. Returns 1 in the range-checked build; the release build ignores the call and
  * returns 0. No CUDA call is made. */
