@@ -407,7 +407,8 @@ def qk_norm_rope(q, k, wq, wk, rope=None, positions=None, eps: float = 1e-6, int
     positions: int32 [B, N], None: 0 .. N-1 (refused if the table has fewer rows). Returns (q_out, k_out), allocated as contiguous
     [B, N, H, d] unless given (transposed views, and q and k themselves, are allowed).
     Launches on `stream` (a torch.cuda.Stream, default: the current one); what it allocates
-    belongs to that stream.
+    belongs to that stream. Not recorded by autograd: in grad mode, inputs that require a gradient
+    are refused (qk_norm_rope_backward computes the gradients).
     """
     r = _calls().norm_rope(q, k, wq, wk, rope, positions, eps, interleaved, q_out, k_out, stream)
     if type(r) is int:
@@ -435,7 +436,8 @@ def paged_append(k, v, k_pages, v_pages, block_table, cu_seqlens, seq_lens, rope
     k, v [T, Hkv, d]; k_pages, v_pages [num_pages, Hkv, page_size, d] with the same strides (a
     transposed view of [num_pages, page_size, Hkv, d] serves); block_table [B, pages], cu_seqlens
     [B + 1] and seq_lens [B] int32: sequence b's new tokens are rows cu_seqlens[b] ..
-    cu_seqlens[b+1]-1, the last of its seq_lens[b] positions (see include/fa_decoder.h).
+    cu_seqlens[b+1]-1, the last of its seq_lens[b] positions (see include/fa_decoder.h). In grad
+    mode, tensors that require a gradient are refused.
     """
     r = _calls().append(k, v, k_pages, v_pages, block_table, cu_seqlens, seq_lens, rope, interleaved, stream)
     if r != 0:
@@ -450,7 +452,8 @@ def attention_paged(q, k_pages, v_pages, block_table, cu_seqlens, seq_lens, max_
     max_q: the most new tokens of a sequence (chooses the kernel). O like q and L [T, Hq] fp32
     are allocated unless given; rows that belong to no sequence are left as they were (in the
     tensors allocated here: uninitialised). `workspace`: a uint8 tensor of at least
-    fa_fwd_paged_workspace_bytes(...) bytes, allocated for the call when None.
+    fa_fwd_paged_workspace_bytes(...) bytes, allocated for the call when None. In grad mode, tensors
+    that require a gradient are refused.
     """
     r = _calls().attend(q, k_pages, v_pages, block_table, cu_seqlens, seq_lens, max_q, causal, scale, out, lse,
                         workspace, stream)

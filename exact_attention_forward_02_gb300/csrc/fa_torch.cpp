@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/as_strided.h>
 #include <ATen/ops/zeros.h>
@@ -20,6 +21,7 @@
 #include <optional>
 #include <stdexcept>
 #include <string>
+#include <utility>
 
 #include "fa_decoder.h"
 
@@ -152,6 +154,15 @@ fa_paged_kv cache_of(const at::Tensor& k, const at::Tensor& v, const at::Tensor&
                      as_int(k.size(3), "the head dimension")};
 }
 
+// Nothing here is recorded by autograd: an input that requires a gradient would lose it unseen.
+void not_recorded(std::initializer_list<std::pair<const at::Tensor*, const char*>> inputs) {
+  if (!at::GradMode::is_enabled()) return;
+  for (const auto& [t, what] : inputs)
+    if (t->requires_grad())
+      bad_value(std::string(what) + " requires grad and the call is not recorded by autograd: make it under "
+                                    "torch.no_grad(), or pass the tensor detached");
+}
+
 // The device and stream of a call: what is allocated inside belongs to that stream.
 struct Launch {
   c10::cuda::CUDAGuard device;
@@ -255,6 +266,7 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (qo.defined()) oq = heads_of(qo, "q_out", q, q.sizes(), true);
     if (ko.defined()) ok = heads_of(ko, "k_out", q, k.sizes(), true);
     OneDevice(q).also(k).also(wq).also(wk).also(table).also(pos).also(qo).also(ko);
+    not_recorded({{&q, "q"}, {&k, "k"}, {&wq, "wq"}, {&wk, "wk"}});
     Launch on(q, a[10]);
     if (!qo.defined()) oq = heads_of(qo = rows_like(q), "q_out", q);
     if (!ko.defined()) ok = heads_of(ko = rows_like(k), "k_out", q);
@@ -332,6 +344,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Batch batch(table, cu, lens);
     const fa_rope rp = rope_of(rope, PyObject_IsTrue(a[8]) == 1, k.size(2));
     OneDevice(k).also(v).also(kp).also(vp).also(table).also(cu).also(lens).also(rope);
+    not_recorded({{&k, "k"}, {&v, "v"}, {&kp, "k_pages"}, {&vp, "v_pages"}});
     Launch on(k, a[9]);
     const int rc = lib.append(&kv, &hk, &hv, batch.B, as_int(k.size(0), "T"), batch.cu, batch.lens, batch.table,
                               batch.width, &rp, dt, on.stream);
@@ -365,6 +378,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (ws.defined() && (ws.scalar_type() != at::kByte || !ws.is_contiguous()))
       bad_value("workspace must be a contiguous uint8 tensor");
     OneDevice(q).also(kp).also(vp).also(table).also(cu).also(lens).also(out).also(lse).also(ws);
+    not_recorded({{&q, "q"}, {&kp, "k_pages"}, {&vp, "v_pages"}});
     Launch on(q, a[12]);
     if (!out.defined()) ho = heads_of(out = rows_like(q), "out", q);
     if (!lse.defined()) lse = fresh(q, {T, hq.H}, at::kFloat);

@@ -253,3 +253,27 @@ def test_append_finds_a_bad_offset_among_many(fa):
         fa.paged_append(k, k, b.k_pages, b.v_pages, b.block_table, b.cu_seqlens, b.seq_lens)
         assert fa.fa_last_status() == 0 and torch.equal(b.k_pages, full)
         b.k_pages.copy_(before)
+
+
+# ---------------------------------------------------------------------- the manner of the calls
+def test_inputs_that_require_gradients_are_refused_where_they_would_be_lost(fa):
+    """The calls are not recorded by autograd: an input that requires a gradient must come without
+    grad mode (or detached), so that its gradient is not lost unseen."""
+    q, w = torch.randn(1, 3, 2, 64).half().cuda(), torch.ones(64).half().cuda()
+    b = lib.Batch([2, 1], [20, 3], 2, 64, 16, torch.float16)
+    rows = b.rows(4)
+    table = (b.block_table, b.cu_seqlens, b.seq_lens)
+    calls = [lambda x: fa.qk_norm_rope(x(q), q, w, w), lambda x: fa.qk_norm_rope(q, q, w, x(w)),
+             lambda x: fa.attention_paged(x(rows), b.k_pages, b.v_pages, *table, 2),
+             lambda x: fa.attention_paged(rows, b.k_pages, x(b.v_pages), *table, 2),
+             lambda x: fa.paged_append(x(rows[:, :2]), rows[:, :2], b.k_pages, b.v_pages, *table)]
+    for call in calls:
+        with pytest.raises(ValueError, match="grad"):
+            call(lambda t: t.detach().clone().requires_grad_())
+        call(lambda t: t)
+        with torch.no_grad():
+            call(lambda t: t.detach().requires_grad_())
+        with torch.inference_mode():
+            call(lambda t: t)
+    leaf = w.clone().requires_grad_()   # gradients from the call that computes them
+    assert fa.qk_norm_rope_backward(q, q, q, q, leaf, leaf)[2].shape == (64,)
