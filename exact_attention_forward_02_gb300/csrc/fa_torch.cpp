@@ -79,6 +79,15 @@ float as_float(PyObject* o, const char* what) {
   return (float)x;
 }
 
+bool as_bool(PyObject* o, const char* what) {
+  const int x = PyObject_IsTrue(o);
+  if (x < 0) {
+    PyErr_Clear();
+    bad_type(std::string(what) + " must be a truth value");
+  }
+  return x;
+}
+
 fa_dtype type_code(const at::Tensor& t, const char* what) {
   if (t.scalar_type() == at::kBFloat16) return FA_BF16;
   if (t.scalar_type() == at::kHalf) return FA_F16;
@@ -259,7 +268,7 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check_qk(q, k, wq, wk);
     const int B = as_int(q.size(0), "B"), N = as_int(q.size(1), "N"), d = as_int(q.size(3), "d");
     const fa_heads hq = heads_of(q, "q", q), hk = heads_of(k, "k", q);
-    const fa_rope rp = rope_of(table, PyObject_IsTrue(a[7]) == 1, d);
+    const fa_rope rp = rope_of(table, as_bool(a[7], "interleaved"), d);
     const int* positions = pos.defined() ? index_of(pos, "positions", {B, N}) : nullptr;
     const float eps = as_float(a[6], "eps");
     fa_heads oq{}, ok{};
@@ -288,7 +297,7 @@ PyObject* norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int B = as_int(q.size(0), "B"), N = as_int(q.size(1), "N"), d = as_int(q.size(3), "d");
     const fa_heads hq = heads_of(q, "q", q), hk = heads_of(k, "k", q);
     const fa_heads hgq = heads_of(gq, "dq_out", q, q.sizes()), hgk = heads_of(gk, "dk_out", q, k.sizes());
-    const fa_rope rp = rope_of(table, PyObject_IsTrue(a[9]) == 1, d);
+    const fa_rope rp = rope_of(table, as_bool(a[9], "interleaved"), d);
     const int* positions = pos.defined() ? index_of(pos, "positions", {B, N}) : nullptr;
     const float eps = as_float(a[8], "eps");
     fa_heads oq{}, ok{};
@@ -342,7 +351,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     for (int i = 0; i < 3; ++i)
       if (kp.size(i) > 1 && kp.stride(i) == 0) bad_value("the rows of the cache must not overlap");
     const Batch batch(table, cu, lens);
-    const fa_rope rp = rope_of(rope, PyObject_IsTrue(a[8]) == 1, k.size(2));
+    const fa_rope rp = rope_of(rope, as_bool(a[8], "interleaved"), k.size(2));
     OneDevice(k).also(v).also(kp).also(vp).also(table).also(cu).also(lens).also(rope);
     not_recorded({{&k, "k"}, {&v, "v"}, {&kp, "k_pages"}, {&vp, "v_pages"}});
     Launch on(k, a[9]);
@@ -368,7 +377,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (kv.d != q.size(2)) bad_value("the cache must have q's head dimension");
     const Batch batch(table, cu, lens);
     const int max_q = as_int(a[6], "max_q");
-    const int causal = PyObject_IsTrue(a[7]);
+    const bool causal = as_bool(a[7], "causal");
     const float scale = a[8] == Py_None ? (float)(1.0 / std::sqrt((double)kv.d)) : as_float(a[8], "scale");
     fa_heads ho{};
     if (out.defined()) ho = heads_of(out, "out", q, q.sizes(), true);

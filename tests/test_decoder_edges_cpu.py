@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import exact_attention_forward_02_gb300 as fa
+from tests import decoder_testlib as lib
 
 
 def _run(code, cwd):
@@ -111,3 +112,17 @@ def test_a_table_as_long_as_the_tokens_is_not_refused():
         rc = fa.fa_qk_norm_rope(heads(), heads(), heads(), heads(), 1, args["N"], 64, P, P, 1e-6,
                                 fa.fa_rope(P, args["length"], rot, 0), args["positions"], fa.FA_F16, None)
         assert rc in (fa.FA_ERR_CUDA, fa.FA_ERR_DEVICE)  # past the checks, and no device here
+
+
+def test_flags_that_have_no_truth_value_are_refused():
+    """An argument whose bool() raises: a TypeError, before anything else is looked at."""
+    b = lib.Batch([2, 1], [20, 3], 2, 64, 16, torch.float16, device="cpu", fill=0.0)
+    q, k = b.rows(4, device="cpu"), b.rows(2, device="cpu")
+    table, two = (b.block_table, b.cu_seqlens, b.seq_lens), torch.zeros(2)
+    x, w = torch.zeros(1, 5, 2, 64).half(), torch.zeros(64).half()
+    for call in (lambda: fa.attention_paged(q, b.k_pages, b.v_pages, *table, 2, causal=two),
+                 lambda: fa.paged_append(k, k, b.k_pages, b.v_pages, *table, interleaved=two),
+                 lambda: fa.qk_norm_rope(x, x, w, w, interleaved=two),
+                 lambda: fa.qk_norm_rope_backward(x, x, x, x, w, w, interleaved=two)):
+        with pytest.raises(TypeError, match="truth value"):
+            call()
