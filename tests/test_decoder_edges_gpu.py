@@ -277,3 +277,18 @@ def test_inputs_that_require_gradients_are_refused_where_they_would_be_lost(fa):
             call(lambda t: t)
     leaf = w.clone().requires_grad_()   # gradients from the call that computes them
     assert fa.qk_norm_rope_backward(q, q, q, q, leaf, leaf)[2].shape == (64,)
+
+
+def test_an_allocation_that_fails_raises_torch_s_own_error(fa):
+    """Out of memory is torch.cuda.OutOfMemoryError, which a server catches."""
+    q, w = torch.randn(1, 1, 8, 128).half().cuda(), torch.ones(128).half().cuda()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (64 << 20)) / total)
+    try:
+        big = q.expand(1, 1 << 18, 8, 128)  # 512 MB of outputs
+        with pytest.raises(torch.cuda.OutOfMemoryError):
+            fa.qk_norm_rope(big, big, w, w)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert fa.qk_norm_rope(q, q, w, w)[0].shape == q.shape
