@@ -48,6 +48,9 @@ int check_kv(const fa_paged_kv* kv) {
   return FA_OK;
 }
 
+// sequences of a batch: the kernels' searches and shares round B up in 32 bits
+constexpr int MAX_SEQUENCES = 1 << 30;
+
 HeadsDev dev(const fa_heads* h) {
   return HeadsDev{static_cast<uint16_t*>(h->ptr), h->batch_stride, h->token_stride, h->head_stride, h->H};
 }
@@ -313,7 +316,7 @@ int fa_paged_append(const fa_paged_kv* kv, const fa_heads* k, const fa_heads* v,
   if (B < 0 || T < 0 || table_stride < 0 || k->H != kv->Hkv || v->H != kv->Hkv) return FA_ERR_SHAPE;
   if ((rc = check_rope(rope, kv->d)) != FA_OK) return rc;
   if (B == 0 || T == 0 || kv->Hkv == 0) return FA_OK;
-  if ((long long)T * 2 * kv->Hkv > 0x7fffffffLL || B == 0x7fffffff) return FA_ERR_SHAPE;
+  if ((long long)T * 2 * kv->Hkv > 0x7fffffffLL || B > MAX_SEQUENCES) return FA_ERR_SHAPE;
   if ((rc = check_heads(k)) != FA_OK || (rc = check_heads(v)) != FA_OK) return rc;
   if (!cu_seqlens || !seq_lens || (!block_table && table_stride)) return FA_ERR_NULL;
   if (!aligned4(cu_seqlens) || !aligned4(seq_lens) || !aligned4(block_table)) return FA_ERR_ALIGN;
@@ -367,7 +370,7 @@ int fa_fwd_paged(const fa_paged_kv* kv, const fa_heads* q, const fa_heads* O, fl
   if (B < 0 || T < 0 || table_stride < 0 || max_q < 1 || q->H < 0 || q->H != O->H) return FA_ERR_SHAPE;
   if (!(scale >= 0.f) || !isfinite(scale)) return FA_ERR_SCALE;
   if (B == 0 || T == 0 || q->H == 0) return FA_OK;
-  if (kv->num_pages == 0 || kv->Hkv == 0 || q->H % kv->Hkv || q->H / kv->Hkv > 128 || B == 0x7fffffff ||
+  if (kv->num_pages == 0 || kv->Hkv == 0 || q->H % kv->Hkv || q->H / kv->Hkv > 128 || B > MAX_SEQUENCES ||
       (long long)T * q->H > 0x7fffffffLL)
     return FA_ERR_SHAPE;
   if ((rc = check_heads(q)) != FA_OK || (rc = check_heads(O)) != FA_OK) return rc;

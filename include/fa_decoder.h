@@ -32,7 +32,7 @@ typedef struct {
  * [pages, Hkv, page_size, d] and [pages, page_size, Hkv, d] are both such caches.
  * page_size is 8, 16, 32, 64 or a multiple of 128.
  *
- * A batch of B sequences over such a cache is given by int32 device arrays:
+ * A batch of B sequences (at most 2^30) over such a cache is given by int32 device arrays:
  *   cu_seqlens  [B + 1]  new tokens cu_seqlens[b] .. cu_seqlens[b+1]-1 of the T packed token rows
  *                        belong to sequence b (a sequence may have none); rows before the first
  *                        and behind the last sequence are neither read nor written

@@ -126,3 +126,12 @@ def test_flags_that_have_no_truth_value_are_refused():
                  lambda: fa.qk_norm_rope_backward(x, x, x, x, w, w, interleaved=two)):
         with pytest.raises(TypeError, match="truth value"):
             call()
+
+
+@pytest.mark.parametrize("B", [(1 << 30) + 1, 0x7ffffff0, 0x7ffffffe, 0x7fffffff])
+def test_more_sequences_than_the_kernels_can_count_are_refused(B):
+    """Rounding B up to whole warps' and blocks' shares would pass 32 bits on the device."""
+    kv = fa.fa_paged_kv(P, P, 16384, 1024, 64, 8, 16, 4, 64)
+    assert fa.fa_paged_append(kv, heads(), heads(), B, 8, P, P, P, 4, None, 1, None) == fa.FA_ERR_SHAPE
+    assert fa.fa_fwd_paged(kv, heads(8), heads(8), P, B, 8, 4, P, P, P, 4, 0.125, 1, 1, P, 1 << 40,
+                           None) == fa.FA_ERR_SHAPE
