@@ -61,14 +61,17 @@ RopeDev dev(const fa_rope* r) {
 
 // How the (token, head) rows are shared out: a group of d/8 lanes walks `chunk` heads of a token,
 // all of them (the token's angles and addresses are then worked out once), or fewer while the
-// tokens alone do not give the SMs enough warps to cover the memory latency.
+// tokens alone do not give the SMs enough warps to cover the memory latency: ROW_MIN_WARPS = 16 per
+// SM (1000 tokens of 32 + 8 heads, d 128, forward: 5.2 us, with 8 warps 6.5, with 32 6.1; 4000 tokens
+// 14.2, 21.9, 16.5; their gradients: 1000 tokens 12.5, 9.8, 12.2, 4000 tokens 32.3 with any of them).
 struct RowShare {
   int chunk, n_chunks;
   uint32_t units;  // warps
 };
 // `walked`: a fixed number of blocks walks the units (the backward pass). Its last round is then a
-// smaller part of the whole with more units: 95 -> 89 us for 16384 tokens of 32 + 8 heads, d = 128;
-// with fewer than 8 heads to a unit it costs more than it gives.
+// smaller part of the whole with more units: 94 -> 88 us for 16384 tokens of 32 + 8 heads, d = 128 (3
+// and 12 times ROW_MIN_WARPS instead of 6: 94 and 101), 60.4 -> 57.4 of 12 + 12; but 28.3 -> 32.3 us for
+// 4000 tokens of 32 + 8. With fewer than 8 heads to a unit it costs more than it gives.
 RowShare share_rows(long long tokens, int heads, int d, int sms, bool walked) {
   const int groups = 256 / d;  // of lanes in a warp
   const long long warps = (tokens + groups - 1) / groups;
@@ -406,7 +409,10 @@ int fa_fwd_paged(const fa_paged_kv* kv, const fa_heads* q, const fa_heads* O, fl
   p.c = scale * 1.4426950408889634f;
   p.wait_limit_ns = fa_host::wait_limit_ns();
   p.whole = whole;
-  // without units: one sequence whose key heads divide (nearly) all SMs, or whole items that fit them
+  // without units: whole items that fit the SMs at once, or one sequence whose key heads share nine
+  // tenths of them (8 heads over 1001 keys: 9.5 us against 12.0 by units, 28 over 8001, 140 SMs, 26.2
+  // against 27.5). With fewer SMs in use it may cost more, 80 heads over 8001 keys 64.7 against 58.2 us,
+  // or less: 27 heads, 135 SMs, 25.7 against 27.3, and over 1001 keys 10.5 against 12.5.
   const long long heads = (long long)B * kv->Hkv;
   if (whole) {
     const int per_item = p.tpt * (form == 0 ? 2 : 1);

@@ -28,9 +28,10 @@
 // hands the others their items through a ring in shared memory, a few ahead, so that nobody waits
 // for the lengths of the next sequence; 0-7: two softmax warpgroups, thread = row = TMEM lane):
 //   PAIR   an item is two tiles of 128 rows, one per warpgroup, over the same keys: chunks. d = 128 is
-//          bound by the tensor cores and the chain S - softmax - P V, d = 64 by the exponentials. 2048
-//          tokens at 30720, Hq 16, Hkv 2, d 128: 331 us replayed in a graph, 1.61 PFLOP/s, and 351 us
-//          called one by one; 4 x 1000 over 4097 keys, 12 heads, d 64: 76 us, 0.66 PFLOP/s.
+//          bound by the tensor cores and the chain S - softmax - P V, d = 64 by that chain, with no pipe
+//          full (exponentials 34 % of theirs, tensor cores 31 %, instruction issue 39 %). 2048 tokens
+//          at 30720, Hq 16, Hkv 2, d 128: 326 to 330 us replayed in a graph, 1.62 PFLOP/s, and 341 to
+//          354 us called one by one; 4 x 1000 over 4097 keys, 12 heads, d 64: 76 us, 0.66 PFLOP/s.
 //   SPLIT  an item is one tile; the warpgroups take the even and the odd key tiles, each with its
 //          own (m, l, O~). Its rows stand REP times in the tile (REP = 4 for up to 32 rows): copy
 //          a covers keys [a 128/REP, (a+1) 128/REP) of each key tile only, with its own (m, l, O~)
@@ -39,7 +40,7 @@
 //          drafts: bound by HBM; the tensor cores run mostly empty and still hide behind the
 //          loads (1024 cycles of products per 64 KB of keys and values, which take 2900 at this
 //          SM's share of the bandwidth). 64 sequences of 201 to 8020 keys, 8 key heads, d 128, pages
-//          of 16: 163 us, 6.45 TB/s; one sequence of 1001 keys: 9.6 us with the join, latency.
+//          of 16: 163 to 165 us, 6.4 TB/s; one sequence of 1001 keys: 9.5 us with the join, latency.
 #pragma once
 
 #include <cuda.h>
@@ -66,10 +67,13 @@ constexpr int SMEM_LIMIT = 232448;
 constexpr int MAX_SLOTS = 8;
 constexpr int COMBINE_THREADS = 256;
 constexpr int WHOLE_TILES = FA_PAGED_WHOLE_KEYS / BN;
-// units of a block at least: with fewer, more pieces of an item to join than the shorter pieces gain
-// (100 tokens over 4000 keys of one head: 25.6 us, with 1 unit 38; 1 to 8 measured on small chunks)
+// units of a block at least: with 1, more pieces of an item to join than the shorter pieces gain, with 5
+// the pieces are long (at least 1, 2, 3, 5 units: 100 tokens of 8 heads over 4000 keys of one, d 128,
+// 22.5, 20.0, 20.4, 22.3 us; three sequences of 1001 keys of 8 heads, d 128, 12.0, 11.6, 12.4, 13.9 us)
 constexpr int MIN_UNITS = 3;
-constexpr int DIRECT_TILES = 2;  // key tiles of a part at least, one for each warpgroup
+// key tiles of a part at least, one for each warpgroup (one sequence of 1001 keys: 9.5 us, with 1 tile
+// 9.7, with 3 10.7)
+constexpr int DIRECT_TILES = 2;
 
 struct Params {
   HeadsDev o;
@@ -426,6 +430,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
   static_assert(SPLIT || REP == 1, "copies of rows belong to the SPLIT form");
   using LY = Layout<D, SPLIT>;
+  // ITEM_UNITS: what an item costs by itself, in key tiles. Against it, us: REP 4, 2 units: 24 drafts, d 64,
+  // 35.8, with 1 41.6, with 4 36.6 (64 ragged single tokens, d 128: 165.0, 163.7, 166.3). REP 2, 3 units: 64
+  // sequences of 16 tokens, d 128, 57.3, with 2 57.4, with 4 56.8. REP 1, 4 units: 256 of 32 tokens, d 64,
+  // 37.7, with 2 40.2, with 6 37.3. PAIR, 2 units: 8 chunks, d 64, 36.8, with 1 37.2, with 4 38.5 (a chunk of
+  // 2048 tokens, d 128: 328, 331, 334; fresh prompts of 2000 tokens 76.0, 74.6, 78.5).
   constexpr int TPT_MUL = SPLIT ? 1 : 2, ITEM_UNITS = SPLIT ? (REP == 1 ? 4 : REP == 2 ? 3 : 2) : 2;
   constexpr int ROWS = SPLIT ? BM / REP : 2 * BM;  // rows of an item's partial state
   constexpr int CW = BN / REP;                     // keys of a tile that one row copy covers
@@ -1170,7 +1179,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // Joins the partial states of the items that lie in several blocks' ranges: blocks (c, y) take the
 // item that begins in block c's range. A warp joins RW rows at once, so that their loads overlap:
 // lane = (row, piece) for the pieces' weights, then all lanes along the columns. (With no bound on the
-// blocks the compiler saved registers by loading one piece after another: 25.8 against 20.4 us.)
+// blocks the compiler saved registers by loading one piece after another: 100 tokens of 8 heads over 4000
+// keys of one, d 128, 21.7 against 20.4 us, one sequence of 1001 keys 9.8 against 9.5.)
 // Latency bounds it for single tokens; a chunk of 2048 tokens reads 37 MB of partial states (16.5 us
 // with cold caches, 6 us for one token of one sequence).
 template <int D, bool BF16, int ROWS>

@@ -1,5 +1,8 @@
 """The decoder-block operators at the edges of what they accept."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -7,6 +10,7 @@ import torch
 from tests import decoder_testlib as lib
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -292,3 +296,33 @@ def test_an_allocation_that_fails_raises_torch_s_own_error(fa):
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
     assert fa.qk_norm_rope(q, q, w, w)[0].shape == q.shape
+
+
+def test_a_first_call_inside_a_capture():
+    """A process whose first call of each operator is captured."""
+    code = """
+import torch
+from tests import decoder_testlib as lib
+import exact_attention_forward_02_gb300 as fa
+b = lib.Batch([1, 1, 1], [3000, 900, 50], 2, 128, 16, torch.bfloat16, seed=1)
+q, k = b.rows(8), b.rows(2)
+w = torch.ones(128).bfloat16().cuda()
+table = lib.rope_table(3000, 128).cuda()
+pos = (b.seq_lens - 1)[None].contiguous()
+torch.cuda.synchronize()
+def step():
+    x, y = fa.qk_norm_rope(q[None], k[None], w, w, table, pos)
+    back = fa.qk_norm_rope_backward(x, y, q[None], k[None], w, w, table, pos)
+    fa.paged_append(y[0], k, b.k_pages, b.v_pages, b.block_table, b.cu_seqlens, b.seq_lens)
+    return (*back, *fa.attention_paged(x[0], b.k_pages, b.v_pages, b.block_table, b.cu_seqlens, b.seq_lens, 1))
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = step()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(x, y) for x, y in zip(got, step()))
+assert fa.fa_last_status() == 0
+print("captured first")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
