@@ -407,7 +407,8 @@ def qk_norm_rope(q, k, wq, wk, rope=None, positions=None, eps: float = 1e-6, int
     positions: int32 [B, N], None: 0 .. N-1 (refused if the table has fewer rows). Returns (q_out, k_out), allocated as contiguous
     [B, N, H, d] unless given (transposed views, and q and k themselves, are allowed).
     Launches on `stream` (a torch.cuda.Stream, default: the current one); what it allocates
-    belongs to that stream. Not recorded by autograd: in grad mode, inputs that require a gradient
+    belongs to that stream, and the caller keeps the inputs until that stream is past the call, as
+    with torch's own calls on another stream. Not recorded by autograd: in grad mode, inputs that require a gradient
     are refused (qk_norm_rope_backward computes the gradients).
     """
     r = _calls().norm_rope(q, k, wq, wk, rope, positions, eps, interleaved, q_out, k_out, stream)

@@ -67,7 +67,8 @@ typedef struct {
  *   positions     int32 [B, N] rows of the table, or NULL for position n of row n (the table then
  *                 has at least N rows, or the call is refused with FA_ERR_RANGE)
  *   d 64 or 128; eps >= 0 and finite
- * Sums and products are fp32, rounded once. A position outside the table records FA_ERR_RANGE in
+ * Sums and products are fp32, rounded once (so a row whose mean square passes the range of fp32 comes
+ * out as zeros, and with eps = 0 a row of zeros as NaN). A position outside the table records FA_ERR_RANGE in
  * the status word; that token's outputs are left as they were. One kernel. B, N == 0: no-op.
  *
  * fa_qk_norm_rope_bwd -- its gradients, from the same inputs and the gradients dq_out, dk_out of

@@ -326,3 +326,18 @@ print("captured first")
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
+
+
+def test_rows_past_the_range_of_the_sum_of_squares(fa):
+    """As the header says: a mean square beyond fp32 gives zeros, zeros with eps = 0 give NaN; other rows
+    are what they are without them."""
+    q = torch.randn(1, 6, 2, 64).bfloat16().cuda()
+    w, table = torch.ones(64).bfloat16().cuda(), lib.rope_table(6, 64).cuda()
+    for eps in (1e-6, 0.0):
+        want = fa.qk_norm_rope(q, q, w, w, table, eps=eps)[0]
+        x = q.clone()
+        x[0, 1], x[0, 4, 0] = 3e38, 0
+        y = fa.qk_norm_rope(x, x, w, w, table, eps=eps)[0]
+        assert not y[0, 1].any()
+        assert torch.isnan(y[0, 4, 0]).all() if eps == 0 else not y[0, 4, 0].any()
+        assert torch.equal(y[0, [0, 2, 3, 5]], want[0, [0, 2, 3, 5]]) and torch.equal(y[0, 4, 1], want[0, 4, 1])
