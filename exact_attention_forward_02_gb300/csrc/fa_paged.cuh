@@ -59,6 +59,10 @@ constexpr int NUM_WARPS = 12, NUM_THREADS = NUM_WARPS * 32;
 constexpr int WARP_LOAD = 8, WARP_MMA = 9, WARP_WALK = 10, WARP_LOAD2 = 11;
 constexpr int ITEM_SLOTS = 4;
 constexpr int ITEM_READERS = 11;  // warps that read an item: two loading, MMA, 8 softmax
+// Waits on the ring of items last as long as an item, up to thousands of key tiles, while the limit is
+// meant for a step of the pipeline: they have this many times it. (Where the pipeline stands still, one
+// of its own waits runs out first and stops these as well.)
+constexpr uint32_t ITEM_WAITS = 1024;
 // 2*128*200 + 128*104 = 64512 = 384*168 registers, the launch's budget
 constexpr uint32_t REGS_SOFTMAX = 200, REGS_OTHER = 104;
 constexpr uint32_t TMEM_COLS = 512, TMEM_S0 = 0, TMEM_O0 = 256;  // S0 | S1 | O0 | O1
@@ -166,23 +170,25 @@ struct Layout {
 
 // ----------------------------------------------------------------------------- waits
 // Bounded: a wait past the limit records FA_ERR_TIMEOUT and stops every role of the block.
-__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, const Params& p) {
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, const Params& p,
+                                          uint32_t limits) {
   const uint64_t t0 = globaltimer_ns();
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 32; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
-    if (globaltimer_ns() - t0 > p.wait_limit_ns) {
+    if (globaltimer_ns() - t0 > p.wait_limit_ns * limits) {
       atomicCAS(p.status, 0, FA_ERR_TIMEOUT);
       *abort_flag = 1;
       return false;
     }
   }
 }
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, const Params& p) {
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, const Params& p,
+                                         uint32_t limits = 1) {
   if (mbar_try_wait(bar, parity)) return true;
-  return wait_slow(bar, parity, abort_flag, p);
+  return wait_slow(bar, parity, abort_flag, p, limits);
 }
 // on the way out after an abort: ignores the flag, still bounded
 __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, const Params& p) {
@@ -498,7 +504,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint32_t n_item = 0;
   auto item_next = [&]() -> const Item* {
     const uint32_t s = n_item % ITEM_SLOTS;
-    const bool w = wait_bar(smem_u32(&bars->item_full[s]), (n_item / ITEM_SLOTS) & 1u, abort_flag, p);
+    const bool w = wait_bar(smem_u32(&bars->item_full[s]), (n_item / ITEM_SLOTS) & 1u, abort_flag, p,
+                            ITEM_WAITS);
     return __all_sync(0xffffffffu, w) ? &bars->items[s] : nullptr;
   };
   auto item_done = [&]() {  // this warp needs nothing more of the item
@@ -804,7 +811,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t i = 0;
         auto publish = [&](const Item& it) -> bool {
           const uint32_t s = i % ITEM_SLOTS;
-          if (i >= ITEM_SLOTS && !wait_bar(smem_u32(&bars->item_empty[s]), (i / ITEM_SLOTS - 1) & 1u, abort_flag, p))
+          if (i >= ITEM_SLOTS && !wait_bar(smem_u32(&bars->item_empty[s]), (i / ITEM_SLOTS - 1) & 1u, abort_flag, p,
+                                           ITEM_WAITS))
             return false;
           bars->items[s] = it;
           mbar_arrive(smem_u32(&bars->item_full[s]));

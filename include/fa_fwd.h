@@ -300,6 +300,7 @@ int fa_selftest_wait_timeout(int limit_us, void* stream);
  * (where a CTA can be descheduled for longer) raise it. No CUDA call is made.
  *   limit_us  FA_WAIT_LIMIT_MIN_US .. FA_WAIT_LIMIT_MAX_US; anything else returns
  *             FA_ERR_RANGE and leaves the limit unchanged.
+ * Waits of fa_fwd_paged that last as long as a whole work item have 1024 times the limit.
  * fa_get_wait_limit_us -- the current limit in microseconds. */
 int fa_set_wait_limit_us(unsigned long long limit_us);
 unsigned long long fa_get_wait_limit_us(void);

@@ -341,3 +341,25 @@ def test_rows_past_the_range_of_the_sum_of_squares(fa):
         assert not y[0, 1].any()
         assert torch.isnan(y[0, 4, 0]).all() if eps == 0 else not y[0, 4, 0].any()
         assert torch.equal(y[0, [0, 2, 3, 5]], want[0, [0, 2, 3, 5]]) and torch.equal(y[0, 4, 1], want[0, 4, 1])
+
+
+@pytest.mark.parametrize("B,new,total,Hkv,d", [(1, 27000, 40000, 8, 128), (100, 20, 16640, 8, 64)])
+def test_long_items_under_the_smallest_wait_limit(fa, B, new, total, Hkv, d):
+    """Several items a block, each of a hundred tiles and more: a wait for a whole item is not a step of the
+    pipeline, which the limit is for. (Sequences share their pages, as those of a common prefix do.)"""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    q = torch.randn(B * new, Hkv, d, generator=g, device="cuda", dtype=torch.bfloat16)
+    k, v = (torch.randn(total // 64, Hkv, 64, d, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    table = torch.arange(total // 64, dtype=torch.int32, device="cuda").repeat(B, 1)
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda") * new
+    lens = torch.full((B,), total, dtype=torch.int32, device="cuda")
+    want = fa.attention_paged(q, k, v, table, cu, lens, 4096)
+    torch.cuda.synchronize()
+    try:
+        assert fa.fa_set_wait_limit_us(100) == fa.FA_OK
+        got = fa.attention_paged(q, k, v, table, cu, lens, 4096)
+    finally:
+        fa.fa_set_wait_limit_us(fa.FA_WAIT_LIMIT_DEFAULT_US)
+    assert fa.fa_last_status() == 0
+    assert torch.isfinite(want[0]).all() and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
