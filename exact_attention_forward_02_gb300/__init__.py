@@ -10,7 +10,8 @@ Function names follow the C ABI:
     fa_fwd(Q, K, V, O, L, B, H, Nq, Nk, d, scale, causal, dtype, stream) -> status
 plus a tensor-level convenience ``attention(q, k, v, causal, scale)`` -> (O, L), and for the
 operators next to it in a decoder block ``qk_norm_rope``, ``qk_norm_rope_backward``,
-``paged_append`` and ``attention_paged``.
+``paged_append`` and ``attention_paged``, for a cache held in 8 bits ``paged_append_fp8`` and
+``attention_paged_fp8``.
 """
 from __future__ import annotations
 
@@ -145,6 +146,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_fwd_paged.argtypes = [kv, heads, heads, vp, i, i, i, vp, vp, vp, i, f, i, i, vp, n, vp]
     lib.fa_fwd_paged_workspace_bytes.restype = n
     lib.fa_fwd_paged_workspace_bytes.argtypes = [i] * 4
+    lib.fa_paged_append_fp8.restype = i
+    lib.fa_paged_append_fp8.argtypes = [kv, vp, vp, heads, heads, i, i, vp, vp, vp, i, rope, i, vp]
+    lib.fa_fwd_paged_fp8.restype = i
+    lib.fa_fwd_paged_fp8.argtypes = [kv, vp, vp, heads, heads, vp, i, i, i, vp, vp, vp, i, f, i, i, vp, n, vp]
     lib.fa_debug_cap_workspace.restype = ctypes.c_int
     lib.fa_debug_cap_workspace.argtypes = [ctypes.c_longlong]
     return lib
@@ -376,6 +381,21 @@ def fa_fwd_paged_workspace_bytes(Hq, Hkv, d, max_q) -> int:
     return int(lib.fa_fwd_paged_workspace_bytes(int(Hq), int(Hkv), int(d), int(max_q)))
 
 
+def fa_paged_append_fp8(kv, k_scale, v_scale, k, v, B, T, cu_seqlens, seq_lens, block_table, table_stride, rope, dtype,
+                        stream) -> int:
+    """C-ABI call writing new keys (rotated) and values into a paged cache held in 8 bits."""
+    return int(lib.fa_paged_append_fp8(kv, k_scale, v_scale, k, v, int(B), int(T), cu_seqlens, seq_lens, block_table,
+                                       int(table_stride), rope, int(dtype), stream))
+
+
+def fa_fwd_paged_fp8(kv, k_scale, v_scale, q, O, L, B, T, max_q, cu_seqlens, seq_lens, block_table, table_stride,
+                     scale, causal, dtype, workspace, workspace_bytes, stream) -> int:
+    """C-ABI call of attention over a paged cache held in 8 bits."""
+    return int(lib.fa_fwd_paged_fp8(kv, k_scale, v_scale, q, O, L, int(B), int(T), int(max_q), cu_seqlens, seq_lens,
+                                    block_table, int(table_stride), float(scale), int(bool(causal)), int(dtype),
+                                    workspace, int(workspace_bytes), stream))
+
+
 _torch_calls = None
 
 
@@ -391,7 +411,7 @@ def _calls():
 
         from . import _fa_torch
         names = ("fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_bytes", "fa_paged_append",
-                 "fa_fwd_paged", "fa_fwd_paged_workspace_bytes")
+                 "fa_fwd_paged", "fa_fwd_paged_workspace_bytes", "fa_paged_append_fp8", "fa_fwd_paged_fp8")
         _fa_torch.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
         _torch_calls = _fa_torch
     return _torch_calls
@@ -460,4 +480,31 @@ def attention_paged(q, k_pages, v_pages, block_table, cu_seqlens, seq_lens, max_
                         workspace, stream)
     if type(r) is int:
         raise FAError(r, "fa_fwd_paged")
+    return r
+
+
+# --------------------------------------------------------------------- a cache held in 8 bits
+def paged_append_fp8(k, v, k_pages, v_pages, k_scale, v_scale, block_table, cu_seqlens, seq_lens, rope=None,
+                     interleaved: bool = False, stream=None):
+    """paged_append for a cache held in 8 bits: k_pages, v_pages float8_e4m3fn [num_pages, Hkv, page_size, d]
+    with the same strides (multiples of 16 elements), k_scale, v_scale fp32 [num_pages, Hkv].
+
+    An element is scale * code. A page that gets its first token takes the smallest power of two that
+    holds its new tokens; one that has older tokens keeps its scale or, where the new ones need a larger
+    one, takes that and its codes are rounded anew (see include/fa_decoder.h).
+    """
+    r = _calls().append_fp8(k, v, k_pages, v_pages, block_table, cu_seqlens, seq_lens, rope, interleaved, stream,
+                            k_scale, v_scale)
+    if r != 0:
+        raise FAError(r, "fa_paged_append_fp8")
+
+
+def attention_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_seqlens, seq_lens, max_q: int,
+                        causal: bool = True, scale: float | None = None, out=None, lse=None, workspace=None,
+                        stream=None):
+    """attention_paged over a cache held in 8 bits (see paged_append_fp8); q, O (fp16/bf16) and L as there."""
+    r = _calls().attend_fp8(q, k_pages, v_pages, block_table, cu_seqlens, seq_lens, max_q, causal, scale, out, lse,
+                            workspace, stream, k_scale, v_scale)
+    if type(r) is int:
+        raise FAError(r, "fa_fwd_paged_fp8")
     return r

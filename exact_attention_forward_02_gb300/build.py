@@ -1,6 +1,6 @@
 """Build libfa.so (the CUDA library behind the C ABI in include/*.h) in-tree.
 
-Two CUDA translation units compiled at the same time, one -gencode (sm_103a), linked against
+CUDA translation units compiled at the same time, one -gencode (sm_103a), linked against
 the static CUDA runtime; the driver entry point for TMA tensor maps is fetched at run time, so
 no libcuda link. Beside it the tensor-level calls (_fa_torch.so), a host-only module over
 libtorch: it is left out where there is no CUDA build of torch, which the library does not need.
@@ -16,9 +16,11 @@ import sysconfig
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-SRCS = [os.path.join(CSRC, "fa_fwd.cu"), os.path.join(CSRC, "fa_decoder.cu")]
+SRCS = [os.path.join(CSRC, "fa_fwd.cu"), os.path.join(CSRC, "fa_decoder.cu"),
+        os.path.join(CSRC, "fa_compact.cu")]
 DEPS = SRCS + [os.path.join(CSRC, h) for h in ("sm103_ptx.cuh", "fa_bwd.cuh", "philox.cuh", "fa_fwd_kernel.cuh",
-                                               "fa_rope.cuh", "fa_paged.cuh", "fa_host.h")] + [
+                                               "fa_rope.cuh", "fa_paged.cuh", "fa_append8.cuh", "fa_host.h",
+                                               "fa_decoder_host.h")] + [
     os.path.join(ROOT, "include", h) for h in ("fa_fwd.h", "fa_decoder.h")]
 LIB = os.path.join(PKG, "libfa.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

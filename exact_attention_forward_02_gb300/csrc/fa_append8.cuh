@@ -1,0 +1,210 @@
+// fa_append8.cuh -- new keys (rotated) and values into a paged cache held in 8 bits.
+// Included by fa_compact.cu.
+//
+// A page of a key head is held as x = s c, c in E4M3 and s one scale of fp32. For the new tokens of a
+// page, a = max |x| over their (rotated) rows asks for s_new = the smallest power of two >= a / 448;
+// with older tokens in the page its scale becomes s = max(s_old, s_new), else s_new. A power of two
+// costs E4M3 no precision (its 4 bits are relative to the value), and codes held under a smaller scale
+// are then rounded anew exactly, but for what falls among the subnormal numbers (below 2^-14 of the
+// largest): so a page's codes hardly depend on how its tokens were cut into calls.
+//
+// Work: a unit is (sequence, page it gets tokens into, head of k or of v), one to W warps, which hold
+// the unit's rows in registers between the maximum and the rounding. No atomics: a page belongs to one
+// unit. Places for pages: a sequence with token rows [c0, c1) reaches at most
+// floor(c1 / page) - floor(c0 / page) + 2 pages, so places floor(c0 / page) + 2 b ... are enough for it,
+// and a place's sequence is found by a search over cu_seqlens. Bound by HBM (reads 2 d bytes, writes d).
+#pragma once
+
+#include "fa_rope.cuh"
+
+namespace fa {
+
+struct Append8Params {
+  HeadsDev k, v;
+  uint8_t *kp, *vp;
+  float *ks, *vs;  // [num_pages][Hkv]
+  long long page_stride, head_stride, token_stride;
+  int num_pages, page_size, Hkv;
+  const int *cu, *lens, *table;
+  int table_stride, B, T;
+  long long units;  // places for pages, times the heads of k and of v
+  RopeDev rope;
+  int* status;
+};
+
+constexpr int APPEND8_ROWS = 8;                    // rows that a lane holds between the two passes
+constexpr uint32_t APPEND8_LEAST = 27u << 23;      // 2^-100, of a page of zeros
+
+// as the 16-bit append has it
+__device__ __forceinline__ bool rows_fit(int begin, int end, int T) { return begin >= 0 && end >= begin && end <= T; }
+// place of sequence b's first page
+__device__ __forceinline__ uint32_t place_of(const Append8Params& p, int b) {
+  return (uint32_t)max(p.cu[b], 0) / (uint32_t)p.page_size + 2u * (uint32_t)b;
+}
+// the last sequence whose first place is at most `place` (the warp's 32 lanes look at 32 at a time)
+__device__ __forceinline__ int sequence_of_place(const Append8Params& p, uint32_t place, int lane) {
+  int lo = 0, n = p.B;
+  while (n > 0) {
+    const int step = (n + 31) / 32;
+    const int i = lo + (lane + 1) * step - 1;
+    const bool le = i < lo + n && place_of(p, i) <= place;
+    const int parts = __popc(__ballot_sync(0xffffffffu, le));
+    lo += parts * step;
+    n = min(step - 1, n - parts * step);
+  }
+  return min(lo, p.B) - 1;
+}
+
+template <int D, bool BF16, bool INTER, bool FULL, int W>
+__global__ void __launch_bounds__(ROW_THREADS, 2) fa_paged_append8_kernel(const __grid_constant__ Append8Params p) {
+  constexpr int LPR = D / 8, GPW = 32 / LPR, TURN = W * GPW;  // lanes of a row, rows of a warp, of a unit's turn
+  __shared__ float tops[ROW_WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR, wu = warp % W;
+  if (blockIdx.x == gridDim.x - 1) {  // looks over the offsets; the others skip what does not fit them
+    launch_dependents();
+    wait_previous_grid();
+    bool bad = false;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < p.B; i += ROW_THREADS) bad |= !rows_fit(p.cu[i], p.cu[i + 1], p.T);
+    if (bad) atomicCAS(p.status, 0, FA_ERR_RANGE);
+    return;
+  }
+  const long long unit = (long long)blockIdx.x * (ROW_WARPS / W) + warp / W;
+  bool alive = unit < p.units;
+  const int heads = 2 * p.Hkv;
+  const uint32_t place = alive ? (uint32_t)(unit / heads) : 0u;
+  const int hs = alive ? (int)(unit - (long long)place * heads) : 0;
+  const bool is_v = hs >= p.Hkv;
+  const int h = is_v ? hs - p.Hkv : hs;
+  const HeadsDev& in = is_v ? p.v : p.k;
+  const bool turned = !is_v && p.rope.rot;
+  Lane<D, BF16, INTER, FULL> ln;
+  ln.place(lane, p.rope.rot);
+  launch_dependents();
+  wait_previous_grid();
+  const int b = sequence_of_place(p, place, lane);
+  int begin = 0, p0 = 0, s0 = 0, s1 = 0, at = 0, page = -1;
+  alive = alive && b >= 0;
+  if (alive) {
+    begin = p.cu[b];
+    const int end = p.cu[b + 1], len = p.lens[b];
+    p0 = len - (end - begin);
+    const int first = max(p0, 0);
+    const int nth = (int)(place - place_of(p, b));
+    at = first / p.page_size + nth;  // page of the sequence
+    const long long from = (long long)at * p.page_size;
+    alive = rows_fit(begin, end, p.T) && end > begin;
+    if (alive && p0 < 0 && nth == 0 && lane == 0) atomicCAS(p.status, 0, FA_ERR_RANGE);  // tokens before position 0
+    alive = alive && from < len;
+    if (alive) {
+      s0 = (int)max(first - from, 0ll);
+      s1 = (int)min((long long)p.page_size, len - from);
+      // tokens behind the rotation table are skipped
+      const int told = p.rope.rot ? (int)min((long long)s1, max(p.rope.length - from, 0ll)) : s1;
+      bool bad = told < s1;
+      s1 = told;
+      if (at < p.table_stride) page = p.table[(size_t)b * p.table_stride + at];
+      if (page < 0 || page >= p.num_pages) bad = true, alive = false;
+      if (bad && lane == 0) atomicCAS(p.status, 0, FA_ERR_RANGE);
+      alive = alive && s0 < s1;
+    }
+  }
+  const int pos0 = alive ? at * p.page_size : 0;  // of the page's first slot
+  const uint16_t* src = in.ptr + (long long)h * in.hs + ((long long)begin + pos0 - p0) * in.ts;  // of that slot
+  uint8_t* dst = (is_v ? p.vp : p.kp) + (long long)page * p.page_stride + (long long)h * p.head_stride;
+  float* scale_at = (is_v ? p.vs : p.ks) + (long long)page * p.Hkv + h;
+  const float s_old = alive && s0 > 0 ? *scale_at : 0.f;
+
+  // a row's elements, rotated, and the maximum of their sizes (of those that are finite)
+  auto load = [&](int slot) { return ln.load(src + (long long)slot * in.ts); };
+  auto values = [&](const uint4& u, int slot) {
+    Pairs x = ln.unpack(u);
+    if (turned) {
+      ln.angles(p.rope, pos0 + slot, 1.f, true);
+      ln.turn(x);
+    }
+    return x;
+  };
+  float top = 0.f;
+  auto grow = [&](const Pairs& x) {
+    auto one = [&](float v) {
+      const float a = fabsf(v);
+      top = fmaxf(top, a <= 3.402823466e38f ? a : 0.f);
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) one(lo_of(x.a[i])), one(hi_of(x.a[i])), one(lo_of(x.b[i])), one(hi_of(x.b[i]));
+  };
+  auto put = [&](int slot, const Pairs& x, float inv) {
+    // (what is not finite becomes NaN, not the largest number)
+    auto q = [&](float v) {
+      const float y = v * inv;
+      return y + (y - y);
+    };
+    uint8_t* row = dst + (long long)slot * p.token_stride;
+    if constexpr (INTER) {
+      const uint32_t w0 = pack4_e4m3(q(lo_of(x.a[0])), q(lo_of(x.b[0])), q(hi_of(x.a[0])), q(hi_of(x.b[0])));
+      const uint32_t w1 = pack4_e4m3(q(lo_of(x.a[1])), q(lo_of(x.b[1])), q(hi_of(x.a[1])), q(hi_of(x.b[1])));
+      *reinterpret_cast<uint2*>(row + 8 * ln.l) = make_uint2(w0, w1);
+    } else {
+      *reinterpret_cast<uint32_t*>(row + ln.ea) =
+          pack4_e4m3(q(lo_of(x.a[0])), q(hi_of(x.a[0])), q(lo_of(x.a[1])), q(hi_of(x.a[1])));
+      *reinterpret_cast<uint32_t*>(row + ln.eb) =
+          pack4_e4m3(q(lo_of(x.b[0])), q(hi_of(x.b[0])), q(lo_of(x.b[1])), q(hi_of(x.b[1])));
+    }
+  };
+
+  const int row0 = s0 + wu * GPW + sub, rows_held = APPEND8_ROWS * TURN;
+  Pairs held[APPEND8_ROWS];
+  if (alive) {
+    uint4 u[APPEND8_ROWS];
+#pragma unroll
+    for (int j = 0; j < APPEND8_ROWS; ++j)
+      if (row0 + j * TURN < s1) u[j] = load(row0 + j * TURN);
+#pragma unroll
+    for (int j = 0; j < APPEND8_ROWS; ++j) {
+      if (row0 + j * TURN >= s1) continue;
+      held[j] = values(u[j], row0 + j * TURN);
+      grow(held[j]);
+    }
+#pragma unroll 2
+    for (int s = row0 + rows_held; s < s1; s += TURN) grow(values(load(s), s));  // (pages too large to be held)
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if constexpr (W > 1) {
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < W; ++i) top = fmaxf(top, tops[warp / W * W + i]);
+  }
+  if (!alive) return;
+  // the smallest power of two that is not below top / 448: 448 = 1.75 2^8
+  const uint32_t bits = (__float_as_uint(top) + 0x1fffffu) >> 23 << 23;
+  float s = __uint_as_float(bits > APPEND8_LEAST + (8u << 23) ? bits - (8u << 23) : APPEND8_LEAST);
+  if (s0 > 0 && s_old >= s) s = s_old;
+  const float inv = 1.f / s;
+#pragma unroll
+  for (int j = 0; j < APPEND8_ROWS; ++j)
+    if (row0 + j * TURN < s1) put(row0 + j * TURN, held[j], inv);
+#pragma unroll 2
+  for (int x = row0 + rows_held; x < s1; x += TURN) put(x, values(load(x), x), inv);
+  if (s0 > 0 && s > s_old) {  // the older tokens' codes under the larger scale
+    const float ratio = s_old * inv;
+    for (int x = wu * GPW + sub; x < s0; x += TURN) {
+      uint2* row = reinterpret_cast<uint2*>(dst + (long long)x * p.token_stride + 8 * ln.l);
+      uint2 c = *row;
+      auto again = [&](uint32_t v) {
+        uint32_t a, e;
+        float f[4];
+        unpack4_e4m3(v, a, e);
+        unpack2<false>(a, f[0], f[1]);
+        unpack2<false>(e, f[2], f[3]);
+        return pack4_e4m3(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
+      };
+      *row = make_uint2(again(c.x), again(c.y));
+    }
+  }
+  if (lane == 0 && wu == 0 && (s0 == 0 || s > s_old)) *scale_at = s;
+}
+
+}  // namespace fa

@@ -55,16 +55,21 @@ namespace fa {
 namespace paged {
 
 constexpr int BM = 128, BN = 128;
-constexpr int NUM_WARPS = 12, NUM_THREADS = NUM_WARPS * 32;
-constexpr int WARP_LOAD = 8, WARP_MMA = 9, WARP_WALK = 10, WARP_LOAD2 = 11;
+constexpr int MAX_WARPS = 16;
+constexpr int WARP_LOAD = 8, WARP_MMA = 9, WARP_WALK = 10, WARP_LOAD2 = 11, WARP_CONVERT = 12;
+// 12 warps, and 4 that convert where the cache is held in 8 bits
+__host__ __device__ constexpr int num_warps(bool f8) { return f8 ? 16 : 12; }
 constexpr int ITEM_SLOTS = 4;
-constexpr int ITEM_READERS = 11;  // warps that read an item: two loading, MMA, 8 softmax
+// warps that read an item: two loading, MMA, 8 softmax, and those that convert
+__host__ __device__ constexpr int item_readers(bool f8) { return f8 ? 15 : 11; }
 // Waits on the ring of items last as long as an item, up to thousands of key tiles, while the limit is
 // meant for a step of the pipeline: they have this many times it. (Where the pipeline stands still, one
 // of its own waits runs out first and stops these as well.)
 constexpr uint32_t ITEM_WAITS = 1024;
-// 2*128*200 + 128*104 = 64512 = 384*168 registers, the launch's budget
-constexpr uint32_t REGS_SOFTMAX = 200, REGS_OTHER = 104;
+// 2*128*200 + 128*104 = 64512 = 384*168 registers, the launch's budget; with the converting warps
+// 2*128*192 + 2*128*64 = 65536 = 512*128
+__host__ __device__ constexpr uint32_t regs_softmax(bool f8) { return f8 ? 192 : 200; }
+__host__ __device__ constexpr uint32_t regs_other(bool f8) { return f8 ? 64 : 104; }
 constexpr uint32_t TMEM_COLS = 512, TMEM_S0 = 0, TMEM_O0 = 256;  // S0 | S1 | O0 | O1
 constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units, as in the dense kernel
 constexpr int SMEM_LIMIT = 232448;
@@ -96,6 +101,9 @@ struct Params {
   int* records;  // [block][8]: the item that begins in a block's range and ends in another's (7 in use)
   float* parts;  // [block][2][rows]: D floats of O~ per row, then [rows][2] of (m, l)
   long long parts_len;  // floats there (checked by debug builds)
+  // a cache in 8 bits: scales [num_pages][Hkv], and the queries, which the kernel splits by itself
+  const float *ks, *vs;
+  HeadsDev q;
 };
 
 // Debug builds (FA_DEBUG) check the places of tile copies, partial states and output rows; one
@@ -137,35 +145,51 @@ struct Start {
 struct Barriers {
   uint64_t q_full, q_empty;
   uint64_t kv_full[MAX_SLOTS], kv_release[MAX_SLOTS];
+  uint64_t v_full[4], v_release[4], held_full[4], held_empty[4];  // F8: V in 16 bits, and as it is held
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t mma_drain, epi;
   uint64_t item_full[ITEM_SLOTS], item_empty[ITEM_SLOTS];
   Item items[ITEM_SLOTS];
-  long long warp_units[NUM_WARPS];
+  long long warp_units[MAX_WARPS];
   Start start;
   uint32_t tmem_base;
   int abort_flag;
 };
 
-template <int D, bool SPLIT>
+// TERMS: 0, or for a cache in 8 bits the E4M3 numbers that a query element is the sum of
+template <int D, bool SPLIT, int TERMS>
 struct Layout {
+  static constexpr bool F8 = TERMS > 0;
   static constexpr int TILE_BYTES = BM * D * 2;
+  static constexpr int Q_BYTES = F8 ? TERMS * BM * D : TILE_BYTES, K_BYTES = F8 ? BM * D : TILE_BYTES;
+  // F8: V's tiles in 16 bits, and as they are held: what is left goes to K's, as the bytes in flight have
+  // to cover the memory's latency (d = 128: 64 to 96 KB, 900 cycles of an SM's share of the bandwidth are 21)
+  static constexpr int V_SLOTS = !F8 ? 0 : D == 64 ? 4 : SPLIT || TERMS < 3 ? 2 : 1;
+  static constexpr int HELD_SLOTS = !F8 ? 0 : D == 64 ? 4 : SPLIT && TERMS < 3 ? 3 : 2;
   static constexpr int CHUNK_BYTES = BM * 128, CHUNKS = D / 64;
   static constexpr int Q_TILES = SPLIT ? 1 : 2;
   // SPLIT: fp32 rows of O~. PAIR: 4 KB per softmax warp, 32 rows of 128 bytes on their way out.
-  static constexpr int STAGE_BYTES = SPLIT ? 65536 : 32768;
+  static constexpr int STAGE_BYTES = SPLIT && !(F8 && D == 128) ? 65536 : 32768;
   static constexpr int STAGE_ROWS = STAGE_BYTES / (D * 4);
   static constexpr int STATE_BYTES = SPLIT ? 2 * BM * 8 : 0;  // (m, l) of both warpgroups' rows
-  static constexpr int HEAD_BYTES = 1024;                     // barriers and items
-  static constexpr int FIT =
-      (SMEM_LIMIT - Q_TILES * TILE_BYTES - STAGE_BYTES - STATE_BYTES - HEAD_BYTES) / TILE_BYTES;
+  // F8: 32 floats of each softmax warp, the scales of its keys' pages; SPLIT: over its own rows' (m, l),
+  // which are written and read between an item's last key tile and the next one's first
+  static constexpr int SCALE_BYTES = F8 && !SPLIT ? 8 * 128 : 0;
+  // barriers and items; F8: and the exponents of the query rows of two items
+  static constexpr int BAR_BYTES = F8 ? 768 : 1024, EXP_ROWS = SPLIT ? BM : 2 * BM;
+  static constexpr int HEAD_BYTES = BAR_BYTES + (F8 ? 2 * EXP_ROWS : 0);
+  static constexpr int FIT = (SMEM_LIMIT - Q_TILES * Q_BYTES - STAGE_BYTES - STATE_BYTES - SCALE_BYTES - HEAD_BYTES -
+                              V_SLOTS * TILE_BYTES - HELD_SLOTS * K_BYTES) / K_BYTES;
   static constexpr int KV_SLOTS = FIT > MAX_SLOTS ? MAX_SLOTS : FIT;
-  static constexpr int OFF_Q = 0, OFF_KV = Q_TILES * TILE_BYTES;
-  static constexpr int OFF_STAGE = OFF_KV + KV_SLOTS * TILE_BYTES;
+  static constexpr int OFF_Q = 0, OFF_KV = Q_TILES * Q_BYTES;
+  static constexpr int OFF_V = OFF_KV + KV_SLOTS * K_BYTES, OFF_HELD = OFF_V + V_SLOTS * TILE_BYTES;
+  static constexpr int OFF_STAGE = OFF_HELD + HELD_SLOTS * K_BYTES;
   static constexpr int OFF_STATE = OFF_STAGE + STAGE_BYTES;
-  static constexpr int OFF_BAR = OFF_STATE + STATE_BYTES;
+  static constexpr int OFF_SCALE = F8 && SPLIT ? OFF_STATE : OFF_STATE + STATE_BYTES;
+  static constexpr int OFF_BAR = OFF_STATE + STATE_BYTES + SCALE_BYTES, OFF_EXP = OFF_BAR + BAR_BYTES;
   static constexpr int SMEM_BYTES = OFF_BAR + HEAD_BYTES;
-  static_assert(sizeof(Barriers) <= 1024 && KV_SLOTS >= 4 && SMEM_BYTES <= SMEM_LIMIT, "shared memory budget");
+  static_assert(sizeof(Barriers) <= BAR_BYTES && KV_SLOTS >= (F8 ? 2 : 4) && SMEM_BYTES <= SMEM_LIMIT,
+                "shared memory budget");
 };
 
 // ----------------------------------------------------------------------------- waits
@@ -351,7 +375,7 @@ __device__ __forceinline__ long long units_of(const Params& p, int b0, int b1, S
 
 // The block's share of the units, and where it begins (bars->start). All threads call this, with
 // the units of their own sequences; it ends with a barrier.
-template <int TPT_MUL, int ITEM_UNITS, int MIN_UNITS>
+template <int TPT_MUL, int ITEM_UNITS, int MIN_UNITS, int NUM_WARPS>
 __device__ __forceinline__ Range plan(const Params& p, Barriers* bars, int b0, int b1, long long mine, Seq s) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tpi = p.tpt * TPT_MUL;
   long long incl = mine;
@@ -430,12 +454,25 @@ __device__ __forceinline__ Range plan(const Params& p, Barriers* bars, int b0, i
 // ----------------------------------------------------------------------------- kernel
 // DIRECT: batches that go without units may come (SPLIT: always; PAIR has an instantiation with and
 // one without that code, whose mere presence slowed the long chunks' loop from 339 to 351 us).
-template <int D, bool BF16, bool SPLIT, int REP, bool DIRECT>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+// F8: the cache is held in E4M3, K = ks k8 and V = vs v8 with a scale for each page and key head.
+//   S   K's tiles go to the tensor cores as they are held (kind::f8f6f4), and a query row as a sum of E4M3
+//       numbers, q = 2^e (q1 + q2 [+ q3]), max |q 2^-e| in [128, 256): q1 takes 4 bits of an element, q2 the
+//       next 4, q3 the last 3, so that 2 terms hold bf16 and 3 hold fp16 exactly, but for what lies under
+//       2^-10 in q 2^-e (2^-17 of the row's largest). 2 terms cost what one 16-bit product does.
+//   PV  v8 is turned into fp16 (exactly), in which P is kept too, with vs in it: P'_j = P_j vs_j / vref 2^7,
+//       where vref is the largest vs so far of the warp's keys: at most 2^15, and O~ comes out in units of
+//       vref 2^-7. P in sums of E4M3 would lose the many small weights under 2^-10.
+// Four more warps split the queries and turn V. Shared memory carries 128 bytes a cycle, and that is what
+// this was laid out by (d = 128, cycles per key tile of one row tile): loads 256, S 512, V turned 384, PV
+// 256 = 1408, about an SM's share of the bandwidth (1400); K turned into 16 bits as well: 1792.
+template <int D, bool BF16, bool SPLIT, int REP, bool DIRECT, bool F8 = false>
+__global__ void __launch_bounds__(num_warps(F8) * 32, 1)
     fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
   static_assert(SPLIT || REP == 1, "copies of rows belong to the SPLIT form");
-  using LY = Layout<D, SPLIT>;
+  constexpr int TERMS = F8 ? (BF16 ? 2 : 3) : 0;
+  using LY = Layout<D, SPLIT, TERMS>;
+  constexpr int NUM_WARPS = num_warps(F8), NUM_THREADS = NUM_WARPS * 32;
   // ITEM_UNITS: what an item costs by itself, in key tiles. Against it, us: REP 4, 2 units: 24 drafts, d 64,
   // 35.8, with 1 41.6, with 4 36.6 (64 ragged single tokens, d 128: 165.0, 163.7, 166.3). REP 2, 3 units: 64
   // sequences of 16 tokens, d 128, 57.3, with 2 57.4, with 4 56.8. REP 1, 4 units: 256 of 32 tokens, d 64,
@@ -456,11 +493,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   volatile int* abort_flag = &bars->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&bars->q_full), 1);
+    mbar_init(smem_u32(&bars->q_full), F8 ? 4 : 1);
     mbar_init(smem_u32(&bars->q_empty), 1);
     for (int s = 0; s < LY::KV_SLOTS; ++s) {
       mbar_init(smem_u32(&bars->kv_full[s]), 1);
       mbar_init(smem_u32(&bars->kv_release[s]), 1);
+    }
+    for (int s = 0; s < LY::V_SLOTS; ++s) {
+      mbar_init(smem_u32(&bars->v_full[s]), 4);
+      mbar_init(smem_u32(&bars->v_release[s]), 1);
+    }
+    for (int s = 0; s < LY::HELD_SLOTS; ++s) {
+      mbar_init(smem_u32(&bars->held_full[s]), 1);
+      mbar_init(smem_u32(&bars->held_empty[s]), 4);
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(smem_u32(&bars->s_full[g]), 1);
@@ -471,13 +516,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     mbar_init(smem_u32(&bars->epi), 8);
     for (int s = 0; s < ITEM_SLOTS; ++s) {
       mbar_init(smem_u32(&bars->item_full[s]), 1);
-      mbar_init(smem_u32(&bars->item_empty[s]), ITEM_READERS);
+      mbar_init(smem_u32(&bars->item_empty[s]), item_readers(F8));
     }
     bars->abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == WARP_LOAD && lane == 0) {
-    tma_prefetch_desc(&tmQ);
+    if (!F8) tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
@@ -496,7 +541,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int b0 = min((int)threadIdx.x * per_thread, p.B), b1 = min(b0 + per_thread, p.B);
     Seq seq = {};
     const long long my_units = units_of<TPT_MUL, ITEM_UNITS>(p, b0, b1, seq, blockIdx.x == 0);
-    range = plan<TPT_MUL, ITEM_UNITS, MIN_UNITS>(p, bars, b0, b1, my_units, seq);
+    range = plan<TPT_MUL, ITEM_UNITS, MIN_UNITS, NUM_WARPS>(p, bars, b0, b1, my_units, seq);
   }
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
@@ -515,7 +560,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   };
 
   if (warp >= WARP_LOAD) {
-    regs_dec<REGS_OTHER>();
+    regs_dec<regs_other(F8)>();
     // Loads are numbered over the block's pieces in the order of their use; load i goes to slot
     // i mod KV_SLOTS. PAIR: K0 V0 K1 V1 ...; unit u = {V of tile u-1, K of tile u} is released at
     // once. SPLIT: K0 K1 V0 K2 V1 K3 ...; every load is released by itself. Loads are released in
@@ -533,9 +578,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const uint32_t me = warp == WARP_LOAD2;
       const int boxes = BN / p.box_keys;                    // page boxes of one 64-column chunk
       const int tiles_per_page = p.page_size > BN ? p.page_size / BN : 1;
+      // F8: rows go in one box; K and V have slots of their own, tile i of the block in slot i mod theirs.
+      // A warp's tiles are at most 2 apart (SPLIT), so with 2 slots or more the parities stay apart as above.
+      constexpr int BOX_CHUNKS = F8 ? 1 : LY::CHUNKS;
+      constexpr uint32_t BOX_ROW = F8 ? D : 128;
       const int my_box = lane % boxes, my_chunk = lane / boxes;
-      const bool issues = my_chunk < LY::CHUNKS;
-      const uint32_t box_bytes = (uint32_t)p.box_keys * 128u;
+      const bool issues = my_chunk < BOX_CHUNKS;
+      const uint32_t box_bytes = (uint32_t)p.box_keys * BOX_ROW;
       const uint32_t box_off = (uint32_t)my_chunk * LY::CHUNK_BYTES + (uint32_t)my_box * box_bytes;
       uint32_t ld0 = 0, n_q = 0, issued_mask = 0, last_par = 0;  // n_q: Q loads of the items so far
       bool ok = true;
@@ -591,7 +640,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         int next = entries(window + 1);
         early_b = -1;
         const int first_i = SPLIT ? (int)(((ld0 >> 1) ^ me) & 1u) : 0;
-        if (me == 0 && first_i != 0 && !(ok = load_q(it))) break;
+        if (!F8 && me == 0 && first_i != 0 && !(ok = load_q(it))) break;
         for (int i = first_i; i < it.n && ok; i += SPLIT ? 2 : 1) {
           const int j = it.j0 + i;
           const int e0 = p.page_size > BN ? j / tiles_per_page : j * boxes;  // the tile's first entry
@@ -607,24 +656,41 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int is_v = SPLIT ? 0 : (int)me; is_v < (SPLIT ? 2 : (int)me + 1); ++is_v) {
             const uint32_t ld =
                 ld0 + (SPLIT ? (is_v ? 2 + i + min(i, it.n - 2) : i < 2 ? i : 2 * i - 1) : 2 * i + is_v);
-            const uint32_t slot = ld % LY::KV_SLOTS, par = (ld / LY::KV_SLOTS) & 1u;
-            if (ld >= (uint32_t)LY::KV_SLOTS) {
-              const uint32_t u = SPLIT ? ld - LY::KV_SLOTS : (ld - LY::KV_SLOTS + 1) >> 1;
-              ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->kv_release[u % LY::KV_SLOTS]),
-                                                    (u / LY::KV_SLOTS) & 1u, abort_flag, p));
-              if (!ok) break;
+            uint32_t slot, par, full, to;
+            if constexpr (F8) {
+              const uint32_t t = (ld0 >> 1) + i, slots = is_v ? LY::HELD_SLOTS : LY::KV_SLOTS;
+              slot = t % slots;
+              par = (t / slots) & 1u;
+              if (t >= slots) {
+                ok = __all_sync(0xffffffffu, wait_bar(smem_u32(is_v ? &bars->held_empty[slot] : &bars->kv_release[slot]),
+                                                      par ^ 1u, abort_flag, p));
+                if (!ok) break;
+              }
+              full = smem_u32(is_v ? &bars->held_full[slot] : &bars->kv_full[slot]);
+              to = (is_v ? smem_u32(smem + LY::OFF_HELD) : sKV) + slot * LY::K_BYTES;
+              slot += is_v ? 16u : 0u;  // (in issued_mask)
+            } else {
+              slot = ld % LY::KV_SLOTS;
+              par = (ld / LY::KV_SLOTS) & 1u;
+              if (ld >= (uint32_t)LY::KV_SLOTS) {
+                const uint32_t u = SPLIT ? ld - LY::KV_SLOTS : (ld - LY::KV_SLOTS + 1) >> 1;
+                ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->kv_release[u % LY::KV_SLOTS]),
+                                                      (u / LY::KV_SLOTS) & 1u, abort_flag, p));
+                if (!ok) break;
+              }
+              full = smem_u32(&bars->kv_full[slot]);
+              to = sKV + slot * LY::TILE_BYTES;
             }
-            const uint32_t full = smem_u32(&bars->kv_full[slot]);
-            if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)live * LY::CHUNKS * box_bytes);
+            if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)live * BOX_CHUNKS * box_bytes);
             __syncwarp();
             in_bounds(p, !issues || my_box >= live || (it.h < p.Hkv && page >= 0 && page <= p.num_pages));
             if (issues && my_box < live)
-              tma_load_4d(sKV + slot * LY::TILE_BYTES + box_off, is_v ? &tmV : &tmK, full, my_chunk * 64,
+              tma_load_4d(to + box_off, is_v ? &tmV : &tmK, full, my_chunk * 64,
                           p.page_size > BN ? j % tiles_per_page * BN : 0, it.h, page);
             issued_mask |= 1u << slot;
             last_par = (last_par & ~(1u << slot)) | (par << slot);
             // Q behind the first K
-            if (me == 0 && is_v == 0 && i == 0 && !(ok = load_q(it))) break;
+            if (!F8 && me == 0 && is_v == 0 && i == 0 && !(ok = load_q(it))) break;
           }
         }
         ld0 += 2 * it.n;
@@ -633,15 +699,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // every issued copy must land before the block may exit
         for (int s = 0; s < LY::KV_SLOTS; ++s)
           if (issued_mask & (1u << s)) wait_drain(smem_u32(&bars->kv_full[s]), (last_par >> s) & 1u, p);
+        for (int s = 0; s < LY::HELD_SLOTS; ++s)
+          if (issued_mask >> 16 & (1u << s)) wait_drain(smem_u32(&bars->held_full[s]), (last_par >> (16 + s)) & 1u, p);
         if (n_q) wait_drain(smem_u32(&bars->q_full), (n_q - 1) & 1u, p);
       }
       __syncwarp();
     } else if (warp == WARP_MMA) {
       // ======================================================================= MMA issuer
-      constexpr uint32_t ID_S = umma_idesc_f16(BF16 ? 1 : 0, 0, 0, BM, BN);
-      constexpr uint32_t ID_O = umma_idesc_f16(BF16 ? 1 : 0, 0, 1, BM, D);
-      const uint64_t dQ0 = umma_smem_desc(sQ, 16, 1024), dK = umma_smem_desc(sKV, 16, 1024);
-      const uint64_t dV = umma_smem_desc(sKV, LY::CHUNK_BYTES, 1024);
+      constexpr uint32_t ID_S = umma_idesc_f16(BF16 ? 1 : 0, 0, 0, BM, BN), ID_S8 = umma_idesc_f16(0, 0, 0, BM, BN);
+      constexpr uint32_t ID_O = umma_idesc_f16(BF16 && !F8 ? 1 : 0, 0, 1, BM, D);
+      // F8, d = 64: rows of 64 bytes, 64-byte swizzle
+      constexpr uint64_t SW = F8 && D == 64 ? UMMA_SWIZZLE_64B : UMMA_SWIZZLE_128B;
+      constexpr uint32_t SBO = F8 && D == 64 ? 512 : 1024;
+      const uint64_t dQ0 = umma_smem_desc<SW>(sQ, 16, SBO), dK = umma_smem_desc<SW>(sKV, 16, SBO);
+      const uint64_t dV = umma_smem_desc(F8 ? smem_u32(smem + LY::OFF_V) : sKV, LY::CHUNK_BYTES, 1024);
       uint32_t q_ph = 0, p_ph[2] = {0, 0};
       bool ok = true;
       Item it = {};
@@ -657,12 +728,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         __syncwarp();
       };
       auto issue_s = [&](int q_tile, int g, uint32_t kslot) {
-        const uint64_t dq = dQ0 + ((q_tile * LY::TILE_BYTES) >> 4), dk = dK + ((kslot * LY::TILE_BYTES) >> 4);
+        const uint64_t dq = dQ0 + ((q_tile * LY::Q_BYTES) >> 4), dk = dK + ((kslot * LY::K_BYTES) >> 4);
         if (elect_one()) {
+          if constexpr (F8) {
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = ((ks >> 2) * LY::CHUNK_BYTES + (ks & 3) * 32) >> 4;
-            umma_ss(tmem + TMEM_S0 + g * 128, dq + off, dk + off, ID_S, ks > 0 ? 1u : 0u);
+            for (int x = 0; x < TERMS; ++x)
+#pragma unroll
+              for (int ks = 0; ks < D / 32; ++ks)
+                umma_ss_f8(tmem + TMEM_S0 + g * 128, dq + ((x * BM * D + ks * 32) >> 4), dk + (ks * 32 >> 4), ID_S8,
+                           x + ks > 0 ? 1u : 0u);
+          } else {
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = ((ks >> 2) * LY::CHUNK_BYTES + (ks & 3) * 32) >> 4;
+              umma_ss(tmem + TMEM_S0 + g * 128, dq + off, dk + off, ID_S, ks > 0 ? 1u : 0u);
+            }
           }
         }
         __syncwarp();
@@ -680,6 +760,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // What lies behind the sequence's last key in its last tile may be anything, NaN included,
       // and P's zeros there do not silence it: those rows of V become zeros before the product.
       auto clear_tail = [&](int j, uint32_t vslot) {
+        if (F8) return;  // the converting warps have written zeros
         const long long keys = it.len - (long long)j * BN;
         if (keys >= BN) return;
         const int from = keys < 0 ? 0 : (int)keys;
@@ -691,7 +772,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         fence_proxy_async_smem();
         __syncwarp();
       };
-      uint32_t ld = 0;  // SPLIT: next load; PAIR: loads of the pieces before (K_i is ld + 2i)
+      uint32_t ld = 0;  // SPLIT: next load; PAIR: loads of the pieces before (K_i is ld + 2i); F8: tiles before
+      auto k_wait = [&](uint32_t t, uint32_t& slot) -> bool { return kv_wait(t, slot); };
+      auto v_wait = [&](uint32_t t, uint32_t& slot) -> bool {
+        slot = t % LY::V_SLOTS;
+        return wait_all(smem_u32(&bars->v_full[slot]), (t / LY::V_SLOTS) & 1u);
+      };
       while (ok) {
         const Item* src = item_next();
         if (!(ok = src != nullptr)) break;
@@ -702,7 +788,63 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ok = wait_all(smem_u32(&bars->q_full), q_ph);
         if (!ok) break;
         q_ph ^= 1;
-        if constexpr (SPLIT) {
+        if constexpr (F8 && SPLIT) {
+          auto next_s = [&](int i) -> bool {  // S of tile i into buffer i & 1
+            if (!k_wait(ld + i, sK)) return false;
+            tc_fence_after();
+            issue_s(0, i & 1, sK);
+            commit(&bars->s_full[i & 1]);
+            commit(&bars->kv_release[sK]);
+            if (i == it.n - 1) commit(&bars->q_empty);
+            return true;
+          };
+          ok = next_s(0) && (it.n < 2 || next_s(1));
+          for (int i = 0; i < it.n && ok; ++i) {
+            const int g = i & 1;
+            ok = v_wait(ld + i, sV) && wait_all(smem_u32(&bars->p_full[g]), p_ph[g]);
+            if (!ok) break;
+            p_ph[g] ^= 1;
+            tc_fence_after();
+            issue_pv(g, sV, i >= 2);
+            commit(&bars->v_release[sV]);
+            // as below: S(i+2)'s commit also says that O~_g is up to date
+            if (i + 2 < it.n) ok = next_s(i + 2);
+            else commit(&bars->o_done[g]);
+          }
+          ld += it.n;
+        } else if constexpr (F8) {
+          const bool has1 = it.nt > p.tpt;
+          const int n0 = it.n0;
+          auto next_s = [&](int i, int g) -> bool {  // S of tile i for row tile g; the last of them gives K back
+            if (!k_wait(ld + i, sK)) return false;
+            tc_fence_after();
+            issue_s(g, g, sK);
+            commit(&bars->s_full[g]);
+            if (g == (has1 ? 1 : 0)) {
+              commit(&bars->kv_release[sK]);
+              if (i == it.n - 1) commit(&bars->q_empty);
+            }
+            return true;
+          };
+          ok = next_s(0, 0) && (!has1 || next_s(0, 1));
+          for (int i = 0; i < it.n && ok; ++i) {
+            ok = v_wait(ld + i, sV);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const int n_g = g == 0 ? n0 : has1 ? it.n : 0;
+              if (!ok || i >= n_g) continue;
+              ok = wait_all(smem_u32(&bars->p_full[g]), p_ph[g]);
+              if (!ok) break;
+              p_ph[g] ^= 1;
+              tc_fence_after();
+              issue_pv(g, sV, i > 0);
+              if (g == (has1 ? 1 : 0)) commit(&bars->v_release[sV]);
+              if (i + 1 < n_g) ok = next_s(i + 1, g);
+              else commit(&bars->o_done[g]);
+            }
+          }
+          ld += it.n;
+        } else if constexpr (SPLIT) {
           auto next_s = [&](int i) -> bool {  // S of tile i into buffer i & 1
             if (!kv_wait(ld, sK)) return false;
             tc_fence_after();
@@ -803,6 +945,128 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       commit(&bars->mma_drain);
       wait_drain(smem_u32(&bars->mma_drain), 0, p);
       __syncwarp();
+    } else if (F8 && warp >= WARP_CONVERT) {
+      // ======================================================================= queries split, V turned
+      const int ct = (int)threadIdx.x - WARP_CONVERT * 32;
+      const uint32_t sHeld = smem_u32(smem + LY::OFF_HELD), sV = smem_u32(smem + LY::OFF_V);
+      // V: thread = 16 elements of a row at a time. The halves of a warp write other 16-byte pieces of
+      // their rows first, so that the swizzled rows of two 64-column halves do not meet in a bank.
+      constexpr int PIECES = D / 16, TURNS = PIECES, BATCH = 4;
+      const int c16 = ct % PIECES, row0 = ct / PIECES;
+      const uint32_t half = (uint32_t)(c16 >> 2) * LY::CHUNK_BYTES, j0 = (c16 & 3) * 2, odd = c16 >> 2;
+      // Q: D/8 lanes a row, 8 elements each
+      constexpr int QL = D / 8, Q_TURN = 128 / QL;
+      const int ql = ct % QL;
+      signed char* exps = reinterpret_cast<signed char*>(smem + LY::OFF_EXP);
+      uint32_t t = 0, n_q = 0;
+      bool ok = true;
+      while (ok) {
+        const Item* src = item_next();
+        if (!(ok = src != nullptr)) break;
+        const Item it = *src;
+        item_done();
+        if (it.n == 0) break;
+        ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->q_empty), (n_q & 1u) ^ 1u, abort_flag, p));
+        if (!ok) break;
+        const int rows = min(it.nt, SPLIT ? p.tpt : 2 * p.tpt) * p.G, per_tile = p.tpt * p.G;
+        in_bounds(p, it.tok0 >= 0 && it.tok0 + it.nt <= p.T && (it.h + 1) * p.G <= p.q.H);
+#pragma unroll 2
+        for (int x = ct / QL; x < (rows + Q_TURN - 1) / Q_TURN * Q_TURN; x += Q_TURN) {
+          const bool live = x < rows;
+          const int tok = token_of_row(p, SPLIT || x < per_tile ? x : x - per_tile) + (SPLIT || x < per_tile ? 0 : p.tpt);
+          const int head = x - tok * p.G;
+          uint4 u = make_uint4(0, 0, 0, 0);
+          if (live) u = *reinterpret_cast<const uint4*>(p.q.ptr + (long long)(it.tok0 + tok) * p.q.ts + (long long)(it.h * p.G + head) * p.q.hs + ql * 8);
+          float e[8];
+          unpack2<BF16>(u.x, e[0], e[1]);
+          unpack2<BF16>(u.y, e[2], e[3]);
+          unpack2<BF16>(u.z, e[4], e[5]);
+          unpack2<BF16>(u.w, e[6], e[7]);
+          uint32_t top = 0;  // sizes in the order of their bits, NaN above infinity
+#pragma unroll
+          for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(e[k]) & 0x7fffffffu);
+#pragma unroll
+          for (int o = QL / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          int ex = (int)(top >> 23) - 127 - 7;
+          if (top >= 0x7f800000u || top == 0) ex = 0;
+          ex = max(ex, -119);  // 2^-ex is a normal number
+          const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            e[k] *= down;
+            e[k] += e[k] - e[k];  // infinities are NaN here
+          }
+          if (live && ql == 0) exps[(n_q & 1u) * LY::EXP_ROWS + (SPLIT || x < per_tile ? x : x - per_tile + BM)] = (signed char)ex;
+          const uint32_t tile = SPLIT || x < per_tile ? 0u : 1u, row = tile ? x - per_tile : x;
+#pragma unroll
+          for (int m = 0; m < TERMS; ++m) {
+            const uint32_t w0 = pack4_e4m3(e[0], e[1], e[2], e[3]), w1 = pack4_e4m3(e[4], e[5], e[6], e[7]);
+            if (live) {
+#pragma unroll
+              for (int a = 0; a < REP; ++a) {
+                const uint32_t r = row + a * (BM / REP);
+                const uint32_t sw = D == 128 ? r & 7u : (r >> 1) & 3u;
+                st_shared_v2(sQ + tile * LY::Q_BYTES + m * (BM * D) + r * D + ((((uint32_t)ql >> 1) ^ sw) << 4) + (ql & 1) * 8, w0, w1);
+              }
+            }
+            if (m + 1 < TERMS) {
+              uint32_t h[4];
+              unpack4_e4m3(w0, h[0], h[1]);
+              unpack4_e4m3(w1, h[2], h[3]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                float a, b;
+                unpack2<false>(h[k], a, b);
+                e[2 * k] -= a;
+                e[2 * k + 1] -= b;
+              }
+            }
+          }
+        }
+        ++n_q;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->q_full));
+#pragma unroll 1
+        for (int i = 0; i < it.n; ++i, ++t) {
+          const uint32_t hs = t % LY::HELD_SLOTS, slot = t % LY::V_SLOTS;
+          ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->held_full[hs]), (t / LY::HELD_SLOTS) & 1u, abort_flag, p));
+          if (!ok) break;
+          uint32_t v[BATCH][4];
+          const uint32_t from = sHeld + hs * LY::K_BYTES + (uint32_t)ct * 16u;
+#pragma unroll
+          for (int y = 0; y < BATCH; ++y) ld_shared_u4(from + y * 2048u, v[y]);
+          if (t >= (uint32_t)LY::V_SLOTS) {
+            ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->v_release[slot]), ((t / LY::V_SLOTS) & 1u) ^ 1u, abort_flag, p));
+            if (!ok) break;
+          }
+          const long long keys = it.len - (long long)(it.j0 + i) * BN;  // rows that hold a key of the sequence
+          const uint32_t to = sV + slot * LY::TILE_BYTES + half;
+#pragma unroll
+          for (int y0 = 0; y0 < TURNS; y0 += BATCH) {
+#pragma unroll
+            for (int y = 0; y < BATCH; ++y) {
+              const uint32_t row = (uint32_t)(row0 + (y0 + y) * (128 / PIECES));
+              if ((long long)row >= keys) v[y][0] = v[y][1] = v[y][2] = v[y][3] = 0;
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) unpack4_e4m3(v[y][e], w[2 * e], w[2 * e + 1]);
+              if (y0 + BATCH < TURNS) ld_shared_u4(from + (y0 + BATCH + y) * 2048u, v[y]);
+              const uint32_t base = to + row * 128u, sw = row & 7u;
+              st_shared_v4(base + (((j0 + odd) ^ sw) << 4), odd ? w[4] : w[0], odd ? w[5] : w[1], odd ? w[6] : w[2],
+                           odd ? w[7] : w[3]);
+              st_shared_v4(base + (((j0 + 1 - odd) ^ sw) << 4), odd ? w[0] : w[4], odd ? w[1] : w[5],
+                           odd ? w[2] : w[6], odd ? w[3] : w[7]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&bars->v_full[slot]));
+            mbar_arrive(smem_u32(&bars->held_empty[hs]));
+          }
+        }
+      }
     } else if (warp == WARP_WALK) {
       // ======================================================================= items
       if (lane == 0) {
@@ -868,7 +1132,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tmem_dealloc(tmem, TMEM_COLS);
     }
   } else {
-    regs_inc<REGS_SOFTMAX>();
+    regs_inc<regs_softmax(F8)>();
     // ======================================================================= softmax
     const int g = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
     const int copy = r / (BM / REP), row = r % (BM / REP);  // REP = 1: copy 0, row r
@@ -878,6 +1142,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t tS = tmem + lane_off + TMEM_S0 + g * 128, tO = tmem + lane_off + TMEM_O0 + g * 128;
     const float c = fmaxf(p.c, 1e-30f);  // a scale of zero: every finite score still counts as zero
     uint32_t s_ph = 0, o_ph = 0, e_ph = 0;
+    const signed char* exps = reinterpret_cast<const signed char*>(smem + LY::OFF_EXP) + (SPLIT ? row : g * BM + row);
     bool ok = true;
     // both warpgroups (8 warps)
     auto epi_sync = [&]() -> bool {
@@ -906,7 +1171,34 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int lim = (!valid ? 0 : p.causal ? max(0, min(item->vis0 + tok, item->len)) : item->len) - item->j0 * BN;
       const int n_my = !SPLIT && g == 0 ? item->n0 : item->n;
       float m_run = -INFINITY, l_run = 0.f;
-      for (int i = SPLIT ? g : 0; i < n_my; i += SPLIT ? 2 : 1) {
+      // F8: lane x has the scale of key group x & 15 (8 keys; a tile of a large page has one scale), of K
+      // for x < 16 and of V behind. The next tile's scale and the page of the one after are on their way.
+      constexpr int STEP = SPLIT ? 2 : 1;
+      float vref = 1.f, vinv = 128.f, scale_now = 0.f, scale_next = 0.f;
+      float cr = c;  // with the row's 2^e
+      int page_next = -1;
+      [[maybe_unused]] const bool small_pages = p.page_size < BN;
+      auto ask_page = [&](int i) -> int {
+        const int group = lane & 15, j = item->j0 + i;
+        const long long key = (long long)j * BN + (small_pages ? copy * CW + group * 8 : 0);
+        if (i >= n_my || group >= CW / 8 || key >= item->len) return -1;
+        return p.table[(size_t)item->b * p.table_stride + (uint32_t)key / (uint32_t)p.page_size];
+      };
+      auto ask_scale = [&](int page) -> float {  // of no key, and of a bad page (which reads as zeros): 1 and 0
+        if (page < 0 || page >= p.num_pages) return lane < 16 ? 1.f : 0.f;
+        return (lane < 16 ? p.ks : p.vs)[(size_t)page * p.Hkv + item->h];
+      };
+      if (F8) {
+        const int page = ask_page(SPLIT ? g : 0);
+        page_next = ask_page((SPLIT ? g : 0) + STEP);
+        scale_next = ask_scale(page);
+      }
+      for (int i = SPLIT ? g : 0; i < n_my; i += STEP) {
+        if (F8) {
+          scale_now = scale_next;
+          scale_next = ask_scale(page_next);
+          page_next = ask_page(i + 2 * STEP);
+        }
         ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->s_full[g]), s_ph, abort_flag, p));
         if (!ok) break;
         s_ph ^= 1;
@@ -918,6 +1210,42 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
         for (int q = 0; q < CW / 32; ++q) reg_fence(sr[q]);
         auto sv = [&](int k) { return __uint_as_float(sr[k >> 5][k & 31]); };
+        if (F8 && i < STEP)  // (the item's exponents, written before its first S; the next but one takes their place)
+          cr = fmaxf(c * __uint_as_float((uint32_t)(127 + exps[(n_item & 1u) * LY::EXP_ROWS]) << 23), 1e-30f);
+        float ct = F8 ? cr : c, beta = 1.f;  // F8: with the tile's scale of K; what O~'s unit shrinks by
+        [[maybe_unused]] float lf = 0.f;
+        [[maybe_unused]] const uint32_t scales = smem_u32(smem + LY::OFF_SCALE) + (uint32_t)warp * (SPLIT ? 256u : 128u);
+        if (F8) {
+          // the largest scale of V (positive numbers in the order of their bits)
+          const float vt = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < 16 ? 0u : __float_as_uint(scale_now)));
+          if (i < STEP || vt > vref) {
+            const float v_new = fmaxf(vt, 7.8886090522101181e-31f);  // 2^-100: pages of zeros
+            beta = vref / v_new;
+            vref = v_new;
+            vinv = 128.f / v_new;
+          }
+          if (small_pages) {
+            st_shared_u32(scales + lane * 4, __float_as_uint(scale_now * (lane < 16 ? 1.f : vinv)));
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < CW / 32; ++q) {
+              float k4[4];
+              ld_shared_v4(scales + q * 16, k4);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const uint64_t kk = f2(k4[k >> 2], k4[k >> 2]);
+                float x0, x1;
+                f2_split(f2_mul(f2(__uint_as_float(sr[q][2 * k]), __uint_as_float(sr[q][2 * k + 1])), kk), x0, x1);
+                sr[q][2 * k] = __float_as_uint(x0);
+                sr[q][2 * k + 1] = __float_as_uint(x1);
+              }
+            }
+          } else {
+            ct = fmaxf(cr * __shfl_sync(0xffffffffu, scale_now, 0), 1e-30f);
+            // a page whose V is below 2^-40 of the largest counts as that
+            lf = log2f(fmaxf(__shfl_sync(0xffffffffu, scale_now, 16) * vinv, 1.1641532182693481e-10f));
+          }
+        }
         const int vis = lim - i * BN - copy * CW;
         // Scores of keys that a row does not see become -inf, 32 columns at a time where some row of
         // the warp needs it (rows that hold no query do not count). c > 0 keeps them at -inf, and
@@ -940,10 +1268,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             t[x] = max3(sv(3 * x), 3 * x + 1 < CW ? sv(3 * x + 1) : -INFINITY, 3 * x + 2 < CW ? sv(3 * x + 2) : -INFINITY);
           mt = tree_max<NT>(t);
         }
-        const float m_tile = (mt == -INFINITY || !valid) ? -INFINITY : mt * c;
+        const float m_tile = (mt == -INFINITY || !valid) ? -INFINITY : mt * ct;
         float m_new = m_run, alpha = 1.f;
-        bool rescale = false;
-        if (i < (SPLIT ? 2 : 1)) {
+        bool rescale = F8 && i >= STEP && beta != 1.f;
+        if (i < STEP) {
           m_new = m_tile;
         } else if (m_tile > m_run + RESCALE_THRESHOLD) {
           m_new = m_tile;
@@ -951,21 +1279,44 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           rescale = true;
         }
         const float nb = (m_new == -INFINITY) ? 0.f : -m_new;
-        const uint64_t c2 = f2(c, c), nb2 = f2(nb, nb);
+        const float nl = F8 ? nb + lf : nb;
+        const uint64_t c2 = f2(ct, ct), nb2 = f2(nl, nl);
         uint64_t acc[4] = {0, 0, 0, 0};
         uint32_t pk[CW / 2];
+        auto weights = [&](auto scaled) {
 #pragma unroll
-        for (int k = 0; k < CW / 2; ++k) {
-          float t0, t1;
-          f2_split(f2_fma(f2(sv(2 * k), sv(2 * k + 1)), c2, nb2), t0, t1);
-          const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
-          acc[k & 3] = f2_add(acc[k & 3], f2(p0, p1));
-          pk[k] = pack2<BF16>(p0, p1);
-        }
+          for (int q = 0; q < CW / 32; ++q) {
+            float v4[4];
+            if (decltype(scaled)::value) ld_shared_v4(scales + 64 + q * 16, v4);
+#pragma unroll
+            for (int kk = 0; kk < 16; ++kk) {
+              const int k = q * 16 + kk;
+              float t0, t1;
+              f2_split(f2_fma(f2(sv(2 * k), sv(2 * k + 1)), c2, nb2), t0, t1);
+              const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+              acc[k & 3] = f2_add(acc[k & 3], f2(p0, p1));
+              if (decltype(scaled)::value) {
+                float y0, y1;
+                f2_split(f2_mul(f2(p0, p1), f2(v4[kk >> 2], v4[kk >> 2])), y0, y1);
+                pk[k] = pack2<false>(y0, y1);
+              } else {
+                pk[k] = pack2<BF16 && !F8>(p0, p1);
+              }
+            }
+          }
+        };
+        if (F8 && small_pages) weights(std::integral_constant<bool, F8>{});
+        else weights(std::false_type{});
         float a0, a1;
         f2_split(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a0, a1);
+        if (F8 && !small_pages) {  // these were P'
+          const float back = ex2_approx(-lf);
+          a0 *= back;
+          a1 *= back;
+        }
         if (__any_sync(0xffffffffu, rescale)) {
-          const uint64_t al2 = f2(alpha, alpha);
+          const float alpha_o = F8 ? alpha * beta : alpha;
+          const uint64_t al2 = f2(alpha_o, alpha_o);
 #pragma unroll
           for (int q = 0; q < D / 32; ++q) {
             uint32_t o[32];
@@ -1036,6 +1387,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       } else {
         f = 1.f;
       }
+      if (F8) f *= vref * 0.0078125f;  // O~'s unit
       // a whole item's O~ is divided by l; a partial state stays as it is
       if (!partial) f *= sees ? 1.f / l : 0.f;
       const int prow = SPLIT ? row : g * BM + row;
@@ -1090,7 +1442,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             tmem_wait_ld();
             reg_fence(o);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) put(k, o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            for (int k = 0; k < 8; ++k) {
+              if (F8)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[4 * k + e] = __float_as_uint(__uint_as_float(o[4 * k + e]) * f);
+              put(k, o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            }
             send(q * 128);
           }
         } else {
@@ -1125,15 +1482,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (worked) {
 #pragma unroll 1
             for (int q = 0; q < COLS; q += 64) {
-              uint32_t o[2][32];
-              tmem_ld32(tO + col0 + q, o[0]);
-              tmem_ld32(tO + col0 + q + 32, o[1]);
+              constexpr int N32 = COLS < 64 ? 1 : 2;  // 32 columns at a time, or 64
+              uint32_t o[N32][32];
+#pragma unroll
+              for (int x = 0; x < N32; ++x) tmem_ld32(tO + col0 + q + x * 32, o[x]);
               tmem_wait_ld();
-              reg_fence(o[0]);
-              reg_fence(o[1]);
+#pragma unroll
+              for (int x = 0; x < N32; ++x) reg_fence(o[x]);
               if (valid) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
+                for (int k = 0; k < 8 * N32; ++k) {
                   const uint32_t* v = &o[k >> 3][4 * (k & 7)];
                   st_shared_v4(stage_at(srow, q / 4 + k), __float_as_uint(__uint_as_float(v[0]) * f),
                                __float_as_uint(__uint_as_float(v[1]) * f), __float_as_uint(__uint_as_float(v[2]) * f),
@@ -1173,7 +1531,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (D == 64 || 2 * REP * R <= LY::STAGE_ROWS) {
           ok = join(std::integral_constant<int, D>{}, 0);
         } else if constexpr (D == 128) {
-          ok = join(std::integral_constant<int, 64>{}, 0) && epi_sync() && join(std::integral_constant<int, 64>{}, 64);
+          if (!F8 || 2 * REP * R <= 2 * LY::STAGE_ROWS) {
+            ok = join(std::integral_constant<int, 64>{}, 0) && epi_sync() && join(std::integral_constant<int, 64>{}, 64);
+          } else if constexpr (F8) {
+            for (int q = 0; q < 128 && ok; q += 32)
+              ok = (q == 0 || epi_sync()) && join(std::integral_constant<int, 32>{}, q);
+          }
         }
         if (!ok) break;
       }

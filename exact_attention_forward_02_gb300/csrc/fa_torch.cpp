@@ -34,6 +34,8 @@ struct Library {
   decltype(&fa_paged_append) append = nullptr;
   decltype(&fa_fwd_paged) attend = nullptr;
   decltype(&fa_fwd_paged_workspace_bytes) attend_bytes = nullptr;
+  decltype(&fa_paged_append_fp8) append8 = nullptr;
+  decltype(&fa_fwd_paged_fp8) attend8 = nullptr;
 } lib;
 
 // A refusal: TypeError or ValueError in Python.
@@ -146,10 +148,11 @@ fa_rope rope_of(const at::Tensor& t, bool interleaved, int64_t d) {
                  as_int(t.size(0), "the table's length"), (int)t.size(1), interleaved};
 }
 
-// fa_paged_kv of [num_pages, Hkv, page_size, d] tensors with the same strides
-fa_paged_kv cache_of(const at::Tensor& k, const at::Tensor& v, const at::Tensor& like) {
-  if (k.scalar_type() != like.scalar_type() || v.scalar_type() != like.scalar_type())
-    bad_type("the cache must have the other tensors' dtype");
+// fa_paged_kv of [num_pages, Hkv, page_size, d] tensors of `type` with the same strides
+fa_paged_kv cache_of(const at::Tensor& k, const at::Tensor& v, at::ScalarType type) {
+  if (k.scalar_type() != type || v.scalar_type() != type)
+    bad_type(type == at::kFloat8_e4m3fn ? "k_pages and v_pages must be float8_e4m3fn"
+                                        : "the cache must have the other tensors' dtype");
   if (k.dim() != 4 || k.sizes() != v.sizes())
     bad_value("k_pages and v_pages must both be [num_pages, Hkv, page_size, d]");
   long long s[4];
@@ -163,11 +166,26 @@ fa_paged_kv cache_of(const at::Tensor& k, const at::Tensor& v, const at::Tensor&
                      as_int(k.size(3), "the head dimension")};
 }
 
+// The rows of a cache that is written do not overlap.
+void apart(const at::Tensor& pages) {
+  for (int i = 0; i < 3; ++i)
+    if (pages.size(i) > 1 && pages.stride(i) == 0) bad_value("the rows of the cache must not overlap");
+}
+
+// The scales [num_pages, Hkv] of an 8-bit cache
+float* scales_of(const at::Tensor& t, const char* what, const fa_paged_kv& kv) {
+  if (t.scalar_type() != at::kFloat) bad_type(std::string(what) + " must be float32");
+  if (t.sizes() != at::IntArrayRef({kv.num_pages, kv.Hkv}) || !t.is_contiguous())
+    bad_value(std::string(what) + " must be contiguous " + shape_text({kv.num_pages, kv.Hkv}) + ", not " +
+              shape_text(t.sizes()));
+  return static_cast<float*>(t.data_ptr());
+}
+
 // Nothing here is recorded by autograd: an input that requires a gradient would lose it unseen.
 void not_recorded(std::initializer_list<std::pair<const at::Tensor*, const char*>> inputs) {
   if (!at::GradMode::is_enabled()) return;
   for (const auto& [t, what] : inputs)
-    if (t->requires_grad())
+    if (t->defined() && t->requires_grad())
       bad_value(std::string(what) + " requires grad and the call is not recorded by autograd: make it under "
                                     "torch.no_grad(), or pass the tensor detached");
 }
@@ -344,45 +362,57 @@ struct Batch {
   }
 };
 
-// (k, v, k_pages, v_pages, block_table, cu_seqlens, seq_lens, rope, interleaved, stream)
+// (k, v, k_pages, v_pages, block_table, cu_seqlens, seq_lens, rope, interleaved, stream), and for a cache held
+// in 8 bits k_scale, v_scale
+template <bool F8>
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 10, [&]() -> PyObject* {
+  return guarded(n, F8 ? 12 : 10, [&]() -> PyObject* {
     const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &kp = tensor(a[2], "k_pages"),
                      &vp = tensor(a[3], "v_pages"), &table = tensor(a[4], "block_table"),
                      &cu = tensor(a[5], "cu_seqlens"), &lens = tensor(a[6], "seq_lens");
     const at::Tensor rope = optional_tensor(a[7], "rope");
+    const at::Tensor ks = F8 ? tensor(a[10], "k_scale") : at::Tensor(), vs = F8 ? tensor(a[11], "v_scale") : at::Tensor();
     const fa_dtype dt = type_code(k, "k and v");
     if (k.dim() != 3) bad_value("k and v must be [T, Hkv, d]");
     const fa_heads hk = heads_of(k, "k", k), hv = heads_of(v, "v", k, k.sizes());
-    const fa_paged_kv kv = cache_of(kp, vp, k);
+    const fa_paged_kv kv = cache_of(kp, vp, F8 ? at::kFloat8_e4m3fn : k.scalar_type());
     if (kv.Hkv != hk.H || kv.d != k.size(2)) bad_value("the cache must have k's heads and head dimension");
-    for (int i = 0; i < 3; ++i)
-      if (kp.size(i) > 1 && kp.stride(i) == 0) bad_value("the rows of the cache must not overlap");
+    apart(kp);
+    float* const k_scale = F8 ? scales_of(ks, "k_scale", kv) : nullptr;
+    float* const v_scale = F8 ? scales_of(vs, "v_scale", kv) : nullptr;
     const Batch batch(table, cu, lens);
     const fa_rope rp = rope_of(rope, as_bool(a[8], "interleaved"), k.size(2));
-    OneDevice(k).also(v).also(kp).also(vp).also(table).also(cu).also(lens).also(rope);
-    not_recorded({{&k, "k"}, {&v, "v"}, {&kp, "k_pages"}, {&vp, "v_pages"}});
+    OneDevice(k).also(v).also(kp).also(vp).also(table).also(cu).also(lens).also(rope).also(ks).also(vs);
+    not_recorded({{&k, "k"}, {&v, "v"}, {&kp, "k_pages"}, {&vp, "v_pages"}, {&ks, "k_scale"}, {&vs, "v_scale"}});
+    const int T = as_int(k.size(0), "T");
     Launch on(k, a[9]);
-    const int rc = lib.append(&kv, &hk, &hv, batch.B, as_int(k.size(0), "T"), batch.cu, batch.lens, batch.table,
-                              batch.width, &rp, dt, on.stream);
+    const int rc = F8 ? lib.append8(&kv, k_scale, v_scale, &hk, &hv, batch.B, T, batch.cu, batch.lens, batch.table,
+                                    batch.width, &rp, dt, on.stream)
+                      : lib.append(&kv, &hk, &hv, batch.B, T, batch.cu, batch.lens, batch.table, batch.width, &rp, dt,
+                                   on.stream);
     return PyLong_FromLong(rc);
   });
 }
 
-// (q, k_pages, v_pages, block_table, cu_seqlens, seq_lens, max_q, causal, scale, out, lse, workspace, stream)
+// (q, k_pages, v_pages, block_table, cu_seqlens, seq_lens, max_q, causal, scale, out, lse, workspace, stream), and
+// for a cache held in 8 bits k_scale, v_scale
+template <bool F8>
 PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 13, [&]() -> PyObject* {
+  return guarded(n, F8 ? 15 : 13, [&]() -> PyObject* {
     const at::Tensor &q = tensor(a[0], "q"), &kp = tensor(a[1], "k_pages"), &vp = tensor(a[2], "v_pages"),
                      &table = tensor(a[3], "block_table"), &cu = tensor(a[4], "cu_seqlens"),
                      &lens = tensor(a[5], "seq_lens");
     at::Tensor out = optional_tensor(a[9], "out"), lse = optional_tensor(a[10], "lse");
     const at::Tensor ws = optional_tensor(a[11], "workspace");
+    const at::Tensor ks = F8 ? tensor(a[13], "k_scale") : at::Tensor(), vs = F8 ? tensor(a[14], "v_scale") : at::Tensor();
     const fa_dtype dt = type_code(q, "q");
     if (q.dim() != 3) bad_value("q must be [T, Hq, d]");
     const int T = as_int(q.size(0), "T");
     const fa_heads hq = heads_of(q, "q", q);
-    const fa_paged_kv kv = cache_of(kp, vp, q);
+    const fa_paged_kv kv = cache_of(kp, vp, F8 ? at::kFloat8_e4m3fn : q.scalar_type());
     if (kv.d != q.size(2)) bad_value("the cache must have q's head dimension");
+    const float* const k_scale = F8 ? scales_of(ks, "k_scale", kv) : nullptr;
+    const float* const v_scale = F8 ? scales_of(vs, "v_scale", kv) : nullptr;
     const Batch batch(table, cu, lens);
     const int max_q = as_int(a[6], "max_q");
     const bool causal = as_bool(a[7], "causal");
@@ -394,43 +424,51 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
       bad_value("lse must be a contiguous [T, Hq] float32 tensor");
     if (ws.defined() && (ws.scalar_type() != at::kByte || !ws.is_contiguous()))
       bad_value("workspace must be a contiguous uint8 tensor");
-    OneDevice(q).also(kp).also(vp).also(table).also(cu).also(lens).also(out).also(lse).also(ws);
-    not_recorded({{&q, "q"}, {&kp, "k_pages"}, {&vp, "v_pages"}});
+    OneDevice(q).also(kp).also(vp).also(table).also(cu).also(lens).also(out).also(lse).also(ws).also(ks).also(vs);
+    not_recorded({{&q, "q"}, {&kp, "k_pages"}, {&vp, "v_pages"}, {&ks, "k_scale"}, {&vs, "v_scale"}});
     Launch on(q, a[12]);
     if (!out.defined()) ho = heads_of(out = rows_like(q), "out", q);
     if (!lse.defined()) lse = fresh(q, {T, hq.H}, at::kFloat);
     const bool narrow = (int64_t)batch.width * kv.page_size <= FA_PAGED_WHOLE_KEYS;  // needs no workspace
     Scratch own;
     if (!ws.defined() && !narrow) own.take(lib.attend_bytes(hq.H, kv.Hkv, kv.d, max_q), on.stream);
-    const int rc = lib.attend(&kv, &hq, &ho, static_cast<float*>(lse.data_ptr()), batch.B, T, max_q, batch.cu,
-                              batch.lens, batch.table, batch.width, scale, causal, dt,
-                              ws.defined() ? ws.data_ptr() : own.ptr, ws.defined() ? (size_t)ws.numel() : own.size,
-                              on.stream);
+    float* const L = static_cast<float*>(lse.data_ptr());
+    void* const work = ws.defined() ? ws.data_ptr() : own.ptr;
+    const size_t bytes = ws.defined() ? (size_t)ws.numel() : own.size;
+    const int rc = F8 ? lib.attend8(&kv, k_scale, v_scale, &hq, &ho, L, batch.B, T, max_q, batch.cu, batch.lens,
+                                    batch.table, batch.width, scale, causal, dt, work, bytes, on.stream)
+                      : lib.attend(&kv, &hq, &ho, L, batch.B, T, max_q, batch.cu, batch.lens, batch.table, batch.width,
+                                   scale, causal, dt, work, bytes, on.stream);
     return rc == FA_OK ? tuple_of({out, lse}) : PyLong_FromLong(rc);
   });
 }
 
-// bind(addresses of the six library functions in Library's order)
+// bind(addresses of the library's functions in Library's order)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 6, [&]() -> PyObject* {
-    void* f[6];
-    for (int i = 0; i < 6; ++i) {
+  constexpr int COUNT = sizeof(Library) / sizeof(void*);
+  return guarded(n, COUNT, [&]() -> PyObject* {
+    void* f[COUNT];
+    for (int i = 0; i < COUNT; ++i) {
       f[i] = PyLong_AsVoidPtr(a[i]);
       if (!f[i]) bad_value("a function is missing");
     }
-    lib.norm_rope = reinterpret_cast<decltype(lib.norm_rope)>(f[0]);
-    lib.norm_rope_bwd = reinterpret_cast<decltype(lib.norm_rope_bwd)>(f[1]);
-    lib.norm_rope_bwd_bytes = reinterpret_cast<decltype(lib.norm_rope_bwd_bytes)>(f[2]);
-    lib.append = reinterpret_cast<decltype(lib.append)>(f[3]);
-    lib.attend = reinterpret_cast<decltype(lib.attend)>(f[4]);
-    lib.attend_bytes = reinterpret_cast<decltype(lib.attend_bytes)>(f[5]);
+    int i = 0;
+    auto set = [&](auto& fn) { fn = reinterpret_cast<std::decay_t<decltype(fn)>>(f[i++]); };
+    set(lib.norm_rope), set(lib.norm_rope_bwd), set(lib.norm_rope_bwd_bytes), set(lib.append), set(lib.attend);
+    set(lib.attend_bytes), set(lib.append8), set(lib.attend8);
     Py_RETURN_NONE;
   });
 }
 
 #define FAST(name, f) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FAST("bind", bind),     FAST("norm_rope", norm_rope), FAST("norm_rope_backward", norm_rope_backward),
-                         FAST("append", append), FAST("attend", attend),       {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {FAST("bind", bind),
+                         FAST("norm_rope", norm_rope),
+                         FAST("norm_rope_backward", norm_rope_backward),
+                         FAST("append", append<false>),
+                         FAST("attend", attend<false>),
+                         FAST("append_fp8", append<true>),
+                         FAST("attend_fp8", attend<true>),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fa_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -130,6 +130,9 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
 }
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
 __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -218,7 +221,8 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
 // Shared-memory matrix descriptor (tcgen05 format): start address, leading- and
 // stride-dimension byte offsets (all >> 4), descriptor version 1 (bits 46-47),
 // base offset 0 (tiles are 1024-byte aligned), swizzle mode in bits 61-63.
-enum : uint64_t { UMMA_SWIZZLE_128B = 2 };
+enum : uint64_t { UMMA_SWIZZLE_128B = 2, UMMA_SWIZZLE_64B = 4 };
+template <uint64_t SWIZZLE = UMMA_SWIZZLE_128B>
 __device__ __forceinline__ uint64_t umma_smem_desc(uint32_t saddr, uint32_t lbo_bytes,
                                                    uint32_t sbo_bytes) {
   uint64_t d = 0;
@@ -226,7 +230,7 @@ __device__ __forceinline__ uint64_t umma_smem_desc(uint32_t saddr, uint32_t lbo_
   d |= (uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16;
   d |= (uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32;
   d |= (uint64_t)1 << 46;
-  d |= UMMA_SWIZZLE_128B << 61;
+  d |= SWIZZLE << 61;
   return d;
 }
 
@@ -407,6 +411,22 @@ __device__ __forceinline__ uint32_t pack4_e4m3(float x0, float x1, float x2, flo
       : "=r"(r)
       : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
   return r;
+}
+
+__device__ __forceinline__ void ld_shared_u4(uint32_t addr, uint32_t (&x)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+               : "r"(addr)
+               : "memory");
+}
+// four E4M3 bytes -> two words of two fp16 values each, exactly (first value in the lowest bits)
+__device__ __forceinline__ void unpack4_e4m3(uint32_t v, uint32_t& w0, uint32_t& w1) {
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "mov.b32 {lo, hi}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(w0), "=r"(w1)
+      : "r"(v));
 }
 
 // unpack one 32-bit word of two 16-bit values (low half first) into fp32

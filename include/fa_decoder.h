@@ -143,6 +143,33 @@ int fa_fwd_paged(const fa_paged_kv* kv, const fa_heads* q, const fa_heads* O, fl
                  int table_stride, float scale, int causal, fa_dtype dtype, void* workspace,
                  size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------- a cache held in 8 bits
+ * A paged cache whose k and v hold E4M3 bytes, with one fp32 scale for each page and key head of K and
+ * of V: k_scale, v_scale [num_pages, Hkv], contiguous; an element is scale * byte. fa_paged_kv then
+ * counts its strides in bytes, multiples of 16.
+ *
+ * fa_paged_append_fp8 -- fa_paged_append for such a cache. For the new tokens of a page, with a the
+ * largest |x| of their keys (rotated, in fp32) or values, s_new is the smallest power of two >= a / 448
+ * (at least 2^-100). If the page's first slot is among them its scale becomes s_new; else it becomes
+ * max(s_old, s_new), and where that is more than s_old the codes of its older tokens are rounded anew
+ * (exactly, but for elements below 2^-14 of the page's largest). An element x is held as x / scale,
+ * rounded to nearest even; what is not finite is held as NaN and does not count in a. Scales given by
+ * others may be any positive numbers.
+ * One kernel. What is skipped and reported: as in fa_paged_append. */
+int fa_paged_append_fp8(const fa_paged_kv* kv, float* k_scale, float* v_scale, const fa_heads* k,
+                        const fa_heads* v, int B, int T, const int* cu_seqlens, const int* seq_lens,
+                        const int* block_table, int table_stride, const fa_rope* rope, fa_dtype dtype,
+                        void* stream);
+
+/* fa_fwd_paged_fp8 -- fa_fwd_paged over such a cache: q and O in `dtype`, everything else as there (the
+ * workspace, too, is fa_fwd_paged_workspace_bytes()). Products take the bytes exactly as they are held; P
+ * is rounded to fp16 with v_scale in it. Scales must be positive and finite, or 0 for a page of zeros;
+ * where the v_scale of a page is below 2^-40 of another's of the same sequence it may count as that. */
+int fa_fwd_paged_fp8(const fa_paged_kv* kv, const float* k_scale, const float* v_scale, const fa_heads* q,
+                     const fa_heads* O, float* L, int B, int T, int max_q, const int* cu_seqlens,
+                     const int* seq_lens, const int* block_table, int table_stride, float scale, int causal,
+                     fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
