@@ -11,7 +11,7 @@ Function names follow the C ABI:
 plus a tensor-level convenience ``attention(q, k, v, causal, scale)`` -> (O, L), and for the
 operators next to it in a decoder block ``qk_norm_rope``, ``qk_norm_rope_backward``,
 ``paged_append`` and ``attention_paged``, for a cache held in 8 bits ``paged_append_fp8`` and
-``attention_paged_fp8``.
+``attention_paged_fp8``, for eviction from either ``paged_key_weights`` and ``paged_evict``.
 """
 from __future__ import annotations
 
@@ -150,6 +150,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_paged_append_fp8.argtypes = [kv, vp, vp, heads, heads, i, i, vp, vp, vp, i, rope, i, vp]
     lib.fa_fwd_paged_fp8.restype = i
     lib.fa_fwd_paged_fp8.argtypes = [kv, vp, vp, heads, heads, vp, i, i, i, vp, vp, vp, i, f, i, i, vp, n, vp]
+    lib.fa_paged_key_weights.restype = i
+    lib.fa_paged_key_weights.argtypes = [kv, vp, heads, vp, vp, i, i, i, vp, vp, vp, i, f, i, i, vp]
+    lib.fa_paged_evict_workspace_bytes.restype = n
+    lib.fa_paged_evict_workspace_bytes.argtypes = [i] * 4
+    lib.fa_paged_evict.restype = i
+    lib.fa_paged_evict.argtypes = [kv, vp, vp, vp, i, vp, vp, i, i, i, vp, vp, vp, n, vp]
     lib.fa_debug_cap_workspace.restype = ctypes.c_int
     lib.fa_debug_cap_workspace.argtypes = [ctypes.c_longlong]
     return lib
@@ -396,6 +402,25 @@ def fa_fwd_paged_fp8(kv, k_scale, v_scale, q, O, L, B, T, max_q, cu_seqlens, seq
                                     workspace, int(workspace_bytes), stream))
 
 
+def fa_paged_key_weights(kv, k_scale, q, L, weights, B, T, max_q, cu_seqlens, seq_lens, block_table, table_stride,
+                         scale, causal, dtype, stream) -> int:
+    """C-ABI call adding new tokens' attention weights to those of the cached tokens."""
+    return int(lib.fa_paged_key_weights(kv, k_scale, q, L, weights, int(B), int(T), int(max_q), cu_seqlens, seq_lens,
+                                        block_table, int(table_stride), float(scale), int(bool(causal)), int(dtype),
+                                        stream))
+
+
+def fa_paged_evict(kv, k_scale, v_scale, weights, B, seq_lens, block_table, table_stride, budget, recent, kept,
+                   new_lens, workspace, workspace_bytes, stream) -> int:
+    """C-ABI call cutting each key head's cached tokens to a budget."""
+    return int(lib.fa_paged_evict(kv, k_scale, v_scale, weights, int(B), seq_lens, block_table, int(table_stride),
+                                  int(budget), int(recent), kept, new_lens, workspace, int(workspace_bytes), stream))
+
+
+def fa_paged_evict_workspace_bytes(B, Hkv, budget, held8) -> int:
+    return int(lib.fa_paged_evict_workspace_bytes(int(B), int(Hkv), int(budget), int(bool(held8))))
+
+
 _torch_calls = None
 
 
@@ -411,7 +436,8 @@ def _calls():
 
         from . import _fa_torch
         names = ("fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_bytes", "fa_paged_append",
-                 "fa_fwd_paged", "fa_fwd_paged_workspace_bytes", "fa_paged_append_fp8", "fa_fwd_paged_fp8")
+                 "fa_fwd_paged", "fa_fwd_paged_workspace_bytes", "fa_paged_append_fp8", "fa_fwd_paged_fp8",
+                 "fa_paged_key_weights", "fa_paged_evict", "fa_paged_evict_workspace_bytes")
         _fa_torch.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
         _torch_calls = _fa_torch
     return _torch_calls
@@ -507,4 +533,37 @@ def attention_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_s
                             workspace, stream, k_scale, v_scale)
     if type(r) is int:
         raise FAError(r, "fa_fwd_paged_fp8")
+    return r
+
+
+# ------------------------------------------------------------------------ eviction from a cache
+def paged_key_weights(q, lse, k_pages, weights, block_table, cu_seqlens, seq_lens, max_q: int, causal: bool = True,
+                      scale: float | None = None, k_scale=None, stream=None):
+    """Adds the attention weight that the new tokens give to each cached token to `weights`, in place.
+
+    q [T, Hq, d] and lse [T, Hq] as attention_paged had and returned them; k_pages, the batch, max_q, causal
+    and scale as there, k_scale for a cache held in 8 bits; weights: fp32 [num_pages, Hkv, page_size]. A
+    new token's own weight starts from 0, whatever stood in its place (see include/fa_decoder.h).
+    """
+    r = _calls().key_weights(q, lse, k_pages, weights, block_table, cu_seqlens, seq_lens, max_q, causal, scale,
+                             k_scale, stream)
+    if r != 0:
+        raise FAError(r, "fa_paged_key_weights")
+
+
+def paged_evict(k_pages, v_pages, weights, block_table, seq_lens, budget: int, recent: int, k_scale=None,
+                v_scale=None, kept=None, new_lens=None, workspace=None, stream=None):
+    """Cuts each key head of every sequence to `budget` cached tokens, in place: the last `recent` and, of
+    those before, the ones of the largest weight (see include/fa_decoder.h).
+
+    k_pages, v_pages, weights (and for a cache held in 8 bits k_scale, v_scale) are moved together; seq_lens is
+    read. Returns (kept, new_lens): int32 [B, Hkv, budget], the position that each place's token had (-1
+    behind the last token of a shorter sequence), and int32 [B], the lengths from now on; allocated unless
+    given (new_lens may be seq_lens). `workspace`: a uint8 tensor of at least
+    fa_paged_evict_workspace_bytes(...) bytes, allocated for the call when None.
+    """
+    r = _calls().evict(k_pages, v_pages, weights, block_table, seq_lens, budget, recent, k_scale, v_scale, kept,
+                       new_lens, workspace, stream)
+    if type(r) is int:
+        raise FAError(r, "fa_paged_evict")
     return r

@@ -178,6 +178,7 @@ struct Layout {
   // barriers and items; F8: and the exponents of the query rows of two items
   static constexpr int BAR_BYTES = F8 ? 768 : 1024, EXP_ROWS = SPLIT ? BM : 2 * BM;
   static constexpr int HEAD_BYTES = BAR_BYTES + (F8 ? 2 * EXP_ROWS : 0);
+  static constexpr int V_RING = F8 ? V_SLOTS : 1, HELD_RING = F8 ? HELD_SLOTS : 1;
   static constexpr int FIT = (SMEM_LIMIT - Q_TILES * Q_BYTES - STAGE_BYTES - STATE_BYTES - SCALE_BYTES - HEAD_BYTES -
                               V_SLOTS * TILE_BYTES - HELD_SLOTS * K_BYTES) / K_BYTES;
   static constexpr int KV_SLOTS = FIT > MAX_SLOTS ? MAX_SLOTS : FIT;
@@ -194,7 +195,8 @@ struct Layout {
 
 // ----------------------------------------------------------------------------- waits
 // Bounded: a wait past the limit records FA_ERR_TIMEOUT and stops every role of the block.
-__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, const Params& p,
+template <typename P>
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, const P& p,
                                           uint32_t limits) {
   const uint64_t t0 = globaltimer_ns();
   while (true) {
@@ -209,13 +211,15 @@ __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatil
     }
   }
 }
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, const Params& p,
+template <typename P>
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, const P& p,
                                          uint32_t limits = 1) {
   if (mbar_try_wait(bar, parity)) return true;
   return wait_slow(bar, parity, abort_flag, p, limits);
 }
 // on the way out after an abort: ignores the flag, still bounded
-__device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, const Params& p) {
+template <typename P>
+__device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, const P& p) {
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity))
     if (globaltimer_ns() - t0 > p.wait_limit_ns) {
@@ -775,8 +779,8 @@ __global__ void __launch_bounds__(num_warps(F8) * 32, 1)
       uint32_t ld = 0;  // SPLIT: next load; PAIR: loads of the pieces before (K_i is ld + 2i); F8: tiles before
       auto k_wait = [&](uint32_t t, uint32_t& slot) -> bool { return kv_wait(t, slot); };
       auto v_wait = [&](uint32_t t, uint32_t& slot) -> bool {
-        slot = t % LY::V_SLOTS;
-        return wait_all(smem_u32(&bars->v_full[slot]), (t / LY::V_SLOTS) & 1u);
+        slot = t % LY::V_RING;
+        return wait_all(smem_u32(&bars->v_full[slot]), (t / LY::V_RING) & 1u);
       };
       while (ok) {
         const Item* src = item_next();
@@ -1029,15 +1033,15 @@ __global__ void __launch_bounds__(num_warps(F8) * 32, 1)
         if (lane == 0) mbar_arrive(smem_u32(&bars->q_full));
 #pragma unroll 1
         for (int i = 0; i < it.n; ++i, ++t) {
-          const uint32_t hs = t % LY::HELD_SLOTS, slot = t % LY::V_SLOTS;
-          ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->held_full[hs]), (t / LY::HELD_SLOTS) & 1u, abort_flag, p));
+          const uint32_t hs = t % LY::HELD_RING, slot = t % LY::V_RING;
+          ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->held_full[hs]), (t / LY::HELD_RING) & 1u, abort_flag, p));
           if (!ok) break;
           uint32_t v[BATCH][4];
           const uint32_t from = sHeld + hs * LY::K_BYTES + (uint32_t)ct * 16u;
 #pragma unroll
           for (int y = 0; y < BATCH; ++y) ld_shared_u4(from + y * 2048u, v[y]);
           if (t >= (uint32_t)LY::V_SLOTS) {
-            ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->v_release[slot]), ((t / LY::V_SLOTS) & 1u) ^ 1u, abort_flag, p));
+            ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->v_release[slot]), ((t / LY::V_RING) & 1u) ^ 1u, abort_flag, p));
             if (!ok) break;
           }
           const long long keys = it.len - (long long)(it.j0 + i) * BN;  // rows that hold a key of the sequence

@@ -36,6 +36,9 @@ struct Library {
   decltype(&fa_fwd_paged_workspace_bytes) attend_bytes = nullptr;
   decltype(&fa_paged_append_fp8) append8 = nullptr;
   decltype(&fa_fwd_paged_fp8) attend8 = nullptr;
+  decltype(&fa_paged_key_weights) weigh = nullptr;
+  decltype(&fa_paged_evict) evict = nullptr;
+  decltype(&fa_paged_evict_workspace_bytes) evict_bytes = nullptr;
 } lib;
 
 // A refusal: TypeError or ValueError in Python.
@@ -443,6 +446,87 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+float* weights_of(const at::Tensor& t, const fa_paged_kv& kv) {
+  if (t.scalar_type() != at::kFloat) bad_type("weights must be float32");
+  if (t.sizes() != at::IntArrayRef({kv.num_pages, kv.Hkv, kv.page_size}) || !t.is_contiguous())
+    bad_value("weights must be contiguous " + shape_text({kv.num_pages, kv.Hkv, kv.page_size}) + ", not " +
+              shape_text(t.sizes()));
+  return static_cast<float*>(t.data_ptr());
+}
+
+// (q, lse, k_pages, weights, block_table, cu_seqlens, seq_lens, max_q, causal, scale, k_scale, stream)
+PyObject* key_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 12, [&]() -> PyObject* {
+    const at::Tensor &q = tensor(a[0], "q"), &lse = tensor(a[1], "lse"), &kp = tensor(a[2], "k_pages"),
+                     &w = tensor(a[3], "weights"), &table = tensor(a[4], "block_table"),
+                     &cu = tensor(a[5], "cu_seqlens"), &lens = tensor(a[6], "seq_lens");
+    const at::Tensor ks = optional_tensor(a[10], "k_scale");
+    const fa_dtype dt = type_code(q, "q");
+    if (q.dim() != 3) bad_value("q must be [T, Hq, d]");
+    const int T = as_int(q.size(0), "T");
+    const fa_heads hq = heads_of(q, "q", q);
+    const fa_paged_kv kv = cache_of(kp, kp, ks.defined() ? at::kFloat8_e4m3fn : q.scalar_type());
+    if (kv.d != q.size(2)) bad_value("the cache must have q's head dimension");
+    const float* const k_scale = ks.defined() ? scales_of(ks, "k_scale", kv) : nullptr;
+    float* const weights = weights_of(w, kv);
+    const Batch batch(table, cu, lens);
+    const int max_q = as_int(a[7], "max_q");
+    const bool causal = as_bool(a[8], "causal");
+    const float scale = a[9] == Py_None ? (float)(1.0 / std::sqrt((double)kv.d)) : as_float(a[9], "scale");
+    if (lse.scalar_type() != at::kFloat || lse.dim() != 2 || lse.size(0) != T || lse.size(1) != hq.H ||
+        !lse.is_contiguous())
+      bad_value("lse must be a contiguous [T, Hq] float32 tensor");
+    OneDevice(q).also(lse).also(kp).also(w).also(table).also(cu).also(lens).also(ks);
+    not_recorded({{&q, "q"}, {&lse, "lse"}, {&kp, "k_pages"}, {&w, "weights"}, {&ks, "k_scale"}});
+    Launch on(q, a[11]);
+    const int rc = lib.weigh(&kv, k_scale, &hq, static_cast<const float*>(lse.data_ptr()), weights, batch.B, T, max_q,
+                             batch.cu, batch.lens, batch.table, batch.width, scale, causal, dt, on.stream);
+    return PyLong_FromLong(rc);
+  });
+}
+
+// (k_pages, v_pages, weights, block_table, seq_lens, budget, recent, k_scale, v_scale, kept, new_lens, workspace, stream)
+PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 13, [&]() -> PyObject* {
+    const at::Tensor &kp = tensor(a[0], "k_pages"), &vp = tensor(a[1], "v_pages"), &w = tensor(a[2], "weights"),
+                     &table = tensor(a[3], "block_table"), &lens = tensor(a[4], "seq_lens");
+    const at::Tensor ks = optional_tensor(a[7], "k_scale"), vs = optional_tensor(a[8], "v_scale");
+    at::Tensor kept = optional_tensor(a[9], "kept"), now = optional_tensor(a[10], "new_lens");
+    const at::Tensor ws = optional_tensor(a[11], "workspace");
+    if (ks.defined() != vs.defined()) bad_value("k_scale and v_scale go together");
+    if (!ks.defined()) type_code(kp, "the pages of a cache without scales");
+    const fa_paged_kv kv = cache_of(kp, vp, ks.defined() ? at::kFloat8_e4m3fn : kp.scalar_type());
+    apart(kp);
+    float* const k_scale = ks.defined() ? scales_of(ks, "k_scale", kv) : nullptr;
+    float* const v_scale = vs.defined() ? scales_of(vs, "v_scale", kv) : nullptr;
+    float* const weights = weights_of(w, kv);
+    if (lens.dim() != 1) bad_value("seq_lens must be [B]");
+    const int B = as_int(lens.size(0), "B");
+    const int* const old = index_of(lens, "seq_lens", {B});
+    if (table.dim() != 2) bad_value("block_table must be [B, pages per sequence]");
+    const int* const pages = index_of(table, "block_table", {B, table.size(1)});
+    const int width = as_int(table.size(1), "the table's width");
+    const int budget = as_int(a[5], "budget"), recent = as_int(a[6], "recent");
+    if (budget < 1 || recent < 0 || recent > budget) bad_value("budget must be at least 1, and recent 0 to budget");
+    if (kept.defined()) index_of(kept, "kept", {B, kv.Hkv, budget});
+    if (now.defined()) index_of(now, "new_lens", {B});
+    if (ws.defined() && (ws.scalar_type() != at::kByte || !ws.is_contiguous()))
+      bad_value("workspace must be a contiguous uint8 tensor");
+    OneDevice(kp).also(vp).also(w).also(table).also(lens).also(ks).also(vs).also(kept).also(now).also(ws);
+    not_recorded({{&kp, "k_pages"}, {&vp, "v_pages"}, {&w, "weights"}, {&ks, "k_scale"}, {&vs, "v_scale"}});
+    Launch on(kp, a[12]);
+    if (!kept.defined()) kept = fresh(kp, {B, kv.Hkv, budget}, at::kInt);
+    if (!now.defined()) now = fresh(kp, {B}, at::kInt);
+    Scratch own;
+    if (!ws.defined()) own.take(lib.evict_bytes(B, kv.Hkv, budget, ks.defined()), on.stream);
+    const int rc = lib.evict(&kv, k_scale, v_scale, weights, B, old, pages, width, budget, recent,
+                             static_cast<int*>(kept.data_ptr()), static_cast<int*>(now.data_ptr()),
+                             ws.defined() ? ws.data_ptr() : own.ptr, ws.defined() ? (size_t)ws.numel() : own.size,
+                             on.stream);
+    return rc == FA_OK ? tuple_of({kept, now}) : PyLong_FromLong(rc);
+  });
+}
+
 // bind(addresses of the library's functions in Library's order)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   constexpr int COUNT = sizeof(Library) / sizeof(void*);
@@ -455,7 +539,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int i = 0;
     auto set = [&](auto& fn) { fn = reinterpret_cast<std::decay_t<decltype(fn)>>(f[i++]); };
     set(lib.norm_rope), set(lib.norm_rope_bwd), set(lib.norm_rope_bwd_bytes), set(lib.append), set(lib.attend);
-    set(lib.attend_bytes), set(lib.append8), set(lib.attend8);
+    set(lib.attend_bytes), set(lib.append8), set(lib.attend8), set(lib.weigh), set(lib.evict), set(lib.evict_bytes);
     Py_RETURN_NONE;
   });
 }
@@ -468,6 +552,8 @@ PyMethodDef methods[] = {FAST("bind", bind),
                          FAST("attend", attend<false>),
                          FAST("append_fp8", append<true>),
                          FAST("attend_fp8", attend<true>),
+                         FAST("key_weights", key_weights),
+                         FAST("evict", evict),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fa_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,551 @@
+// fa_weigh.cuh -- the attention weight that the new tokens of each sequence give to every cached token.
+// Included by fa_evict.cu.
+//
+//   w_j = (w_j of before, for tokens that are not new) + sum over the rows i that see j of exp(scale <q_i, k_j> - L_i)
+// for every key head, over the rows of all its query heads; L is what the attention returned.
+//
+// Products are transposed, S^T = K Q^T: a tile of 128 keys is the left operand (TMEM lane = thread = key)
+// and rows of q are the columns, so that a key's weight is a sum along the thread's own columns: no
+// exchange between threads, no atomics, one order of summation. A unit is (sequence, key head, 256 keys):
+// its two key tiles stay in shared memory, one to each softmax warpgroup, while tiles of up to 128 rows
+// of q go by. Units are shared out to the SMs from the lengths on the device, by cost. With a causal mask
+// later keys are seen by fewer rows: a head's units are dealt from both ends in turn, so that any run of
+// them costs about its share.
+//
+// 12 warps: 0-7 softmax, 8 and 11 loads (a key tile each, pages box by box), 9 MMA issuer; F8 (a cache in
+// 8 bits): 4 more turn each key tile into the type of q, exactly; its scale is the thread's own factor.
+// Single tokens are bound by HBM (K is read once), chunks by the tensor cores and the exponentials, which
+// take the same time (128 x 128 scores: 545 and 512 cycles).
+#pragma once
+
+#include "fa_paged.cuh"
+
+namespace fa {
+namespace weigh {
+
+using paged::BM;
+using paged::BN;
+using paged::wait_bar;
+using paged::wait_drain;
+constexpr int WARP_LOAD = 8, WARP_MMA = 9, WARP_LOAD2 = 11, WARP_CONVERT = 12;
+constexpr int MAX_SLOTS = 8;
+constexpr int COST_UNIT = 2;  // what a unit costs beside its row tiles, in those
+
+struct Params {
+  const float* L;
+  const float* ks;  // F8: scales [num_pages][Hkv]
+  float* w;         // [num_pages][Hkv][page_size]
+  int num_pages, page_size, box_keys;
+  int Hkv, G, Hq, tpt, cols;  // tpt: tokens per tile of rows; cols = tpt G
+  uint32_t by_g;              // ceil(2^16 / G)
+  const int *cu, *lens, *table;
+  int table_stride, B, T, causal, cap;
+  float c;  // scale * log2(e)
+  unsigned long long wait_limit_ns;
+  int* status;
+};
+
+struct Barriers {
+  uint64_t q_full[4], q_empty[4];
+  uint64_t k_full[MAX_SLOTS], k_empty[MAX_SLOTS];
+  uint64_t held_full[MAX_SLOTS], held_empty[MAX_SLOTS];
+  uint64_t s_full[2][2], s_empty[2][2];
+  uint64_t mma_drain;
+  long long warp_cost[16];
+  long long start_rem;
+  int start_b;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+template <int D, bool F8>
+struct Layout {
+  static constexpr int TILE_BYTES = BM * D * 2, HELD_BYTES = BM * D, CHUNK_BYTES = BM * 128, CHUNKS = D / 64;
+  static constexpr int Q_SLOTS = D == 64 ? 4 : 2;
+  static constexpr int K_SLOTS = D == 64 ? (F8 ? 4 : 6) : (F8 ? 3 : 4);
+  static constexpr int HELD_SLOTS = !F8 ? 0 : D == 64 ? 6 : 3, HELD_RING = F8 ? HELD_SLOTS : 1;
+  static constexpr int OFF_Q = 0, OFF_K = Q_SLOTS * TILE_BYTES, OFF_HELD = OFF_K + K_SLOTS * TILE_BYTES;
+  static constexpr int OFF_L = OFF_HELD + HELD_SLOTS * HELD_BYTES;  // 128 floats for each softmax warp
+  static constexpr int OFF_BAR = OFF_L + 8 * 512;
+  static constexpr int SMEM_BYTES = OFF_BAR + 1024;
+  static_assert(sizeof(Barriers) <= 1024 && SMEM_BYTES <= paged::SMEM_LIMIT, "shared memory budget");
+};
+
+struct Seq {
+  int t0, n, len, units;  // first row of q, new tokens, cached tokens, units of a head
+  int cost;               // of a unit
+};
+struct Unit {
+  int b, h, t0, n, len, key0, q0, qn;  // first key; tiles of rows [q0, qn) see one of its keys
+  bool two;                            // its second key tile holds a key
+};
+
+__device__ __forceinline__ Seq load_seq(const Params& p, int b, bool report) {
+  Seq s;
+  s.t0 = p.cu[b];
+  const int end = p.cu[b + 1], len = p.lens[b];
+  const bool rows_ok = s.t0 >= 0 && end >= s.t0 && end <= p.T;
+  s.n = rows_ok ? end - s.t0 : 0;
+  s.len = s.n ? max(0, min(len, p.cap)) : 0;
+  s.units = (int)(((uint32_t)s.len + 255u) / 256u);
+  const int qt = s.n ? (s.n - 1) / p.tpt + 1 : 0;
+  s.cost = COST_UNIT + qt;
+  if (p.causal && s.len) {  // rows see the new keys in part
+    const long long seen = 2ll * s.len - min(s.n, s.len);
+    s.cost = COST_UNIT + (int)((qt * seen + 2ll * s.len - 1) / (2ll * s.len));
+  }
+  if (report && (!rows_ok || (s.n && len > p.cap))) atomicCAS(p.status, 0, FA_ERR_RANGE);
+  return s;
+}
+
+// Walks a block's units; every role does so by itself.
+struct Walk {
+  Seq s;
+  int b, idx;  // unit of the sequence: head * units + place
+  long long u, u1;
+  __device__ __forceinline__ void begin(const Params& p, const Barriers* bars, long long u0, long long end) {
+    u1 = end;
+    u = u0;
+    b = bars->start_b;
+    idx = 0;
+    s = Seq{};
+    if (u0 >= u1) return;
+    s = load_seq(p, b, false);
+    // the first unit that begins in the range
+    const long long skip = (bars->start_rem + s.cost - 1) / s.cost;
+    idx = (int)skip;
+    u += skip * s.cost - bars->start_rem;
+  }
+  __device__ __forceinline__ bool next(const Params& p, Unit& x) {
+    while (u < u1) {
+      if (idx < p.Hkv * s.units) {
+        const int h = idx / s.units, i = idx - h * s.units;
+        ++idx;
+        u += s.cost;
+        const int j = i & 1 ? s.units - 1 - (i >> 1) : i >> 1;
+        x.b = b;
+        x.h = h;
+        x.t0 = s.t0;
+        x.n = s.n;
+        x.len = s.len;
+        x.key0 = j * 256;
+        x.q0 = p.causal ? max(0, x.key0 - (s.len - s.n)) / p.tpt : 0;
+        x.qn = (s.n - 1) / p.tpt + 1;
+        x.two = s.len - x.key0 > BN;
+        return true;
+      }
+      do {
+        if (++b >= p.B) return false;
+        s = load_seq(p, b, false);
+      } while (s.units == 0);
+      idx = 0;
+    }
+    return false;
+  }
+};
+
+template <int D, bool BF16, bool F8>
+__global__ void __launch_bounds__(F8 ? 512 : 384, 1)
+    fa_weigh_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ Params p) {
+  using LY = Layout<D, F8>;
+  constexpr int NUM_WARPS = F8 ? 16 : 12, NUM_THREADS = NUM_WARPS * 32;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw;
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, FA_ERR_ALIGN);
+    return;
+  }
+  Barriers* bars = reinterpret_cast<Barriers*>(smem + LY::OFF_BAR);
+  const uint32_t sQ = smem_u32(smem + LY::OFF_Q), sK = smem_u32(smem + LY::OFF_K), sHeld = smem_u32(smem + LY::OFF_HELD);
+  volatile int* abort_flag = &bars->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < LY::Q_SLOTS; ++s) {
+      mbar_init(smem_u32(&bars->q_full[s]), 1);
+      mbar_init(smem_u32(&bars->q_empty[s]), 1);
+    }
+    for (int s = 0; s < LY::K_SLOTS; ++s) {
+      mbar_init(smem_u32(&bars->k_full[s]), F8 ? 4 : 1);
+      mbar_init(smem_u32(&bars->k_empty[s]), 1);
+    }
+    for (int s = 0; s < LY::HELD_SLOTS; ++s) {
+      mbar_init(smem_u32(&bars->held_full[s]), 1);
+      mbar_init(smem_u32(&bars->held_empty[s]), 4);
+    }
+    for (int x = 0; x < 4; ++x) {
+      mbar_init(smem_u32(&bars->s_full[x >> 1][x & 1]), 1);
+      mbar_init(smem_u32(&bars->s_empty[x >> 1][x & 1]), 4);
+    }
+    mbar_init(smem_u32(&bars->mma_drain), 1);
+    bars->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == WARP_LOAD && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+  }
+  if (warp == WARP_MMA) {
+    tmem_alloc(smem_u32(&bars->tmem_base), 512);
+    tmem_relinquish();
+  }
+  launch_dependents();
+  wait_previous_grid();  // no global memory is read or written before this
+  tc_fence_before();
+  // The block's share [u0, u1) of all units' costs, and the sequence that u0 lies in.
+  long long u0, u1;
+  {
+    const int per_thread = (p.B + NUM_THREADS - 1) / NUM_THREADS;
+    const int b0 = min((int)threadIdx.x * per_thread, p.B), b1 = min(b0 + per_thread, p.B);
+    auto cost_of = [&](int b, bool report) -> long long {
+      const Seq s = load_seq(p, b, report);
+      return (long long)p.Hkv * s.units * s.cost;
+    };
+    long long mine = 0;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) mine += cost_of(b, blockIdx.x == 0);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) bars->warp_cost[warp] = incl;
+    __syncthreads();
+    long long before = incl - mine, W = 0;
+#pragma unroll
+    for (int w = 0; w < NUM_WARPS; ++w) {
+      if (w < warp) before += bars->warp_cost[w];
+      W += bars->warp_cost[w];
+    }
+    u0 = paged::divide((long long)blockIdx.x * W, (int)gridDim.x);
+    u1 = paged::divide((blockIdx.x + 1ll) * W, (int)gridDim.x);
+    if (u0 < u1 && before <= u0 && u0 < before + mine) {
+      int b = b0;
+#pragma unroll 1
+      for (; b + 1 < b1; ++b) {
+        const long long x = cost_of(b, false);
+        if (u0 < before + x) break;
+        before += x;
+      }
+      bars->start_b = b;
+      bars->start_rem = u0 - before;
+    }
+    __syncthreads();
+  }
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  Walk walk;
+  walk.begin(p, bars, u0, u1);
+  Unit it;
+
+  if (warp == WARP_LOAD || warp == WARP_LOAD2) {
+    // ========================================================================= loads
+    // Key tile x of a unit (x: the warp) goes box by box, a page each; warp 8 loads the rows of q as well. Table
+    // entries are asked for a unit ahead.
+    const int x = warp == WARP_LOAD2;
+    constexpr int BOX_CHUNKS = F8 ? 1 : LY::CHUNKS, SLOTS = F8 ? LY::HELD_SLOTS : LY::K_SLOTS;
+    constexpr uint32_t BOX_ROW = F8 ? D : 128, SLOT_BYTES = F8 ? LY::HELD_BYTES : LY::TILE_BYTES;
+    uint64_t* const full = F8 ? bars->held_full : bars->k_full;
+    uint64_t* const empty = F8 ? bars->held_empty : bars->k_empty;
+    const uint32_t sLoad = F8 ? sHeld : sK;
+    const int boxes = BN / p.box_keys, my_box = lane % boxes, my_chunk = lane / boxes;
+    const uint32_t box_bytes = (uint32_t)p.box_keys * BOX_ROW;
+    const uint32_t box_off = (uint32_t)my_chunk * LY::CHUNK_BYTES + (uint32_t)my_box * box_bytes;
+    const uint32_t q_bytes = (uint32_t)(LY::CHUNKS * p.cols) * 128u;
+    uint32_t t = 0, nq = 0, k_mask = 0, k_par = 0;  // key tiles and row tiles so far
+    bool ok = true;
+    auto entry = [&](const Unit& u) -> int {  // of the lane's box; -1: it holds no key of the sequence
+      const int key = u.key0 + x * BN + my_box * p.box_keys;
+      if (key >= u.len) return -1;
+      const int page = p.table[(size_t)u.b * p.table_stride + (uint32_t)key / (uint32_t)p.page_size];
+      return page;
+    };
+    bool have = walk.next(p, it);
+    int page = have ? entry(it) : -1;
+    while (ok && have) {
+      Unit nx;
+      const bool more = walk.next(p, nx);
+      const int next_page = more ? entry(nx) : -1;
+      if (page != -1 && (page < 0 || page >= p.num_pages)) {
+        atomicCAS(p.status, 0, FA_ERR_RANGE);
+        page = p.num_pages;  // reads as zeros
+      }
+      const int key = it.key0 + x * BN + my_box * p.box_keys;
+      if (key < it.len && page == -1) {  // (a table entry of -1)
+        atomicCAS(p.status, 0, FA_ERR_RANGE);
+        page = p.num_pages;
+      }
+      // A warp waits for the release of every slot in turn, its own or not, so that no barrier lies two phases
+      // behind the one that it waits for (where the parity would fit as well).
+      for (int y = 0; y < (it.two ? 2 : 1) && ok; ++y) {
+        const uint32_t slot = (t + y) % SLOTS, round = (t + y) / SLOTS;
+        if (round > 0) ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&empty[slot]), (round - 1) & 1u, abort_flag, p));
+        if (!ok || y != x) continue;
+        const int keys = it.len - it.key0 - x * BN;
+        const int live = min(boxes, (keys + p.box_keys - 1) / p.box_keys);
+        if (lane == 0) mbar_arrive_expect_tx(smem_u32(&full[slot]), (uint32_t)(live * BOX_CHUNKS) * box_bytes);
+        __syncwarp();
+        if (my_chunk < BOX_CHUNKS && my_box < live)
+          tma_load_4d(sLoad + slot * SLOT_BYTES + box_off, &tmK, smem_u32(&full[slot]), my_chunk * 64,
+                      p.page_size > BN ? key % p.page_size : 0, it.h, page);
+        k_mask |= 1u << slot;
+        k_par = (k_par & ~(1u << slot)) | ((round & 1u) << slot);
+      }
+      if (!ok) break;
+      t += it.two ? 2 : 1;
+      if (x == 0) {
+        for (int q = it.q0; q < it.qn && ok; ++q, ++nq) {
+          const uint32_t slot = nq % LY::Q_SLOTS, round = nq / LY::Q_SLOTS;
+          if (round > 0)
+            ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->q_empty[slot]), (round - 1) & 1u, abort_flag, p));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bars->q_full[slot]), q_bytes);
+          __syncwarp();
+          if (lane < LY::CHUNKS)
+            tma_load_3d(sQ + slot * LY::TILE_BYTES + lane * LY::CHUNK_BYTES, &tmQ, smem_u32(&bars->q_full[slot]),
+                        lane * 64, it.h * p.G, it.t0 + q * p.tpt);
+        }
+      }
+      it = nx;
+      page = next_page;
+      have = more;
+    }
+    if (!ok && lane == 0) {  // every issued copy must land before the block may exit
+      for (int s = 0; s < SLOTS; ++s)
+        if (k_mask & (1u << s)) wait_drain(smem_u32(&full[s]), (k_par >> s) & 1u, p);
+      for (uint32_t q = nq > LY::Q_SLOTS ? nq - LY::Q_SLOTS : 0; x == 0 && q < nq; ++q)
+        wait_drain(smem_u32(&bars->q_full[q % LY::Q_SLOTS]), (q / LY::Q_SLOTS) & 1u, p);
+    }
+    __syncwarp();
+  } else if (warp == WARP_MMA) {
+    // ========================================================================= MMA issuer
+    const uint32_t id = umma_idesc_f16(BF16 ? 1 : 0, 0, 0, BM, (uint32_t)(p.cols + 15) / 16 * 16);
+    const uint64_t dQ = umma_smem_desc(sQ, 16, 1024), dK = umma_smem_desc(sK, 16, 1024);
+    uint32_t t = 0, nq = 0;
+    uint32_t sn[2] = {0, 0};  // products of each warpgroup
+    bool ok = true;
+    auto wait_all = [&](uint64_t* bar, uint32_t par) -> bool {
+      return __all_sync(0xffffffffu, wait_bar(smem_u32(bar), par, abort_flag, p));
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) umma_commit(smem_u32(bar));
+      __syncwarp();
+    };
+    while (ok && walk.next(p, it)) {
+      const int tiles = it.two ? 2 : 1;
+      for (int q = it.q0; q < it.qn && ok; ++q, ++nq) {
+        const uint32_t qs = nq % LY::Q_SLOTS;
+        ok = wait_all(&bars->q_full[qs], (nq / LY::Q_SLOTS) & 1u);
+        for (int x = 0; x < tiles && ok; ++x) {
+          const uint32_t ks = (t + x) % LY::K_SLOTS, buf = sn[x] & 1u;
+          if (q == it.q0) ok = wait_all(&bars->k_full[ks], ((t + x) / LY::K_SLOTS) & 1u);
+          ok = ok && wait_all(&bars->s_empty[x][buf], ((sn[x] >> 1) & 1u) ^ 1u);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t da = dK + ((ks * LY::TILE_BYTES) >> 4), db = dQ + ((qs * LY::TILE_BYTES) >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = ((k >> 2) * LY::CHUNK_BYTES + (k & 3) * 32) >> 4;
+              umma_ss(tmem + x * 256 + buf * 128, da + off, db + off, id, k > 0 ? 1u : 0u);
+            }
+          }
+          __syncwarp();
+          commit(&bars->s_full[x][buf]);
+          if (q + 1 == it.qn) commit(&bars->k_empty[ks]);
+          ++sn[x];
+        }
+        if (ok) commit(&bars->q_empty[qs]);
+      }
+      t += tiles;
+    }
+    commit(&bars->mma_drain);
+    wait_drain(smem_u32(&bars->mma_drain), 0, p);
+    __syncwarp();
+  } else if (F8 && warp >= WARP_CONVERT) {
+    // ========================================================================= 8 bits to 16
+    // Thread = 16 elements of a row at a time, as in the attention; behind the last key anything may stand.
+    const int ct = (int)threadIdx.x - WARP_CONVERT * 32;
+    constexpr int PIECES = D / 16, TURNS = PIECES, BATCH = 4;
+    const int c16 = ct % PIECES, row0 = ct / PIECES;
+    const uint32_t half = (uint32_t)(c16 >> 2) * LY::CHUNK_BYTES, j0 = (c16 & 3) * 2, odd = c16 >> 2;
+    uint32_t t = 0;
+    bool ok = true;
+    while (ok && walk.next(p, it)) {
+      for (const uint32_t end = t + (it.two ? 2 : 1); t < end && ok; ++t) {
+        const uint32_t hs = t % LY::HELD_RING, ks = t % LY::K_SLOTS, round = t / LY::K_SLOTS;
+        ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->held_full[hs]), (t / LY::HELD_RING) & 1u, abort_flag, p));
+        if (ok && round > 0)
+          ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->k_empty[ks]), (round - 1) & 1u, abort_flag, p));
+        if (!ok) break;
+        const uint32_t from = sHeld + hs * LY::HELD_BYTES + (uint32_t)ct * 16u, to = sK + ks * LY::TILE_BYTES + half;
+#pragma unroll
+        for (int y0 = 0; y0 < TURNS; y0 += BATCH) {
+          uint32_t v[BATCH][4];
+#pragma unroll
+          for (int y = 0; y < BATCH; ++y) ld_shared_u4(from + (y0 + y) * 2048u, v[y]);
+#pragma unroll
+          for (int y = 0; y < BATCH; ++y) {
+            const uint32_t row = (uint32_t)(row0 + (y0 + y) * (128 / PIECES));
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              unpack4_e4m3(v[y][e], w[2 * e], w[2 * e + 1]);
+              if (BF16) {  // 4 of fp16's 11 bits are in use, and bf16 has 8
+                float a, b;
+                unpack2<false>(w[2 * e], a, b);
+                w[2 * e] = pack2<true>(a, b);
+                unpack2<false>(w[2 * e + 1], a, b);
+                w[2 * e + 1] = pack2<true>(a, b);
+              }
+            }
+            const uint32_t base = to + row * 128u, sw = row & 7u;
+            st_shared_v4(base + (((j0 + odd) ^ sw) << 4), odd ? w[4] : w[0], odd ? w[5] : w[1], odd ? w[6] : w[2],
+                         odd ? w[7] : w[3]);
+            st_shared_v4(base + (((j0 + 1 - odd) ^ sw) << 4), odd ? w[0] : w[4], odd ? w[1] : w[5], odd ? w[2] : w[6],
+                         odd ? w[3] : w[7]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&bars->k_full[ks]));
+          mbar_arrive(smem_u32(&bars->held_empty[hs]));
+        }
+      }
+    }
+  } else if (warp < 8) {
+    // ========================================================================= softmax
+    const int g = warp >> 2, wq = warp & 3;
+    const uint32_t tS = tmem + ((uint32_t)(wq * 32) << 16) + g * 256;
+    const uint32_t sL = smem_u32(smem + LY::OFF_L) + (uint32_t)warp * 512u;
+    const int chunks = (p.cols + 31) / 32;
+    // The thread's key in a unit: place of its weight, found two units ahead, so that its table entry, and then
+    // its weight and scale, are there in time.
+    struct Place {
+      int page, off;  // off: in the page's weights
+      bool held, old; // a cached token; not a new one
+    };
+    auto place_of = [&](const Unit& u) {
+      Place x;
+      const int key = u.key0 + g * BN + wq * 32 + lane;
+      x.held = key < u.len;
+      x.old = key < u.len - u.n;
+      x.page = x.held ? p.table[(size_t)u.b * p.table_stride + (uint32_t)key / (uint32_t)p.page_size] : -1;
+      x.off = u.h * p.page_size + (int)((uint32_t)key % (uint32_t)p.page_size);
+      return x;
+    };
+    auto weight_at = [&](const Place& x) { return p.w + (size_t)x.page * p.Hkv * p.page_size + x.off; };
+    auto fetch = [&](Place& x, float& w, float& k) {
+      if (x.held && (x.page < 0 || x.page >= p.num_pages)) x.held = false;  // (reported by the loading warps)
+      w = x.held && x.old ? *weight_at(x) : 0.f;
+      k = F8 && x.held ? p.ks[(size_t)x.page * p.Hkv + (uint32_t)x.off / (uint32_t)p.page_size] : 1.f;
+    };
+    // -L log2 e of the lane's columns (lane, lane + 32, ...) of a tile of rows
+    auto ask_rows = [&](const Unit& u, int q, float (&v)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = 0.f;
+        const int col = lane + 32 * i;
+        if (col >= p.cols) continue;
+        const int tok = (int)((uint32_t)col * p.by_g >> 16), t = q * p.tpt + tok;
+        if (t < u.n) v[i] = p.L[(size_t)(u.t0 + t) * p.Hq + u.h * p.G + col - tok * p.G];
+      }
+    };
+    Unit nx, ny;
+    bool have = walk.next(p, it), more = have && walk.next(p, nx), most = more && walk.next(p, ny);
+    Place here = {}, then = {}, last = {};
+    float w_here = 0.f, k_here = 1.f, w_then = 0.f, k_then = 1.f, rows[4] = {};
+    if (have) {
+      here = place_of(it);
+      ask_rows(it, it.q0, rows);
+    }
+    if (more) then = place_of(nx);
+    if (have) fetch(here, w_here, k_here);
+    uint32_t sn = 0;
+    bool ok = true;
+    while (ok && have) {
+      if (most) last = place_of(ny);
+      if (more) fetch(then, w_then, k_then);
+      const bool mine = g == 0 || it.two;
+      const int key = it.key0 + g * BN + wq * 32 + lane, ctx = it.len - it.n;
+      const float ct = fmaxf(p.c * k_here, 1e-30f);
+      const uint64_t c2 = f2(ct, ct);
+      uint64_t acc[4] = {0, 0, 0, 0};
+      for (int q = it.q0; q < it.qn && ok; ++q) {
+        if (mine) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st_shared_u32(sL + (lane + 32 * i) * 4, __float_as_uint(rows[i] * -1.4426950408889634f));
+          __syncwarp();
+        }
+        if (q + 1 < it.qn) ask_rows(it, q + 1, rows);
+        else if (more) ask_rows(nx, nx.q0, rows);
+        if (!mine) continue;
+        const uint32_t buf = sn & 1u;
+        ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->s_full[g][buf]), (sn >> 1) & 1u, abort_flag, p));
+        if (!ok) break;
+        ++sn;
+        tc_fence_after();
+        // columns [lo, hi) are rows that see the thread's key
+        const int hi = min(p.tpt, it.n - q * p.tpt) * p.G;
+        const int lo = p.causal ? min(max(key - ctx - q * p.tpt, 0), p.tpt) * p.G : 0;
+#pragma unroll 1
+        for (int x = 0; x < chunks; ++x) {
+          uint32_t s[32];
+          tmem_ld32(tS + buf * 128 + x * 32, s);
+          tmem_wait_ld();
+          reg_fence(s);
+          if (x == chunks - 1) {  // the scores are read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->s_empty[g][buf]));
+          }
+          const bool whole = __all_sync(0xffffffffu, lo <= 32 * x && hi >= 32 * (x + 1));
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float l4[4], e[4];
+            ld_shared_v4(sL + x * 128 + k * 16, l4);
+            f2_split(f2_fma(f2(__uint_as_float(s[4 * k]), __uint_as_float(s[4 * k + 1])), c2, f2(l4[0], l4[1])), e[0], e[1]);
+            f2_split(f2_fma(f2(__uint_as_float(s[4 * k + 2]), __uint_as_float(s[4 * k + 3])), c2, f2(l4[2], l4[3])), e[2], e[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              e[i] = ex2_approx(e[i]);
+              if (!whole) {
+                const int col = 32 * x + 4 * k + i;
+                e[i] = col >= lo && col < hi ? e[i] : 0.f;
+              }
+            }
+            acc[(2 * k) & 3] = f2_add(acc[(2 * k) & 3], f2(e[0], e[1]));
+            acc[(2 * k + 1) & 3] = f2_add(acc[(2 * k + 1) & 3], f2(e[2], e[3]));
+          }
+        }
+      }
+      if (!ok) break;
+      if (mine && here.held) {
+        float a, b;
+        f2_split(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a, b);
+        *weight_at(here) = w_here + (a + b);
+      }
+      here = then;
+      then = last;
+      w_here = w_then;
+      k_here = k_then;
+      it = nx;
+      nx = ny;
+      have = more;
+      more = most;
+      most = most && walk.next(p, ny);
+    }
+  }
+  tc_fence_before();
+  named_bar_sync(1, NUM_THREADS);
+  if (warp == WARP_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace weigh
+}  // namespace fa

@@ -170,6 +170,46 @@ int fa_fwd_paged_fp8(const fa_paged_kv* kv, const float* k_scale, const float* v
                      const int* seq_lens, const int* block_table, int table_stride, float scale, int causal,
                      fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------- eviction from a cache
+ * Both operators work on 16-bit caches (scales NULL) and on 8-bit ones (with their scales), and keep
+ * a weight for every cached token and key head: weights, fp32 [num_pages, Hkv, page_size], contiguous.
+ *
+ * fa_paged_key_weights -- adds to them what the new tokens of each sequence give, from their q and the
+ * L that the attention returned for them (natural logarithms, [T, Hq]):
+ *     w_j = (w_j if j < seq_lens[b] - n, else 0) + sum over the query heads of the key head and the new
+ *           tokens i that see j of exp(scale <q_i, k_j> - L_i)
+ * for every j < seq_lens[b] of the sequences that have new tokens; other places are left as they are.
+ *   kv        the cache; v and dtype-independent fields as in fa_fwd_paged, V is not looked at
+ *   k_scale   NULL for a 16-bit cache in `dtype`
+ *   max_q     the most new tokens of a sequence; more still give right results, more slowly
+ * Sums are fp32, in an order that does not change. A page with tokens of a sequence that has new ones must
+ * not stand twice in the tables. Reported and passed over: as in fa_fwd_paged. One kernel. */
+int fa_paged_key_weights(const fa_paged_kv* kv, const float* k_scale, const fa_heads* q, const float* L,
+                         float* weights, int B, int T, int max_q, const int* cu_seqlens, const int* seq_lens,
+                         const int* block_table, int table_stride, float scale, int causal, fa_dtype dtype,
+                         void* stream);
+
+/* fa_paged_evict -- cuts every sequence that has more than `budget` tokens to that many, for each key
+ * head by itself: the last `recent` (0 .. budget) stay, and of those before them the budget - recent of
+ * the largest weight (ties: the lowest positions; NaN counts as the largest). The kept tokens' keys, values
+ * and weights move together, in order, to positions 0 .. budget - 1 of the sequence's pages; what stands
+ * behind is left as it is, and so are shorter sequences.
+ * 8-bit caches: the scale of a page becomes the largest of those that its tokens come from, and codes from
+ * under smaller ones are rounded anew.
+ *   kept       int32 [B, Hkv, budget], output: the position that each place's token had, -1 behind the
+ *              last token of a shorter sequence
+ *   new_lens   int32 [B], output: min(seq_lens[b], budget); may be seq_lens itself
+ *   workspace  fa_paged_evict_workspace_bytes() bytes, 256-byte aligned, no initialisation
+ * Positions count from the front of the cache afterwards: rotate new keys by their own positions
+ * (fa_qk_norm_rope) and append them without a table.
+ * No page may stand twice in the tables. Weights on a page outside [0, num_pages) count as the smallest
+ * and rows there are not moved; a length past the table's width is cut to it; either records FA_ERR_RANGE.
+ * Two kernels. */
+size_t fa_paged_evict_workspace_bytes(int B, int Hkv, int budget, int held8);
+int fa_paged_evict(const fa_paged_kv* kv, float* k_scale, float* v_scale, float* weights, int B,
+                   const int* seq_lens, const int* block_table, int table_stride, int budget, int recent,
+                   int* kept, int* new_lens, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
