@@ -155,11 +155,21 @@ int launch_paged(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap
                           dim3(paged::COMBINE_THREADS), 0, st, p);
 }
 
+// Rows of a tile of fa_rows8.cuh for groups of G query heads and at most max_q new tokens, 0: more than it takes. (More
+// rows take its threads too long: 32 rows of 64 ragged sequences, d 128, 320 us against 161 in fa_paged.cuh.)
+inline int rows8_of(int G, int max_q) { return (long long)G * max_q <= 8 ? 8 : (long long)G * max_q <= 16 ? 16 : 0; }
+
+// The launch of fa_rows8.cuh's kernels (fa_rows8.cu).
+__attribute__((visibility("hidden"))) int launch_rows8(int d, bool bf16, const CUtensorMap& mk, const CUtensorMap& mv,
+                                                       const paged::Params& p, int index, int blocks, cudaStream_t st);
+
 template <int D, bool BF16, bool F8>
 int paged_forms(int form, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                 const paged::Params& p, int index, int blocks, cudaStream_t st) {
   switch (form) {
-    case 4: return launch_paged<D, BF16, true, 4, F8>(mq, mk, mv, p, index, blocks, st);
+    case 4:
+      if (F8 && p.rows8) return launch_rows8(D, BF16, mk, mv, p, index, blocks, st);
+      return launch_paged<D, BF16, true, 4, F8>(mq, mk, mv, p, index, blocks, st);
     case 2: return launch_paged<D, BF16, true, 2, F8>(mq, mk, mv, p, index, blocks, st);
     case 1: return launch_paged<D, BF16, true, 1, F8>(mq, mk, mv, p, index, blocks, st);
     default:
@@ -202,11 +212,15 @@ int attend_paged(const fa_paged_kv* kv, const float* k_scale, const float* v_sca
   p.L = L;
   p.num_pages = kv->num_pages;
   p.page_size = kv->page_size;
+  p.page_shift = -1;
+  for (int x = 0; x < 31; ++x)
+    if (kv->page_size == 1 << x) p.page_shift = x;
   p.box_keys = kv->page_size < 128 ? kv->page_size : 128;
   p.Hkv = kv->Hkv;
   p.G = G;
   p.by_g = (65536u + G - 1) / G;
   p.tpt = (form == 0 ? 128 : 128 / form) / G;
+  if (F8 && (p.rows8 = rows8_of(G, max_q)) != 0) p.tpt = p.rows8 / G;
   p.cu = cu_seqlens;
   p.lens = seq_lens;
   p.table = block_table;
@@ -251,7 +265,8 @@ int attend_paged(const fa_paged_kv* kv, const float* k_scale, const float* v_sca
   for (int i = 0; i < 2; ++i)
     if ((rc = paged_map(i ? &mv : &mk, i ? kv->v : kv->k, bf16, 4, kv->d,
                         {(uint64_t)kv->page_size, (uint64_t)kv->Hkv, (uint64_t)kv->num_pages},
-                        {kv->token_stride, kv->head_stride, kv->page_stride}, {(uint32_t)p.box_keys, 1, 1}, !F8 ? ROWS16 : i ? ROWS8 : ROWS8_SWIZZLED)) != FA_OK)
+                        {kv->token_stride, kv->head_stride, kv->page_stride}, {(uint32_t)p.box_keys, 1, 1},
+                        !F8 ? ROWS16 : i && !p.rows8 ? ROWS8 : ROWS8_SWIZZLED)) != FA_OK)
       return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (kv->d == 64) return bf16 ? paged_forms<64, true, F8>(form, mq, mk, mv, p, index, blocks, st) : paged_forms<64, false, F8>(form, mq, mk, mv, p, index, blocks, st);

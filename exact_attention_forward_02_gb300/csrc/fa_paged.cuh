@@ -104,6 +104,8 @@ struct Params {
   // a cache in 8 bits: scales [num_pages][Hkv], and the queries, which the kernel splits by itself
   const float *ks, *vs;
   HeadsDev q;
+  int rows8;       // rows of a tile in fa_rows8.cuh
+  int page_shift;  // log2 of the page size, -1 where that is none
 };
 
 // Debug builds (FA_DEBUG) check the places of tile copies, partial states and output rows; one
@@ -453,6 +455,107 @@ __device__ __forceinline__ Range plan(const Params& p, Barriers* bars, int b0, i
     __syncthreads();
   }
   return r;
+}
+
+// Hands the block's items to its other warps, a few ahead, through the ring in shared memory (one thread).
+template <int TPT_MUL, int ITEM_UNITS, bool DIRECT>
+__device__ __forceinline__ void publish_items(const Params& p, Barriers* bars, const Range& range,
+                                              volatile int* abort_flag) {
+  int* rec = p.records + blockIdx.x * 8;
+  if (!p.whole) rec[0] = 0;  // no item begins here and ends elsewhere, as yet
+  uint32_t i = 0;
+  auto publish = [&](const Item& it) -> bool {
+    const uint32_t s = i % ITEM_SLOTS;
+    if (i >= ITEM_SLOTS && !wait_bar(smem_u32(&bars->item_empty[s]), (i / ITEM_SLOTS - 1) & 1u, abort_flag, p,
+                                     ITEM_WAITS))
+      return false;
+    bars->items[s] = it;
+    mbar_arrive(smem_u32(&bars->item_full[s]));
+    ++i;
+    return true;
+  };
+  auto record = [&](const Item& it, int last) {  // its last block
+    rec[1] = it.slot;
+    rec[2] = last;
+    rec[3] = it.h;
+    rec[4] = it.tok0;
+    rec[5] = it.nt;
+    rec[6] = p.causal ? it.vis0 : it.len;  // keys that its first token sees
+    rec[0] = 1;
+  };
+  bool go = true;
+  if (DIRECT && p.direct) {
+    const int item = (int)blockIdx.x / p.direct, part = (int)blockIdx.x - item * p.direct;
+    const int b = item / p.Hkv, h = item - b * p.Hkv, tpi = p.tpt * TPT_MUL;
+    const Seq s = load_seq(p, b, tpi, part == 0 && h == 0);
+    // more blocks of tokens than the host knew of (max_q was too small): whole, by the last part
+    // (whole items) or the first
+    for (int q = p.whole ? part : 0; q < s.nq && go; ++q) {
+      const int ntot = tiles_of(p, s, q, tpi);
+      const int np = p.whole || q > 0 ? 1 : min(p.direct, (ntot + DIRECT_TILES - 1) / DIRECT_TILES);
+      const int k = p.whole ? 0 : part;
+      if (k >= np) continue;
+      const uint32_t n = (uint32_t)ntot, j0 = k * n / np, j1 = (k + 1) * n / np;
+      const Item it = make_item<TPT_MUL>(p, s, b, h, q, ntot, (int)j0, (int)j1, 0);
+      go = publish(it);
+      if (go && k == 0 && np > 1) record(it, (int)blockIdx.x + np - 1);
+      if (p.whole && part < p.direct - 1) break;
+    }
+  } else {
+    Walk<TPT_MUL, ITEM_UNITS> walk;
+    walk.begin(range, bars->start);
+    Item it;
+    long long ustart;
+    while (go && walk.next(p, range, it, ustart)) {
+      go = publish(it);
+      if (go && it.j0 == 0 && it.n != it.ntot) record(it, owner_of(ustart + ITEM_UNITS + it.ntot - 1, range));
+    }
+  }
+  Item end = {};
+  if (go) publish(end);
+}
+
+// A query row as a sum of E4M3 numbers: q = 2^e (q1 + q2 [+ q3]). The row's D/8 lanes call this with 8 elements
+// each; w[m]: their bytes of q_m. Infinities become NaN.
+template <int D, bool BF16, int TERMS>
+__device__ __forceinline__ int split_row(const uint4& u, uint32_t (&w)[TERMS][2]) {
+  float e[8];
+  unpack2<BF16>(u.x, e[0], e[1]);
+  unpack2<BF16>(u.y, e[2], e[3]);
+  unpack2<BF16>(u.z, e[4], e[5]);
+  unpack2<BF16>(u.w, e[6], e[7]);
+  uint32_t top = 0;  // sizes in the order of their bits, NaN above infinity
+#pragma unroll
+  for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(e[k]) & 0x7fffffffu);
+#pragma unroll
+  for (int o = D / 16; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  int ex = (int)(top >> 23) - 127 - 7;
+  if (top >= 0x7f800000u || top == 0) ex = 0;
+  ex = max(ex, -119);  // 2^-ex is a normal number
+  const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    e[k] *= down;
+    e[k] += e[k] - e[k];
+  }
+#pragma unroll
+  for (int m = 0; m < TERMS; ++m) {
+    w[m][0] = pack4_e4m3(e[0], e[1], e[2], e[3]);
+    w[m][1] = pack4_e4m3(e[4], e[5], e[6], e[7]);
+    if (m + 1 < TERMS) {
+      uint32_t h[4];
+      unpack4_e4m3(w[m][0], h[0], h[1]);
+      unpack4_e4m3(w[m][1], h[2], h[3]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float a, b;
+        unpack2<false>(h[k], a, b);
+        e[2 * k] -= a;
+        e[2 * k + 1] -= b;
+      }
+    }
+  }
+  return ex;
 }
 
 // ----------------------------------------------------------------------------- kernel
@@ -981,49 +1084,19 @@ __global__ void __launch_bounds__(num_warps(F8) * 32, 1)
           const int head = x - tok * p.G;
           uint4 u = make_uint4(0, 0, 0, 0);
           if (live) u = *reinterpret_cast<const uint4*>(p.q.ptr + (long long)(it.tok0 + tok) * p.q.ts + (long long)(it.h * p.G + head) * p.q.hs + ql * 8);
-          float e[8];
-          unpack2<BF16>(u.x, e[0], e[1]);
-          unpack2<BF16>(u.y, e[2], e[3]);
-          unpack2<BF16>(u.z, e[4], e[5]);
-          unpack2<BF16>(u.w, e[6], e[7]);
-          uint32_t top = 0;  // sizes in the order of their bits, NaN above infinity
-#pragma unroll
-          for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(e[k]) & 0x7fffffffu);
-#pragma unroll
-          for (int o = QL / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          int ex = (int)(top >> 23) - 127 - 7;
-          if (top >= 0x7f800000u || top == 0) ex = 0;
-          ex = max(ex, -119);  // 2^-ex is a normal number
-          const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            e[k] *= down;
-            e[k] += e[k] - e[k];  // infinities are NaN here
-          }
-          if (live && ql == 0) exps[(n_q & 1u) * LY::EXP_ROWS + (SPLIT || x < per_tile ? x : x - per_tile + BM)] = (signed char)ex;
+          uint32_t w[TERMS > 0 ? TERMS : 1][2];
+          const int ex = split_row<D, BF16>(u, w);
           const uint32_t tile = SPLIT || x < per_tile ? 0u : 1u, row = tile ? x - per_tile : x;
+          if (live && ql == 0) exps[(n_q & 1u) * LY::EXP_ROWS + tile * BM + row] = (signed char)ex;
 #pragma unroll
           for (int m = 0; m < TERMS; ++m) {
-            const uint32_t w0 = pack4_e4m3(e[0], e[1], e[2], e[3]), w1 = pack4_e4m3(e[4], e[5], e[6], e[7]);
-            if (live) {
+            if (!live) break;
 #pragma unroll
-              for (int a = 0; a < REP; ++a) {
-                const uint32_t r = row + a * (BM / REP);
-                const uint32_t sw = D == 128 ? r & 7u : (r >> 1) & 3u;
-                st_shared_v2(sQ + tile * LY::Q_BYTES + m * (BM * D) + r * D + ((((uint32_t)ql >> 1) ^ sw) << 4) + (ql & 1) * 8, w0, w1);
-              }
-            }
-            if (m + 1 < TERMS) {
-              uint32_t h[4];
-              unpack4_e4m3(w0, h[0], h[1]);
-              unpack4_e4m3(w1, h[2], h[3]);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                float a, b;
-                unpack2<false>(h[k], a, b);
-                e[2 * k] -= a;
-                e[2 * k + 1] -= b;
-              }
+            for (int a = 0; a < REP; ++a) {
+              const uint32_t r = row + a * (BM / REP);
+              const uint32_t sw = D == 128 ? r & 7u : (r >> 1) & 3u;
+              st_shared_v2(sQ + tile * LY::Q_BYTES + m * (BM * D) + r * D + ((((uint32_t)ql >> 1) ^ sw) << 4) + (ql & 1) * 8,
+                           w[m][0], w[m][1]);
             }
           }
         }
@@ -1073,60 +1146,7 @@ __global__ void __launch_bounds__(num_warps(F8) * 32, 1)
       }
     } else if (warp == WARP_WALK) {
       // ======================================================================= items
-      if (lane == 0) {
-        int* rec = p.records + blockIdx.x * 8;
-        if (!p.whole) rec[0] = 0;  // no item begins here and ends elsewhere, as yet
-        uint32_t i = 0;
-        auto publish = [&](const Item& it) -> bool {
-          const uint32_t s = i % ITEM_SLOTS;
-          if (i >= ITEM_SLOTS && !wait_bar(smem_u32(&bars->item_empty[s]), (i / ITEM_SLOTS - 1) & 1u, abort_flag, p,
-                                           ITEM_WAITS))
-            return false;
-          bars->items[s] = it;
-          mbar_arrive(smem_u32(&bars->item_full[s]));
-          ++i;
-          return true;
-        };
-        auto record = [&](const Item& it, int last) {  // its last block
-          rec[1] = it.slot;
-          rec[2] = last;
-          rec[3] = it.h;
-          rec[4] = it.tok0;
-          rec[5] = it.nt;
-          rec[6] = p.causal ? it.vis0 : it.len;  // keys that its first token sees
-          rec[0] = 1;
-        };
-        bool go = true;
-        if (DIRECT && p.direct) {
-          const int item = (int)blockIdx.x / p.direct, part = (int)blockIdx.x - item * p.direct;
-          const int b = item / p.Hkv, h = item - b * p.Hkv, tpi = p.tpt * TPT_MUL;
-          const Seq s = load_seq(p, b, tpi, part == 0 && h == 0);
-          // more blocks of tokens than the host knew of (max_q was too small): whole, by the last part
-          // (whole items) or the first
-          for (int q = p.whole ? part : 0; q < s.nq && go; ++q) {
-            const int ntot = tiles_of(p, s, q, tpi);
-            const int np = p.whole || q > 0 ? 1 : min(p.direct, (ntot + DIRECT_TILES - 1) / DIRECT_TILES);
-            const int k = p.whole ? 0 : part;
-            if (k >= np) continue;
-            const uint32_t n = (uint32_t)ntot, j0 = k * n / np, j1 = (k + 1) * n / np;
-            const Item it = make_item<TPT_MUL>(p, s, b, h, q, ntot, (int)j0, (int)j1, 0);
-            go = publish(it);
-            if (go && k == 0 && np > 1) record(it, (int)blockIdx.x + np - 1);
-            if (p.whole && part < p.direct - 1) break;
-          }
-        } else {
-          Walk<TPT_MUL, ITEM_UNITS> walk;
-          walk.begin(range, bars->start);
-          Item it;
-          long long ustart;
-          while (go && walk.next(p, range, it, ustart)) {
-            go = publish(it);
-            if (go && it.j0 == 0 && it.n != it.ntot) record(it, owner_of(ustart + ITEM_UNITS + it.ntot - 1, range));
-          }
-        }
-        Item end = {};
-        if (go) publish(end);
-      }
+      if (lane == 0) publish_items<TPT_MUL, ITEM_UNITS, DIRECT>(p, bars, range, abort_flag);
       __syncwarp();
     }
     tc_fence_before();

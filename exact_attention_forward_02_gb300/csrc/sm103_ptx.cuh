@@ -175,6 +175,20 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// (the same with 8 and 16 columns: tmem_ld8, tmem_ld16)
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 // 32 lanes x 32 columns of 32-bit: thread t of the warp receives lane (base_lane + t),
 // columns [col, col + 32).
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -191,9 +205,10 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
 }
 // after tcgen05.wait::ld: make every later use of the loaded registers depend on this
 // point, so that the compiler cannot move a use above the wait
-__device__ __forceinline__ void reg_fence(uint32_t (&r)[32]) {
+template <int N>
+__device__ __forceinline__ void reg_fence(uint32_t (&r)[N]) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -217,11 +232,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // ----------------------------------------------------------------------------- UMMA
 // Shared-memory matrix descriptor (tcgen05 format): start address, leading- and
 // stride-dimension byte offsets (all >> 4), descriptor version 1 (bits 46-47),
 // base offset 0 (tiles are 1024-byte aligned), swizzle mode in bits 61-63.
-enum : uint64_t { UMMA_SWIZZLE_128B = 2, UMMA_SWIZZLE_64B = 4 };
+enum : uint64_t { UMMA_SWIZZLE_128B = 2, UMMA_SWIZZLE_64B = 4, UMMA_SWIZZLE_32B = 6 };
 template <uint64_t SWIZZLE = UMMA_SWIZZLE_128B>
 __device__ __forceinline__ uint64_t umma_smem_desc(uint32_t saddr, uint32_t lbo_bytes,
                                                    uint32_t sbo_bytes) {
@@ -427,6 +448,27 @@ __device__ __forceinline__ void unpack4_e4m3(uint32_t v, uint32_t& w0, uint32_t&
       "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
       : "=r"(w0), "=r"(w1)
       : "r"(v));
+}
+
+// two fp16 values (one word) -> two E5M2 bytes (nearest even, saturating) in the low half, and back, exactly
+__device__ __forceinline__ uint32_t pack2_e5m2(uint32_t h2) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 b;\n\tcvt.rn.satfinite.e5m2x2.f16x2 b, %1;\n\tcvt.u32.u16 %0, b;\n\t}" : "=r"(r) : "r"(h2));
+  return r;
+}
+__device__ __forceinline__ uint32_t unpack2_e5m2(uint32_t b2) {
+  return __byte_perm(b2, 0u, 0x1404);  // a byte of E5M2 is the upper half of the same number in fp16
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// maximum over the warp's lanes, NaN left out (sm_100a+)
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 // unpack one 32-bit word of two 16-bit values (low half first) into fp32

@@ -64,9 +64,10 @@ class Batch8(lib.Batch):
 def attend64(b, q, scale, causal):
     """O, L and how far each may be off, from b.keys and b.values (64 bits).
 
-    As in decoder_testlib.attend64, with P rounded to fp16 whatever q's type: u = 2^-11 relative to each
-    P, and where P' = P v_scale / (largest v_scale) 2^7 is subnormal in fp16 half a step of those, 2^-25,
-    which is 2^-32 (largest v_scale) times the code. (Each row's sum is at least 1 in P's unit.)"""
+    As in decoder_testlib.attend64, with P held in 11 bits whatever q's type: u = 2^-11 relative to each P.
+    Small ones are cut off, at half a step of E5M2's subnormal numbers (2^-17) in P' = P v_scale / (largest
+    v_scale) 2^11, at half a step of fp16's (2^-25) in 2^7 of it with more rows: either way by less than
+    2^-28 (largest v_scale) times the code. (Each row's sum is at least 1 in P's unit.)"""
     u16 = torch.finfo(torch.float16).eps / 2
     T, Hq, d = q.shape
     u, sub = lib.step(q.dtype), lib.tiny(q.dtype)
@@ -92,7 +93,9 @@ def attend64(b, q, scale, causal):
         e = d * 2.0 ** -22 * scale * (x.abs() @ kk.abs().transpose(1, 2)).amax(-1)
         O[rows] = (p @ vv).transpose(0, 1)
         L[rows] = lse.transpose(0, 1)
-        small = 2.0 ** -32 * b.vscales[i].amax(0).repeat_interleave(group)[:, None, None] * 448 * t
+        unit = b.vscales[i].repeat_interleave(b.page, 0)[:t].T[..., None]
+        codes = torch.where(unit > 0, b.values[i] / unit, 0.0).abs().sum(1, keepdim=True)
+        small = (2.0 ** -28 * b.vscales[i].amax(0)[:, None, None] * codes).repeat_interleave(group, 0)
         weight = (u16 + 2 * e)[..., None] * (p @ vv.abs()) + small
         tol_o[rows] = weight.transpose(0, 1) + u * O[rows].abs() + sub + 2.0 ** -18 * weight.transpose(0, 1) + (
             2.0 ** -19 * (p @ vv.abs()).transpose(0, 1))
