@@ -67,9 +67,9 @@ __host__ __device__ constexpr int item_readers(bool f8) { return f8 ? 15 : 11; }
 // of its own waits runs out first and stops these as well.)
 constexpr uint32_t ITEM_WAITS = 1024;
 // 2*128*200 + 128*104 = 64512 = 384*168 registers, the launch's budget; with the converting warps
-// 2*128*192 + 2*128*64 = 65536 = 512*128
-__host__ __device__ constexpr uint32_t regs_softmax(bool f8) { return f8 ? 192 : 200; }
-__host__ __device__ constexpr uint32_t regs_other(bool f8) { return f8 ? 64 : 104; }
+// 2*128*168 + 2*128*88 = 65536 = 512*128
+__host__ __device__ constexpr uint32_t regs_softmax(bool f8) { return f8 ? 168 : 200; }
+__host__ __device__ constexpr uint32_t regs_other(bool f8) { return f8 ? 88 : 104; }
 constexpr uint32_t TMEM_COLS = 512, TMEM_S0 = 0, TMEM_O0 = 256;  // S0 | S1 | O0 | O1
 constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units, as in the dense kernel
 constexpr int SMEM_LIMIT = 232448;
@@ -1227,154 +1227,238 @@ __global__ void __launch_bounds__(num_warps(F8) * 32, 1)
         if (!ok) break;
         s_ph ^= 1;
         tc_fence_after();
-        uint32_t sr[CW / 32][32];
-#pragma unroll
-        for (int q = 0; q < CW / 32; ++q) tmem_ld32(tS + copy * CW + q * 32, sr[q]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int q = 0; q < CW / 32; ++q) reg_fence(sr[q]);
-        auto sv = [&](int k) { return __uint_as_float(sr[k >> 5][k & 31]); };
-        if (F8 && i < STEP)  // (the item's exponents, written before its first S; the next but one takes their place)
-          cr = fmaxf(c * __uint_as_float((uint32_t)(127 + exps[(n_item & 1u) * LY::EXP_ROWS]) << 23), 1e-30f);
-        float ct = F8 ? cr : c, beta = 1.f;  // F8: with the tile's scale of K; what O~'s unit shrinks by
-        [[maybe_unused]] float lf = 0.f;
-        [[maybe_unused]] const uint32_t scales = smem_u32(smem + LY::OFF_SCALE) + (uint32_t)warp * (SPLIT ? 256u : 128u);
-        if (F8) {
+        if constexpr (F8) {
+          // As below, in code that is small enough for the instruction cache next to that of the converting warps
+          // (unrolled over all columns, with the scores held from one pass to the other, a chunk of 2048 tokens at 30720
+          // took 525 us): CH columns at a time, read again for the second pass. Each group of 8 columns has scales of its own.
+          constexpr int CH = CW < 64 ? CW : 64;
+          if (i < STEP)  // (the item's exponents, written before its first S; the next but one takes their place)
+            cr = fmaxf(c * __uint_as_float((uint32_t)(127 + exps[(n_item & 1u) * LY::EXP_ROWS]) << 23), 1e-30f);
           // the largest scale of V (positive numbers in the order of their bits)
           const float vt = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < 16 ? 0u : __float_as_uint(scale_now)));
+          float beta = 1.f;  // what O~'s unit shrinks by
           if (i < STEP || vt > vref) {
             const float v_new = fmaxf(vt, 7.8886090522101181e-31f);  // 2^-100: pages of zeros
             beta = vref / v_new;
             vref = v_new;
             vinv = 128.f / v_new;
           }
-          if (small_pages) {
-            st_shared_u32(scales + lane * 4, __float_as_uint(scale_now * (lane < 16 ? 1.f : vinv)));
-            __syncwarp();
+          // K's scales, and log2 of V's in the unit of P' (a page whose V is below 2^-40 of the largest counts as that)
+          const uint32_t scales = smem_u32(smem + LY::OFF_SCALE) + (uint32_t)warp * (SPLIT ? 256u : 128u);
+          st_shared_u32(scales + lane * 4, __float_as_uint(lane < 16 ? fmaxf(scale_now, 1e-30f)
+                                                                     : log2f(fmaxf(scale_now * vinv, 1.1641532182693481e-10f))));
+          __syncwarp();
+          const uint32_t tC = tS + copy * CW;
+          const int vis = lim - i * BN - copy * CW;
+          if (!__all_sync(0xffffffffu, !valid || vis >= CW)) {  // keys that a row does not see become -inf
+#pragma unroll 1
+            for (int q = 0; q < CW; q += 32) {
+              if (__all_sync(0xffffffffu, !valid || vis >= q + 32)) continue;
+              uint32_t x[32];
+              tmem_ld32(tC + q, x);
+              tmem_wait_ld();
+              reg_fence(x);
 #pragma unroll
-            for (int q = 0; q < CW / 32; ++q) {
+              for (int k = 0; k < 32; ++k)
+                if (q + k >= vis) x[k] = 0xff800000u;
+              tmem_st32(tC + q, x);
+            }
+            tmem_wait_st();
+          }
+          auto load = [&](int q, uint32_t (&x)[CH / 32][32]) {
+#pragma unroll
+            for (int y = 0; y < CH / 32; ++y) tmem_ld32(tC + q + y * 32, x[y]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < CH / 32; ++y) reg_fence(x[y]);
+          };
+          float mt = -INFINITY;
+#pragma unroll 1
+          for (int q = 0; q < CW; q += CH) {
+            uint32_t x[CH / 32][32];
+            load(q, x);
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int y = 0; y < CH / 32; ++y) {
               float k4[4];
-              ld_shared_v4(scales + q * 16, k4);
+              ld_shared_v4(scales + (q / 8 + y * 4) * 4, k4);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                auto v = [&](int k) { return __uint_as_float(x[y][8 * e + k]); };
+                const float m8 = max3(max3(v(0), v(1), v(2)), max3(v(3), v(4), v(5)), fmaxf(v(6), v(7)));
+                m4[e] = fmaxf(m4[e], m8 * k4[e]);
+              }
+            }
+            mt = max3(mt, fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          }
+          const float m_tile = (mt == -INFINITY || !valid) ? -INFINITY : mt * cr;
+          float m_new = m_run, alpha = 1.f;
+          bool rescale = i >= STEP && beta != 1.f;
+          if (i < STEP) {
+            m_new = m_tile;
+          } else if (m_tile > m_run + RESCALE_THRESHOLD) {
+            m_new = m_tile;
+            alpha = ex2_approx(m_run - m_new);
+            rescale = true;
+          }
+          if (__any_sync(0xffffffffu, rescale)) {
+            const uint64_t al2 = f2(alpha * beta, alpha * beta);
+#pragma unroll 1
+            for (int q = 0; q < D; q += 32) {
+              uint32_t o[32];
+              tmem_ld32(tO + q, o);
+              tmem_wait_ld();
+              reg_fence(o);
 #pragma unroll
               for (int k = 0; k < 16; ++k) {
-                const uint64_t kk = f2(k4[k >> 2], k4[k >> 2]);
                 float x0, x1;
-                f2_split(f2_mul(f2(__uint_as_float(sr[q][2 * k]), __uint_as_float(sr[q][2 * k + 1])), kk), x0, x1);
-                sr[q][2 * k] = __float_as_uint(x0);
-                sr[q][2 * k + 1] = __float_as_uint(x1);
+                f2_split(f2_mul(f2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), al2), x0, x1);
+                o[2 * k] = __float_as_uint(x0);
+                o[2 * k + 1] = __float_as_uint(x1);
+              }
+              tmem_st32(tO + q, o);
+            }
+          }
+          const float nb = (m_new == -INFINITY) ? 0.f : -m_new;
+          float sum = 0.f;
+#pragma unroll 1
+          for (int q = 0; q < CW; q += CH) {
+            uint32_t x[CH / 32][32], pk[CH / 2];
+            load(q, x);
+#pragma unroll
+            for (int y = 0; y < CH / 32; ++y) {
+              float k4[4], l4[4];
+              ld_shared_v4(scales + (q / 8 + y * 4) * 4, k4);
+              ld_shared_v4(scales + 64 + (q / 8 + y * 4) * 4, l4);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float cg = fmaxf(cr * k4[e], 1e-30f), ng = nb + l4[e];
+                const uint64_t c2 = f2(cg, cg), n2 = f2(ng, ng);
+                uint64_t acc[2];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  float t0, t1;
+                  f2_split(f2_fma(f2(__uint_as_float(x[y][8 * e + 2 * k]), __uint_as_float(x[y][8 * e + 2 * k + 1])), c2, n2), t0, t1);
+                  const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+                  acc[k & 1] = k < 2 ? f2(p0, p1) : f2_add(acc[k & 1], f2(p0, p1));
+                  pk[y * 16 + e * 4 + k] = pack2<false>(p0, p1);
+                }
+                float a0, a1;
+                f2_split(f2_add(acc[0], acc[1]), a0, a1);
+                sum = fmaf(a0 + a1, ex2_approx(-l4[e]), sum);  // these were P'
               }
             }
-          } else {
-            ct = fmaxf(cr * __shfl_sync(0xffffffffu, scale_now, 0), 1e-30f);
-            // a page whose V is below 2^-40 of the largest counts as that
-            lf = log2f(fmaxf(__shfl_sync(0xffffffffu, scale_now, 16) * vinv, 1.1641532182693481e-10f));
-          }
-        }
-        const int vis = lim - i * BN - copy * CW;
-        // Scores of keys that a row does not see become -inf, 32 columns at a time where some row of
-        // the warp needs it (rows that hold no query do not count). c > 0 keeps them at -inf, and
-        // their weights at zero.
-        if (!__all_sync(0xffffffffu, !valid || vis >= CW)) {
-#pragma unroll
-          for (int q = 0; q < CW / 32; ++q) {
-            if (__all_sync(0xffffffffu, !valid || vis >= 32 * (q + 1))) continue;
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (32 * q + k >= vis) sr[q][k] = 0xff800000u;
-          }
-        }
-        float mt;
-        {
-          constexpr int NT = (CW + 2) / 3;
-          float t[NT];
-#pragma unroll
-          for (int x = 0; x < NT; ++x)
-            t[x] = max3(sv(3 * x), 3 * x + 1 < CW ? sv(3 * x + 1) : -INFINITY, 3 * x + 2 < CW ? sv(3 * x + 2) : -INFINITY);
-          mt = tree_max<NT>(t);
-        }
-        const float m_tile = (mt == -INFINITY || !valid) ? -INFINITY : mt * ct;
-        float m_new = m_run, alpha = 1.f;
-        bool rescale = F8 && i >= STEP && beta != 1.f;
-        if (i < STEP) {
-          m_new = m_tile;
-        } else if (m_tile > m_run + RESCALE_THRESHOLD) {
-          m_new = m_tile;
-          alpha = ex2_approx(m_run - m_new);
-          rescale = true;
-        }
-        const float nb = (m_new == -INFINITY) ? 0.f : -m_new;
-        const float nl = F8 ? nb + lf : nb;
-        const uint64_t c2 = f2(ct, ct), nb2 = f2(nl, nl);
-        uint64_t acc[4] = {0, 0, 0, 0};
-        uint32_t pk[CW / 2];
-        auto weights = [&](auto scaled) {
-#pragma unroll
-          for (int q = 0; q < CW / 32; ++q) {
-            float v4[4];
-            if (decltype(scaled)::value) ld_shared_v4(scales + 64 + q * 16, v4);
-#pragma unroll
-            for (int kk = 0; kk < 16; ++kk) {
-              const int k = q * 16 + kk;
-              float t0, t1;
-              f2_split(f2_fma(f2(sv(2 * k), sv(2 * k + 1)), c2, nb2), t0, t1);
-              const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
-              acc[k & 3] = f2_add(acc[k & 3], f2(p0, p1));
-              if (decltype(scaled)::value) {
-                float y0, y1;
-                f2_split(f2_mul(f2(p0, p1), f2(v4[kk >> 2], v4[kk >> 2])), y0, y1);
-                pk[k] = pack2<false>(y0, y1);
-              } else {
-                pk[k] = pack2<BF16 && !F8>(p0, p1);
-              }
+            // P over the first 64 columns of the scores, always behind what has been read: this copy's keys, and
+            // below zeros for the other copies'
+            if constexpr (REP == 1) tmem_st32(tS + q / 2, pk);
+            else if constexpr (REP == 2) {
+              tmem_st16(tS + copy * 32, pk);
+              tmem_st16(tS + copy * 32 + 16, pk + 16);
+            } else {
+              tmem_st16(tS + copy * 16, pk);
             }
           }
-        };
-        if (F8 && small_pages) weights(std::integral_constant<bool, F8>{});
-        else weights(std::false_type{});
-        float a0, a1;
-        f2_split(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a0, a1);
-        if (F8 && !small_pages) {  // these were P'
-          const float back = ex2_approx(-lf);
-          a0 *= back;
-          a1 *= back;
-        }
-        if (__any_sync(0xffffffffu, rescale)) {
-          const float alpha_o = F8 ? alpha * beta : alpha;
-          const uint64_t al2 = f2(alpha_o, alpha_o);
+          l_run = l_run * alpha + sum;
+          m_run = m_new;
+          if constexpr (REP > 1) {
+            const uint32_t zero[16] = {};
 #pragma unroll
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t o[32];
-            tmem_ld32(tO + q * 32, o);
-            tmem_wait_ld();
-            reg_fence(o);
+            for (int x = 1; x < REP; ++x) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float x0, x1;
-              f2_split(f2_mul(f2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), al2), x0, x1);
-              o[2 * k] = __float_as_uint(x0);
-              o[2 * k + 1] = __float_as_uint(x1);
+              for (int y = 0; y < 4 / REP; ++y) tmem_st16(tS + ((copy + x) % REP) * (64 / REP) + y * 16, zero);
             }
-            tmem_st32(tO + q * 32, o);
           }
-        }
-        l_run = l_run * alpha + a0 + a1;
-        m_run = m_new;
-        // P over the first 64 columns of the scores: this copy's keys, zeros for the other copies'
-        if constexpr (REP == 1) {
-          tmem_st32(tS, reinterpret_cast<const uint32_t(&)[32]>(pk[0]));
-          tmem_st32(tS + 32, reinterpret_cast<const uint32_t(&)[32]>(pk[32]));
         } else {
-          uint32_t zero[16] = {};
-          if constexpr (REP == 2) {
+          uint32_t sr[CW / 32][32];
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              tmem_st16(tS + copy * 32 + hh * 16, pk + hh * 16);
-              tmem_st16(tS + (copy ^ 1) * 32 + hh * 16, zero);
+          for (int q = 0; q < CW / 32; ++q) tmem_ld32(tS + copy * CW + q * 32, sr[q]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < CW / 32; ++q) reg_fence(sr[q]);
+          auto sv = [&](int k) { return __uint_as_float(sr[k >> 5][k & 31]); };
+          const int vis = lim - i * BN - copy * CW;
+          // Scores of keys that a row does not see become -inf, 32 columns at a time where some row of
+          // the warp needs it (rows that hold no query do not count). c > 0 keeps them at -inf, and
+          // their weights at zero.
+          if (!__all_sync(0xffffffffu, !valid || vis >= CW)) {
+#pragma unroll
+            for (int q = 0; q < CW / 32; ++q) {
+              if (__all_sync(0xffffffffu, !valid || vis >= 32 * (q + 1))) continue;
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (32 * q + k >= vis) sr[q][k] = 0xff800000u;
             }
-          } else {
-            tmem_st16(tS + copy * 16, pk);
+          }
+          float mt;
+          {
+            constexpr int NT = (CW + 2) / 3;
+            float t[NT];
 #pragma unroll
-            for (int x = 1; x < 4; ++x) tmem_st16(tS + ((copy + x) & 3) * 16, zero);
+            for (int x = 0; x < NT; ++x)
+              t[x] = max3(sv(3 * x), 3 * x + 1 < CW ? sv(3 * x + 1) : -INFINITY, 3 * x + 2 < CW ? sv(3 * x + 2) : -INFINITY);
+            mt = tree_max<NT>(t);
+          }
+          const float m_tile = (mt == -INFINITY || !valid) ? -INFINITY : mt * c;
+          float m_new = m_run, alpha = 1.f;
+          bool rescale = false;
+          if (i < (SPLIT ? 2 : 1)) {
+            m_new = m_tile;
+          } else if (m_tile > m_run + RESCALE_THRESHOLD) {
+            m_new = m_tile;
+            alpha = ex2_approx(m_run - m_new);
+            rescale = true;
+          }
+          const float nb = (m_new == -INFINITY) ? 0.f : -m_new;
+          const uint64_t c2 = f2(c, c), nb2 = f2(nb, nb);
+          uint64_t acc[4] = {0, 0, 0, 0};
+          uint32_t pk[CW / 2];
+#pragma unroll
+          for (int k = 0; k < CW / 2; ++k) {
+            float t0, t1;
+            f2_split(f2_fma(f2(sv(2 * k), sv(2 * k + 1)), c2, nb2), t0, t1);
+            const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+            acc[k & 3] = f2_add(acc[k & 3], f2(p0, p1));
+            pk[k] = pack2<BF16>(p0, p1);
+          }
+          float a0, a1;
+          f2_split(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a0, a1);
+          if (__any_sync(0xffffffffu, rescale)) {
+            const uint64_t al2 = f2(alpha, alpha);
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t o[32];
+              tmem_ld32(tO + q * 32, o);
+              tmem_wait_ld();
+              reg_fence(o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                float x0, x1;
+                f2_split(f2_mul(f2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), al2), x0, x1);
+                o[2 * k] = __float_as_uint(x0);
+                o[2 * k + 1] = __float_as_uint(x1);
+              }
+              tmem_st32(tO + q * 32, o);
+            }
+          }
+          l_run = l_run * alpha + a0 + a1;
+          m_run = m_new;
+          // P over the first 64 columns of the scores: this copy's keys, zeros for the other copies'
+          if constexpr (REP == 1) {
+            tmem_st32(tS, reinterpret_cast<const uint32_t(&)[32]>(pk[0]));
+            tmem_st32(tS + 32, reinterpret_cast<const uint32_t(&)[32]>(pk[32]));
+          } else {
+            uint32_t zero[16] = {};
+            if constexpr (REP == 2) {
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                tmem_st16(tS + copy * 32 + hh * 16, pk + hh * 16);
+                tmem_st16(tS + (copy ^ 1) * 32 + hh * 16, zero);
+              }
+            } else {
+              tmem_st16(tS + copy * 16, pk);
+#pragma unroll
+              for (int x = 1; x < 4; ++x) tmem_st16(tS + ((copy + x) & 3) * 16, zero);
+            }
           }
         }
         tmem_wait_st();
