@@ -1056,11 +1056,11 @@ __global__ void __launch_bounds__(num_warps(F8) * 32, 1)
       // ======================================================================= queries split, V turned
       const int ct = (int)threadIdx.x - WARP_CONVERT * 32;
       const uint32_t sHeld = smem_u32(smem + LY::OFF_HELD), sV = smem_u32(smem + LY::OFF_V);
-      // V: thread = 16 elements of a row at a time. The halves of a warp write other 16-byte pieces of
-      // their rows first, so that the swizzled rows of two 64-column halves do not meet in a bank.
+      // V: thread = 16 elements of a row at a time. The lanes of the second 64-column half take their rows in other
+      // pairs (row ^ 1), so that the swizzled rows of the two halves do not meet in a bank.
       constexpr int PIECES = D / 16, TURNS = PIECES, BATCH = 4;
-      const int c16 = ct % PIECES, row0 = ct / PIECES;
-      const uint32_t half = (uint32_t)(c16 >> 2) * LY::CHUNK_BYTES, j0 = (c16 & 3) * 2, odd = c16 >> 2;
+      const int c16 = ct % PIECES, row0 = (ct / PIECES) ^ (c16 >> 2);
+      const uint32_t half = (uint32_t)(c16 >> 2) * LY::CHUNK_BYTES, j0 = (c16 & 3) * 2;
       // Q: D/8 lanes a row, 8 elements each
       constexpr int QL = D / 8, Q_TURN = 128 / QL;
       const int ql = ct % QL;
@@ -1073,32 +1073,49 @@ __global__ void __launch_bounds__(num_warps(F8) * 32, 1)
         const Item it = *src;
         item_done();
         if (it.n == 0) break;
-        ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->q_empty), (n_q & 1u) ^ 1u, abort_flag, p));
-        if (!ok) break;
         const int rows = min(it.nt, SPLIT ? p.tpt : 2 * p.tpt) * p.G, per_tile = p.tpt * p.G;
         in_bounds(p, it.tok0 >= 0 && it.tok0 + it.nt <= p.T && (it.h + 1) * p.G <= p.q.H);
-#pragma unroll 2
-        for (int x = ct / QL; x < (rows + Q_TURN - 1) / Q_TURN * Q_TURN; x += Q_TURN) {
-          const bool live = x < rows;
-          const int tok = token_of_row(p, SPLIT || x < per_tile ? x : x - per_tile) + (SPLIT || x < per_tile ? 0 : p.tpt);
-          const int head = x - tok * p.G;
-          uint4 u = make_uint4(0, 0, 0, 0);
-          if (live) u = *reinterpret_cast<const uint4*>(p.q.ptr + (long long)(it.tok0 + tok) * p.q.ts + (long long)(it.h * p.G + head) * p.q.hs + ql * 8);
-          uint32_t w[TERMS > 0 ? TERMS : 1][2];
-          const int ex = split_row<D, BF16>(u, w);
-          const uint32_t tile = SPLIT || x < per_tile ? 0u : 1u, row = tile ? x - per_tile : x;
-          if (live && ql == 0) exps[(n_q & 1u) * LY::EXP_ROWS + tile * BM + row] = (signed char)ex;
+        // rows of a lane, some at a time, the first of them before the buffer is free
+        constexpr int HELD = SPLIT ? 4 : 8;
+        uint4 u[HELD];
+        auto ask = [&](int x0) {
 #pragma unroll
-          for (int m = 0; m < TERMS; ++m) {
-            if (!live) break;
-#pragma unroll
-            for (int a = 0; a < REP; ++a) {
-              const uint32_t r = row + a * (BM / REP);
-              const uint32_t sw = D == 128 ? r & 7u : (r >> 1) & 3u;
-              st_shared_v2(sQ + tile * LY::Q_BYTES + m * (BM * D) + r * D + ((((uint32_t)ql >> 1) ^ sw) << 4) + (ql & 1) * 8,
-                           w[m][0], w[m][1]);
+          for (int y = 0; y < HELD; ++y) {
+            const int x = x0 + y * Q_TURN;
+            u[y] = make_uint4(0, 0, 0, 0);
+            if (x < rows) {
+              const int tok = token_of_row(p, SPLIT || x < per_tile ? x : x - per_tile) + (SPLIT || x < per_tile ? 0 : p.tpt);
+              u[y] = *reinterpret_cast<const uint4*>(p.q.ptr + (long long)(it.tok0 + tok) * p.q.ts +
+                                                     (long long)(it.h * p.G + x - tok * p.G) * p.q.hs + ql * 8);
             }
           }
+        };
+        ask(ct / QL);
+        ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->q_empty), (n_q & 1u) ^ 1u, abort_flag, p));
+        if (!ok) break;
+#pragma unroll 1
+        for (int x0 = ct / QL; x0 - ct / QL < rows; x0 += HELD * Q_TURN) {
+#pragma unroll
+          for (int y = 0; y < HELD; ++y) {
+            const int x = x0 + y * Q_TURN;
+            if (x - ct / QL >= rows) break;  // (the same for all threads)
+            uint32_t w[TERMS > 0 ? TERMS : 1][2];
+            const int ex = split_row<D, BF16>(u[y], w);
+            if (x >= rows) continue;
+            const uint32_t tile = SPLIT || x < per_tile ? 0u : 1u, row = tile ? x - per_tile : x;
+            if (ql == 0) exps[(n_q & 1u) * LY::EXP_ROWS + tile * BM + row] = (signed char)ex;
+#pragma unroll
+            for (int m = 0; m < TERMS; ++m) {
+#pragma unroll
+              for (int a = 0; a < REP; ++a) {
+                const uint32_t r = row + a * (BM / REP);
+                const uint32_t sw = D == 128 ? r & 7u : (r >> 1) & 3u;
+                st_shared_v2(sQ + tile * LY::Q_BYTES + m * (BM * D) + r * D + ((((uint32_t)ql >> 1) ^ sw) << 4) + (ql & 1) * 8,
+                             w[m][0], w[m][1]);
+              }
+            }
+          }
+          if (x0 - ct / QL + HELD * Q_TURN < rows) ask(x0 + HELD * Q_TURN);
         }
         ++n_q;
         fence_proxy_async_smem();
@@ -1110,7 +1127,7 @@ __global__ void __launch_bounds__(num_warps(F8) * 32, 1)
           ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->held_full[hs]), (t / LY::HELD_RING) & 1u, abort_flag, p));
           if (!ok) break;
           uint32_t v[BATCH][4];
-          const uint32_t from = sHeld + hs * LY::K_BYTES + (uint32_t)ct * 16u;
+          const uint32_t from = sHeld + hs * LY::K_BYTES + (uint32_t)(row0 * D + c16 * 16);
 #pragma unroll
           for (int y = 0; y < BATCH; ++y) ld_shared_u4(from + y * 2048u, v[y]);
           if (t >= (uint32_t)LY::V_SLOTS) {
@@ -1119,7 +1136,7 @@ __global__ void __launch_bounds__(num_warps(F8) * 32, 1)
           }
           const long long keys = it.len - (long long)(it.j0 + i) * BN;  // rows that hold a key of the sequence
           const uint32_t to = sV + slot * LY::TILE_BYTES + half;
-#pragma unroll
+#pragma unroll 1
           for (int y0 = 0; y0 < TURNS; y0 += BATCH) {
 #pragma unroll
             for (int y = 0; y < BATCH; ++y) {
@@ -1130,10 +1147,8 @@ __global__ void __launch_bounds__(num_warps(F8) * 32, 1)
               for (int e = 0; e < 4; ++e) unpack4_e4m3(v[y][e], w[2 * e], w[2 * e + 1]);
               if (y0 + BATCH < TURNS) ld_shared_u4(from + (y0 + BATCH + y) * 2048u, v[y]);
               const uint32_t base = to + row * 128u, sw = row & 7u;
-              st_shared_v4(base + (((j0 + odd) ^ sw) << 4), odd ? w[4] : w[0], odd ? w[5] : w[1], odd ? w[6] : w[2],
-                           odd ? w[7] : w[3]);
-              st_shared_v4(base + (((j0 + 1 - odd) ^ sw) << 4), odd ? w[0] : w[4], odd ? w[1] : w[5],
-                           odd ? w[2] : w[6], odd ? w[3] : w[7]);
+              st_shared_v4(base + ((j0 ^ sw) << 4), w[0], w[1], w[2], w[3]);
+              st_shared_v4(base + (((j0 + 1) ^ sw) << 4), w[4], w[5], w[6], w[7]);
             }
           }
           fence_proxy_async_smem();
