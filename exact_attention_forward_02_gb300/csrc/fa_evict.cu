@@ -20,15 +20,15 @@ int allow_smem(const void* kernel, int bytes, bool* done) {
   return FA_OK;
 }
 
-template <int D, bool BF16, bool F8>
+template <int D, bool BF16, int MODE>
 int launch_weigh(const CUtensorMap& mq, const CUtensorMap& mk, const weigh::Params& p, int index, int sms,
                  cudaStream_t st) {
-  constexpr int SMEM = weigh::Layout<D, F8>::SMEM_BYTES;
-  auto kern = weigh::fa_weigh_kernel<D, BF16, F8>;
+  constexpr int SMEM = weigh::Layout<D, BF16, MODE>::SMEM_BYTES;
+  auto kern = weigh::fa_weigh_kernel<D, BF16, MODE>;
   static bool done[fa_host::MAX_DEVICES] = {};
   const int rc = allow_smem(reinterpret_cast<const void*>(kern), SMEM, &done[index]);
   if (rc != FA_OK) return rc;
-  return launch_dependent(kern, dim3(sms), dim3(F8 ? 512 : 384), SMEM, st, mq, mk, p);
+  return launch_dependent(kern, dim3(sms), dim3(weigh::num_warps(MODE) * 32), SMEM, st, mq, mk, p);
 }
 
 size_t evict_list_bytes(int B, int Hkv, int budget) { return round256((size_t)B * Hkv * budget * sizeof(int2)); }
@@ -104,23 +104,28 @@ int fa_paged_key_weights(const fa_paged_kv* kv, const float* k_scale, const fa_h
   p.cap = cap < 0x7fffff00LL ? (int)cap : 0x7fffff00;
   p.c = scale * 1.4426950408889634f;
   p.wait_limit_ns = fa_host::wait_limit_ns();
-  const bool bf16 = dtype == FA_BF16;
-  CUtensorMap mq, mk;
-  if ((rc = paged_map(&mq, q->ptr, bf16, 3, kv->d, {(uint64_t)q->H, (uint64_t)T}, {q->head_stride, q->token_stride},
+  const bool bf16 = dtype == FA_BF16, held = f8 && p.cols <= weigh::HELD_ROWS;
+  p.page_shift = -1;
+  for (int x = 0; x < 31; ++x)
+    if (kv->page_size == 1 << x) p.page_shift = x;
+  if (held) p.q = dev(q);
+  CUtensorMap mq = {}, mk;
+  if (!held && (rc = paged_map(&mq, q->ptr, bf16, 3, kv->d, {(uint64_t)q->H, (uint64_t)T}, {q->head_stride, q->token_stride},
                       {(uint32_t)p.G, (uint32_t)p.tpt})) != FA_OK)
     return rc;
   if ((rc = paged_map(&mk, kv->k, bf16, 4, kv->d, {(uint64_t)kv->page_size, (uint64_t)kv->Hkv, (uint64_t)kv->num_pages},
                       {kv->token_stride, kv->head_stride, kv->page_stride}, {(uint32_t)p.box_keys, 1, 1},
-                      f8 ? ROWS8 : ROWS16)) != FA_OK)
+                      held ? ROWS8_SWIZZLED : f8 ? ROWS8 : ROWS16)) != FA_OK)
     return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  auto go = [&](auto f) {
-    constexpr bool F = decltype(f)::value;
+  auto go = [&](auto m) {
+    constexpr int M = decltype(m)::value;
     if (kv->d == 64)
-      return bf16 ? launch_weigh<64, true, F>(mq, mk, p, index, sms, st) : launch_weigh<64, false, F>(mq, mk, p, index, sms, st);
-    return bf16 ? launch_weigh<128, true, F>(mq, mk, p, index, sms, st) : launch_weigh<128, false, F>(mq, mk, p, index, sms, st);
+      return bf16 ? launch_weigh<64, true, M>(mq, mk, p, index, sms, st) : launch_weigh<64, false, M>(mq, mk, p, index, sms, st);
+    return bf16 ? launch_weigh<128, true, M>(mq, mk, p, index, sms, st) : launch_weigh<128, false, M>(mq, mk, p, index, sms, st);
   };
-  return f8 ? go(std::true_type{}) : go(std::false_type{});
+  if (held) return go(std::integral_constant<int, weigh::HELD>{});
+  return f8 ? go(std::integral_constant<int, weigh::TURNED>{}) : go(std::integral_constant<int, weigh::HALF>{});
 }
 
 size_t fa_paged_evict_workspace_bytes(int B, int Hkv, int budget, int held8) {

@@ -219,6 +219,22 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   if (mbar_try_wait(bar, parity)) return true;
   return wait_slow(bar, parity, abort_flag, p, limits);
 }
+// The same in fewer instructions, for kernels of many roles, whose code passes the instruction cache.
+template <typename P>
+__device__ __forceinline__ bool wait_compact(uint32_t bar, uint32_t parity, volatile int* abort_flag, const P& p,
+                                             uint32_t limits = 1) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  do {
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > p.wait_limit_ns * limits) {
+      atomicCAS(p.status, 0, FA_ERR_TIMEOUT);
+      *abort_flag = 1;
+      return false;
+    }
+  } while (!mbar_try_wait(bar, parity));
+  return true;
+}
 // on the way out after an abort: ignores the flag, still bounded
 template <typename P>
 __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, const P& p) {

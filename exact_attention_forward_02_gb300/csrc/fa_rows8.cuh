@@ -20,6 +20,10 @@
 // and O~ rescaled. P' = P v_scale / vref 2^11 <= 2^15, vref as in fa_paged.cuh.
 // l stays spread over the threads until the item ends.
 //
+// The code that an item needs is kept small (wait_compact, loops that are not unrolled): with 16 warps in eight roles
+// it passes the instruction cache, and what was fetched again for each item cost 5 us an item (64 ragged sequences:
+// 125 us with two key tiles a step and unrolled ends, 94 without).
+//
 // 16 warps: 0-7 softmax, 8 loads K and 11 V, 9 issues S and 12 PV, 10 walks the items, 13 splits queries, up to two
 // items ahead, 14 and 15 join the two warpgroups' states and write them out, while those go on with the next item.
 #pragma once
@@ -41,23 +45,6 @@ struct Barriers8 : Barriers {
   uint64_t join_full[2], join_empty[2];  // [item & 1]
   alignas(16) int said[2][2][4];  // [warpgroup][round & 1][warp]
 };
-
-// wait_bar in fewer instructions: with 16 warps in seven roles the code that an item needs passes the instruction
-// cache, and what is fetched again for each item costs more than what a wait does.
-__device__ __forceinline__ bool wait8(uint32_t bar, uint32_t parity, volatile int* abort_flag, const Params& p,
-                                      uint32_t limits = 1) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  do {
-    if (*abort_flag) return false;
-    if (globaltimer_ns() - t0 > p.wait_limit_ns * limits) {
-      atomicCAS(p.status, 0, FA_ERR_TIMEOUT);
-      *abort_flag = 1;
-      return false;
-    }
-  } while (!mbar_try_wait(bar, parity));
-  return true;
-}
 
 template <int D, int TERMS, int R>
 struct Layout8 {
@@ -186,7 +173,7 @@ __global__ void __launch_bounds__(R8_THREADS, 1)
   uint32_t n_item = 0;
   auto item_next = [&]() -> const Item* {
     const uint32_t s = n_item % ITEM_SLOTS;
-    const bool w = wait8(smem_u32(&bars->item_full[s]), (n_item / ITEM_SLOTS) & 1u, abort_flag, p, ITEM_WAITS);
+    const bool w = wait_compact(smem_u32(&bars->item_full[s]), (n_item / ITEM_SLOTS) & 1u, abort_flag, p, ITEM_WAITS);
     return __all_sync(0xffffffffu, w) ? &bars->items[s] : nullptr;
   };
   auto item_done = [&]() {  // this warp needs nothing more of the item
@@ -195,7 +182,7 @@ __global__ void __launch_bounds__(R8_THREADS, 1)
     ++n_item;
   };
   auto wait_all = [&](uint64_t* bar, uint32_t par) -> bool {
-    return __all_sync(0xffffffffu, wait8(smem_u32(bar), par, abort_flag, p));
+    return __all_sync(0xffffffffu, wait_compact(smem_u32(bar), par, abort_flag, p));
   };
 
   if (warp >= WARP_LOAD) {
@@ -418,7 +405,7 @@ __global__ void __launch_bounds__(R8_THREADS, 1)
         const uint32_t n = n_item, at = n % LY::JOINS;
         item_done();
         if (it.n == 0) break;
-        ok = __all_sync(0xffffffffu, wait8(smem_u32(&bars->join_full[at]), (n / LY::JOINS) & 1u, abort_flag, p, ITEM_WAITS));
+        ok = __all_sync(0xffffffffu, wait_compact(smem_u32(&bars->join_full[at]), (n / LY::JOINS) & 1u, abort_flag, p, ITEM_WAITS));
         if (!ok) break;
         const float* st = reinterpret_cast<const float*>(smem + LY::OFF_STATE) + at * LY::STATE_FLOATS;
         const float* stage = reinterpret_cast<const float*>(smem + LY::OFF_STAGE) + at * (2 * R * D);

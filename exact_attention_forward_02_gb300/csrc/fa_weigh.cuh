@@ -12,10 +12,16 @@
 // later keys are seen by fewer rows: a head's units are dealt from both ends in turn, so that any run of
 // them costs about its share.
 //
-// 12 warps: 0-7 softmax, 8 and 11 loads (a key tile each, pages box by box), 9 MMA issuer; F8 (a cache in
-// 8 bits): 4 more turn each key tile into the type of q, exactly; its scale is the thread's own factor.
-// Single tokens are bound by HBM (K is read once), chunks by the tensor cores and the exponentials, which
-// take the same time (128 x 128 scores: 545 and 512 cycles).
+// Three forms, by the cache and the rows (MODE):
+//   HALF    a 16-bit cache
+//   TURNED  a cache in 8 bits, more than 16 rows: 4 more warps turn each key tile into the type of q, exactly, once
+//           for all rows
+//   HELD    a cache in 8 bits, up to 16 rows (single tokens, drafts): the products take K as it is held, and a warp
+//           splits the rows into sums of E4M3 numbers (split_row), side by side as columns; turning K would cost
+//           shared memory as many cycles as HBM takes to bring it (fa_paged.cuh)
+// A key's scale is its thread's own factor. 12 warps and those: 0-7 softmax, 8 and 11 loads (a key tile each, pages
+// box by box), 9 MMA issuer. Single tokens are bound by HBM (K is read once), chunks by the tensor cores and the
+// exponentials, which take the same time (128 x 128 scores: 545 and 512 cycles).
 #pragma once
 
 #include "fa_paged.cuh"
@@ -25,17 +31,20 @@ namespace weigh {
 
 using paged::BM;
 using paged::BN;
-using paged::wait_bar;
+using paged::wait_compact;
 using paged::wait_drain;
+enum Mode { HALF, TURNED, HELD };
+constexpr int HELD_ROWS = 16;
 constexpr int WARP_LOAD = 8, WARP_MMA = 9, WARP_LOAD2 = 11, WARP_CONVERT = 12;
-constexpr int MAX_SLOTS = 8;
+constexpr int MAX_SLOTS = 4;
 constexpr int COST_UNIT = 2;  // what a unit costs beside its row tiles, in those
 
 struct Params {
   const float* L;
   const float* ks;  // F8: scales [num_pages][Hkv]
   float* w;         // [num_pages][Hkv][page_size]
-  int num_pages, page_size, box_keys;
+  HeadsDev q;       // HELD
+  int num_pages, page_size, page_shift, box_keys;  // page_shift: log2 of the page size, -1 where that is none
   int Hkv, G, Hq, tpt, cols;  // tpt: tokens per tile of rows; cols = tpt G
   uint32_t by_g;              // ceil(2^16 / G)
   const int *cu, *lens, *table;
@@ -47,8 +56,8 @@ struct Params {
 
 struct Barriers {
   uint64_t q_full[4], q_empty[4];
-  uint64_t k_full[MAX_SLOTS], k_empty[MAX_SLOTS];
-  uint64_t held_full[MAX_SLOTS], held_empty[MAX_SLOTS];
+  uint64_t k_full[2][MAX_SLOTS], k_empty[2][MAX_SLOTS];  // [key tile of a unit]
+  uint64_t raw_full[2][MAX_SLOTS], raw_empty[2][MAX_SLOTS];
   uint64_t s_full[2][2], s_empty[2][2];
   uint64_t mma_drain;
   long long warp_cost[16];
@@ -58,26 +67,35 @@ struct Barriers {
   int abort_flag;
 };
 
-template <int D, bool F8>
+template <int D, bool BF16, int MODE>
 struct Layout {
-  static constexpr int TILE_BYTES = BM * D * 2, HELD_BYTES = BM * D, CHUNK_BYTES = BM * 128, CHUNKS = D / 64;
-  static constexpr int Q_SLOTS = D == 64 ? 4 : 2;
-  static constexpr int K_SLOTS = D == 64 ? (F8 ? 4 : 6) : (F8 ? 3 : 4);
-  static constexpr int HELD_SLOTS = !F8 ? 0 : D == 64 ? 6 : 3, HELD_RING = F8 ? HELD_SLOTS : 1;
-  static constexpr int OFF_Q = 0, OFF_K = Q_SLOTS * TILE_BYTES, OFF_HELD = OFF_K + K_SLOTS * TILE_BYTES;
-  static constexpr int OFF_L = OFF_HELD + HELD_SLOTS * HELD_BYTES;  // 128 floats for each softmax warp
-  static constexpr int OFF_BAR = OFF_L + 8 * 512;
+  static constexpr int TERMS = BF16 ? 2 : 3, NQ = TERMS * HELD_ROWS;  // HELD: columns, term by term
+  static constexpr int CHUNK_BYTES = BM * 128, CHUNKS = D / 64;
+  // tiles that the products read, and tiles as they are loaded where they have to be turned
+  static constexpr int TILE_BYTES = MODE == HELD ? BM * D : BM * D * 2, RAW_BYTES = BM * D;
+  static constexpr int Q_BYTES = MODE == HELD ? NQ * D : BM * D * 2;
+  static constexpr int Q_SLOTS = D == 64 || MODE == HELD ? 4 : 2;
+  // slots of each of a unit's two key tiles, which have rings of their own: a unit may have one tile only, and a ring
+  // shared by two loading warps would pass the one that has nothing to load
+  static constexpr int K_SLOTS = MODE == HELD ? 4 : D == 64 ? (MODE == TURNED ? 2 : 3) : (MODE == TURNED ? 1 : 2);
+  static constexpr int RAW_SLOTS = MODE != TURNED ? 0 : D == 64 ? 3 : 2, RAW_RING = MODE == TURNED ? RAW_SLOTS : 1;
+  static constexpr int S_COLS = MODE == HELD ? 64 : 128;  // of one of the four buffers of S^T
+  static constexpr int OFF_Q = 0, OFF_K = (Q_SLOTS * Q_BYTES + 1023) / 1024 * 1024, OFF_RAW = OFF_K + 2 * K_SLOTS * TILE_BYTES;
+  static constexpr int OFF_L = OFF_RAW + 2 * RAW_SLOTS * RAW_BYTES;  // 128 floats for each softmax warp
+  static constexpr int OFF_EXP = OFF_L + 8 * 512;                // HELD: 2^e of the rows, [8][HELD_ROWS]
+  static constexpr int OFF_BAR = OFF_EXP + (MODE == HELD ? 8 * HELD_ROWS * 4 : 0);
   static constexpr int SMEM_BYTES = OFF_BAR + 1024;
   static_assert(sizeof(Barriers) <= 1024 && SMEM_BYTES <= paged::SMEM_LIMIT, "shared memory budget");
 };
 
 struct Seq {
   int t0, n, len, units;  // first row of q, new tokens, cached tokens, units of a head
-  int cost;               // of a unit
+  int cost, qn;           // of a unit; tiles of rows
 };
 struct Unit {
   int b, h, t0, n, len, key0, q0, qn;  // first key; tiles of rows [q0, qn) see one of its keys
   bool two;                            // its second key tile holds a key
+  bool same;                           // its one tile of rows is that of the unit before
 };
 
 __device__ __forceinline__ Seq load_seq(const Params& p, int b, bool report) {
@@ -88,7 +106,8 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int b, bool report) {
   s.n = rows_ok ? end - s.t0 : 0;
   s.len = s.n ? max(0, min(len, p.cap)) : 0;
   s.units = (int)(((uint32_t)s.len + 255u) / 256u);
-  const int qt = s.n ? (s.n - 1) / p.tpt + 1 : 0;
+  const int qt = s.n <= p.tpt ? (s.n > 0) : (s.n - 1) / p.tpt + 1;
+  s.qn = qt;
   s.cost = COST_UNIT + qt;
   if (p.causal && s.len) {  // rows see the new keys in part
     const long long seen = 2ll * s.len - min(s.n, s.len);
@@ -102,6 +121,8 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int b, bool report) {
 struct Walk {
   Seq s;
   int b, idx;  // unit of the sequence: head * units + place
+  int h, i;    // those two
+  bool one;    // the last unit had one tile of rows, the first
   long long u, u1;
   __device__ __forceinline__ void begin(const Params& p, const Barriers* bars, long long u0, long long end) {
     u1 = end;
@@ -109,19 +130,22 @@ struct Walk {
     b = bars->start_b;
     idx = 0;
     s = Seq{};
+    h = i = 0;
+    one = false;
     if (u0 >= u1) return;
     s = load_seq(p, b, false);
     // the first unit that begins in the range
     const long long skip = (bars->start_rem + s.cost - 1) / s.cost;
     idx = (int)skip;
     u += skip * s.cost - bars->start_rem;
+    if (idx < p.Hkv * s.units) {
+      h = idx / s.units;
+      i = idx - h * s.units;
+    }
   }
   __device__ __forceinline__ bool next(const Params& p, Unit& x) {
     while (u < u1) {
       if (idx < p.Hkv * s.units) {
-        const int h = idx / s.units, i = idx - h * s.units;
-        ++idx;
-        u += s.cost;
         const int j = i & 1 ? s.units - 1 - (i >> 1) : i >> 1;
         x.b = b;
         x.h = h;
@@ -129,27 +153,36 @@ struct Walk {
         x.n = s.n;
         x.len = s.len;
         x.key0 = j * 256;
-        x.q0 = p.causal ? max(0, x.key0 - (s.len - s.n)) / p.tpt : 0;
-        x.qn = (s.n - 1) / p.tpt + 1;
+        x.q0 = p.causal && s.qn > 1 && x.key0 > s.len - s.n ? (x.key0 - (s.len - s.n)) / p.tpt : 0;
+        x.qn = s.qn;
         x.two = s.len - x.key0 > BN;
+        x.same = one && x.qn == 1;
+        one = x.qn == 1;
+        ++idx;
+        u += s.cost;
+        if (++i == s.units) i = 0, ++h, one = false;
         return true;
       }
       do {
         if (++b >= p.B) return false;
         s = load_seq(p, b, false);
       } while (s.units == 0);
-      idx = 0;
+      idx = h = i = 0;
+      one = false;
     }
     return false;
   }
 };
 
-template <int D, bool BF16, bool F8>
-__global__ void __launch_bounds__(F8 ? 512 : 384, 1)
+__host__ __device__ constexpr int num_warps(int mode) { return mode == TURNED ? 16 : mode == HELD ? 13 : 12; }
+
+template <int D, bool BF16, int MODE>
+__global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
     fa_weigh_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ Params p) {
-  using LY = Layout<D, F8>;
-  constexpr int NUM_WARPS = F8 ? 16 : 12, NUM_THREADS = NUM_WARPS * 32;
+  using LY = Layout<D, BF16, MODE>;
+  constexpr int NUM_WARPS = num_warps(MODE), NUM_THREADS = NUM_WARPS * 32;
+  constexpr bool F8 = MODE != HALF;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
   if (smem_u32(smem) & 1023u) {
@@ -157,7 +190,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     return;
   }
   Barriers* bars = reinterpret_cast<Barriers*>(smem + LY::OFF_BAR);
-  const uint32_t sQ = smem_u32(smem + LY::OFF_Q), sK = smem_u32(smem + LY::OFF_K), sHeld = smem_u32(smem + LY::OFF_HELD);
+  const uint32_t sQ = smem_u32(smem + LY::OFF_Q), sK = smem_u32(smem + LY::OFF_K), sRaw = smem_u32(smem + LY::OFF_RAW);
   volatile int* abort_flag = &bars->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -166,12 +199,16 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
       mbar_init(smem_u32(&bars->q_empty[s]), 1);
     }
     for (int s = 0; s < LY::K_SLOTS; ++s) {
-      mbar_init(smem_u32(&bars->k_full[s]), F8 ? 4 : 1);
-      mbar_init(smem_u32(&bars->k_empty[s]), 1);
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(smem_u32(&bars->k_full[x][s]), MODE == TURNED ? 4 : 1);
+        mbar_init(smem_u32(&bars->k_empty[x][s]), 1);
+      }
     }
-    for (int s = 0; s < LY::HELD_SLOTS; ++s) {
-      mbar_init(smem_u32(&bars->held_full[s]), 1);
-      mbar_init(smem_u32(&bars->held_empty[s]), 4);
+    for (int s = 0; s < LY::RAW_SLOTS; ++s) {
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(smem_u32(&bars->raw_full[x][s]), 1);
+        mbar_init(smem_u32(&bars->raw_empty[x][s]), 4);
+      }
     }
     for (int x = 0; x < 4; ++x) {
       mbar_init(smem_u32(&bars->s_full[x >> 1][x & 1]), 1);
@@ -182,7 +219,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     fence_mbar_init();
   }
   if (warp == WARP_LOAD && lane == 0) {
-    tma_prefetch_desc(&tmQ);
+    if (MODE != HELD) tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
   }
   if (warp == WARP_MMA) {
@@ -238,73 +275,70 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
   Walk walk;
   walk.begin(p, bars, u0, u1);
   Unit it;
+  auto wait_all = [&](uint64_t* bar, uint32_t par) -> bool {
+    return __all_sync(0xffffffffu, wait_compact(smem_u32(bar), par, abort_flag, p));
+  };
+  auto page_of = [&](int key) { return p.page_shift >= 0 ? (uint32_t)key >> p.page_shift : (uint32_t)key / (uint32_t)p.page_size; };
 
   if (warp == WARP_LOAD || warp == WARP_LOAD2) {
     // ========================================================================= loads
     // Key tile x of a unit (x: the warp) goes box by box, a page each; warp 8 loads the rows of q as well. Table
     // entries are asked for a unit ahead.
     const int x = warp == WARP_LOAD2;
-    constexpr int BOX_CHUNKS = F8 ? 1 : LY::CHUNKS, SLOTS = F8 ? LY::HELD_SLOTS : LY::K_SLOTS;
-    constexpr uint32_t BOX_ROW = F8 ? D : 128, SLOT_BYTES = F8 ? LY::HELD_BYTES : LY::TILE_BYTES;
-    uint64_t* const full = F8 ? bars->held_full : bars->k_full;
-    uint64_t* const empty = F8 ? bars->held_empty : bars->k_empty;
-    const uint32_t sLoad = F8 ? sHeld : sK;
-    const int boxes = BN / p.box_keys, my_box = lane % boxes, my_chunk = lane / boxes;
+    constexpr int BOX_CHUNKS = F8 ? 1 : LY::CHUNKS, SLOTS = MODE == TURNED ? LY::RAW_SLOTS : LY::K_SLOTS;
+    constexpr uint32_t BOX_ROW = F8 ? D : 128, SLOT_BYTES = MODE == TURNED ? LY::RAW_BYTES : LY::TILE_BYTES;
+    uint64_t* const full = MODE == TURNED ? bars->raw_full[x] : bars->k_full[x];
+    uint64_t* const empty = MODE == TURNED ? bars->raw_empty[x] : bars->k_empty[x];
+    const uint32_t sLoad = (MODE == TURNED ? sRaw : sK) + x * SLOTS * SLOT_BYTES;
+    const int box_shift = 31 - __clz(p.box_keys), boxes = BN >> box_shift, my_box = lane & (boxes - 1);
+    const int my_chunk = lane / boxes;
     const uint32_t box_bytes = (uint32_t)p.box_keys * BOX_ROW;
     const uint32_t box_off = (uint32_t)my_chunk * LY::CHUNK_BYTES + (uint32_t)my_box * box_bytes;
     const uint32_t q_bytes = (uint32_t)(LY::CHUNKS * p.cols) * 128u;
-    uint32_t t = 0, nq = 0, k_mask = 0, k_par = 0;  // key tiles and row tiles so far
+    uint32_t slot = 0, par = 0, nq = 0, k_mask = 0, k_par = 0;  // par: uses of the ring so far, as a parity
+    uint32_t used = 0;                                          // key tiles so far, up to SLOTS
     bool ok = true;
-    auto entry = [&](const Unit& u) -> int {  // of the lane's box; -1: it holds no key of the sequence
-      const int key = u.key0 + x * BN + my_box * p.box_keys;
-      if (key >= u.len) return -1;
-      const int page = p.table[(size_t)u.b * p.table_stride + (uint32_t)key / (uint32_t)p.page_size];
-      return page;
+    auto entry = [&](const Unit& u) -> int {  // of the lane's box
+      const int key = u.key0 + x * BN + (my_box << box_shift);
+      return key < u.len ? p.table[(size_t)u.b * p.table_stride + page_of(key)] : 0;
     };
     bool have = walk.next(p, it);
-    int page = have ? entry(it) : -1;
+    int page = have ? entry(it) : 0;
     while (ok && have) {
       Unit nx;
       const bool more = walk.next(p, nx);
-      const int next_page = more ? entry(nx) : -1;
-      if (page != -1 && (page < 0 || page >= p.num_pages)) {
+      const int next_page = more ? entry(nx) : 0;
+      const int key = it.key0 + x * BN + (my_box << box_shift);
+      if (key < it.len && (page < 0 || page >= p.num_pages)) {
         atomicCAS(p.status, 0, FA_ERR_RANGE);
         page = p.num_pages;  // reads as zeros
       }
-      const int key = it.key0 + x * BN + my_box * p.box_keys;
-      if (key < it.len && page == -1) {  // (a table entry of -1)
-        atomicCAS(p.status, 0, FA_ERR_RANGE);
-        page = p.num_pages;
-      }
-      // A warp waits for the release of every slot in turn, its own or not, so that no barrier lies two phases
-      // behind the one that it waits for (where the parity would fit as well).
-      for (int y = 0; y < (it.two ? 2 : 1) && ok; ++y) {
-        const uint32_t slot = (t + y) % SLOTS, round = (t + y) / SLOTS;
-        if (round > 0) ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&empty[slot]), (round - 1) & 1u, abort_flag, p));
-        if (!ok || y != x) continue;
+      if (x == 0 || it.two) {
+        if (used == SLOTS) ok = wait_all(&empty[slot], par ^ 1u);
+        else ++used;
+        if (!ok) break;
         const int keys = it.len - it.key0 - x * BN;
-        const int live = min(boxes, (keys + p.box_keys - 1) / p.box_keys);
-        if (lane == 0) mbar_arrive_expect_tx(smem_u32(&full[slot]), (uint32_t)(live * BOX_CHUNKS) * box_bytes);
+        const int live = min(boxes, (keys + p.box_keys - 1) >> box_shift);
+        const uint32_t bar = smem_u32(&full[slot]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(live * BOX_CHUNKS) * box_bytes);
         __syncwarp();
         if (my_chunk < BOX_CHUNKS && my_box < live)
-          tma_load_4d(sLoad + slot * SLOT_BYTES + box_off, &tmK, smem_u32(&full[slot]), my_chunk * 64,
-                      p.page_size > BN ? key % p.page_size : 0, it.h, page);
+          tma_load_4d(sLoad + slot * SLOT_BYTES + box_off, &tmK, bar, my_chunk * 64, p.page_size > BN ? key % p.page_size : 0,
+                      it.h, page);
         k_mask |= 1u << slot;
-        k_par = (k_par & ~(1u << slot)) | ((round & 1u) << slot);
+        k_par = (k_par & ~(1u << slot)) | (par << slot);
+        if (++slot == SLOTS) slot = 0, par ^= 1u;
       }
-      if (!ok) break;
-      t += it.two ? 2 : 1;
-      if (x == 0) {
+      if (MODE != HELD && x == 0 && !it.same) {
+#pragma unroll 1
         for (int q = it.q0; q < it.qn && ok; ++q, ++nq) {
-          const uint32_t slot = nq % LY::Q_SLOTS, round = nq / LY::Q_SLOTS;
-          if (round > 0)
-            ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->q_empty[slot]), (round - 1) & 1u, abort_flag, p));
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bars->q_full[slot]), q_bytes);
+          const uint32_t qs = nq % LY::Q_SLOTS, round = nq / LY::Q_SLOTS;
+          if (round > 0 && !(ok = wait_all(&bars->q_empty[qs], (round - 1) & 1u))) break;
+          if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bars->q_full[qs]), q_bytes);
           __syncwarp();
           if (lane < LY::CHUNKS)
-            tma_load_3d(sQ + slot * LY::TILE_BYTES + lane * LY::CHUNK_BYTES, &tmQ, smem_u32(&bars->q_full[slot]),
-                        lane * 64, it.h * p.G, it.t0 + q * p.tpt);
+            tma_load_3d(sQ + qs * LY::Q_BYTES + lane * LY::CHUNK_BYTES, &tmQ, smem_u32(&bars->q_full[qs]), lane * 64,
+                        it.h * p.G, it.t0 + q * p.tpt);
         }
       }
       it = nx;
@@ -320,67 +354,124 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     __syncwarp();
   } else if (warp == WARP_MMA) {
     // ========================================================================= MMA issuer
-    const uint32_t id = umma_idesc_f16(BF16 ? 1 : 0, 0, 0, BM, (uint32_t)(p.cols + 15) / 16 * 16);
-    const uint64_t dQ = umma_smem_desc(sQ, 16, 1024), dK = umma_smem_desc(sK, 16, 1024);
-    uint32_t t = 0, nq = 0;
-    uint32_t sn[2] = {0, 0};  // products of each warpgroup
+    constexpr uint64_t SW = MODE == HELD && D == 64 ? UMMA_SWIZZLE_64B : UMMA_SWIZZLE_128B;
+    constexpr uint32_t SBO = MODE == HELD && D == 64 ? 512 : 1024;
+    const uint32_t id = MODE == HELD ? umma_idesc_f16(0, 0, 0, BM, LY::NQ)
+                                     : umma_idesc_f16(BF16 ? 1 : 0, 0, 0, BM, (uint32_t)(p.cols + 15) / 16 * 16);
+    const uint64_t dQ = umma_smem_desc<SW>(sQ, 16, SBO), dK = umma_smem_desc<SW>(sK, 16, SBO);
+    uint32_t ks[2] = {0, 0}, k_par[2] = {0, 0}, nq = 0;  // places in K's rings; tiles of rows so far
+    uint32_t sn[2] = {0, 0};                             // products of each warpgroup
     bool ok = true;
-    auto wait_all = [&](uint64_t* bar, uint32_t par) -> bool {
-      return __all_sync(0xffffffffu, wait_bar(smem_u32(bar), par, abort_flag, p));
-    };
-    auto commit = [&](uint64_t* bar) {
-      if (elect_one()) umma_commit(smem_u32(bar));
-      __syncwarp();
-    };
     while (ok && walk.next(p, it)) {
       const int tiles = it.two ? 2 : 1;
-      for (int q = it.q0; q < it.qn && ok; ++q, ++nq) {
-        const uint32_t qs = nq % LY::Q_SLOTS;
-        ok = wait_all(&bars->q_full[qs], (nq / LY::Q_SLOTS) & 1u);
-        for (int x = 0; x < tiles && ok; ++x) {
-          const uint32_t ks = (t + x) % LY::K_SLOTS, buf = sn[x] & 1u;
-          if (q == it.q0) ok = wait_all(&bars->k_full[ks], ((t + x) / LY::K_SLOTS) & 1u);
-          ok = ok && wait_all(&bars->s_empty[x][buf], ((sn[x] >> 1) & 1u) ^ 1u);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t da = dK + ((ks * LY::TILE_BYTES) >> 4), db = dQ + ((qs * LY::TILE_BYTES) >> 4);
-          if (elect_one()) {
+#pragma unroll 1
+      for (int q = it.q0; q < it.qn && ok; ++q) {
+        if (!it.same) {  // the rows of before are given back when others come
+          if (nq && elect_one()) umma_commit(smem_u32(&bars->q_empty[(nq - 1) % LY::Q_SLOTS]));
+          __syncwarp();
+          // HELD: a warpgroup that has no part in the unit must not fall behind the rows' exponents
+          if (MODE == HELD && !it.two)
+            for (uint32_t y = 1; y <= 2 && y <= sn[1] && ok; ++y)
+              ok = wait_all(&bars->s_empty[1][(sn[1] - y) & 1u], ((sn[1] - y) >> 1) & 1u);
+          if (!ok || !(ok = wait_all(&bars->q_full[nq % LY::Q_SLOTS], (nq / LY::Q_SLOTS) & 1u))) break;
+          ++nq;
+        }
+        const uint64_t db = dQ + (((nq - 1) % LY::Q_SLOTS * LY::Q_BYTES) >> 4);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = ((k >> 2) * LY::CHUNK_BYTES + (k & 3) * 32) >> 4;
-              umma_ss(tmem + x * 256 + buf * 128, da + off, db + off, id, k > 0 ? 1u : 0u);
+        for (int x = 0; x < 2; ++x) {
+          if (x >= tiles) break;
+          const uint32_t n = sn[x]++, buf = n & 1u;
+          if (q == it.q0 && !(ok = wait_all(&bars->k_full[x][ks[x]], k_par[x]))) break;
+          if (!(ok = wait_all(&bars->s_empty[x][buf], ((n >> 1) & 1u) ^ 1u))) break;
+          tc_fence_after();
+          const uint64_t da = dK + (((x * LY::K_SLOTS + ks[x]) * LY::TILE_BYTES) >> 4);
+          const uint32_t to = tmem + x * 256 + buf * LY::S_COLS;
+          if (elect_one()) {
+            if constexpr (MODE == HELD) {
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k) umma_ss_f8(to, da + (k * 32 >> 4), db + (k * 32 >> 4), id, k > 0 ? 1u : 0u);
+            } else {
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = ((k >> 2) * LY::CHUNK_BYTES + (k & 3) * 32) >> 4;
+                umma_ss(to, da + off, db + off, id, k > 0 ? 1u : 0u);
+              }
             }
+            umma_commit(smem_u32(&bars->s_full[x][buf]));
+            if (q + 1 == it.qn) umma_commit(smem_u32(&bars->k_empty[x][ks[x]]));
           }
           __syncwarp();
-          commit(&bars->s_full[x][buf]);
-          if (q + 1 == it.qn) commit(&bars->k_empty[ks]);
-          ++sn[x];
         }
-        if (ok) commit(&bars->q_empty[qs]);
       }
-      t += tiles;
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (x < tiles && ++ks[x] == LY::K_SLOTS) ks[x] = 0, k_par[x] ^= 1u;
     }
-    commit(&bars->mma_drain);
+    if (elect_one()) umma_commit(smem_u32(&bars->mma_drain));
+    __syncwarp();
     wait_drain(smem_u32(&bars->mma_drain), 0, p);
     __syncwarp();
-  } else if (F8 && warp >= WARP_CONVERT) {
-    // ========================================================================= 8 bits to 16
-    // Thread = 16 elements of a row at a time, as in the attention; behind the last key anything may stand.
-    const int ct = (int)threadIdx.x - WARP_CONVERT * 32;
-    constexpr int PIECES = D / 16, TURNS = PIECES, BATCH = 4;
-    const int c16 = ct % PIECES, row0 = ct / PIECES;
-    const uint32_t half = (uint32_t)(c16 >> 2) * LY::CHUNK_BYTES, j0 = (c16 & 3) * 2, odd = c16 >> 2;
-    uint32_t t = 0;
+  } else if (MODE == HELD && warp >= WARP_CONVERT) {
+    // ========================================================================= rows split
+    constexpr int QL = D / 8, Q_TURN = 32 / QL, TERMS = LY::TERMS;  // lanes of a row, rows at a time
+    const int ql = lane % QL;
+    float* exps = reinterpret_cast<float*>(smem + LY::OFF_EXP);
+    uint32_t nq = 0;
     bool ok = true;
     while (ok && walk.next(p, it)) {
-      for (const uint32_t end = t + (it.two ? 2 : 1); t < end && ok; ++t) {
-        const uint32_t hs = t % LY::HELD_RING, ks = t % LY::K_SLOTS, round = t / LY::K_SLOTS;
-        ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->held_full[hs]), (t / LY::HELD_RING) & 1u, abort_flag, p));
-        if (ok && round > 0)
-          ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->k_empty[ks]), (round - 1) & 1u, abort_flag, p));
-        if (!ok) break;
-        const uint32_t from = sHeld + hs * LY::HELD_BYTES + (uint32_t)ct * 16u, to = sK + ks * LY::TILE_BYTES + half;
+      if (it.same) continue;
+#pragma unroll 1
+      for (int q = it.q0; q < it.qn && ok; ++q, ++nq) {
+        const uint32_t qs = nq % LY::Q_SLOTS, round = nq / LY::Q_SLOTS;
+        const int rows = min(p.tpt, it.n - q * p.tpt) * p.G;
+        auto load = [&](int r) {  // (zeros where there is no row)
+          if (r >= rows) return make_uint4(0, 0, 0, 0);
+          const int tok = (int)((uint32_t)r * p.by_g >> 16);
+          return *reinterpret_cast<const uint4*>(p.q.ptr + (long long)(it.t0 + q * p.tpt + tok) * p.q.ts +
+                                                 (long long)(it.h * p.G + r - tok * p.G) * p.q.hs + ql * 8);
+        };
+        uint4 u = load(lane / QL);
+        if (round > 0 && !(ok = wait_all(&bars->q_empty[qs], (round - 1) & 1u))) break;
+#pragma unroll 1
+        for (int r = lane / QL; r < HELD_ROWS; r += Q_TURN) {
+          const uint4 next = load(r + Q_TURN);
+          uint32_t w[TERMS][2];
+          const int ex = paged::split_row<D, BF16>(u, w);
+          u = next;
+          // Of tile m when the products of m - 4 are done, so those of m - 3 have been asked for at most, and a warpgroup
+          // has read all but its last two: tiles m - 5 and on are still looked at.
+          if (ql == 0) exps[(nq & 7u) * HELD_ROWS + r] = __uint_as_float((uint32_t)(127 + ex) << 23);
+          const uint32_t sw = D == 128 ? r & 7u : (r >> 1) & 3u;
 #pragma unroll
+          for (int m = 0; m < TERMS; ++m)
+            st_shared_v2(sQ + qs * LY::Q_BYTES + (m * HELD_ROWS + r) * D + ((((uint32_t)ql >> 1) ^ sw) << 4) + (ql & 1) * 8,
+                         w[m][0], w[m][1]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[qs]));
+      }
+    }
+  } else if (MODE == TURNED && warp >= WARP_CONVERT) {
+    // ========================================================================= 8 bits to 16
+    // Thread = 16 elements of a row at a time, as in fa_paged.cuh; behind the last key anything may stand.
+    const int ct = (int)threadIdx.x - WARP_CONVERT * 32;
+    constexpr int PIECES = D / 16, TURNS = PIECES, BATCH = 4;
+    const int c16 = ct % PIECES, row0 = (ct / PIECES) ^ (c16 >> 2);
+    const uint32_t half = (uint32_t)(c16 >> 2) * LY::CHUNK_BYTES, j0 = (c16 & 3) * 2;
+    uint32_t n[2] = {0, 0};  // tiles so far
+    bool ok = true;
+    while (ok && walk.next(p, it)) {
+#pragma unroll 1
+      for (int x = 0; x < (it.two ? 2 : 1) && ok; ++x) {
+        const uint32_t t = x ? n[1]++ : n[0]++;
+        const uint32_t hs = t % LY::RAW_RING, ks = t % LY::K_SLOTS, round = t / LY::K_SLOTS;
+        ok = wait_all(&bars->raw_full[x][hs], (t / LY::RAW_RING) & 1u);
+        if (ok && round > 0) ok = wait_all(&bars->k_empty[x][ks], (round - 1) & 1u);
+        if (!ok) break;
+        const uint32_t from = sRaw + (x * LY::RAW_SLOTS + hs) * LY::RAW_BYTES + (uint32_t)(row0 * D + c16 * 16);
+        const uint32_t to = sK + (x * LY::K_SLOTS + ks) * LY::TILE_BYTES + half;
+#pragma unroll 1
         for (int y0 = 0; y0 < TURNS; y0 += BATCH) {
           uint32_t v[BATCH][4];
 #pragma unroll
@@ -401,17 +492,15 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
               }
             }
             const uint32_t base = to + row * 128u, sw = row & 7u;
-            st_shared_v4(base + (((j0 + odd) ^ sw) << 4), odd ? w[4] : w[0], odd ? w[5] : w[1], odd ? w[6] : w[2],
-                         odd ? w[7] : w[3]);
-            st_shared_v4(base + (((j0 + 1 - odd) ^ sw) << 4), odd ? w[0] : w[4], odd ? w[1] : w[5], odd ? w[2] : w[6],
-                         odd ? w[3] : w[7]);
+            st_shared_v4(base + ((j0 ^ sw) << 4), w[0], w[1], w[2], w[3]);
+            st_shared_v4(base + (((j0 + 1) ^ sw) << 4), w[4], w[5], w[6], w[7]);
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_u32(&bars->k_full[ks]));
-          mbar_arrive(smem_u32(&bars->held_empty[hs]));
+          mbar_arrive(smem_u32(&bars->k_full[x][ks]));
+          mbar_arrive(smem_u32(&bars->raw_empty[x][hs]));
         }
       }
     }
@@ -420,7 +509,8 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     const int g = warp >> 2, wq = warp & 3;
     const uint32_t tS = tmem + ((uint32_t)(wq * 32) << 16) + g * 256;
     const uint32_t sL = smem_u32(smem + LY::OFF_L) + (uint32_t)warp * 512u;
-    const int chunks = (p.cols + 31) / 32;
+    constexpr int CH = MODE == HELD ? 8 : 32;  // columns at a time
+    const int chunks = (p.cols + CH - 1) / CH;
     // The thread's key in a unit: place of its weight, found two units ahead, so that its table entry, and then
     // its weight and scale, are there in time.
     struct Place {
@@ -430,95 +520,139 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     auto place_of = [&](const Unit& u) {
       Place x;
       const int key = u.key0 + g * BN + wq * 32 + lane;
+      const uint32_t entry = page_of(key);
       x.held = key < u.len;
       x.old = key < u.len - u.n;
-      x.page = x.held ? p.table[(size_t)u.b * p.table_stride + (uint32_t)key / (uint32_t)p.page_size] : -1;
-      x.off = u.h * p.page_size + (int)((uint32_t)key % (uint32_t)p.page_size);
+      x.page = x.held ? p.table[(size_t)u.b * p.table_stride + entry] : -1;
+      x.off = u.h * p.page_size + (key - (int)entry * p.page_size);
       return x;
     };
     auto weight_at = [&](const Place& x) { return p.w + (size_t)x.page * p.Hkv * p.page_size + x.off; };
-    auto fetch = [&](Place& x, float& w, float& k) {
+    auto fetch = [&](Place& x, int h, float& w, float& k) {
       if (x.held && (x.page < 0 || x.page >= p.num_pages)) x.held = false;  // (reported by the loading warps)
       w = x.held && x.old ? *weight_at(x) : 0.f;
-      k = F8 && x.held ? p.ks[(size_t)x.page * p.Hkv + (uint32_t)x.off / (uint32_t)p.page_size] : 1.f;
+      k = F8 && x.held ? p.ks[(size_t)x.page * p.Hkv + h] : 1.f;
     };
-    // -L log2 e of the lane's columns (lane, lane + 32, ...) of a tile of rows
-    auto ask_rows = [&](const Unit& u, int q, float (&v)[4]) {
+    // L of the lane's columns (lane, lane + 32, ...) of a tile of rows
+    constexpr int LV = MODE == HELD ? 1 : 4;
+    auto ask_rows = [&](const Unit& u, int q, float (&v)[LV]) {
+      const float* from = p.L + (size_t)(u.t0 + q * p.tpt) * p.Hq + u.h * p.G;
+      const int rows = min(p.tpt, u.n - q * p.tpt) * p.G;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < LV; ++i) {
         v[i] = 0.f;
         const int col = lane + 32 * i;
-        if (col >= p.cols) continue;
-        const int tok = (int)((uint32_t)col * p.by_g >> 16), t = q * p.tpt + tok;
-        if (t < u.n) v[i] = p.L[(size_t)(u.t0 + t) * p.Hq + u.h * p.G + col - tok * p.G];
+        if (col >= rows) continue;
+        const int tok = (int)((uint32_t)col * p.by_g >> 16);
+        v[i] = from[(size_t)tok * (p.Hq - p.G) + col];
       }
     };
     Unit nx, ny;
     bool have = walk.next(p, it), more = have && walk.next(p, nx), most = more && walk.next(p, ny);
     Place here = {}, then = {}, last = {};
-    float w_here = 0.f, k_here = 1.f, w_then = 0.f, k_then = 1.f, rows[4] = {};
+    float w_here = 0.f, k_here = 1.f, w_then = 0.f, k_then = 1.f, rows[LV] = {};
     if (have) {
       here = place_of(it);
       ask_rows(it, it.q0, rows);
     }
     if (more) then = place_of(nx);
-    if (have) fetch(here, w_here, k_here);
-    uint32_t sn = 0;
-    bool ok = true;
+    if (have) fetch(here, it.h, w_here, k_here);
+    uint32_t sn = 0, nq = 0;
+    bool ok = true, kept = false;
     while (ok && have) {
+      if (!it.same) kept = false;
       if (most) last = place_of(ny);
-      if (more) fetch(then, w_then, k_then);
+      if (more) fetch(then, nx.h, w_then, k_then);
       const bool mine = g == 0 || it.two;
       const int key = it.key0 + g * BN + wq * 32 + lane, ctx = it.len - it.n;
       const float ct = fmaxf(p.c * k_here, 1e-30f);
       const uint64_t c2 = f2(ct, ct);
       uint64_t acc[4] = {0, 0, 0, 0};
-      for (int q = it.q0; q < it.qn && ok; ++q) {
-        if (mine) {
+#pragma unroll 1
+      for (int q = it.q0; q < it.qn; ++q) {
+        if (!it.same) ++nq;
+        if (g == 0 ? !it.same : it.two && !kept) {
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) st_shared_u32(sL + (lane + 32 * i) * 4, __float_as_uint(rows[i] * -1.4426950408889634f));
+          for (int i = 0; i < LV; ++i) st_shared_u32(sL + (lane + 32 * i) * 4, __float_as_uint(rows[i] * -1.4426950408889634f));
           __syncwarp();
         }
+        // (as long as the rows are the same they stay in the warp's shared memory: kept, where the second warpgroup had
+        // a part in a unit since they came)
+        kept = it.qn == 1 && (mine || (it.same && kept));
         if (q + 1 < it.qn) ask_rows(it, q + 1, rows);
-        else if (more) ask_rows(nx, nx.q0, rows);
+        else if (more && !nx.same) ask_rows(nx, nx.q0, rows);
         if (!mine) continue;
-        const uint32_t buf = sn & 1u;
-        ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->s_full[g][buf]), (sn >> 1) & 1u, abort_flag, p));
+        const uint32_t buf = sn & 1u, from = tS + buf * LY::S_COLS;
+        ok = wait_all(&bars->s_full[g][buf], (sn >> 1) & 1u);
         if (!ok) break;
         ++sn;
         tc_fence_after();
         // columns [lo, hi) are rows that see the thread's key
         const int hi = min(p.tpt, it.n - q * p.tpt) * p.G;
         const int lo = p.causal ? min(max(key - ctx - q * p.tpt, 0), p.tpt) * p.G : 0;
+        auto done = [&](int x) {  // the scores are read
+          if (x < chunks - 1) return;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->s_empty[g][buf]));
+        };
+        if constexpr (MODE == HELD) {
+          const uint32_t sE = smem_u32(smem + LY::OFF_EXP) + ((nq - 1) & 7u) * (HELD_ROWS * 4);
 #pragma unroll 1
-        for (int x = 0; x < chunks; ++x) {
-          uint32_t s[32];
-          tmem_ld32(tS + buf * 128 + x * 32, s);
-          tmem_wait_ld();
-          reg_fence(s);
-          if (x == chunks - 1) {  // the scores are read
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->s_empty[g][buf]));
-          }
-          const bool whole = __all_sync(0xffffffffu, lo <= 32 * x && hi >= 32 * (x + 1));
+          for (int x = 0; x < chunks; ++x) {
+            uint32_t s[LY::TERMS][8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float l4[4], e[4];
-            ld_shared_v4(sL + x * 128 + k * 16, l4);
-            f2_split(f2_fma(f2(__uint_as_float(s[4 * k]), __uint_as_float(s[4 * k + 1])), c2, f2(l4[0], l4[1])), e[0], e[1]);
-            f2_split(f2_fma(f2(__uint_as_float(s[4 * k + 2]), __uint_as_float(s[4 * k + 3])), c2, f2(l4[2], l4[3])), e[2], e[3]);
+            for (int m = 0; m < LY::TERMS; ++m) tmem_ld8(from + m * HELD_ROWS + x * 8, s[m]);
+            tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              e[i] = ex2_approx(e[i]);
-              if (!whole) {
-                const int col = 32 * x + 4 * k + i;
-                e[i] = col >= lo && col < hi ? e[i] : 0.f;
+            for (int m = 0; m < LY::TERMS; ++m) reg_fence(s[m]);
+            done(x);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float l4[4], e4[4], y[4];
+              ld_shared_v4(sL + x * 32 + k * 16, l4);
+              ld_shared_v4(sE + x * 32 + k * 16, e4);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float sum = __uint_as_float(s[LY::TERMS - 1][4 * k + i]);  // small ones first
+#pragma unroll
+                for (int m = LY::TERMS - 2; m >= 0; --m) sum += __uint_as_float(s[m][4 * k + i]);
+                const int col = 8 * x + 4 * k + i;
+                y[i] = ex2_approx(fmaf(sum * e4[i], ct, l4[i]));
+                y[i] = col >= lo && col < hi ? y[i] : 0.f;
               }
+              acc[2 * k] = f2_add(acc[2 * k], f2(y[0], y[1]));
+              acc[2 * k + 1] = f2_add(acc[2 * k + 1], f2(y[2], y[3]));
             }
-            acc[(2 * k) & 3] = f2_add(acc[(2 * k) & 3], f2(e[0], e[1]));
-            acc[(2 * k + 1) & 3] = f2_add(acc[(2 * k + 1) & 3], f2(e[2], e[3]));
+          }
+        } else {
+          auto add = [&](const uint32_t (&s)[32], int x, auto whole) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float l4[4], e[4];
+              ld_shared_v4(sL + x * 128 + k * 16, l4);
+              f2_split(f2_fma(f2(__uint_as_float(s[4 * k]), __uint_as_float(s[4 * k + 1])), c2, f2(l4[0], l4[1])), e[0], e[1]);
+              f2_split(f2_fma(f2(__uint_as_float(s[4 * k + 2]), __uint_as_float(s[4 * k + 3])), c2, f2(l4[2], l4[3])), e[2], e[3]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                e[i] = ex2_approx(e[i]);
+                if (!decltype(whole)::value) e[i] = 32 * x + 4 * k + i >= lo && 32 * x + 4 * k + i < hi ? e[i] : 0.f;
+              }
+              acc[(2 * k) & 3] = f2_add(acc[(2 * k) & 3], f2(e[0], e[1]));
+              acc[(2 * k + 1) & 3] = f2_add(acc[(2 * k + 1) & 3], f2(e[2], e[3]));
+            }
+          };
+          const bool whole = __all_sync(0xffffffffu, lo == 0 && hi >= 32 * chunks);
+#pragma unroll 1
+          for (int x = 0; x < chunks; ++x) {
+            uint32_t s[32];
+            tmem_ld32(from + x * 32, s);
+            tmem_wait_ld();
+            reg_fence(s);
+            done(x);
+            if (whole) add(s, x, std::true_type{});
+            else add(s, x, std::false_type{});
           }
         }
       }

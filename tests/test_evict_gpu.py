@@ -34,7 +34,8 @@ def weights_for(b, seed=0):
 def weigh64(b, q, lse, w, scale, causal):
     """The weights after a call and how far each may be off: a score's 32-bit sum is off by at most
     e = d 2^-22 scale sum |q||k| (see decoder_testlib.attend64), its exponent in base 2 by 2^-22 of its terms, the
-    exponential by 2^-21 and a sum of n terms by n/2 2^-23 of them at most (here: 2^-17)."""
+    exponential by 2^-21 and a sum of n terms by n/2 2^-23 of them at most (here: 2^-17). Exponentials below the
+    smallest normal number, 2^-126, may be flushed to zero, one for every row."""
     w = w.double().clone()
     tol = torch.zeros_like(w)
     group = q.shape[1] // b.Hkv
@@ -57,7 +58,7 @@ def weigh64(b, q, lse, w, scale, causal):
         at, slot = b.block_table[i].long()[pos // b.page], pos % b.page
         old = w[at, :, slot] * (pos < t - n)[:, None]
         w[at, :, slot] = old + gain.T
-        tol[at, :, slot] = off.T + 2.0 ** -23 * (old + gain.T)
+        tol[at, :, slot] = off.T + 2.0 ** -23 * (old + gain.T) + n * group * 2.0 ** -126
     return w, tol
 
 
@@ -110,6 +111,16 @@ def test_key_weights_of_sharp_scores_and_other_scales(fa, held8):
     check_weigh(fa, b, q, True)
     check_weigh(fa, b, q, False, scale=0.0)
     check_weigh(fa, b, q, True, scale=1e-3)
+
+
+@pytest.mark.parametrize("held8", [False, True])
+@pytest.mark.parametrize("d,Hkv,group", [(128, 4, 32), (64, 3, 4), (128, 2, 16), (64, 2, 100)])
+def test_key_weights_units_of_one_and_two_tiles(fa, d, Hkv, group, held8):
+    """Ragged sequences whose last 256 keys are one tile of 128 or two, in long runs and in turn, for rows of each
+    form: the loads of the two tiles then run far apart."""
+    total = [(90, 100, 300, 20, 1000, 513, 640, 130)[i % 8] + i for i in range(60)] + [120] * 40 + [700] * 30 + [60] * 30
+    b = batch(held8, [1] * len(total), total, Hkv, d, 16, torch.bfloat16, seed=d + group)
+    check_weigh(fa, b, b.rows(Hkv * group), True)
 
 
 def test_key_weights_sum_to_the_rows(fa):
