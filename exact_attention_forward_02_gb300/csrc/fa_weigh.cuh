@@ -81,8 +81,10 @@ struct Layout {
   static constexpr int RAW_SLOTS = MODE != TURNED ? 0 : D == 64 ? 3 : 2, RAW_RING = MODE == TURNED ? RAW_SLOTS : 1;
   static constexpr int S_COLS = MODE == HELD ? 64 : 128;  // of one of the four buffers of S^T
   static constexpr int OFF_Q = 0, OFF_K = (Q_SLOTS * Q_BYTES + 1023) / 1024 * 1024, OFF_RAW = OFF_K + 2 * K_SLOTS * TILE_BYTES;
-  static constexpr int OFF_L = OFF_RAW + 2 * RAW_SLOTS * RAW_BYTES;  // 128 floats for each softmax warp
-  static constexpr int OFF_EXP = OFF_L + 8 * 512;                // HELD: 2^e of the rows, [8][HELD_ROWS]
+  // -L log2 e of the rows, of eight tiles of them, and with HELD their 2^e
+  static constexpr int L_ROWS = MODE == HELD ? HELD_ROWS : BM;
+  static constexpr int OFF_L = OFF_RAW + 2 * RAW_SLOTS * RAW_BYTES;
+  static constexpr int OFF_EXP = OFF_L + 8 * L_ROWS * 4;
   static constexpr int OFF_BAR = OFF_EXP + (MODE == HELD ? 8 * HELD_ROWS * 4 : 0);
   static constexpr int SMEM_BYTES = OFF_BAR + 1024;
   static_assert(sizeof(Barriers) <= 1024 && SMEM_BYTES <= paged::SMEM_LIMIT, "shared memory budget");
@@ -278,6 +280,14 @@ __global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
   auto wait_all = [&](uint64_t* bar, uint32_t par) -> bool {
     return __all_sync(0xffffffffu, wait_compact(smem_u32(bar), par, abort_flag, p));
   };
+  // L of column `col` of a tile of rows, in base 2 and negative; 0 for a column without a row
+  auto ask_row = [&](const Unit& u, int q, int col) {
+    const int tok = (int)((uint32_t)col * p.by_g >> 16), t = q * p.tpt + tok;
+    return col < p.cols && t < u.n ? p.L[(size_t)(u.t0 + t) * p.Hq + u.h * p.G + col - tok * p.G] * -1.4426950408889634f : 0.f;
+  };
+  // Whoever brings tile m of the rows writes what belongs to them when the products of tile m - Q_SLOTS are done, so those
+  // of m - Q_SLOTS + 1 have been asked for at most, and a warpgroup has read all but its last two: tiles m - 6 and on
+  // are still looked at, and there is room for eight.
   auto page_of = [&](int key) { return p.page_shift >= 0 ? (uint32_t)key >> p.page_shift : (uint32_t)key / (uint32_t)p.page_size; };
 
   if (warp == WARP_LOAD || warp == WARP_LOAD2) {
@@ -333,7 +343,12 @@ __global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
 #pragma unroll 1
         for (int q = it.q0; q < it.qn && ok; ++q, ++nq) {
           const uint32_t qs = nq % LY::Q_SLOTS, round = nq / LY::Q_SLOTS;
+          float l4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) l4[i] = ask_row(it, q, lane * 4 + i);
           if (round > 0 && !(ok = wait_all(&bars->q_empty[qs], (round - 1) & 1u))) break;
+          *reinterpret_cast<float4*>(smem + LY::OFF_L + ((nq & 7u) * LY::L_ROWS + lane * 4) * 4) = make_float4(l4[0], l4[1], l4[2], l4[3]);
+          __syncwarp();
           if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bars->q_full[qs]), q_bytes);
           __syncwarp();
           if (lane < LY::CHUNKS)
@@ -369,8 +384,8 @@ __global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
         if (!it.same) {  // the rows of before are given back when others come
           if (nq && elect_one()) umma_commit(smem_u32(&bars->q_empty[(nq - 1) % LY::Q_SLOTS]));
           __syncwarp();
-          // HELD: a warpgroup that has no part in the unit must not fall behind the rows' exponents
-          if (MODE == HELD && !it.two)
+          // a warpgroup that has no part in the unit must not fall behind what is kept of the rows
+          if (!it.two)
             for (uint32_t y = 1; y <= 2 && y <= sn[1] && ok; ++y)
               ok = wait_all(&bars->s_empty[1][(sn[1] - y) & 1u], ((sn[1] - y) >> 1) & 1u);
           if (!ok || !(ok = wait_all(&bars->q_full[nq % LY::Q_SLOTS], (nq / LY::Q_SLOTS) & 1u))) break;
@@ -431,6 +446,7 @@ __global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
                                                  (long long)(it.h * p.G + r - tok * p.G) * p.q.hs + ql * 8);
         };
         uint4 u = load(lane / QL);
+        const float l = ask_row(it, q, lane);
         if (round > 0 && !(ok = wait_all(&bars->q_empty[qs], (round - 1) & 1u))) break;
 #pragma unroll 1
         for (int r = lane / QL; r < HELD_ROWS; r += Q_TURN) {
@@ -438,8 +454,6 @@ __global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
           uint32_t w[TERMS][2];
           const int ex = paged::split_row<D, BF16>(u, w);
           u = next;
-          // Of tile m when the products of m - 4 are done, so those of m - 3 have been asked for at most, and a warpgroup
-          // has read all but its last two: tiles m - 5 and on are still looked at.
           if (ql == 0) exps[(nq & 7u) * HELD_ROWS + r] = __uint_as_float((uint32_t)(127 + ex) << 23);
           const uint32_t sw = D == 128 ? r & 7u : (r >> 1) & 3u;
 #pragma unroll
@@ -447,6 +461,7 @@ __global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
             st_shared_v2(sQ + qs * LY::Q_BYTES + (m * HELD_ROWS + r) * D + ((((uint32_t)ql >> 1) ^ sw) << 4) + (ql & 1) * 8,
                          w[m][0], w[m][1]);
         }
+        if (lane < HELD_ROWS) *reinterpret_cast<float*>(smem + LY::OFF_L + ((nq & 7u) * HELD_ROWS + lane) * 4) = l;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[qs]));
@@ -508,7 +523,6 @@ __global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
     // ========================================================================= softmax
     const int g = warp >> 2, wq = warp & 3;
     const uint32_t tS = tmem + ((uint32_t)(wq * 32) << 16) + g * 256;
-    const uint32_t sL = smem_u32(smem + LY::OFF_L) + (uint32_t)warp * 512u;
     constexpr int CH = MODE == HELD ? 8 : 32;  // columns at a time
     const int chunks = (p.cols + CH - 1) / CH;
     // The thread's key in a unit: place of its weight, found two units ahead, so that its table entry, and then
@@ -533,34 +547,16 @@ __global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
       w = x.held && x.old ? *weight_at(x) : 0.f;
       k = F8 && x.held ? p.ks[(size_t)x.page * p.Hkv + h] : 1.f;
     };
-    // L of the lane's columns (lane, lane + 32, ...) of a tile of rows
-    constexpr int LV = MODE == HELD ? 1 : 4;
-    auto ask_rows = [&](const Unit& u, int q, float (&v)[LV]) {
-      const float* from = p.L + (size_t)(u.t0 + q * p.tpt) * p.Hq + u.h * p.G;
-      const int rows = min(p.tpt, u.n - q * p.tpt) * p.G;
-#pragma unroll
-      for (int i = 0; i < LV; ++i) {
-        v[i] = 0.f;
-        const int col = lane + 32 * i;
-        if (col >= rows) continue;
-        const int tok = (int)((uint32_t)col * p.by_g >> 16);
-        v[i] = from[(size_t)tok * (p.Hq - p.G) + col];
-      }
-    };
     Unit nx, ny;
     bool have = walk.next(p, it), more = have && walk.next(p, nx), most = more && walk.next(p, ny);
     Place here = {}, then = {}, last = {};
-    float w_here = 0.f, k_here = 1.f, w_then = 0.f, k_then = 1.f, rows[LV] = {};
-    if (have) {
-      here = place_of(it);
-      ask_rows(it, it.q0, rows);
-    }
+    float w_here = 0.f, k_here = 1.f, w_then = 0.f, k_then = 1.f;
+    if (have) here = place_of(it);
     if (more) then = place_of(nx);
     if (have) fetch(here, it.h, w_here, k_here);
     uint32_t sn = 0, nq = 0;
-    bool ok = true, kept = false;
+    bool ok = true;
     while (ok && have) {
-      if (!it.same) kept = false;
       if (most) last = place_of(ny);
       if (more) fetch(then, nx.h, w_then, k_then);
       const bool mine = g == 0 || it.two;
@@ -571,23 +567,13 @@ __global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
 #pragma unroll 1
       for (int q = it.q0; q < it.qn; ++q) {
         if (!it.same) ++nq;
-        if (g == 0 ? !it.same : it.two && !kept) {
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < LV; ++i) st_shared_u32(sL + (lane + 32 * i) * 4, __float_as_uint(rows[i] * -1.4426950408889634f));
-          __syncwarp();
-        }
-        // (as long as the rows are the same they stay in the warp's shared memory: kept, where the second warpgroup had
-        // a part in a unit since they came)
-        kept = it.qn == 1 && (mine || (it.same && kept));
-        if (q + 1 < it.qn) ask_rows(it, q + 1, rows);
-        else if (more && !nx.same) ask_rows(nx, nx.q0, rows);
         if (!mine) continue;
         const uint32_t buf = sn & 1u, from = tS + buf * LY::S_COLS;
         ok = wait_all(&bars->s_full[g][buf], (sn >> 1) & 1u);
         if (!ok) break;
         ++sn;
         tc_fence_after();
+        const uint32_t sL = smem_u32(smem + LY::OFF_L) + ((nq - 1) & 7u) * (LY::L_ROWS * 4);
         // columns [lo, hi) are rows that see the thread's key
         const int hi = min(p.tpt, it.n - q * p.tpt) * p.G;
         const int lo = p.causal ? min(max(key - ctx - q * p.tpt, 0), p.tpt) * p.G : 0;
