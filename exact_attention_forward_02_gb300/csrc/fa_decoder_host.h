@@ -15,7 +15,9 @@
 #include "fa_paged.cuh"
 #include "fa_rope.cuh"
 
-namespace fa_decoder {
+// hidden: two copies of the library in one process (the range-checked build beside the release build) each
+// keep their own launch_paged<>::attr_set, which would else be one symbol for the whole process
+namespace fa_decoder __attribute__((visibility("hidden"))) {
 
 using namespace fa;
 

@@ -144,7 +144,8 @@ int fa_paged_evict(const fa_paged_kv* kv, float* k_scale, float* v_scale, float*
   if (rc != FA_OK) return rc;
   if (B < 0 || table_stride < 0 || budget < 1 || recent < 0 || recent > budget) return FA_ERR_SHAPE;
   if (B == 0 || kv->Hkv == 0) return FA_OK;
-  if (B > MAX_SEQUENCES || (long long)B * kv->Hkv > 0x1ffffff) return FA_ERR_SHAPE;
+  // (a budget that leaves the kernels' strides over it room in 32 bits)
+  if (B > MAX_SEQUENCES || (long long)B * kv->Hkv > 0x1ffffff || budget > 0x7fff0000) return FA_ERR_SHAPE;
   if (!seq_lens || !kept || !new_lens || (!block_table && table_stride) || (kv->num_pages && !weights)) return FA_ERR_NULL;
   if (!aligned4(seq_lens) || !aligned4(block_table) || !aligned4(kept) || !aligned4(new_lens) || !aligned4(weights) ||
       !aligned4(k_scale) || !aligned4(v_scale) || ((uintptr_t)workspace & 255))

@@ -70,10 +70,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) fa_evict_select_kernel(cons
   const int* table = p.table + (size_t)b * p.table_stride;
   const size_t at0 = (size_t)blockIdx.x * p.budget;
   int* kept = p.kept + at0;
-  if (tid == 0) {
-    if (told > p.cap) atomicCAS(p.status, 0, FA_ERR_RANGE);
-    if (h == 0) p.new_lens[b] = min(len, p.budget);
-  }
+  if (tid == 0 && told > p.cap) atomicCAS(p.status, 0, FA_ERR_RANGE);
   if (len <= p.budget) {
     for (int j = tid; j < p.budget; j += SELECT_THREADS) kept[j] = j < len ? j : -1;
     if (tid == 0) p.first[blockIdx.x] = p.budget;
@@ -239,6 +236,8 @@ __global__ void __launch_bounds__(MOVE_THREADS) fa_evict_move_kernel(const __gri
   const int b = bh / p.Hkv, h = bh - b * p.Hkv;
   launch_dependents();
   wait_previous_grid();
+  // here, not beside the selection: new_lens may be lens, which that reads in every block of the sequence
+  if (h == 0 && unit == 0 && threadIdx.x == 0) p.new_lens[b] = min(max(0, min(p.lens[b], p.cap)), p.budget);
   const int first = p.first[bh];
   if (first >= p.budget) return;
   const int* table = p.table + (size_t)b * p.table_stride;

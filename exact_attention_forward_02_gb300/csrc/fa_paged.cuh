@@ -1146,7 +1146,7 @@ __global__ void __launch_bounds__(num_warps(F8) * 32, 1)
           const uint32_t from = sHeld + hs * LY::K_BYTES + (uint32_t)(row0 * D + c16 * 16);
 #pragma unroll
           for (int y = 0; y < BATCH; ++y) ld_shared_u4(from + y * 2048u, v[y]);
-          if (t >= (uint32_t)LY::V_SLOTS) {
+          if ((int)t >= LY::V_SLOTS) {
             ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->v_release[slot]), ((t / LY::V_RING) & 1u) ^ 1u, abort_flag, p));
             if (!ok) break;
           }

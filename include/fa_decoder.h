@@ -163,7 +163,7 @@ int fa_paged_append_fp8(const fa_paged_kv* kv, float* k_scale, float* v_scale, c
 
 /* fa_fwd_paged_fp8 -- fa_fwd_paged over such a cache: q and O in `dtype`, everything else as there (the
  * workspace, too, is fa_fwd_paged_workspace_bytes()). Products take the bytes exactly as they are held; P
- * is rounded to fp16 with v_scale in it. Scales must be positive and finite, or 0 for a page of zeros;
+ * is held in 11 bits with v_scale in it. Scales must be positive and finite, or 0 for a page of zeros;
  * where the v_scale of a page is below 2^-40 of another's of the same sequence it may count as that. */
 int fa_fwd_paged_fp8(const fa_paged_kv* kv, const float* k_scale, const float* v_scale, const fa_heads* q,
                      const fa_heads* O, float* L, int B, int T, int max_q, const int* cu_seqlens,

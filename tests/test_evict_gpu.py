@@ -325,6 +325,14 @@ def test_evict_in_place_lengths_streams_and_graphs(fa):
     assert torch.equal(x, w) and torch.equal(kept[0, 0], torch.arange(200, device="cuda").int())
 
 
+@pytest.mark.parametrize("held8", [False, True])
+def test_evict_many_heads_with_lengths_in_place(fa, held8):
+    """More heads than run at once: the last ones still see the lengths that new_lens overwrites."""
+    b = batch(held8, [0] * 12, [90 + i for i in range(12)], 64, 64, 16, torch.float16, seed=8)
+    kept, _ = check_evict(fa, b, weights_for(b, 8), 70, 9, new_lens=b.seq_lens)
+    assert int(kept[:, :, -1].min()) == 89
+
+
 def test_evict_reports_bad_pages(fa):
     b = lib.Batch([0], [300], 1, 64, 16, torch.float16, seed=6)
     w = weights_for(b)
@@ -378,3 +386,28 @@ def test_prompt_then_tokens_with_eviction(fa):
         want = (s.softmax(-1)[:, None] @ vv)[:, 0]
         assert ((out[0].double() - want).abs() <= 2.0 ** -7 * vv.abs().amax((1, 2))[:, None]).all()
     assert fa.fa_last_status() == 0 and torch.isfinite(w[table[0, :13].long()][:12]).all()
+
+
+def test_calls_that_autograd_would_record_are_refused(fa):
+    def grad(x):
+        return x.clone().requires_grad_()
+
+    b = c8.Batch8([2, 1], [20, 3], 2, 64, 16, torch.float16, seed=9)
+    q, w = b.rows(4), torch.zeros(b.k_pages.shape[0], 2, 16, device="cuda")
+    table = (b.block_table, b.cu_seqlens, b.seq_lens)
+    _, L = fa.attention_paged_fp8(q, b.k_pages, b.v_pages, b.k_scale, b.v_scale, *table, 2)
+    before = w.clone()
+    with torch.enable_grad():
+        with pytest.raises(ValueError, match="autograd"):
+            fa.attention_paged_fp8(grad(q), b.k_pages, b.v_pages, b.k_scale, b.v_scale, *table, 2)
+        with pytest.raises(ValueError, match="autograd"):
+            fa.paged_append_fp8(grad(b.rows(2)), b.rows(2), b.k_pages, b.v_pages, b.k_scale, b.v_scale, *table)
+        with pytest.raises(ValueError, match="autograd"):
+            fa.paged_key_weights(q, grad(L), b.k_pages, w, *table, 2, k_scale=b.k_scale)
+        with pytest.raises(ValueError, match="autograd"):
+            fa.paged_evict(b.k_pages, b.v_pages, grad(w), b.block_table, b.seq_lens, 2, 1, k_scale=b.k_scale,
+                           v_scale=b.v_scale)
+    assert torch.equal(w, before)
+    with torch.no_grad():
+        fa.paged_key_weights(grad(q), grad(L), b.k_pages, w, *table, 2, k_scale=b.k_scale)
+    assert not torch.equal(w, before)
