@@ -8,21 +8,24 @@ namespace {
 using namespace fa;
 using namespace fa_decoder;
 
-// Warps of a unit: as many as hold the rows that a page may get in their lanes.
+// Warps of a unit: as many as hold the rows that a page may get in their lanes, 4 rows of a lane (4 blocks of an
+// SM; with 8 rows, 2 blocks, 29582 ragged tokens of 8 heads, d 128, took 72 us for 56) or for large pages 8.
 template <int D, bool BF16, bool INTER, bool FULL>
 int launch_append8(const Append8Params& p, cudaStream_t st) {
-  constexpr int ROWS = APPEND8_ROWS * 256 / D;  // of a warp
+  constexpr int LANES = 256 / D;  // rows of a warp
   const int rows = p.page_size < p.T ? p.page_size : p.T;
-  auto go = [&](auto w) {
-    constexpr int W = decltype(w)::value, UNITS = ROW_WARPS / W;
+  auto go = [&](auto w, auto r) {
+    constexpr int W = decltype(w)::value, ROWS = decltype(r)::value, UNITS = ROW_WARPS / W;
     const long long blocks = (p.units + UNITS - 1) / UNITS + 1;  // the last one looks over cu_seqlens
     if (blocks > 0x7fffffffLL) return (int)FA_ERR_SHAPE;
-    return launch_dependent(fa_paged_append8_kernel<D, BF16, INTER, FULL, W>, dim3((unsigned)blocks), dim3(ROW_THREADS),
+    return launch_dependent(fa_paged_append8_kernel<D, BF16, INTER, FULL, W, ROWS>, dim3((unsigned)blocks), dim3(ROW_THREADS),
                             0, st, p);
   };
-  if (rows <= ROWS) return go(std::integral_constant<int, 1>{});
-  if (rows <= 4 * ROWS) return go(std::integral_constant<int, 4>{});
-  return go(std::integral_constant<int, 8>{});
+  using std::integral_constant;
+  if (rows <= 8 * LANES) return go(integral_constant<int, 1>{}, integral_constant<int, 8>{});
+  if (rows <= 16 * LANES) return go(integral_constant<int, 4>{}, integral_constant<int, 4>{});
+  if (rows <= 32 * LANES) return go(integral_constant<int, 8>{}, integral_constant<int, 4>{});
+  return go(integral_constant<int, 8>{}, integral_constant<int, 8>{});
 }
 
 }  // namespace

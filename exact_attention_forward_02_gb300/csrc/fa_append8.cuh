@@ -32,7 +32,6 @@ struct Append8Params {
   int* status;
 };
 
-constexpr int APPEND8_ROWS = 8;                    // rows that a lane holds between the two passes
 constexpr uint32_t APPEND8_LEAST = 27u << 23;      // 2^-100, of a page of zeros
 
 // as the 16-bit append has it
@@ -55,10 +54,11 @@ __device__ __forceinline__ int sequence_of_place(const Append8Params& p, uint32_
   return min(lo, p.B) - 1;
 }
 
-template <int D, bool BF16, bool INTER, bool FULL, int W>
-__global__ void __launch_bounds__(ROW_THREADS, 2) fa_paged_append8_kernel(const __grid_constant__ Append8Params p) {
+// ROWS: rows that a lane holds between the two passes
+template <int D, bool BF16, bool INTER, bool FULL, int W, int ROWS>
+__global__ void __launch_bounds__(ROW_THREADS, ROWS > 4 ? 2 : 4) fa_paged_append8_kernel(const __grid_constant__ Append8Params p) {
   constexpr int LPR = D / 8, GPW = 32 / LPR, TURN = W * GPW;  // lanes of a row, rows of a warp, of a unit's turn
-  __shared__ float tops[ROW_WARPS];
+  __shared__ float tops[2][ROW_WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR, wu = warp % W;
   if (blockIdx.x == gridDim.x - 1) {  // looks over the offsets; the others skip what does not fit them
     launch_dependents();
@@ -126,20 +126,27 @@ __global__ void __launch_bounds__(ROW_THREADS, 2) fa_paged_append8_kernel(const 
     return x;
   };
   float top = 0.f;
-  auto grow = [&](const Pairs& x) {
-    auto one = [&](float v) {
-      const float a = fabsf(v);
-      top = fmaxf(top, a <= 3.402823466e38f ? a : 0.f);
+  bool wild = false;  // there are infinities: they become NaN first (a maximum passes over NaN)
+  auto tame = [&](Pairs& x) {
+    auto one = [&](uint64_t v) {
+      const float a = lo_of(v), b = hi_of(v);
+      return f2(a + (a - a), b + (b - b));
     };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x.a[i] = one(x.a[i]), x.b[i] = one(x.b[i]);
+  };
+  auto far = [&](int slot) {
+    Pairs x = values(load(slot), slot);
+    if (wild) tame(x);
+    return x;
+  };
+  auto grow = [&](const Pairs& x) {
+    auto one = [&](float v) { top = fmaxf(top, fabsf(v)); };
 #pragma unroll
     for (int i = 0; i < 2; ++i) one(lo_of(x.a[i])), one(hi_of(x.a[i])), one(lo_of(x.b[i])), one(hi_of(x.b[i]));
   };
   auto put = [&](int slot, const Pairs& x, float inv) {
-    // (what is not finite becomes NaN, not the largest number)
-    auto q = [&](float v) {
-      const float y = v * inv;
-      return y + (y - y);
-    };
+    auto q = [&](float v) { return v * inv; };
     uint8_t* row = dst + (long long)slot * p.token_stride;
     if constexpr (INTER) {
       const uint32_t w0 = pack4_e4m3(q(lo_of(x.a[0])), q(lo_of(x.b[0])), q(hi_of(x.a[0])), q(hi_of(x.b[0])));
@@ -153,41 +160,54 @@ __global__ void __launch_bounds__(ROW_THREADS, 2) fa_paged_append8_kernel(const 
     }
   };
 
-  const int row0 = s0 + wu * GPW + sub, rows_held = APPEND8_ROWS * TURN;
-  Pairs held[APPEND8_ROWS];
+  const int row0 = s0 + wu * GPW + sub, rows_held = ROWS * TURN;
+  Pairs held[ROWS];
   if (alive) {
-    uint4 u[APPEND8_ROWS];
+    uint4 u[ROWS];
 #pragma unroll
-    for (int j = 0; j < APPEND8_ROWS; ++j)
+    for (int j = 0; j < ROWS; ++j)
       if (row0 + j * TURN < s1) u[j] = load(row0 + j * TURN);
 #pragma unroll
-    for (int j = 0; j < APPEND8_ROWS; ++j) {
+    for (int j = 0; j < ROWS; ++j) {
       if (row0 + j * TURN >= s1) continue;
       held[j] = values(u[j], row0 + j * TURN);
       grow(held[j]);
     }
 #pragma unroll 2
-    for (int s = row0 + rows_held; s < s1; s += TURN) grow(values(load(s), s));  // (pages too large to be held)
+    for (int s = row0 + rows_held; s < s1; s += TURN) grow(far(s));  // (pages too large to be held)
   }
+  auto join = [&](int set) {  // over the unit's warps
 #pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if constexpr (W > 1) {
-    if (lane == 0) tops[warp] = top;
-    __syncthreads();
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if constexpr (W > 1) {
+      if (lane == 0) tops[set][warp] = top;
+      named_bar_sync(1 + warp / W, W * 32);
 #pragma unroll
-    for (int i = 0; i < W; ++i) top = fmaxf(top, tops[warp / W * W + i]);
-  }
+      for (int i = 0; i < W; ++i) top = fmaxf(top, tops[set][warp / W * W + i]);
+    }
+  };
+  join(0);
   if (!alive) return;
+  if (top > 3.402823466e38f) {
+    wild = true;
+    top = 0.f;
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j)
+      if (row0 + j * TURN < s1) tame(held[j]), grow(held[j]);
+#pragma unroll 1
+    for (int s = row0 + rows_held; s < s1; s += TURN) grow(far(s));
+    join(1);
+  }
   // the smallest power of two that is not below top / 448: 448 = 1.75 2^8
   const uint32_t bits = (__float_as_uint(top) + 0x1fffffu) >> 23 << 23;
   float s = __uint_as_float(bits > APPEND8_LEAST + (8u << 23) ? bits - (8u << 23) : APPEND8_LEAST);
   if (s0 > 0 && s_old >= s) s = s_old;
   const float inv = 1.f / s;
 #pragma unroll
-  for (int j = 0; j < APPEND8_ROWS; ++j)
+  for (int j = 0; j < ROWS; ++j)
     if (row0 + j * TURN < s1) put(row0 + j * TURN, held[j], inv);
 #pragma unroll 2
-  for (int x = row0 + rows_held; x < s1; x += TURN) put(x, values(load(x), x), inv);
+  for (int x = row0 + rows_held; x < s1; x += TURN) put(x, far(x), inv);
   if (s0 > 0 && s > s_old) {  // the older tokens' codes under the larger scale
     const float ratio = s_old * inv;
     for (int x = wu * GPW + sub; x < s0; x += TURN) {
