@@ -166,6 +166,9 @@ int fa_paged_evict(const fa_paged_kv* kv, float* k_scale, float* v_scale, float*
   p.token_bytes = kv->token_stride * elem;
   p.num_pages = kv->num_pages;
   p.page_size = kv->page_size;
+  p.page_shift = -1;
+  for (int x = 0; x < 31; ++x)
+    if (kv->page_size == 1 << x) p.page_shift = x;
   p.Hkv = kv->Hkv;
   p.lens = seq_lens;
   p.table = block_table;

@@ -21,7 +21,7 @@ constexpr int SELECT_THREADS = 1024, SELECT_WARPS = 32;
 constexpr int BINS = 2048;
 constexpr int SCALE_PAGES = 2048;  // pages whose scales are worked out at a time
 constexpr int MOVE_THREADS = 256;
-constexpr int MOVE_UNROLL = 4;     // rows of a thread in a round
+__host__ __device__ constexpr int move_unroll(bool f8) { return f8 ? 2 : 4; }  // rows of a thread in a round
 constexpr int KEY_CAP = 40960;     // weights that a block keeps in shared memory
 
 struct Params {
@@ -30,6 +30,7 @@ struct Params {
   float* w;
   long long page_bytes, head_bytes, token_bytes;
   int num_pages, page_size, Hkv;
+  int page_shift;        // log2 of the page size, -1 where that is none
   const int *lens, *table;
   int table_stride, B, cap;
   int budget, recent;
@@ -48,6 +49,33 @@ __device__ __forceinline__ uint32_t order_of(float w) {
   const uint32_t b = __float_as_uint(w + 0.f);
   if (w != w) return 0xffffffffu;
   return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// page and slot of position j
+__device__ __forceinline__ int2 place_of(const Params& p, int j) {
+  const int at = p.page_shift >= 0 ? j >> p.page_shift : (int)((uint32_t)j / (uint32_t)p.page_size);
+  return make_int2(at, j - at * p.page_size);
+}
+
+// four codes under a smaller scale. In fp16 by a power of two, exactly: below 2^-24, where fp16 cuts off, nothing
+// reaches half of E4M3's least number (2^-10).
+__device__ __forceinline__ uint32_t codes_times(uint32_t c, float r, bool power) {
+  uint32_t lo, hi;
+  unpack4_e4m3(c, lo, hi);
+  if (power) {
+    const uint32_t r2 = pack2<false>(r, r);
+    asm("{\n\t.reg .b32 a, b;\n\t.reg .b16 x, y;\n\t"
+        "mul.rn.f16x2 a, %1, %3;\n\tmul.rn.f16x2 b, %2, %3;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 x, a;\n\tcvt.rn.satfinite.e4m3x2.f16x2 y, b;\n\t"
+        "mov.b32 %0, {x, y};\n\t}"
+        : "=r"(c)
+        : "r"(lo), "r"(hi), "r"(r2));
+    return c;
+  }
+  float f[4];
+  unpack2<false>(lo, f[0], f[1]);
+  unpack2<false>(hi, f[2], f[3]);
+  return pack4_e4m3(f[0] * r, f[1] * r, f[2] * r, f[3] * r);
 }
 
 struct SelectSmem {
@@ -77,18 +105,28 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) fa_evict_select_kernel(cons
     return;
   }
   const int early = len - p.recent, need = p.budget - p.recent;  // 0 <= need < early
+  // (straight code: the loads of several positions are on their way together)
+  bool bad = false;
   auto load_key = [&](int i) -> uint32_t {
-    const int page = table[(uint32_t)i / (uint32_t)p.page_size];
-    if (page < 0 || page >= p.num_pages) {
-      atomicCAS(p.status, 0, FA_ERR_RANGE);
-      return 0;
-    }
-    return order_of(p.w[((size_t)page * p.Hkv + h) * p.page_size + (uint32_t)i % (uint32_t)p.page_size]);
+    const int2 at = place_of(p, i);
+    const int page = table[at.x];
+    const bool fine = page >= 0 && page < p.num_pages;
+    const uint32_t key = order_of(p.w[((size_t)(fine ? page : 0) * p.Hkv + h) * p.page_size + at.y]);
+    bad |= !fine;
+    return fine ? key : 0u;
   };
   const bool cached = early <= p.keys;
   if (cached) {
-#pragma unroll 8
-    for (int i = tid; i < early; i += SELECT_THREADS) keys[i] = load_key(i);
+    constexpr int AT_ONCE = 8;
+#pragma unroll 1
+    for (int i0 = tid; i0 < early; i0 += AT_ONCE * SELECT_THREADS) {
+      uint32_t k[AT_ONCE];
+#pragma unroll
+      for (int y = 0; y < AT_ONCE; ++y) k[y] = load_key(min(i0 + y * SELECT_THREADS, early - 1));
+#pragma unroll
+      for (int y = 0; y < AT_ONCE; ++y)
+        if (i0 + y * SELECT_THREADS < early) keys[i0 + y * SELECT_THREADS] = k[y];
+    }
   }
   auto key_at = [&](int i) { return cached ? keys[i] : load_key(i); };
   // the need-th largest: its bits from the top, and how many of those equal to it stay
@@ -117,8 +155,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) fa_evict_select_kernel(cons
       }
       if (lane == 31) sm.part[warp] = incl;
       __syncthreads();
-      uint32_t before = 0;
-      for (int w = 0; w < warp; ++w) before += sm.part[w];
+      const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? sm.part[lane] : 0u);
       const uint32_t up = before + incl - hi - lo;  // in bins above the thread's
       if (up < left && left <= up + hi + lo) {
         const bool first = left <= up + hi;
@@ -150,72 +187,92 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) fa_evict_select_kernel(cons
   }
   if (tid == 0) sm.lowest = early;
   __syncthreads();
-  uint32_t place = 0, ties = 0;
-  for (int w = 0; w < warp; ++w) {
-    place += sm.part[w] + min(sm.part2[w], left - min(ties, left));
-    ties += sm.part2[w];
-  }
+  uint32_t ties = __reduce_add_sync(0xffffffffu, lane < warp ? sm.part2[lane] : 0u);
+  uint32_t place = __reduce_add_sync(0xffffffffu, lane < warp ? sm.part[lane] : 0u) + min(ties, left);
   int2* src = p.src + at0;
-  auto keep = [&](int j, int i) {
+  auto keep = [&](int j, int i, int page) {
     kept[j] = i;
-    const int page = table[(uint32_t)i / (uint32_t)p.page_size];
-    src[j] = make_int2(page, (int)((uint32_t)i % (uint32_t)p.page_size));
+    src[j] = make_int2(page, place_of(p, i).y);
   };
   int lowest = early;
-#pragma unroll 2
+  auto page_of = [&](int i) { return i < i1 ? table[place_of(p, i).x] : -1; };
+  int ahead[4];  // the pages of the next 128 positions
+#pragma unroll
+  for (int y = 0; y < 4; ++y) ahead[y] = page_of(i0 + y * 32 + lane);
+#pragma unroll 1
   for (int i = i0; i < i1; i += 32) {
+    const int page = ahead[0];
+    ahead[0] = ahead[1], ahead[1] = ahead[2], ahead[2] = ahead[3];
+    ahead[3] = page_of(i + 128 + lane);
     const bool in = i + lane < i1;
     const uint32_t k = in && need > 0 ? key_at(i + lane) : 0u;
     const bool is_same = in && need > 0 && k == border;
     const uint32_t tied = __ballot_sync(0xffffffffu, is_same), below = (1u << lane) - 1u;
     const bool stays = in && need > 0 && (k > border || (is_same && ties + __popc(tied & below) < left));
     const uint32_t all = __ballot_sync(0xffffffffu, stays);
-    if (stays) keep((int)(place + __popc(all & below)), i + lane);
+    if (stays) keep((int)(place + __popc(all & below)), i + lane, page);
     else if (in) lowest = min(lowest, i + lane);
     place += __popc(all);
     ties += __popc(tied);
   }
-  for (int r = tid; r < p.recent; r += SELECT_THREADS) keep(need + r, early + r);
+  for (int r = tid; r < p.recent; r += SELECT_THREADS) keep(need + r, early + r, table[place_of(p, early + r).x]);
   atomicMin(&sm.lowest, lowest);
   __syncthreads();  // (with the block's own global writes)
+  if (bad) atomicCAS(p.status, 0, FA_ERR_RANGE);
   if (tid == 0) p.first[blockIdx.x] = F8 ? sm.lowest / p.page_size * p.page_size : sm.lowest;
   if constexpr (F8) {
     // New scales, some pages at a time; the sources of later pages lie in later pages, whose scales still stand.
     uint32_t* tops = keys;  // [2][SCALE_PAGES], positive numbers in the order of their bits
-    const int group = p.page_size >= SELECT_THREADS * 8 ? 1 : min(SCALE_PAGES, SELECT_THREADS * 8 / p.page_size);
+    constexpr int AT_ONCE = 8, CHUNK = AT_ONCE * SELECT_THREADS;
+    const int group = p.page_size >= CHUNK ? 1 : min(SCALE_PAGES, CHUNK / p.page_size);
     const size_t plane = (size_t)p.B * p.Hkv * p.budget;
     const int pages = (p.budget + p.page_size - 1) / p.page_size;
     for (int g0 = 0; g0 < pages; g0 += group) {
       const int n = min(group, pages - g0), j0 = g0 * p.page_size;
       const int j1 = (int)min((long long)p.budget, (long long)(g0 + n) * p.page_size);
+      float s[AT_ONCE][2];
+      auto fetch = [&](int c0) {  // the scales that a thread's tokens come from
+        int from[AT_ONCE];
+#pragma unroll
+        for (int y = 0; y < AT_ONCE; ++y) {
+          const int j = c0 + y * SELECT_THREADS + tid;
+          from[y] = j < j1 ? src[j].x : -1;
+        }
+#pragma unroll
+        for (int y = 0; y < AT_ONCE; ++y) {
+          const bool ok = from[y] >= 0 && from[y] < p.num_pages;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) s[y][x] = ok ? p.scale[x][(size_t)from[y] * p.Hkv + h] : 0.f;
+        }
+      };
       __syncthreads();
       for (int i = tid; i < 2 * SCALE_PAGES; i += SELECT_THREADS) tops[i] = 0;
       __syncthreads();
-      auto scales_of = [&](int j, float (&s)[2]) {
-        const int page = src[j].x;
-        const bool ok = page >= 0 && page < p.num_pages;
+#pragma unroll 1
+      for (int c0 = j0; c0 < j1; c0 += CHUNK) {  // more than one chunk only where a page is larger
+        fetch(c0);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) s[x] = ok ? p.scale[x][(size_t)page * p.Hkv + h] : 0.f;
-      };
-#pragma unroll 4
-      for (int j = j0 + tid; j < j1; j += SELECT_THREADS) {
-        float s[2];
-        scales_of(j, s);
-        const int at = (j - j0) / p.page_size;
+        for (int y = 0; y < AT_ONCE; ++y) {
+          const int at = place_of(p, c0 + y * SELECT_THREADS + tid - j0).x;
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (s[x] > 0.f) atomicMax(&tops[x * SCALE_PAGES + at], __float_as_uint(s[x]));
+          for (int x = 0; x < 2; ++x)
+            if (s[y][x] > 0.f) atomicMax(&tops[x * SCALE_PAGES + at], __float_as_uint(s[y][x]));
+        }
       }
       __syncthreads();
-#pragma unroll 4
-      for (int j = j0 + tid; j < j1; j += SELECT_THREADS) {
-        float s[2];
-        scales_of(j, s);
-        const int at = (j - j0) / p.page_size;
+#pragma unroll 1
+      for (int c0 = j0; c0 < j1; c0 += CHUNK) {
+        if (j1 - j0 > CHUNK) fetch(c0);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float top = __uint_as_float(tops[x * SCALE_PAGES + at]);
-          p.ratio[x * plane + at0 + j] = top > 0.f ? s[x] / top : 1.f;
+        for (int y = 0; y < AT_ONCE; ++y) {
+          const int j = c0 + y * SELECT_THREADS + tid;
+          if (j >= j1) break;
+          const int at = place_of(p, j - j0).x;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float top = __uint_as_float(tops[x * SCALE_PAGES + at]);
+            p.ratio[x * plane + at0 + j] = top > 0.f ? s[y][x] / top : 1.f;
+          }
         }
       }
       __syncthreads();
@@ -230,7 +287,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) fa_evict_select_kernel(cons
 
 // Blocks of a (sequence, key head): `slices` of k, of v, and one for its weights.
 template <bool F8>
-__global__ void __launch_bounds__(MOVE_THREADS) fa_evict_move_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(MOVE_THREADS, 4) fa_evict_move_kernel(const __grid_constant__ Params p) {
   const int per = 2 * p.slices + 1;
   const int bh = blockIdx.x / per, unit = blockIdx.x - bh * per;
   const int b = bh / p.Hkv, h = bh - b * p.Hkv;
@@ -243,86 +300,78 @@ __global__ void __launch_bounds__(MOVE_THREADS) fa_evict_move_kernel(const __gri
   const int* table = p.table + (size_t)b * p.table_stride;
   const size_t at0 = (size_t)bh * p.budget;
   const int2* src = p.src + at0;
-  auto fine = [&](int page) { return page >= 0 && page < p.num_pages; };
-  constexpr int U = MOVE_UNROLL;
-  if (unit == 2 * p.slices) {
-    float* w = p.w + (size_t)h * p.page_size;
-    const size_t stride = (size_t)p.Hkv * p.page_size;
-    float cur[U], nxt[U];
-    auto load = [&](int j0, float (&v)[U]) {
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int j = j0 + i * MOVE_THREADS + (int)threadIdx.x;
-        if (j >= p.budget) continue;
-        const int2 s = src[j];
-        v[i] = fine(s.x) ? w[(size_t)s.x * stride + s.y] : 0.f;
-      }
-    };
-    load(first, cur);
-    for (int j0 = first; j0 < p.budget; j0 += U * MOVE_THREADS) {
-      load(j0 + U * MOVE_THREADS, nxt);
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int j = j0 + i * MOVE_THREADS + (int)threadIdx.x;
-        if (j < p.budget) {
-          const int page = table[(uint32_t)j / (uint32_t)p.page_size];
-          if (fine(page)) w[(size_t)page * stride + (uint32_t)j % (uint32_t)p.page_size] = cur[i];
-        }
-        cur[i] = nxt[i];
-      }
-    }
-    return;
-  }
+  constexpr int U = move_unroll(F8);
+  // Three rounds at once: one's stores, the next one's rows on their way, and where those after it come from.
+  const bool weights = unit == 2 * p.slices;
   const int set = unit >= p.slices, slice = set ? unit - p.slices : unit;
-  const int rows = MOVE_THREADS / p.slice_pieces, row = (int)threadIdx.x / p.slice_pieces;
-  const int piece = slice * p.slice_pieces + (int)threadIdx.x - row * p.slice_pieces;
-  uint8_t* base = p.pages[set] + (long long)h * p.head_bytes + piece * 16;
-  const float* ratios = F8 ? p.ratio + (set ? (size_t)p.B * p.Hkv * p.budget : 0) + at0 : nullptr;
+  const int rows = weights ? MOVE_THREADS : MOVE_THREADS / p.slice_pieces;
+  const int row = weights ? (int)threadIdx.x : (int)threadIdx.x / p.slice_pieces;
   const int round = rows * U;
-  uint4 cur[U], nxt[U];
-  float cur_r[U], nxt_r[U];
-  auto load = [&](int j0, uint4 (&v)[U], float (&r)[U]) {
-    int2 s[U];
+  const float* ratios = F8 && !weights ? p.ratio + (set ? (size_t)p.B * p.Hkv * p.budget : 0) + at0 : nullptr;
+  auto sources = [&](int j0, int2 (&s)[U]) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int j = j0 + i * rows + row;
       s[i] = j < p.budget ? src[j] : make_int2(-1, 0);
-      r[i] = F8 && j < p.budget ? ratios[j] : 1.f;
     }
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-      if (fine(s[i].x)) v[i] = *reinterpret_cast<const uint4*>(base + (long long)s[i].x * p.page_bytes + (long long)s[i].y * p.token_bytes);
   };
-  load(first, cur, cur_r);
-  for (int j0 = first; j0 < p.budget; j0 += round) {
-    load(j0 + round, nxt, nxt_r);
-    __syncthreads();
+  auto walk = [&](auto zero, auto load, auto store) {
+    decltype(zero) cur[U], nxt[U];
+    float cur_r[U], nxt_r[U];
+    int2 s[U];
+    uint32_t cur_ok = 0, nxt_ok = 0;
+    auto rows_of = [&](int j0, decltype(cur)& v, float (&r)[U], uint32_t& ok) {
+      ok = 0;
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int j = j0 + i * rows + row;
-      if (j < p.budget) {
-        const int page = table[(uint32_t)j / (uint32_t)p.page_size];
-        if (F8 && cur_r[i] != 1.f) {
-          uint32_t* c = reinterpret_cast<uint32_t*>(&cur[i]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t lo, hi;
-            float f[4];
-            unpack4_e4m3(c[e], lo, hi);
-            unpack2<false>(lo, f[0], f[1]);
-            unpack2<false>(hi, f[2], f[3]);
-            c[e] = pack4_e4m3(f[0] * cur_r[i], f[1] * cur_r[i], f[2] * cur_r[i], f[3] * cur_r[i]);
-          }
-        }
-        if (fine(page) && fine(src[j].x))
-          *reinterpret_cast<uint4*>(base + (long long)page * p.page_bytes +
-                                    (long long)((uint32_t)j % (uint32_t)p.page_size) * p.token_bytes) = cur[i];
+      for (int i = 0; i < U; ++i) {
+        if (s[i].x < 0 || s[i].x >= p.num_pages) continue;
+        ok |= 1u << i;
+        v[i] = load(s[i]);
+        r[i] = F8 && !weights ? ratios[j0 + i * rows + row] : 1.f;
       }
-      cur[i] = nxt[i];
-      cur_r[i] = nxt_r[i];
+    };
+    sources(first, s);
+    rows_of(first, cur, cur_r, cur_ok);
+    sources(first + round, s);
+#pragma unroll 1
+    for (int j0 = first; j0 < p.budget; j0 += round) {
+      rows_of(j0 + round, nxt, nxt_r, nxt_ok);
+      sources(j0 + 2 * round, s);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (cur_ok >> i & 1u) {
+          const int2 at = place_of(p, j0 + i * rows + row);
+          const int page = table[at.x];
+          if (page >= 0 && page < p.num_pages) store(make_int2(page, at.y), cur[i], cur_r[i]);
+        }
+        cur[i] = nxt[i];
+        cur_r[i] = nxt_r[i];
+      }
+      cur_ok = nxt_ok;
     }
+  };
+  if (weights) {
+    float* w = p.w + (size_t)h * p.page_size;
+    const size_t stride = (size_t)p.Hkv * p.page_size;
+    walk(0.f, [&](int2 s) { return w[(size_t)s.x * stride + s.y]; },
+         [&](int2 to, float v, float) { w[(size_t)to.x * stride + to.y] = v; });
+    return;
   }
+  const int piece = slice * p.slice_pieces + (int)threadIdx.x - row * p.slice_pieces;
+  uint8_t* base = p.pages[set] + (long long)h * p.head_bytes + piece * 16;
+  auto at = [&](int2 s) {
+    return reinterpret_cast<uint4*>(base + (long long)s.x * p.page_bytes + (long long)s.y * p.token_bytes);
+  };
+  walk(uint4{}, [&](int2 s) { return *at(s); },
+       [&](int2 to, uint4 v, float r) {
+         if (F8 && r != 1.f) {
+           const bool power = (__float_as_uint(r) & 0x7fffffu) == 0;
+           v = make_uint4(codes_times(v.x, r, power), codes_times(v.y, r, power), codes_times(v.z, r, power),
+                          codes_times(v.w, r, power));
+         }
+         *at(to) = v;
+       });
 }
 
 }  // namespace evict
