@@ -9,7 +9,12 @@
 // Kernel 2 moves rows: token j of the kept ones comes from position src(j) >= j. A block takes some
 // 16-byte columns of one head's rows of K or V (or its weights) and walks them in order: columns do not
 // meet, and a round's stores go to places below every later round's sources, so that one barrier a round, between
-// its loads and its stores, makes the move safe in place. Bound by HBM where there are heads enough.
+// its loads and its stores, makes the move safe in place.
+//
+// 8 sequences of 8 heads cut from 30 thousand tokens and more to 16384, d 128, 8 bits: 55 us for the selection, whose 64
+// blocks have 64 SMs and issue in 56 % of their slots, and 114 for the move, 4.6 TB/s: with narrow columns each
+// request of a warp touches up to 16 rows. Wider ones leave too few blocks (64 bytes: 191 us in all for 170), copies
+// through shared memory, more rounds ahead, gained nothing (172 to 201). One sequence: 13.7 us, latency.
 #pragma once
 
 #include "fa_rope.cuh"

@@ -588,6 +588,9 @@ __device__ __forceinline__ int split_row(const uint4& u, uint32_t (&w)[TERMS][2]
 // Four more warps split the queries and turn V. Shared memory carries 128 bytes a cycle, and that is what
 // this was laid out by (d = 128, cycles per key tile of one row tile): loads 256, S 512, V turned 384, PV
 // 256 = 1408, about an SM's share of the bandwidth (1400); K turned into 16 bits as well: 1792.
+// Chunks are bound by the chain S - softmax - P V, as over 16 bits, with less registers to a softmax thread and 16
+// warps' code past the instruction cache: 2048 tokens at 30720, Hq 16, Hkv 2, d 128: 455 us, 1.17 PFLOP/s (330 over
+// 16 bits), tensor pipe 50 %; 4 x 2000 fresh ones, Hkv 4: 168 us (76), as the split of an item's queries comes on top.
 template <int D, bool BF16, bool SPLIT, int REP, bool DIRECT, bool F8 = false>
 __global__ void __launch_bounds__(num_warps(F8) * 32, 1)
     fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -1261,7 +1264,7 @@ __global__ void __launch_bounds__(num_warps(F8) * 32, 1)
         if constexpr (F8) {
           // As below, in code that is small enough for the instruction cache next to that of the converting warps
           // (unrolled over all columns, with the scores held from one pass to the other, a chunk of 2048 tokens at 30720
-          // took 525 us): CH columns at a time, read again for the second pass. Each group of 8 columns has scales of its own.
+          // took 525 us, now 455): CH columns at a time, read again for the second pass. Each group of 8 columns has scales of its own.
           constexpr int CH = CW < 64 ? CW : 64;
           if (i < STEP)  // (the item's exponents, written before its first S; the next but one takes their place)
             cr = fmaxf(c * __uint_as_float((uint32_t)(127 + exps[(n_item & 1u) * LY::EXP_ROWS]) << 23), 1e-30f);
