@@ -116,9 +116,9 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) fa_evict_select_kernel(cons
     const int2 at = place_of(p, i);
     const int page = table[at.x];
     const bool fine = page >= 0 && page < p.num_pages;
-    const uint32_t key = order_of(p.w[((size_t)(fine ? page : 0) * p.Hkv + h) * p.page_size + at.y]);
+    const float w = fine ? p.w[((size_t)page * p.Hkv + h) * p.page_size + at.y] : 0.f;
     bad |= !fine;
-    return fine ? key : 0u;
+    return fine ? order_of(w) : 0u;
   };
   const bool cached = early <= p.keys;
   if (cached) {

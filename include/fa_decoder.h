@@ -199,7 +199,8 @@ int fa_paged_key_weights(const fa_paged_kv* kv, const float* k_scale, const fa_h
  *   kept       int32 [B, Hkv, budget], output: the position that each place's token had, -1 behind the
  *              last token of a shorter sequence
  *   new_lens   int32 [B], output: min(seq_lens[b], budget); may be seq_lens itself
- *   workspace  fa_paged_evict_workspace_bytes() bytes, 256-byte aligned, no initialisation
+ *   workspace  fa_paged_evict_workspace_bytes() bytes, 256-byte aligned, no initialisation; calls (or
+ *              replayed graphs) that may run at the same time need one each
  * Positions count from the front of the cache afterwards: rotate new keys by their own positions
  * (fa_qk_norm_rope) and append them without a table.
  * No page may stand twice in the tables. Weights on a page outside [0, num_pages) count as the smallest

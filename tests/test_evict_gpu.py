@@ -388,6 +388,20 @@ def test_prompt_then_tokens_with_eviction(fa):
     assert fa.fa_last_status() == 0 and torch.isfinite(w[table[0, :13].long()][:12]).all()
 
 
+def test_evict_from_a_cache_without_pages(fa):
+    """Every page is bad: nothing is looked at or moved, all weights count the same."""
+    empty = torch.empty(0, 3, 16, 64, dtype=torch.float16, device="cuda")
+    w = torch.empty(0, 3, 16, device="cuda")
+    table = torch.zeros(2, 2, dtype=torch.int32, device="cuda")
+    lens = torch.tensor([20, 3], dtype=torch.int32, device="cuda")
+    kept, now = fa.paged_evict(empty, empty.clone(), w, table, lens, 4, 1)
+    torch.cuda.synchronize()
+    assert fa.fa_last_status() == fa.FA_ERR_RANGE
+    fa.fa_clear_status()
+    assert kept[0].tolist() == [[0, 1, 2, 19]] * 3 and kept[1].tolist() == [[0, 1, 2, -1]] * 3
+    assert now.tolist() == [4, 3]
+
+
 def test_calls_that_autograd_would_record_are_refused(fa):
     def grad(x):
         return x.clone().requires_grad_()
