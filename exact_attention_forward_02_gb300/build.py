@@ -19,8 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 SRCS = [os.path.join(CSRC, f) for f in ("fa_fwd.cu", "fa_decoder.cu", "fa_compact.cu", "fa_rows8.cu", "fa_append8.cu",
                                          "fa_evict.cu")]
 DEPS = SRCS + [os.path.join(CSRC, h) for h in ("sm103_ptx.cuh", "fa_bwd.cuh", "philox.cuh", "fa_fwd_kernel.cuh",
-                                               "fa_rope.cuh", "fa_paged.cuh", "fa_append8.cuh", "fa_rows8.cuh", "fa_weigh.cuh",
-                                               "fa_evict.cuh", "fa_host.h",
+                                               "fa_rope.cuh", "fa_paged.cuh", "fa_append8.cuh", "append8_places.h",
+                                               "fa_rows8.cuh", "fa_weigh.cuh", "fa_evict.cuh", "fa_host.h",
                                                "fa_decoder_host.h")] + [
     os.path.join(ROOT, "include", h) for h in ("fa_fwd.h", "fa_decoder.h")]
 LIB = os.path.join(PKG, "libfa.so")

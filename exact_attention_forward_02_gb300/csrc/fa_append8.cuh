@@ -10,9 +10,7 @@
 //
 // Work: a unit is (sequence, page it gets tokens into, head of k or of v), one to W warps, which hold
 // the unit's rows in registers between the maximum and the rounding. No atomics: a page belongs to one
-// unit. Places for pages: a sequence with token rows [c0, c1) reaches at most
-// floor(c1 / page) - floor(c0 / page) + 2 pages, so places floor(c0 / page) + 2 b ... are enough for it,
-// and a place's sequence is found by a search over cu_seqlens.
+// unit. Places for pages, and whose they are: append8_places.h.
 //
 // HBM would allow a time of 3 d bytes an element row; what bounds it is the issue of instructions (69 % of the slots,
 // about 200 instructions to 256 elements, a warp's part of the search among them) and the one chain of a unit's loads,
@@ -20,6 +18,7 @@
 // several heads of a page, one search for many rows, took 74 to 82. 64 single tokens: 3.6 us, latency.
 #pragma once
 
+#include "append8_places.h"
 #include "fa_rope.cuh"
 
 namespace fa {
@@ -41,22 +40,13 @@ constexpr uint32_t APPEND8_LEAST = 27u << 23;      // 2^-100, of a page of zeros
 
 // as the 16-bit append has it
 __device__ __forceinline__ bool rows_fit(int begin, int end, int T) { return begin >= 0 && end >= begin && end <= T; }
-// place of sequence b's first page
-__device__ __forceinline__ uint32_t place_of(const Append8Params& p, int b) {
-  return (uint32_t)max(p.cu[b], 0) / (uint32_t)p.page_size + 2u * (uint32_t)b;
-}
-// the last sequence whose first place is at most `place` (the warp's 32 lanes look at 32 at a time)
+// (the warp's 32 lanes look at 32 sequences at a time)
 __device__ __forceinline__ int sequence_of_place(const Append8Params& p, uint32_t place, int lane) {
-  int lo = 0, n = p.B;
-  while (n > 0) {
-    const int step = (n + 31) / 32;
+  return search_places(p.B, [&](int lo, int step, int end) {
     const int i = lo + (lane + 1) * step - 1;
-    const bool le = i < lo + n && place_of(p, i) <= place;
-    const int parts = __popc(__ballot_sync(0xffffffffu, le));
-    lo += parts * step;
-    n = min(step - 1, n - parts * step);
-  }
-  return min(lo, p.B) - 1;
+    const bool le = i < end && first_place(p.cu[i], p.page_size, i) <= place;
+    return __popc(__ballot_sync(0xffffffffu, le));
+  });
 }
 
 // ROWS: rows that a lane holds between the two passes
@@ -93,17 +83,12 @@ __global__ void __launch_bounds__(ROW_THREADS, ROWS > 4 ? 2 : 4) fa_paged_append
   if (alive) {
     begin = p.cu[b];
     const int end = p.cu[b + 1], len = p.lens[b];
-    p0 = len - (end - begin);
-    const int first = max(p0, 0);
-    const int nth = (int)(place - place_of(p, b));
-    at = first / p.page_size + nth;  // page of the sequence
-    const long long from = (long long)at * p.page_size;
-    alive = rows_fit(begin, end, p.T) && end > begin;
-    if (alive && p0 < 0 && nth == 0 && lane == 0) atomicCAS(p.status, 0, FA_ERR_RANGE);  // tokens before position 0
-    alive = alive && from < len;
+    const Piece x = piece_of(place, b, begin, end, len, p.T, p.page_size);
+    if (x.early && lane == 0) atomicCAS(p.status, 0, FA_ERR_RANGE);  // tokens before position 0
+    alive = x.alive;
     if (alive) {
-      s0 = (int)max(first - from, 0ll);
-      s1 = (int)min((long long)p.page_size, len - from);
+      p0 = len - (end - begin), at = x.at, s0 = x.s0, s1 = x.s1;
+      const long long from = (long long)at * p.page_size;
       // tokens behind the rotation table are skipped
       const int told = p.rope.rot ? (int)min((long long)s1, max(p.rope.length - from, 0ll)) : s1;
       bool bad = told < s1;
