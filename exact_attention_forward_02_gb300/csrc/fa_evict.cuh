@@ -220,7 +220,13 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) fa_evict_select_kernel(cons
     place += __popc(all);
     ties += __popc(tied);
   }
-  for (int r = tid; r < p.recent; r += SELECT_THREADS) keep(need + r, early + r, table[place_of(p, early + r).x]);
+  for (int r = tid; r < p.recent; r += SELECT_THREADS) {
+    const int page = table[place_of(p, early + r).x];
+    bad |= page < 0 || page >= p.num_pages;
+    keep(need + r, early + r, page);
+  }
+  if (need == 0 && !cached)  // no weight has been asked for
+    for (int e = tid; e < place_of(p, early).x; e += SELECT_THREADS) bad |= table[e] < 0 || table[e] >= p.num_pages;
   atomicMin(&sm.lowest, lowest);
   __syncthreads();  // (with the block's own global writes)
   if (bad) atomicCAS(p.status, 0, FA_ERR_RANGE);

@@ -66,3 +66,34 @@ def test_append_with_offsets_that_decrease(fa, cu, lens, page):
                      list(range(half, 2 * half)) + list(range(2 * half + 4, 2 * half + 8))):
             assert ((x[..., part] == y[..., part]).all(-1) | (x[..., part] == old[..., part]).all(-1)).all()
     assert torch.equal(held(got)[~may], held(before)[~may])
+
+
+# total, budget, recent; with 45000 tokens and recent = budget no weight is looked at
+@pytest.mark.parametrize("total,budget,recent", [(300, 100, 40), (300, 100, 100), (300, 100, 0), (45000, 100, 100),
+                                                 (45000, 100, 30)])
+@pytest.mark.parametrize("where", ["to", "between", "last"])
+def test_eviction_reports_every_bad_page(fa, total, budget, recent, where):
+    """A bad entry among the places that rows move to, among tokens that go, among the last ones: always reported, and
+    what has no source or no place stays as it was."""
+    page, Hkv = 16, 2
+    b = c8.Batch8([0], [total], Hkv, 64, page, torch.float16, seed=total + recent, spread=1.0)
+    w = torch.rand(b.k_pages.shape[0], Hkv, page, generator=b.g).cuda()
+    at = {"to": 2, "between": 10, "last": (total - 1) // page}[where]
+    was = int(b.block_table[0, at])
+    b.block_table[0, at] = -1 if recent else b.k_pages.shape[0]
+    before = {n: getattr(b, n).clone() for n in CACHE}
+    before["w"] = w.clone()
+    kept, lens = fa.paged_evict(b.k_pages, b.v_pages, w, b.block_table, b.seq_lens, budget, recent, k_scale=b.k_scale,
+                                v_scale=b.v_scale)
+    assert status(fa) == fa.FA_ERR_RANGE and lens.tolist() == [budget]
+    kept, pages = kept[0].cpu().long(), b.block_table[0].cpu().long()
+    assert (kept[:, 1:] > kept[:, :-1]).all() and (kept[:, budget - recent:] == torch.arange(total - recent, total)).all()
+    now = {n: getattr(b, n) for n in CACHE}
+    assert torch.equal(held(now)[was], held(before)[was]) and torch.equal(w[was], before["w"][was])
+    for h in range(Hkv):
+        for j, i in enumerate(kept[h].tolist()):
+            to, src = int(pages[j // page]), int(pages[i // page])
+            if j // page == at:
+                continue  # no place
+            moved = before["w"][src, h, i % page] if i // page != at else before["w"][to, h, j % page]
+            assert w[to, h, j % page] == moved
