@@ -62,6 +62,7 @@ struct Barriers {
   uint64_t k_full[2][MAX_SLOTS], k_empty[2][MAX_SLOTS];  // [key tile of a unit]
   uint64_t raw_full[2][MAX_SLOTS], raw_empty[2][MAX_SLOTS];
   uint64_t s_full[2][2], s_empty[2][2];
+  uint64_t paused;  // the second warpgroup has read all it wants, and the next unit has one key tile
   uint64_t mma_drain;
   long long warp_cost[16];
   long long start_rem;
@@ -219,6 +220,7 @@ __global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
       mbar_init(smem_u32(&bars->s_full[x >> 1][x & 1]), 1);
       mbar_init(smem_u32(&bars->s_empty[x >> 1][x & 1]), 4);
     }
+    mbar_init(smem_u32(&bars->paused), 4);
     mbar_init(smem_u32(&bars->mma_drain), 1);
     bars->abort_flag = 0;
     fence_mbar_init();
@@ -288,9 +290,11 @@ __global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
     const int tok = (int)((uint32_t)col * p.by_g >> 16), t = q * p.tpt + tok;
     return col < p.cols && t < u.n ? p.L[(size_t)(u.t0 + t) * p.Hq + u.h * p.G + col - tok * p.G] * -1.4426950408889634f : 0.f;
   };
-  // Whoever brings tile m of the rows writes what belongs to them when the products of tile m - Q_SLOTS are done, so those
-  // of m - Q_SLOTS + 1 have been asked for at most, and a warpgroup has read all but its last two: tiles m - 6 and on
-  // are still looked at, and there is room for eight.
+  // Whoever brings tile m of the rows writes what belongs to them when the products of tile m - Q_SLOTS are done. The last
+  // of those were issued when the warpgroup's scores of the product but two before had been read, so it may still look
+  // at what belongs to tile m - Q_SLOTS - 2 and on, and there is room for eight. The second warpgroup has no part in
+  // units of one key tile, however many: before rows are brought for those, it has read all that its own last product
+  // wants (paused; s_empty says only that scores have been read).
   auto page_of = [&](int key) { return p.page_shift >= 0 ? (uint32_t)key >> p.page_shift : (uint32_t)key / (uint32_t)p.page_size; };
 
   if (warp == WARP_LOAD || warp == WARP_LOAD2) {
@@ -379,19 +383,28 @@ __global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
     const uint64_t dQ = umma_smem_desc<SW>(sQ, 16, SBO), dK = umma_smem_desc<SW>(sK, 16, SBO);
     uint32_t ks[2] = {0, 0}, k_par[2] = {0, 0}, nq = 0;  // places in K's rings; tiles of rows so far
     uint32_t sn[2] = {0, 0};                             // products of each warpgroup
+    // A pause of the second warpgroup is waited for when other rows come, or before its next product, so that its
+    // barrier is never a phase ahead.
+    bool pause = false, two = false;
+    uint32_t pauses = 0;
     bool ok = true;
+    auto ok_pause = [&]() {
+      if (pause) ok = wait_all(&bars->paused, pauses++ & 1u);
+      pause = false;
+      return ok;
+    };
     while (ok && walk.next(p, it)) {
       const int tiles = it.two ? 2 : 1;
+      if (it.two && !ok_pause()) break;
+      pause = pause || (two && !it.two);
+      two = it.two;
 #pragma unroll 1
       for (int q = it.q0; q < it.qn && ok; ++q) {
         if (!it.same) {  // the rows of before are given back when others come
           if (nq && elect_one()) umma_commit(smem_u32(&bars->q_empty[(nq - 1) % LY::Q_SLOTS]));
           __syncwarp();
-          // a warpgroup that has no part in the unit must not fall behind what is kept of the rows
-          if (!it.two)
-            for (uint32_t y = 1; y <= 2 && y <= sn[1] && ok; ++y)
-              ok = wait_all(&bars->s_empty[1][(sn[1] - y) & 1u], ((sn[1] - y) >> 1) & 1u);
-          if (!ok || !(ok = wait_all(&bars->q_full[nq % LY::Q_SLOTS], (nq / LY::Q_SLOTS) & 1u))) break;
+          if (!ok_pause()) break;
+          if (!(ok = wait_all(&bars->q_full[nq % LY::Q_SLOTS], (nq / LY::Q_SLOTS) & 1u))) break;
           ++nq;
         }
         const uint64_t db = dQ + (((nq - 1) % LY::Q_SLOTS * LY::Q_BYTES) >> 4);
@@ -646,6 +659,10 @@ __global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
         }
       }
       if (!ok) break;
+      if (g == 1 && mine && more && !nx.two) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->paused));
+      }
       if (mine && here.held) {
         float a, b;
         f2_split(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a, b);
