@@ -174,8 +174,9 @@ int fa_paged_evict(const fa_paged_kv* kv, float* k_scale, float* v_scale, float*
   p.table = block_table;
   p.table_stride = table_stride;
   p.B = B;
+  // (and a length that leaves them room: a block's steps over its positions are up to 1024 wide)
   const long long cap = (long long)table_stride * kv->page_size;
-  p.cap = cap < 0x7fffff00LL ? (int)cap : 0x7fffff00;
+  p.cap = cap < 0x7fff0000LL ? (int)cap : 0x7fff0000;
   p.budget = budget;
   p.recent = recent;
   p.kept = kept;

@@ -97,3 +97,14 @@ def test_eviction_reports_every_bad_page(fa, total, budget, recent, where):
                 continue  # no place
             moved = before["w"][src, h, i % page] if i // page != at else before["w"][to, h, j % page]
             assert w[to, h, j % page] == moved
+
+
+def test_eviction_with_a_length_at_the_end_of_32_bits(fa):
+    """A corrupt length over a table that covers 2^31 keys (all of its pages outside a cache without pages): cut, reported,
+    and the steps over the positions stay within 32 bits."""
+    empty = torch.empty(0, 1, 1 << 27, 64, dtype=torch.float16, device="cuda")
+    table = torch.zeros(1, 16, dtype=torch.int32, device="cuda")
+    lens = torch.tensor([0x7fffffff], dtype=torch.int32, device="cuda")
+    kept, now = fa.paged_evict(empty, empty.clone(), torch.empty(0, 1, 1 << 27, device="cuda"), table, lens, 5, 2)
+    assert status(fa) == fa.FA_ERR_RANGE
+    assert kept[0, 0].tolist() == [0, 1, 2, 0x7fff0000 - 2, 0x7fff0000 - 1] and now.tolist() == [5]
