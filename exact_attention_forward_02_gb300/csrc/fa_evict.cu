@@ -69,7 +69,7 @@ int fa_paged_key_weights(const fa_paged_kv* kv, const float* k_scale, const fa_h
   if (!(scale >= 0.f) || !isfinite(scale)) return FA_ERR_SCALE;
   if (B == 0 || T == 0 || q->H == 0) return FA_OK;
   if (kv->num_pages == 0 || kv->Hkv == 0 || q->H % kv->Hkv || q->H / kv->Hkv > 128 || B > MAX_SEQUENCES ||
-      (long long)T * q->H > 0x7fffffffLL)
+      (long long)T * q->H > 0x7fffffffLL || (long long)kv->Hkv * kv->page_size > 0xffffffffLL)
     return FA_ERR_SHAPE;
   if ((rc = check_heads(q)) != FA_OK) return rc;
   if (!L || !weights || !cu_seqlens || !seq_lens || (!block_table && table_stride)) return FA_ERR_NULL;

@@ -544,7 +544,8 @@ __global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
     // The thread's key in a unit: place of its weight, found two units ahead, so that its table entry, and then
     // its weight and scale, are there in time.
     struct Place {
-      int page, off;  // off: in the page's weights
+      int page;
+      uint32_t off;   // in the page's weights, which are fewer than 2^32
       bool held, old; // a cached token; not a new one
     };
     auto place_of = [&](const Unit& u) {
@@ -554,7 +555,7 @@ __global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
       x.held = key < u.len;
       x.old = key < u.len - u.n;
       x.page = x.held ? p.table[(size_t)u.b * p.table_stride + entry] : -1;
-      x.off = u.h * p.page_size + (key - (int)entry * p.page_size);
+      x.off = (uint32_t)u.h * (uint32_t)p.page_size + ((uint32_t)key - entry * (uint32_t)p.page_size);
       return x;
     };
     auto weight_at = [&](const Place& x) { return p.w + (size_t)x.page * p.Hkv * p.page_size + x.off; };

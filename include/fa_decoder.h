@@ -180,6 +180,7 @@ int fa_fwd_paged_fp8(const fa_paged_kv* kv, const float* k_scale, const float* v
  *           tokens i that see j of exp(scale <q_i, k_j> - L_i)
  * for every j < seq_lens[b] of the sequences that have new tokens; other places are left as they are.
  *   kv        the cache; v and dtype-independent fields as in fa_fwd_paged, V is not looked at
+ *             (a page holds fewer than 2^32 weights, Hkv * page_size, else FA_ERR_SHAPE)
  *   k_scale   NULL for a 16-bit cache in `dtype`
  *   max_q     the most new tokens of a sequence; more still give right results, more slowly
  * Sums are fp32, in an order that does not change. A page with tokens of a sequence that has new ones must
