@@ -233,7 +233,8 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) fa_evict_select_kernel(cons
   if (tid == 0) p.first[blockIdx.x] = F8 ? sm.lowest / p.page_size * p.page_size : sm.lowest;
   if constexpr (F8) {
     // New scales, some pages at a time; the sources of later pages lie in later pages, whose scales still stand.
-    uint32_t* tops = keys;  // [2][SCALE_PAGES], positive numbers in the order of their bits
+    // [2][SCALE_PAGES], numbers that are not negative in the order of their bits, + 1; 0: no token came from a page
+    uint32_t* tops = keys;
     constexpr int AT_ONCE = 8, CHUNK = AT_ONCE * SELECT_THREADS;
     const int group = p.page_size >= CHUNK ? 1 : min(SCALE_PAGES, CHUNK / p.page_size);
     const size_t plane = (size_t)p.B * p.Hkv * p.budget;
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) fa_evict_select_kernel(cons
         for (int y = 0; y < AT_ONCE; ++y) {
           const bool ok = from[y] >= 0 && from[y] < p.num_pages;
 #pragma unroll
-          for (int x = 0; x < 2; ++x) s[y][x] = ok ? p.scale[x][(size_t)from[y] * p.Hkv + h] : 0.f;
+          for (int x = 0; x < 2; ++x) s[y][x] = ok ? p.scale[x][(size_t)from[y] * p.Hkv + h] : -1.f;
         }
       };
       __syncthreads();
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) fa_evict_select_kernel(cons
           const int at = place_of(p, c0 + y * SELECT_THREADS + tid - j0).x;
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            if (s[y][x] > 0.f) atomicMax(&tops[x * SCALE_PAGES + at], __float_as_uint(s[y][x]));
+            if (s[y][x] >= 0.f) atomicMax(&tops[x * SCALE_PAGES + at], s[y][x] > 0.f ? __float_as_uint(s[y][x]) + 1u : 1u);
         }
       }
       __syncthreads();
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) fa_evict_select_kernel(cons
           const int at = place_of(p, j - j0).x;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float top = __uint_as_float(tops[x * SCALE_PAGES + at]);
+            const float top = __uint_as_float(max(tops[x * SCALE_PAGES + at], 1u) - 1u);
             p.ratio[x * plane + at0 + j] = top > 0.f ? s[y][x] / top : 1.f;
           }
         }
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) fa_evict_select_kernel(cons
       for (int i = tid; i < 2 * n; i += SELECT_THREADS) {
         const int x = i >= n, at = x ? i - n : i, page = table[g0 + at];
         const uint32_t top = tops[x * SCALE_PAGES + at];
-        if (page >= 0 && page < p.num_pages && top) p.scale[x][(size_t)page * p.Hkv + h] = __uint_as_float(top);
+        if (page >= 0 && page < p.num_pages && top) p.scale[x][(size_t)page * p.Hkv + h] = __uint_as_float(top - 1u);
       }
     }
   }
