@@ -508,6 +508,7 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int width = as_int(table.size(1), "the table's width");
     const int budget = as_int(a[5], "budget"), recent = as_int(a[6], "recent");
     if (budget < 1 || recent < 0 || recent > budget) bad_value("budget must be at least 1, and recent 0 to budget");
+    if (kv.Hkv == 0) bad_value("the cache must have heads");  // (the library's call would leave new_lens as it is)
     if (kept.defined()) index_of(kept, "kept", {B, kv.Hkv, budget});
     if (now.defined()) index_of(now, "new_lens", {B});
     if (ws.defined() && (ws.scalar_type() != at::kByte || !ws.is_contiguous()))

@@ -207,7 +207,7 @@ int fa_paged_key_weights(const fa_paged_kv* kv, const float* k_scale, const fa_h
  * No page may stand twice in the tables. Weights on a page outside [0, num_pages) count as the smallest
  * and rows there are not moved; a length past the table's width, or past 2^31 - 2^16, is cut to it; either
  * records FA_ERR_RANGE.
- * Two kernels. */
+ * Two kernels. B or kv->Hkv == 0: no-op (kept and new_lens are not written). */
 size_t fa_paged_evict_workspace_bytes(int B, int Hkv, int budget, int held8);
 int fa_paged_evict(const fa_paged_kv* kv, float* k_scale, float* v_scale, float* weights, int B,
                    const int* seq_lens, const int* block_table, int table_stride, int budget, int recent,
