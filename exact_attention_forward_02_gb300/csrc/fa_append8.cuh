@@ -97,6 +97,8 @@ __global__ void __launch_bounds__(ROW_THREADS, ROWS > 4 ? 2 : 4) fa_paged_append
       if (page < 0 || page >= p.num_pages) bad = true, alive = false;
       if (bad && lane == 0) atomicCAS(p.status, 0, FA_ERR_RANGE);
       alive = alive && s0 < s1;
+      // the slots that are written, and the rows that go there
+      alive = alive && in_bounds(p, s0 >= 0 && s1 <= p.page_size && h < p.Hkv && from + s0 >= p0 && from + s1 - p0 <= end - begin);
     }
   }
   const int pos0 = alive ? at * p.page_size : 0;  // of the page's first slot

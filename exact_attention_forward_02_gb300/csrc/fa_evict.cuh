@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) fa_evict_select_kernel(cons
   uint32_t place = __reduce_add_sync(0xffffffffu, lane < warp ? sm.part[lane] : 0u) + min(ties, left);
   int2* src = p.src + at0;
   auto keep = [&](int j, int i, int page) {
+    if (!in_bounds(p, j >= 0 && j < p.budget && i >= j && i < len)) return;
     kept[j] = i;
     src[j] = make_int2(page, place_of(p, i).y);
   };
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(MOVE_THREADS, 4) fa_evict_move_kernel(const __
       ok = 0;
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        if (s[i].x < 0 || s[i].x >= p.num_pages) continue;
+        if (s[i].x < 0 || s[i].x >= p.num_pages || !in_bounds(p, s[i].y >= 0 && s[i].y < p.page_size)) continue;
         ok |= 1u << i;
         v[i] = load(s[i]);
         r[i] = F8 && !weights ? ratios[j0 + i * rows + row] : 1.f;
@@ -355,7 +356,8 @@ __global__ void __launch_bounds__(MOVE_THREADS, 4) fa_evict_move_kernel(const __
         if (cur_ok >> i & 1u) {
           const int2 at = place_of(p, j0 + i * rows + row);
           const int page = table[at.x];
-          if (page >= 0 && page < p.num_pages) store(make_int2(page, at.y), cur[i], cur_r[i]);
+          if (page >= 0 && page < p.num_pages && in_bounds(p, at.x < p.table_stride && at.y >= 0 && at.y < p.page_size))
+            store(make_int2(page, at.y), cur[i], cur_r[i]);
         }
         cur[i] = nxt[i];
         cur_r[i] = nxt_r[i];

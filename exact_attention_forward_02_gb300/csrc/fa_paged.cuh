@@ -108,20 +108,6 @@ struct Params {
   int page_shift;  // log2 of the page size, -1 where that is none
 };
 
-// Debug builds (FA_DEBUG) check the places of tile copies, partial states and output rows; one
-// outside records FA_ERR_BOUNDS. Stores, and the join of an item whose pieces it concerns, are then
-// skipped; a tile copy is only recorded (TMA reads zeros outside, and its barrier expects the bytes).
-// Release builds compile it out.
-__device__ __forceinline__ bool in_bounds(const Params& p, bool ok) {
-#ifdef FA_DEBUG
-  if (!ok) atomicCAS(p.status, 0, FA_ERR_BOUNDS);
-  return ok;
-#else
-  (void)p, (void)ok;
-  return true;
-#endif
-}
-
 __device__ __forceinline__ int token_of_row(const Params& p, int row) { return (int)((uint32_t)row * p.by_g >> 16); }
 __host__ __device__ constexpr int part_floats(int d, int rows) { return rows * (d + 2); }
 

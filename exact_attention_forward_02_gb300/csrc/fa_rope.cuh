@@ -22,6 +22,21 @@
 
 namespace fa {
 
+// Debug builds (FA_DEBUG) check the places of tile copies, partial states, rows and weights; one outside records
+// FA_ERR_BOUNDS in the status word of the kernel's parameters. Stores, and the join of an item whose pieces it
+// concerns, are then skipped; a tile copy is only recorded (TMA reads zeros outside, and its barrier expects
+// the bytes). Release builds compile it out.
+template <typename P>
+__device__ __forceinline__ bool in_bounds(const P& p, bool ok) {
+#ifdef FA_DEBUG
+  if (!ok) atomicCAS(p.status, 0, FA_ERR_BOUNDS);
+  return ok;
+#else
+  (void)p, (void)ok;
+  return true;
+#endif
+}
+
 struct HeadsDev {
   uint16_t* ptr;
   long long bs, ts, hs;  // batch, token and head stride in elements

@@ -339,6 +339,7 @@ __global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
         const uint32_t bar = smem_u32(&full[slot]);
         if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(live * BOX_CHUNKS) * box_bytes);
         __syncwarp();
+        in_bounds(p, my_chunk >= BOX_CHUNKS || my_box >= live || (it.h < p.Hkv && page >= 0 && page <= p.num_pages));
         if (my_chunk < BOX_CHUNKS && my_box < live)
           tma_load_4d(sLoad + slot * SLOT_BYTES + box_off, &tmK, bar, my_chunk * 64, p.page_size > BN ? key % p.page_size : 0,
                       it.h, page);
@@ -358,6 +359,7 @@ __global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bars->q_full[qs]), q_bytes);
           __syncwarp();
+          in_bounds(p, it.t0 >= 0 && it.t0 + q * p.tpt < p.T && (it.h + 1) * p.G <= p.Hq);
           if (lane < LY::CHUNKS)
             tma_load_3d(sQ + qs * LY::Q_BYTES + lane * LY::CHUNK_BYTES, &tmQ, smem_u32(&bars->q_full[qs]), lane * 64,
                         it.h * p.G, it.t0 + q * p.tpt);
@@ -456,8 +458,9 @@ __global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
         const uint32_t qs = nq % LY::Q_SLOTS, round = nq / LY::Q_SLOTS;
         const int rows = min(p.tpt, it.n - q * p.tpt) * p.G;
         auto load = [&](int r) {  // (zeros where there is no row)
-          if (r >= rows) return make_uint4(0, 0, 0, 0);
           const int tok = (int)((uint32_t)r * p.by_g >> 16);
+          if (r >= rows || !in_bounds(p, it.t0 >= 0 && it.t0 + q * p.tpt + tok < p.T && it.h * p.G + r - tok * p.G < p.q.H))
+            return make_uint4(0, 0, 0, 0);
           return *reinterpret_cast<const uint4*>(p.q.ptr + (long long)(it.t0 + q * p.tpt + tok) * p.q.ts +
                                                  (long long)(it.h * p.G + r - tok * p.G) * p.q.hs + ql * 8);
         };
@@ -664,7 +667,8 @@ __global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->paused));
       }
-      if (mine && here.held) {
+      if (mine && here.held && in_bounds(p, here.page >= 0 && here.page < p.num_pages && it.h < p.Hkv &&
+                                                here.off / (uint32_t)p.page_size == (uint32_t)it.h)) {
         float a, b;
         f2_split(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a, b);
         *weight_at(here) = w_here + (a + b);
