@@ -518,6 +518,9 @@ def paged_append_fp8(k, v, k_pages, v_pages, k_scale, v_scale, block_table, cu_s
     An element is scale * code. A page that gets its first token takes the smallest power of two that
     holds its new tokens; one that has older tokens keeps its scale or, where the new ones need a larger
     one, takes that and its codes are rounded anew (see include/fa_decoder.h).
+
+    `rope` turns a key by its place in the cache. After paged_evict that is not the token's position any more: rotate
+    by qk_norm_rope with `positions` and leave `rope` out.
     """
     r = _calls().append_fp8(k, v, k_pages, v_pages, block_table, cu_seqlens, seq_lens, rope, interleaved, stream,
                             k_scale, v_scale)
@@ -561,6 +564,9 @@ def paged_evict(k_pages, v_pages, weights, block_table, seq_lens, budget: int, r
     behind the last token of a shorter sequence), and int32 [B], the lengths from now on; allocated unless
     given (new_lens may be seq_lens). `workspace`: a uint8 tensor of at least
     fa_paged_evict_workspace_bytes(...) bytes, allocated for the call when None.
+
+    From then on a cached token's place is not its position: rotate new queries and keys by the tokens' own positions
+    (qk_norm_rope with `positions`) and append them without `rope`.
     """
     r = _calls().evict(k_pages, v_pages, weights, block_table, seq_lens, budget, recent, k_scale, v_scale, kept,
                        new_lens, workspace, stream)

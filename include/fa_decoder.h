@@ -202,8 +202,9 @@ int fa_paged_key_weights(const fa_paged_kv* kv, const float* k_scale, const fa_h
  *   new_lens   int32 [B], output: min(seq_lens[b], budget); may be seq_lens itself
  *   workspace  fa_paged_evict_workspace_bytes() bytes, 256-byte aligned, no initialisation; calls (or
  *              replayed graphs) that may run at the same time need one each
- * Positions count from the front of the cache afterwards: rotate new keys by their own positions
- * (fa_qk_norm_rope) and append them without a table.
+ * A cached token's place is no longer its position afterwards, and a table given to the append would turn
+ * new keys by their places: rotate new queries and keys by the tokens' own positions (fa_qk_norm_rope with
+ * `positions`) and append them without a table.
  * No page may stand twice in the tables. Weights on a page outside [0, num_pages) count as the smallest
  * and rows there are not moved; a length past the table's width, or past 2^31 - 2^16, is cut to it; either
  * records FA_ERR_RANGE.
