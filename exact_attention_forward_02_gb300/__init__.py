@@ -531,7 +531,11 @@ def paged_append_fp8(k, v, k_pages, v_pages, k_scale, v_scale, block_table, cu_s
 def attention_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_seqlens, seq_lens, max_q: int,
                         causal: bool = True, scale: float | None = None, out=None, lse=None, workspace=None,
                         stream=None):
-    """attention_paged over a cache held in 8 bits (see paged_append_fp8); q, O (fp16/bf16) and L as there."""
+    """attention_paged over a cache held in 8 bits (see paged_append_fp8); q, O (fp16/bf16) and L as there.
+
+    Pages whose v_scale lies far below the largest of their sequence count with fewer bits: with an error of 2^-28 / r of
+    their weights at a ratio of r (see include/fa_decoder.h).
+    """
     r = _calls().attend_fp8(q, k_pages, v_pages, block_table, cu_seqlens, seq_lens, max_q, causal, scale, out, lse,
                             workspace, stream, k_scale, v_scale)
     if type(r) is int:

@@ -162,9 +162,13 @@ int fa_paged_append_fp8(const fa_paged_kv* kv, float* k_scale, float* v_scale, c
                         void* stream);
 
 /* fa_fwd_paged_fp8 -- fa_fwd_paged over such a cache: q and O in `dtype`, everything else as there (the
- * workspace, too, is fa_fwd_paged_workspace_bytes()). Products take the bytes exactly as they are held; P
- * is held in 11 bits with v_scale in it. Scales must be positive and finite, or 0 for a page of zeros;
- * where the v_scale of a page is below 2^-40 of another's of the same sequence it may count as that. */
+ * workspace, too, is fa_fwd_paged_workspace_bytes()). Products take the bytes exactly as they are held, and
+ * an element of q to within 2^-17 of its row's largest. P is held in 11 bits with v_scale in it, but no
+ * finer than 2^-28 of the row's largest weight times the largest v_scale of the sequence's pages (2^-32 of
+ * it with more than 16 rows of q to a key head, max_q Hq / Hkv). So a page whose v_scale is r times the
+ * largest, r < 2^-16, counts with an error of 2^-28 / r of its largest weights, and from r = 2^-28 on not at
+ * all (2^-20 and 2^-32), even where the page of the large scale carries next to no weight. Scales must be
+ * positive and finite, or 0 for a page of zeros. */
 int fa_fwd_paged_fp8(const fa_paged_kv* kv, const float* k_scale, const float* v_scale, const fa_heads* q,
                      const fa_heads* O, float* L, int B, int T, int max_q, const int* cu_seqlens,
                      const int* seq_lens, const int* block_table, int table_stride, float scale, int causal,
