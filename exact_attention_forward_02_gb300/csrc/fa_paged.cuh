@@ -72,6 +72,9 @@ __host__ __device__ constexpr uint32_t regs_softmax(bool f8) { return f8 ? 168 :
 __host__ __device__ constexpr uint32_t regs_other(bool f8) { return f8 ? 88 : 104; }
 constexpr uint32_t TMEM_COLS = 512, TMEM_S0 = 0, TMEM_O0 = 256;  // S0 | S1 | O0 | O1
 constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units, as in the dense kernel
+// F8: factors of scores (scale, a row's 2^e, a page's k_scale) are at least this, so that what a row does not see stays at
+// -inf where one of them is 0
+constexpr float LEAST_NORMAL = 1.17549435e-38f;  // 2^-126
 constexpr int SMEM_LIMIT = 232448;
 constexpr int MAX_SLOTS = 8;
 constexpr int COMBINE_THREADS = 256;
@@ -1253,7 +1256,7 @@ __global__ void __launch_bounds__(num_warps(F8) * 32, 1)
           // took 525 us, now 455): CH columns at a time, read again for the second pass. Each group of 8 columns has scales of its own.
           constexpr int CH = CW < 64 ? CW : 64;
           if (i < STEP)  // (the item's exponents, written before its first S; the next but one takes their place)
-            cr = fmaxf(c * __uint_as_float((uint32_t)(127 + exps[(n_item & 1u) * LY::EXP_ROWS]) << 23), 1e-30f);
+            cr = fmaxf(p.c * __uint_as_float((uint32_t)(127 + exps[(n_item & 1u) * LY::EXP_ROWS]) << 23), LEAST_NORMAL);
           // the largest scale of V (positive numbers in the order of their bits)
           const float vt = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < 16 ? 0u : __float_as_uint(scale_now)));
           float beta = 1.f;  // what O~'s unit shrinks by
@@ -1265,7 +1268,7 @@ __global__ void __launch_bounds__(num_warps(F8) * 32, 1)
           }
           // K's scales, and log2 of V's in the unit of P' (a page whose V is below 2^-40 of the largest counts as that)
           const uint32_t scales = smem_u32(smem + LY::OFF_SCALE) + (uint32_t)warp * (SPLIT ? 256u : 128u);
-          st_shared_u32(scales + lane * 4, __float_as_uint(lane < 16 ? fmaxf(scale_now, 1e-30f)
+          st_shared_u32(scales + lane * 4, __float_as_uint(lane < 16 ? fmaxf(scale_now, LEAST_NORMAL)
                                                                      : log2f(fmaxf(scale_now * vinv, 1.1641532182693481e-10f))));
           __syncwarp();
           const uint32_t tC = tS + copy * CW;
@@ -1352,7 +1355,7 @@ __global__ void __launch_bounds__(num_warps(F8) * 32, 1)
               ld_shared_v4(scales + 64 + (q / 8 + y * 4) * 4, l4);
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const float cg = fmaxf(cr * k4[e], 1e-30f), ng = nb + l4[e];
+                const float cg = fmaxf(cr * k4[e], LEAST_NORMAL), ng = nb + l4[e];
                 const uint64_t c2 = f2(cg, cg), n2 = f2(ng, ng);
                 uint64_t acc[2];
 #pragma unroll

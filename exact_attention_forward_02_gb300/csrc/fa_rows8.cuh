@@ -489,7 +489,6 @@ __global__ void __launch_bounds__(R8_THREADS, 1)
     const uint32_t myP = sP + (uint32_t)(g * LY::P_BYTES + kk * LY::NP);
     const uint32_t sw = R == 8 ? (kk >> 2) & 1 : (kk >> 1) & 3;  // swizzle of the row's pieces
     float* const tops = reinterpret_cast<float*>(smem + LY::OFF_STATE) + LY::JOINS * LY::STATE_FLOATS + g * 4 * R;  // [4][R]
-    const float c = fmaxf(p.c, 1e-30f);
     // Tiles of the warpgroup so far. Its products P V are waited for one by one, before the next one's weights are
     // given out, so that their barrier is never a phase ahead (which its parity could not tell).
     uint32_t kt = 0;
@@ -557,8 +556,8 @@ __global__ void __launch_bounds__(R8_THREADS, 1)
           const signed char* ex = exps + (n_item & 7u) * 32;
 #pragma unroll
           for (int r = 0; r < R / 2; ++r) {
-            const float x = r * 2 < rows ? fmaxf(c * __uint_as_float((uint32_t)(127 + ex[2 * r]) << 23), 1e-30f) : 0.f;
-            const float y = r * 2 + 1 < rows ? fmaxf(c * __uint_as_float((uint32_t)(127 + ex[2 * r + 1]) << 23), 1e-30f) : 0.f;
+            const float x = r * 2 < rows ? p.c * __uint_as_float((uint32_t)(127 + ex[2 * r]) << 23) : 0.f;
+            const float y = r * 2 + 1 < rows ? p.c * __uint_as_float((uint32_t)(127 + ex[2 * r + 1]) << 23) : 0.f;
             c2[r] = f2(x, y);
           }
         }

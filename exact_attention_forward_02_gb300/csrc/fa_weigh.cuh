@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(num_warps(MODE) * 32, 1)
       if (more) fetch(then, nx.h, w_then, k_then);
       const bool mine = g == 0 || it.two;
       const int key = it.key0 + g * BN + wq * 32 + lane, ctx = it.len - it.n;
-      const float ct = fmaxf(p.c * k_here, 1e-30f);
+      const float ct = p.c * k_here;
       const uint64_t c2 = f2(ct, ct);
       uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll 1
