@@ -14,8 +14,8 @@
 //
 // HBM would allow a time of 3 d bytes an element row; what bounds it is the issue of instructions (69 % of the slots,
 // about 200 instructions to 256 elements, a warp's part of the search among them) and the one chain of a unit's loads,
-// search to scale. 29582 ragged tokens of 8 heads, d 128, pages of 64, fp16: 56 us, 3.4 TB/s of 6.8. Units that walk
-// several heads of a page, one search for many rows, took 74 to 82. 64 single tokens: 3.6 us, latency.
+// search to scale. 29582 ragged tokens of 8 heads, d 128, pages of 64, fp16: 57 us, 3.4 TB/s of 6.8. Units that walk
+// several heads of a page, one search for many rows, took 74 to 82. 64 single tokens: 3.5 us, latency.
 #pragma once
 
 #include "append8_places.h"

@@ -11,10 +11,10 @@
 // meet, and a round's stores go to places below every later round's sources, so that one barrier a round, between
 // its loads and its stores, makes the move safe in place.
 //
-// 8 sequences of 8 heads cut from 30 thousand tokens and more to 16384, d 128, 8 bits: 55 us for the selection, whose 64
-// blocks have 64 SMs and issue in 56 % of their slots, and 114 for the move, 4.6 TB/s: with narrow columns each
+// 8 sequences of 8 heads cut from 30 thousand tokens and more to 16384, d 128, 8 bits: 56 us for the selection, whose 64
+// blocks have 64 SMs and issue in 56 % of their slots, and 113 for the move, 4.7 TB/s: with narrow columns each
 // request of a warp touches up to 16 rows. Wider ones leave too few blocks (64 bytes: 191 us in all for 170), copies
-// through shared memory, more rounds ahead, gained nothing (172 to 201). One sequence: 13.7 us, latency.
+// through shared memory, more rounds ahead, gained nothing (172 to 201). One sequence: 16 us, latency.
 #pragma once
 
 #include "fa_rope.cuh"

@@ -9,7 +9,8 @@
 //                   rows of bf16
 //   O^T = V^T P^T   [d x rows]: a V tile as it is held is the left operand too (its keys along K), and P^T is
 //                   split into four E5M2 numbers side by side, N = 4 R columns: P' = p1 + p2 + p3 + p4 takes
-//                   all 11 bits of P' in fp16, and E5M2 has fp16's exponents, so that small weights count
+//                   all 11 bits of P' in fp16; what is cut off is half of E5M2's least number, 2^-17, of P' that
+//                   reaches 2^11 in the row's largest weight
 // A product then costs by its N instead of 128: shared memory carries 256 (loads) + 128 (S) + 128 (PV) of the
 // 1400 cycles. What is left is the issue of the products, about 95 cycles each: with 12 of them to a tile from one
 // warp the kernel took 1600 cycles a tile, so there are 8, and a warp for S and one for PV.

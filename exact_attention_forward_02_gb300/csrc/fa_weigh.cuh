@@ -23,8 +23,8 @@
 // box by box), 9 MMA issuer. Single tokens are bound by HBM (K is read once), chunks by the tensor cores and the
 // exponentials, which take the same time (128 x 128 scores: 545 and 512 cycles). Neither is reached: a unit of few rows
 // takes 2600 cycles where its bytes take 1400, the chain from its keys to its sums (64 ragged sequences, 8 key heads,
-// d 128, pages of 16: 80 us in 8 bits, 3.7 TB/s, 95 in 16, 6.0 TB/s), and a chunk is held up by that chain and by 256
-// units for 152 SMs (2048 tokens at 30720, Hq 16, Hkv 2, d 128: 305 us, 0.87 PFLOP/s, tensor pipe 35 %).
+// d 128, pages of 16: 81 us in 8 bits, 3.6 TB/s, 94 in 16, 6.0 TB/s), and a chunk is held up by that chain and by 256
+// units for 152 SMs (2048 tokens at 30720, Hq 16, Hkv 2, d 128: 304 us, 0.87 PFLOP/s, tensor pipe 35 %).
 #pragma once
 
 #include "fa_paged.cuh"

@@ -200,7 +200,7 @@ int fa_paged_key_weights(const fa_paged_kv* kv, const float* k_scale, const fa_h
  * and weights move together, in order, to positions 0 .. budget - 1 of the sequence's pages; what stands
  * behind is left as it is, and so are shorter sequences.
  * 8-bit caches: the scale of a page becomes the largest of those that its tokens come from, and codes from
- * under smaller ones are rounded anew.
+ * under smaller ones are rounded anew (times the ratio of the scales, exact for powers of two, else in fp32).
  *   kept       int32 [B, Hkv, budget], output: the position that each place's token had, -1 behind the
  *              last token of a shorter sequence
  *   new_lens   int32 [B], output: min(seq_lens[b], budget); may be seq_lens itself
