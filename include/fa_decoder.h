@@ -168,7 +168,8 @@ int fa_paged_append_fp8(const fa_paged_kv* kv, float* k_scale, float* v_scale, c
  * it with more than 16 rows of q to a key head, max_q Hq / Hkv). So a page whose v_scale is r times the
  * largest, r < 2^-16, counts with an error of 2^-28 / r of its largest weights, and from r = 2^-28 on not at
  * all (2^-20 and 2^-32), even where the page of the large scale carries next to no weight. Scales must be
- * positive and finite, or 0 for a page of zeros. */
+ * positive and at most 2^126, or 0 for a page of zeros; where all v_scale of a sequence lie below 2^-100, P
+ * counts with fewer bits. */
 int fa_fwd_paged_fp8(const fa_paged_kv* kv, const float* k_scale, const float* v_scale, const fa_heads* q,
                      const fa_heads* O, float* L, int B, int T, int max_q, const int* cu_seqlens,
                      const int* seq_lens, const int* block_table, int table_stride, float scale, int causal,
